@@ -78,6 +78,11 @@ def _log(rng, lo, hi):
     return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
 
 
+def _odd(rng, lo, hi):
+    """An odd number of groups: the last tile is not a whole one."""
+    return 2 * rng.randint(lo // 2, (hi - 1) // 2) + 1
+
+
 def draw(rng):
     op = rng.choice(["route", "route", "backward", "exchange", "experts", "experts"])
     dtype = rng.choice(["f32", "bf16", "f16"])
@@ -116,7 +121,7 @@ def draw(rng):
     topk = rng.randint(1, min(8, experts))
     elsewhere = tokens * topk >= 32 and rng.random() < 0.33
     return _experts(tokens, topk, experts, experts * (4 if elsewhere else 1),
-                    group * rng.randint(4, 5120 // group), group * rng.randint(2, 2048 // group),
+                    group * _odd(rng, 4, 5120 // group), group * _odd(rng, 2, 2048 // group),
                     group, rng.choice(["bf16", "f16"]))
 
 
