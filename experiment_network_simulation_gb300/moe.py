@@ -1,0 +1,296 @@
+"""Routed-expert operators on torch tensors: the binding of mv_route,
+mv_route_backward, mv_exchange and mv_experts (``include/mv.h``).
+
+    ids, weights = route(logits, topk, ...)          # the router
+    dlogits = route_backward(logits, ids, dweights)  # its gradient
+    load, sent = exchange(ids, place, ranks)         # tokens from rank to rank
+    y = experts(x, ids, weights, w13, s13, w2, s2)   # the chosen experts' products
+
+``sent`` times the bytes of a token is the byte matrix that
+:func:`.inputs.moe_workload` makes an all-to-all of.  Every call is enqueued
+on ``stream`` (default: the current one of the inputs' device) and returns
+without waiting; outputs and workspaces come from torch's allocator on that
+stream.  Malformed arguments raise ValueError, what the library refuses
+:class:`.mv.MVError`.  There is no CPU fallback: tensors have to be on a CUDA
+device.
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+
+import torch
+
+from . import mv
+
+SOFTMAX, SIGMOID = 0, 1
+_SCORES = {"softmax": SOFTMAX, "sigmoid": SIGMOID}
+_RULES = {"max": 0, "top2": 1}
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+MAX_EXPERTS, MAX_TOPK, MAX_GROUPS, MAX_RANKS = 1024, 32, 32, 8192
+
+_vp, _u32, _u64, _f32 = C.c_void_p, C.c_uint32, C.c_uint64, C.c_float
+
+
+class RouteDesc(C.Structure):
+    _fields_ = [("tokens", _u64), ("row_stride", _u64), ("experts", _u32), ("topk", _u32),
+                ("groups", _u32), ("top_groups", _u32), ("dtype", _u32), ("scores", _u32),
+                ("group_rule", _u32), ("renorm", _u32), ("scale", _f32), ("logits", _vp),
+                ("bias", _vp), ("ids", _vp), ("weights", _vp)]
+
+
+class RouteGradDesc(C.Structure):
+    _fields_ = [("tokens", _u64), ("row_stride", _u64), ("experts", _u32), ("topk", _u32),
+                ("dtype", _u32), ("scores", _u32), ("renorm", _u32), ("scale", _f32),
+                ("logits", _vp), ("ids", _vp), ("dweights", _vp), ("dlogits", _vp)]
+
+
+class ExchangeDesc(C.Structure):
+    _fields_ = [("batches", _u64), ("tokens", _u64), ("topk", _u32), ("experts", _u32),
+                ("sources", _u32), ("ranks", _u32), ("once", _u32), ("ids", _vp), ("place", _vp),
+                ("starts", _vp), ("load", _vp), ("sent", _vp)]
+
+
+class ExpertsDesc(C.Structure):
+    _fields_ = [("tokens", _u64), ("row_stride", _u64), ("topk", _u32), ("experts", _u32),
+                ("hidden", _u32), ("inner", _u32), ("group", _u32), ("dtype", _u32), ("x", _vp),
+                ("ids", _vp), ("weights", _vp), ("w13", _vp), ("s13", _vp), ("w2", _vp),
+                ("s2", _vp), ("y", _vp)]
+
+
+_lib = None
+
+
+def _library() -> C.CDLL:
+    global _lib
+    if _lib is None:
+        lib = mv.library()
+        lib.mv_route.argtypes = [C.POINTER(RouteDesc), _vp]
+        lib.mv_route_backward.argtypes = [C.POINTER(RouteGradDesc), _vp]
+        lib.mv_exchange.argtypes = [C.POINTER(ExchangeDesc), _vp]
+        lib.mv_experts_workspace_bytes.argtypes = [C.POINTER(ExpertsDesc), C.POINTER(_u64)]
+        lib.mv_experts.argtypes = [C.POINTER(ExpertsDesc), _vp, _u64, _vp]
+        for f in ("mv_route", "mv_route_backward", "mv_exchange", "mv_experts_workspace_bytes",
+                  "mv_experts"):
+            getattr(lib, f).restype = C.c_int
+        _lib = lib
+    return _lib
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(name: str, t, dtype, shape, device=None, rows_apart: bool = False):
+    """Check one argument: type, device, shape (None: any size), dense layout."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is a torch tensor, not {type(t).__name__}")
+    if not t.is_cuda:
+        raise RuntimeError(f"{name} is on {t.device}; the operators need a CUDA device, "
+                           "there is no CPU fallback")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dtype not in dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {' or '.join(str(d) for d in dtype)}")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not "
+                         f"({', '.join('any' if s is None else str(s) for s in shape)})")
+    if rows_apart:
+        if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError(f"{name}'s rows are not dense and apart (strides {t.stride()})")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous (strides {t.stride()})")
+
+
+def _stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+class _On:
+    """The device and the stream of one call."""
+
+    def __init__(self, device, stream, inputs):
+        self.stack = []
+        if device.index != torch.cuda.current_device():
+            self.stack.append(torch.cuda.device(device))
+        if stream is not None:
+            _need(stream.device == device, f"the stream is on {stream.device}, not on {device}")
+            if stream != torch.cuda.current_stream(device):
+                self.stack.append(torch.cuda.stream(stream))
+                for t in inputs:
+                    if t is not None:
+                        t.record_stream(stream)
+        self.device = device
+
+    def __enter__(self):
+        for c in self.stack:
+            c.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.stack):
+            c.__exit__(*exc)
+
+
+def _done(rc: int, what: str):
+    if rc != mv.MV_OK:
+        raise mv.MVError(rc, what)
+
+
+def _choice(what: str, value, table: dict) -> int:
+    if value not in table:
+        raise ValueError(f"{what} is one of {', '.join(table)}, not {value!r}")
+    return table[value]
+
+
+def route(logits, topk: int, *, scores: str = "softmax", bias=None, groups: int = 1,
+          top_groups: int = 1, group_rule: str = "max", renorm: bool = True, scale: float = 1.0,
+          stream=None):
+    """Choose ``topk`` experts for every token: (ids int32, weights float32), [tokens, topk].
+
+    ``logits`` [tokens, experts] (float32, float16 or bfloat16; rows may lie
+    apart).  Experts are ordered by their ``scores`` ("softmax" or "sigmoid")
+    plus ``bias`` (float32 [experts]), within the ``top_groups`` of ``groups``
+    equal groups that have the greatest value: their best expert's ("max") or
+    the sum of their two best ("top2").  Equal values go to the lowest index.
+    The weights are the chosen experts' scores, without the bias, divided by
+    their sum if ``renorm``, times ``scale``.  An expert whose logit or bias is
+    -inf or NaN is closed; slots that no open expert is left for hold id -1
+    and weight 0.
+    """
+    _tensor("logits", logits, _DTYPES, (None, None), rows_apart=True)
+    tokens, n = logits.shape
+    _need(1 <= n <= MAX_EXPERTS, f"{n} experts: 1 to {MAX_EXPERTS} are taken")
+    _need(1 <= groups <= MAX_GROUPS and n % groups == 0,
+          f"{groups} groups: at most {MAX_GROUPS}, and {n} experts divide into them evenly")
+    _need(1 <= top_groups <= groups, f"top_groups is 1 to {groups}, not {top_groups}")
+    most = min(MAX_TOPK, top_groups * (n // groups))
+    _need(1 <= topk <= most, f"topk is 1 to {most}, not {topk}")
+    _need(math.isfinite(scale), f"scale is {scale}")
+    s, r = _choice("scores", scores, _SCORES), _choice("group_rule", group_rule, _RULES)
+    if bias is not None:
+        _tensor("bias", bias, (torch.float32,), (n,), logits.device)
+    with _On(logits.device, stream, (logits, bias)) as on:
+        ids = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
+        d = RouteDesc(tokens, _stride(logits), n, topk, groups, top_groups, _DTYPES[logits.dtype],
+                      s, r, bool(renorm), scale, logits.data_ptr(),
+                      None if bias is None else bias.data_ptr(), ids.data_ptr(),
+                      weights.data_ptr())
+        _done(_library().mv_route(C.byref(d), on), "mv_route")
+    return ids, weights
+
+
+def route_backward(logits, ids, dweights, *, scores: str = "softmax", renorm: bool = True,
+                   scale: float = 1.0, stream=None):
+    """Gradient of :func:`route`'s weights: dlogits, like ``logits`` and dense.
+
+    ``ids`` are route's for these logits, ``dweights`` (float32) the weights'
+    gradient.  The choice of experts and the bias have no gradient.
+    """
+    _tensor("logits", logits, _DTYPES, (None, None), rows_apart=True)
+    tokens, n = logits.shape
+    _need(1 <= n <= MAX_EXPERTS, f"{n} experts: 1 to {MAX_EXPERTS} are taken")
+    _tensor("ids", ids, (torch.int32,), (tokens, None), logits.device)
+    topk = ids.shape[1]
+    _need(1 <= topk <= min(MAX_TOPK, n), f"topk is 1 to {min(MAX_TOPK, n)}, not {topk}")
+    _tensor("dweights", dweights, (torch.float32,), (tokens, topk), logits.device)
+    _need(math.isfinite(scale), f"scale is {scale}")
+    s = _choice("scores", scores, _SCORES)
+    with _On(logits.device, stream, (logits, ids, dweights)) as on:
+        out = torch.empty((tokens, n), dtype=logits.dtype, device=logits.device)
+        d = RouteGradDesc(tokens, _stride(logits), n, topk, _DTYPES[logits.dtype], s, bool(renorm),
+                          scale, logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(),
+                          out.data_ptr())
+        _done(_library().mv_route_backward(C.byref(d), on), "mv_route_backward")
+    return out
+
+
+def exchange(ids, place, ranks: int, *, sources: int | None = None, starts=None,
+             once: bool = True, stream=None):
+    """Count an expert-parallel exchange: (load [experts], sent [sources, ranks]), int32.
+
+    ``ids`` int32 [tokens, topk], or [batches, tokens, topk] for as many
+    independent exchanges (both results then get that dimension).  Tokens lie
+    by source rank: equal shares of ``sources`` (default: ``ranks``), or
+    ``starts`` (int64 [sources + 1], on the device).  ``place`` int32
+    [experts] is the rank an expert lives on.  ``sent[s, d]`` counts the
+    tokens of s with an expert on d, or without ``once`` every one of their
+    experts there; ``load[e]`` the slots that hold e.  Ids outside [0,
+    experts) are empty slots.
+    """
+    if isinstance(ids, torch.Tensor) and ids.dim() == 2:
+        _tensor("ids", ids, (torch.int32,), (None, None))
+        batches, (tokens, topk), lead = 1, ids.shape, ()
+    else:
+        _tensor("ids", ids, (torch.int32,), (None, None, None))
+        batches, tokens, topk = ids.shape
+        lead = (batches,)
+    _tensor("place", place, (torch.int32,), (None,), ids.device)
+    n = place.shape[0]
+    _need(1 <= n <= MAX_EXPERTS, f"{n} experts: 1 to {MAX_EXPERTS} are taken")
+    _need(1 <= topk <= MAX_TOPK, f"topk is 1 to {MAX_TOPK}, not {topk}")
+    _need(1 <= ranks <= MAX_RANKS, f"ranks is 1 to {MAX_RANKS}, not {ranks}")
+    if starts is not None:
+        _tensor("starts", starts, (torch.int64,), (None,), ids.device)
+        _need(starts.shape[0] >= 2 and sources in (None, starts.shape[0] - 1),
+              f"starts holds {starts.shape[0]} offsets, not one more than the sources")
+        sources = starts.shape[0] - 1
+    else:
+        sources = ranks if sources is None else sources
+        _need(sources >= 1 and tokens % sources == 0,
+              f"{tokens} tokens do not divide evenly over {sources} sources; give starts")
+    with _On(ids.device, stream, (ids, place, starts)) as on:
+        load = torch.empty((*lead, n), dtype=torch.int32, device=ids.device)
+        sent = torch.empty((*lead, sources, ranks), dtype=torch.int32, device=ids.device)
+        d = ExchangeDesc(batches, tokens, topk, n, sources, ranks, bool(once), ids.data_ptr(),
+                         place.data_ptr(), None if starts is None else starts.data_ptr(),
+                         load.data_ptr(), sent.data_ptr())
+        _done(_library().mv_exchange(C.byref(d), on), "mv_exchange")
+    return load, sent
+
+
+def experts(x, ids, weights, w13, s13, w2, s2, *, stream=None):
+    """The chosen experts' products, [tokens, hidden] of ``x``'s type:
+    sum over a token's slots of weight * W2 (silu(W1 x) * (W3 x)).
+
+    ``x`` [tokens, hidden] (float16 or bfloat16; rows may lie apart by a
+    multiple of 8), ``ids`` int32 and ``weights`` float32 [tokens, topk].
+    ``w13`` uint8 [experts, 2 * inner, hidden / 2] holds W1's rows, then W3's,
+    two 4-bit numbers to a byte (the even column in the low half), ``s13``
+    [experts, 2 * inner, hidden / group] their scales in ``x``'s type:
+    W = (q - 8) * scale.  ``w2`` [experts, hidden, inner / 2] and ``s2``
+    [experts, hidden, inner / group] likewise, group 32, 64 or 128.  Ids
+    outside [0, experts) add nothing (experts of other ranks).
+    """
+    _tensor("x", x, (torch.float16, torch.bfloat16), (None, None), rows_apart=True)
+    tokens, hidden = x.shape
+    dev = x.device
+    _tensor("w13", w13, (torch.uint8,), (None, None, None), dev)
+    n, inner2 = w13.shape[0], w13.shape[1]
+    inner = inner2 // 2
+    _need(1 <= n <= MAX_EXPERTS, f"{n} experts: 1 to {MAX_EXPERTS} are taken")
+    _need(hidden >= 32 and inner2 >= 64 and inner2 % 2 == 0 and 2 * w13.shape[2] == hidden,
+          f"w13 has shape {tuple(w13.shape)}, not [experts, 2 * inner, {hidden} / 2]")
+    _tensor("s13", s13, (x.dtype,), (n, inner2, None), dev)
+    group = hidden // s13.shape[2] if s13.shape[2] else 0
+    _need(group in (32, 64, 128) and hidden == group * s13.shape[2] and inner % group == 0,
+          f"s13 has shape {tuple(s13.shape)}: a scale stands for 32, 64 or 128 of {hidden} columns, "
+          f"and {inner} inner rows divide by that too")
+    _tensor("w2", w2, (torch.uint8,), (n, hidden, inner // 2), dev)
+    _tensor("s2", s2, (x.dtype,), (n, hidden, inner // group), dev)
+    _tensor("ids", ids, (torch.int32,), (tokens, None), dev)
+    topk = ids.shape[1]
+    _need(1 <= topk <= MAX_TOPK, f"topk is 1 to {MAX_TOPK}, not {topk}")
+    _tensor("weights", weights, (torch.float32,), (tokens, topk), dev)
+    with _On(dev, stream, (x, ids, weights, w13, s13, w2, s2)) as on:
+        y = torch.empty((tokens, hidden), dtype=x.dtype, device=dev)
+        d = ExpertsDesc(tokens, _stride(x), topk, n, hidden, inner, group, _DTYPES[x.dtype],
+                        x.data_ptr(), ids.data_ptr(), weights.data_ptr(), w13.data_ptr(),
+                        s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr())
+        need = _u64()
+        _done(_library().mv_experts_workspace_bytes(C.byref(d), C.byref(need)), "mv_experts")
+        ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        _done(_library().mv_experts(C.byref(d), ws.data_ptr(), need.value, on), "mv_experts")
+    return y

@@ -329,6 +329,147 @@ int mv_destroy(mv_ctx *ctx);
 int mv_simulate_static(const mv_batch_desc *desc, uint32_t max_ticks, void *stream,
                        const mv_results_view *out, uint64_t *steps_done);
 
+/*
+ * ---- routed-expert operators ------------------------------------------
+ *
+ * The operators of a mixture-of-experts layer around the exchange that the
+ * simulator steps: the router (mv_route, mv_route_backward), the token
+ * counts an expert-parallel exchange carries from rank to rank (mv_exchange:
+ * the byte counts of a MV_COLL_ALLTOALL collective, by one multiplication),
+ * and the products of the chosen experts (mv_experts: what a compute node
+ * between dispatch and combine stands for).  The pplx MoE page describes the
+ * exchange; these are the sides of it that the page leaves to the caller.
+ *
+ * Unlike a batch descriptor, these descriptors hold DEVICE pointers, except
+ * where noted; arrays are dense and row-major.  Every call is enqueued on
+ * `stream` (a cudaStream_t of the current device, NULL = legacy default
+ * stream) and returns without waiting; it allocates nothing, may be captured
+ * in a CUDA graph, keeps nothing from one call to the next, and gives the
+ * same bits on every run.  The arrays have to stay alive until the stream
+ * has passed the call; outputs may not overlap inputs.
+ *
+ * Returns MV_OK, MV_EINVAL (a null pointer or a malformed field),
+ * MV_EOVERFLOW (a size beyond the limits below), MV_ENOMEM (mv_experts'
+ * workspace), MV_ECUDA.  Nothing is written unless MV_OK or MV_ECUDA is
+ * returned.  Zero tokens (zero batches) are valid and do nothing.
+ */
+#define MV_F32 0
+#define MV_F16 1
+#define MV_BF16 2
+#define MV_SCORE_SOFTMAX 0
+#define MV_SCORE_SIGMOID 1
+#define MV_GROUP_MAX 0       /* a group counts as much as its best expert     */
+#define MV_GROUP_TOPTWO 1    /* ... as the sum of its two best                */
+#define MV_MOE_MAX_EXPERTS 1024
+#define MV_MOE_MAX_TOPK 32
+#define MV_MOE_MAX_GROUPS 32
+#define MV_MOE_MAX_RANKS 8192
+
+/*
+ * Router.  Per token t, with logits x[t, e] (rows `row_stride` elements
+ * apart) of type `dtype`, computed in 32 bits:
+ *   score   s_e = softmax(x)_e, or sigmoid(x_e) = 1 / (1 + exp(-x_e));
+ *   order   v_e = s_e + bias_e; with no bias (NULL), and unless groups are
+ *           ranked by sums of two, v_e = x_e, which orders alike;
+ *   closed  an expert whose logit or bias is -inf or NaN: it is never chosen
+ *           and adds nothing to the softmax;
+ *   groups  the `experts` in `groups` equal consecutive groups; the
+ *           top_groups of greatest value stay, the others close.  A group's
+ *           value is its greatest v, or the sum of its two greatest (with one
+ *           expert open, that one's); ignored when groups = 1;
+ *   choice  ids[t, 0..topk): the open experts of greatest v, greatest first;
+ *           equal values, of experts and of groups, go to the lowest index.
+ *           Slots beyond the open experts get id -1 and weight 0;
+ *   weight  weights[t, j] = scale * s, or with `renorm` scale * s / sum of
+ *           the chosen s (0 where that sum is 0).  The bias is not part of it.
+ * An infinite logit is the limit: it has all of its row's softmax (with
+ * several, each an equal share).  topk <= top_groups * experts / groups,
+ * MV_MOE_MAX_EXPERTS, _TOPK, _GROUPS.
+ */
+typedef struct mv_route_desc {
+    uint64_t tokens, row_stride;
+    uint32_t experts, topk, groups, top_groups;
+    uint32_t dtype, scores, group_rule, renorm;
+    float scale;
+    const void *logits;               /* [tokens, experts]                     */
+    const float *bias;                /* [experts], or NULL                    */
+    int32_t *ids;                     /* out [tokens, topk]                    */
+    float *weights;                   /* out [tokens, topk]                    */
+} mv_route_desc;
+int mv_route(const mv_route_desc *desc, void *stream);
+
+/*
+ * Router's gradient: dlogits[t, e] = sum over the slots j of dweights[t, j]
+ * * d weights[t, j] / d x[t, e], of type `dtype`, dense [tokens, experts]
+ * (0 for every expert that no weight depends on).  `logits` and `ids` are
+ * mv_route's; the choice itself and the bias have no gradient.  Ids outside
+ * [0, experts) are empty slots; a row's other ids are distinct.
+ */
+typedef struct mv_route_grad_desc {
+    uint64_t tokens, row_stride;
+    uint32_t experts, topk;
+    uint32_t dtype, scores, renorm;
+    float scale;
+    const void *logits;               /* [tokens, experts]                     */
+    const int32_t *ids;               /* [tokens, topk]                        */
+    const float *dweights;            /* [tokens, topk]                        */
+    void *dlogits;                    /* out [tokens, experts], contiguous     */
+} mv_route_grad_desc;
+int mv_route_backward(const mv_route_grad_desc *desc, void *stream);
+
+/*
+ * Exchange counts.  `batches` independent sets of `tokens` tokens, each with
+ * topk ids.  A set's tokens lie by source rank: source s holds tokens
+ * starts[s] to starts[s + 1] (ascending, 0 to tokens; each read is clamped to
+ * that), the same in every set; with starts = NULL every source holds an equal
+ * share (sources divides tokens).  Expert e lives on rank place[e].
+ *   load[b, e]     slots of set b that hold e;
+ *   sent[b, s, d]  slots of source s whose expert lives on rank d, or with
+ *                  `once` its tokens with at least one such slot.
+ * Ids outside [0, experts) are empty slots; experts placed outside [0, ranks)
+ * count in load only.  ranks <= MV_MOE_MAX_RANKS, tokens * topk < 2^31.
+ */
+typedef struct mv_exchange_desc {
+    uint64_t batches, tokens;
+    uint32_t topk, experts, sources, ranks, once;
+    const int32_t *ids;               /* [batches, tokens, topk]               */
+    const int32_t *place;             /* [experts]                             */
+    const int64_t *starts;            /* [sources + 1], or NULL                */
+    int32_t *load;                    /* out [batches, experts]                */
+    int32_t *sent;                    /* out [batches, sources, ranks]         */
+} mv_exchange_desc;
+int mv_exchange(const mv_exchange_desc *desc, void *stream);
+
+/*
+ * Routed experts' products for the few tokens of a decode step:
+ *   y[t] = sum over slots j of weights[t, j] * W2_e (silu(W1_e x[t]) * (W3_e x[t])),
+ *   e = ids[t, j], silu(z) = z / (1 + exp(-z)).
+ * Weights are 4-bit numbers with one scale per `group` (32, 64 or 128)
+ * consecutive columns: W = (q - 8) * scale, two numbers to a byte, the even
+ * column in the low half.  w13 holds W1's `inner` rows, then W3's.  x, y and
+ * the scales are of type `dtype` (MV_F16 or MV_BF16); sums are held in 32
+ * bits.  hidden and inner are multiples of group, x's rows are row_stride
+ * elements apart (a multiple of 8), arrays of `dtype` and bytes are 16-byte
+ * aligned.  Ids outside [0, experts) are experts that are not here: they add
+ * nothing, and their weights are not read.  A token without any gets zeros.
+ * The workspace (256-byte aligned) takes mv_experts_workspace_bytes, which
+ * reads the sizes alone; its contents do not matter.
+ */
+typedef struct mv_experts_desc {
+    uint64_t tokens, row_stride;
+    uint32_t topk, experts, hidden, inner, group, dtype;
+    const void *x;                    /* [tokens, hidden]                      */
+    const int32_t *ids;               /* [tokens, topk]                        */
+    const float *weights;             /* [tokens, topk]                        */
+    const uint8_t *w13;               /* [experts, 2 * inner, hidden / 2]      */
+    const void *s13;                  /* [experts, 2 * inner, hidden / group]  */
+    const uint8_t *w2;                /* [experts, hidden, inner / 2]          */
+    const void *s2;                   /* [experts, hidden, inner / group]      */
+    void *y;                          /* out [tokens, hidden], contiguous      */
+} mv_experts_desc;
+int mv_experts_workspace_bytes(const mv_experts_desc *desc, uint64_t *bytes);
+int mv_experts(const mv_experts_desc *desc, void *workspace, uint64_t ws_bytes, void *stream);
+
 const char *mv_strerror(int code);
 
 #ifdef __cplusplus
