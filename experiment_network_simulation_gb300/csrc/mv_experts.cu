@@ -6,6 +6,14 @@
 
 namespace mvmoe {
 
+// A token's slot is a pair; pairs are grouped by expert, and up to 8, 16 or 32
+// of one expert's pairs make an item: what one pass over its weights serves.
+u32 item_pairs(u64 tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : 32; }
+
+struct Item {
+    u32 expert, first, count;       // pairs[first .. first + count)
+};
+
 struct ExpertArgs {
     const void *x;
     const int32_t *ids;
@@ -13,63 +21,371 @@ struct ExpertArgs {
     const uint8_t *w13, *w2;
     const void *s13, *s2;
     void *y;
-    float *h;                       // [pairs, inner]
     u64 tokens, stride;
-    u32 topk, experts, hidden, inner, group;
+    u32 topk, experts, hidden, inner, group, item_pairs;
+    // workspace
+    void *xp;                       // x, permuted               [tokens, hidden]
+    void *h;                        // silu(W1 x) (W3 x), permuted [pairs, inner]
+    float *o;                       // W2 h                      [pairs, hidden]
+    u32 *pairs;                     // pairs by expert
+    Item *items;
+    u32 *n_items;
 };
 
-constexpr u32 kExpertWarps = 8;
+// ---- packed weights against 16-bit activations ---------------------------
+// A 32-bit word holds the 4-bit numbers of columns 0..7.  Masking nibbles i
+// and i + 4 into the halves of a word that holds a power of two makes that
+// power plus q in both halves, exactly; one subtraction leaves q - 8.  The
+// columns then come as pairs (0,4) (1,5) (2,6) (3,7), so activations are kept
+// with every eight columns in that order.
+__device__ __forceinline__ u32 column_place(u32 c) { return (c & ~7u) | ((c & 3) << 1) | ((c >> 2) & 1); }
 
-// Sum over a row of packed weights: (q - 8) x scale x value, by one warp.
-template <class T, class X>
-__device__ float dot_row(const uint8_t *q, const T *scale, const X *v, u32 n, u32 group)
-{
-    float sum = 0.0f;
-    for (u32 k = (threadIdx.x & 31) * 2; k < n; k += 64) {
-        const u32 b = q[k >> 1];
-        const float s = to_float(scale[k / group]);
-        sum += s * ((float)((int)(b & 15) - 8) * to_float(v[k]) +
-                    (float)((int)(b >> 4) - 8) * to_float(v[k + 1]));
+template <class T> struct Math;
+template <> struct Math<__half> {
+    static constexpr u32 kPower = 0x64006400, kOffset = 0x64086408;      // 1024, 1032
+    static __device__ __forceinline__ u32 sub(u32 a, u32 b)
+    {
+        u32 d;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
     }
-    return group_sum<32>(sum);
+    static __device__ __forceinline__ void mma(float (&c)[4], u32 a0, u32 a1, u32 a2, u32 a3, u32 b0, u32 b1)
+    {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    }
+};
+template <> struct Math<__nv_bfloat16> {
+    static constexpr u32 kPower = 0x43004300, kOffset = 0x43084308;      // 128, 136
+    static __device__ __forceinline__ u32 sub(u32 a, u32 b)
+    {
+        u32 d;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], u32 a0, u32 a1, u32 a2, u32 a3, u32 b0, u32 b1)
+    {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    }
+};
+template <class T> __device__ __forceinline__ void widen(u32 word, u32 (&p)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        p[i] = Math<T>::sub(((word >> (4 * i)) & 0x000F000Fu) | Math<T>::kPower, Math<T>::kOffset);
 }
 
-// h = silu(W1 x) (W3 x) of one (token, slot) a grid row, one inner row a warp.
-template <class T> __global__ void __launch_bounds__(kExpertWarps * 32) k_gate_up(const ExpertArgs a)
+__device__ __forceinline__ void copy16(u32 to, const void *from)
 {
-    for (u64 p = blockIdx.y; p < a.tokens * a.topk; p += gridDim.y) {
-        const u32 e = (u32)a.ids[p];
-        if (e >= a.experts) continue;
-        const T *x = static_cast<const T *>(a.x) + p / a.topk * a.stride;
-        for (u32 i = blockIdx.x * kExpertWarps + (threadIdx.x >> 5); i < a.inner;
-             i += gridDim.x * kExpertWarps) {
-            const u64 r1 = (u64)e * 2 * a.inner + i, r3 = r1 + a.inner;
-            const T *s = static_cast<const T *>(a.s13);
-            const u32 groups = a.hidden / a.group;
-            const float g = dot_row(a.w13 + r1 * (a.hidden / 2), s + r1 * groups, x, a.hidden, a.group);
-            const float u = dot_row(a.w13 + r3 * (a.hidden / 2), s + r3 * groups, x, a.hidden, a.group);
-            if ((threadIdx.x & 31) == 0) a.h[p * a.inner + i] = g / (1.0f + expf(-g)) * u;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+template <int N> __device__ __forceinline__ void copies_left()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- grouping ------------------------------------------------------------
+constexpr u32 kPrepThreads = 512;
+
+// Block 0 groups the pairs by expert (counts, their prefix sums, a cursor an
+// expert); the other blocks write x in the products' column order.  The order
+// of an expert's pairs may differ from run to run: a pair's result does not
+// depend on its place.
+template <class T> __global__ void __launch_bounds__(kPrepThreads) k_prepare(const ExpertArgs a)
+{
+    const u32 tid = threadIdx.x;
+    if (blockIdx.x) {
+        const u64 eights = a.hidden / 8, n = a.tokens * eights;
+        for (u64 i = (u64)(blockIdx.x - 1) * kPrepThreads + tid; i < n; i += (u64)(gridDim.x - 1) * kPrepThreads) {
+            const u64 t = i / eights, c = (i % eights) * 8;
+            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + t * a.stride + c);
+            const uint4 w = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                       __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.xp) + t * a.hidden + c) = w;
         }
+        return;
+    }
+    __shared__ u32 count[kMaxExperts], first[kMaxExperts], item[kMaxExperts];
+    const u32 n = (u32)(a.tokens * a.topk), most = a.item_pairs;
+    for (u32 e = tid; e < a.experts; e += kPrepThreads) count[e] = 0;
+    __syncthreads();
+    for (u32 p = tid; p < n; p += kPrepThreads) {
+        const u32 e = (u32)a.ids[p];
+        if (e < a.experts) atomicAdd(&count[e], 1u);
+    }
+    __syncthreads();
+    if (tid < 32) {                                     // prefix sums by one warp
+        u32 pairs = 0, items = 0;
+        for (u32 base = 0; base < a.experts; base += 32) {
+            const u32 e = base + tid, c = e < a.experts ? count[e] : 0;
+            const u32 k = (c + most - 1) / most;
+            u32 sc = c, sk = k;
+            for (u32 d = 1; d < 32; d <<= 1) {
+                const u32 oc = __shfl_up_sync(kFull, sc, d), ok = __shfl_up_sync(kFull, sk, d);
+                if (tid >= d) { sc += oc; sk += ok; }
+            }
+            if (e < a.experts) { first[e] = pairs + sc - c; item[e] = items + sk - k; }
+            pairs += __shfl_sync(kFull, sc, 31);
+            items += __shfl_sync(kFull, sk, 31);
+        }
+        if (tid == 0) *a.n_items = items;
+    }
+    __syncthreads();
+    for (u32 e = tid; e < a.experts; e += kPrepThreads)
+        for (u32 i = 0; i * most < count[e]; i++)
+            a.items[item[e] + i] = {e, first[e] + i * most, min(most, count[e] - i * most)};
+    __syncthreads();
+    for (u32 p = tid; p < n; p += kPrepThreads) {
+        const u32 e = (u32)a.ids[p];
+        if (e < a.experts) a.pairs[atomicAdd(&first[e], 1u)] = p;
+    }
+}
+
+// ---- products ------------------------------------------------------------
+constexpr u32 kWarps = 4, kThreads = kWarps * 32;
+constexpr u32 kRows = kWarps * 32;              // weight rows a block
+constexpr u32 kStep = 128;                      // columns a stage
+constexpr u32 kWPitch = kStep / 2 + 16;         // bytes; 16-byte pieces of eight rows fall in eight bank groups
+constexpr u32 kXPitch = kStep * 2 + 64;
+
+constexpr u32 kScaleBytes = 2 * 4 * kRows * 4;  // two stages' scales: up to four groups a row
+
+// A stage that holds up to 8 NT pairs' activations, and the shared memory of
+// a block whose items hold that many.
+template <int NT> struct Stage {
+    static constexpr u32 kBytes = kRows * kWPitch + NT * 8 * kXPitch;
+    static constexpr u32 kBudget = kScaleBytes + (NT == 4 ? 3 : 4) * kBytes;
+    template <u32 BUDGET>
+    static constexpr int kCount = (BUDGET - kScaleBytes) / kBytes < 6 ? (BUDGET - kScaleBytes) / kBytes : 6;
+};
+
+// One tile of weight rows against up to 8 NT pairs' activations.  A warp
+// holds 32 rows as two matrix operands of 16; an operand of 16 x 16 weights
+// meets 16 x 8 activations in one mma.  Sums of a group of columns start at
+// zero and are then added, times the rows' scales, in 32 bits.  The order of
+// additions depends on the sizes alone, never on the other tokens.
+template <class T, int NT, bool GATE, u32 BUDGET>
+__device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 tile, unsigned char *smem)
+{
+    constexpr int S = Stage<NT>::template kCount<BUDGET>;
+    static_assert(S >= 2, "at least two stages");
+    const u32 tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const u32 K = GATE ? a.hidden : a.inner;
+    const u32 groups = K / a.group, per_stage = kStep / a.group;
+    float *scales = reinterpret_cast<float *>(smem);
+    const u32 ring = (u32)__cvta_generic_to_shared(smem + kScaleBytes);
+    // block row r: warp r / 32's operand (r / 16) & 1, row r & 15
+    auto weight_row = [&](u32 r) -> int64_t {
+        if (GATE) {
+            const u32 i = tile * (kRows / 2) + (r >> 5) * 16 + (r & 15);
+            return i < a.inner ? (int64_t)((r & 16) ? a.inner + i : i) : -1;
+        }
+        const u32 i = tile * kRows + r;
+        return i < a.hidden ? (int64_t)i : -1;
+    };
+    const u64 base_row = (u64)it.expert * (GATE ? 2 * a.inner : a.hidden);
+    const uint8_t *W = (GATE ? a.w13 : a.w2) + base_row * (K / 2);
+    // this thread's pieces of a stage
+    const uint8_t *wp[4];
+    u32 wd[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const u32 c = tid + j * kThreads, r = c >> 2;
+        const int64_t row = weight_row(r);
+        wp[j] = row < 0 ? nullptr : W + (u64)row * (K / 2) + (c & 3) * 16;
+        wd[j] = ring + r * kWPitch + (c & 3) * 16;
+    }
+    const T *xpnt[NT];
+    u32 xd[NT];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+        const u32 c = tid + j * kThreads, r = c >> 4;
+        xpnt[j] = nullptr;
+        if (r < it.count) {
+            const u32 p = a.pairs[it.first + r];
+            xpnt[j] = (GATE ? static_cast<const T *>(a.xp) + (u64)(p / a.topk) * K
+                            : static_cast<const T *>(a.h) + (u64)p * K) + (c & 15) * 8;
+        }
+        xd[j] = ring + kRows * kWPitch + r * kXPitch + (c & 15) * 16;
+    }
+    auto fetch = [&](u32 s, u32 slot) {
+        const u32 k0 = s * kStep, off = slot * Stage<NT>::kBytes;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (wp[j] && k0 + (tid & 3) * 32 < K) copy16(wd[j] + off, wp[j] + k0 / 2);
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+            if (xpnt[j] && k0 + (tid & 15) * 8 < K) copy16(xd[j] + off, xpnt[j] + k0);
+    };
+    const int64_t srow = weight_row(tid);
+    const T *sp = srow < 0 ? nullptr : static_cast<const T *>(GATE ? a.s13 : a.s2) + (base_row + (u64)srow) * groups;
+    auto scale_of = [&](u32 s, float (&v)[4]) {
+#pragma unroll
+        for (u32 i = 0; i < 4; i++)
+            v[i] = i < per_stage && sp && s * per_stage + i < groups ? to_float(sp[s * per_stage + i]) : 0.0f;
+    };
+    auto put_scales = [&](u32 s, const float (&v)[4]) {
+#pragma unroll
+        for (u32 i = 0; i < 4; i++)
+            if (i < per_stage) scales[((s & 1) * 4 + i) * kRows + tid] = v[i];
+    };
+
+    float total[2][NT][4], part[2][NT][4];
+#pragma unroll
+    for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) total[m][n][i] = part[m][n][i] = 0.0f;
+
+    const u32 steps = (K + kStep - 1) / kStep, per = a.group / 32, shift = per >> 1;   // per: 1, 2 or 4
+    float next[4];
+    scale_of(0, next);
+    put_scales(0, next);
+    scale_of(1, next);
+#pragma unroll
+    for (int s = 0; s < S - 1; s++) {
+        if ((u32)s < steps) fetch(s, s);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    const u32 a_at = ring + (warp * 32 + (lane & 7) + ((lane >> 3) & 1) * 8 + (lane >> 4) * 16) * kWPitch;
+    const u32 x_at = ring + kRows * kWPitch + g * kXPitch + t * 16;
+    u32 slot = 0, ahead = S - 1;
+    for (u32 s = 0; s < steps; s++) {
+        copies_left<S - 2>();
+        __syncthreads();
+        if (s + S - 1 < steps) fetch(s + S - 1, ahead);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        put_scales(s + 1, next);
+        scale_of(s + 2, next);
+        const u32 off = slot * Stage<NT>::kBytes;
+        const u32 blocks = min(kStep, K - s * kStep) / 32;
+#pragma unroll
+        for (u32 b = 0; b < kStep / 32; b++) {
+            if (b < blocks) {
+                u32 w[4];
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a_at + off + b * 16));
+                u32 q[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) widen<T>(w[i], q[i]);
+#pragma unroll
+                for (int n = 0; n < NT; n++) {
+                    u32 x0, x1, x2, x3;
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                                 : "r"(x_at + off + n * 8 * kXPitch + b * 64));
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        Math<T>::mma(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], x0, x1);
+                        Math<T>::mma(part[m][n], q[2 * m][2], q[2 * m + 1][2], q[2 * m][3], q[2 * m + 1][3], x2, x3);
+                    }
+                }
+                if (((b + 1) & (per - 1)) == 0) {       // the group's last columns
+                    const float *sc = scales + ((s & 1) * 4 + (b >> shift)) * kRows + warp * 32 + g;
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        const float s0 = sc[m * 16], s1 = sc[m * 16 + 8];
+#pragma unroll
+                        for (int n = 0; n < NT; n++) {
+                            total[m][n][0] += s0 * part[m][n][0];
+                            total[m][n][1] += s0 * part[m][n][1];
+                            total[m][n][2] += s1 * part[m][n][2];
+                            total[m][n][3] += s1 * part[m][n][3];
+                            part[m][n][0] = part[m][n][1] = part[m][n][2] = part[m][n][3] = 0.0f;
+                        }
+                    }
+                }
+            }
+        }
+        slot = slot + 1 == S ? 0 : slot + 1;
+        ahead = ahead + 1 == S ? 0 : ahead + 1;
+    }
+    copies_left<0>();
+    // element i of operand m, tile n: row g + 8 (i / 2), pair 8 n + 2 t + (i & 1)
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const u32 c = n * 8 + 2 * t + (i & 1), r = g + (i >> 1) * 8;
+            if (c >= it.count) continue;
+            const u64 p = a.pairs[it.first + c];
+            if (GATE) {
+                const u32 row = tile * (kRows / 2) + warp * 16 + r;
+                const float z = total[0][n][i], up = total[1][n][i];
+                if (row < a.inner)
+                    static_cast<T *>(a.h)[p * a.inner + column_place(row)] = from_float<T>(z / (1.0f + expf(-z)) * up);
+            } else {
+#pragma unroll
+                for (int m = 0; m < 2; m++) {
+                    const u32 row = tile * kRows + warp * 32 + m * 16 + r;
+                    if (row < a.hidden) a.o[p * a.hidden + row] = total[m][n][i];
+                }
+            }
+        }
+}
+
+template <class T, bool GATE, int MOST> __global__ void __launch_bounds__(kThreads) k_product(const ExpertArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr u32 B = Stage<MOST>::kBudget;
+    for (u32 i = blockIdx.y; i < *a.n_items; i += gridDim.y) {
+        const Item it = a.items[i];
+        if (MOST == 1 || it.count <= 8) product<T, 1, GATE, B>(a, it, blockIdx.x, smem);
+        else if (MOST == 2 || it.count <= 16) product<T, 2, GATE, B>(a, it, blockIdx.x, smem);
+        else product<T, MOST < 4 ? 1 : 4, GATE, B>(a, it, blockIdx.x, smem);
+        __syncthreads();
     }
 }
 
 // y = sum over the slots, in their order, of weight x (W2 h).
-template <class T> __global__ void __launch_bounds__(kExpertWarps * 32) k_down(const ExpertArgs a)
+constexpr u32 kCombineThreads = 256;
+
+template <class T> __global__ void __launch_bounds__(kCombineThreads) k_combine(const ExpertArgs a)
 {
-    for (u64 t = blockIdx.y; t < a.tokens; t += gridDim.y)
-        for (u32 i = blockIdx.x * kExpertWarps + (threadIdx.x >> 5); i < a.hidden;
-             i += gridDim.x * kExpertWarps) {
-            float y = 0.0f;
-            for (u64 p = t * a.topk; p < (t + 1) * a.topk; p++) {
-                const u32 e = (u32)a.ids[p];
-                if (e >= a.experts) continue;
-                const u64 r = (u64)e * a.hidden + i;
-                y += a.weights[p] * dot_row(a.w2 + r * (a.inner / 2),
-                                            static_cast<const T *>(a.s2) + r * (a.inner / a.group),
-                                            a.h + p * a.inner, a.inner, a.group);
-            }
-            if ((threadIdx.x & 31) == 0) static_cast<T *>(a.y)[t * a.hidden + i] = from_float<T>(y);
+    const u64 quads = a.hidden / 4, n = a.tokens * quads;
+    for (u64 i = (u64)blockIdx.x * kCombineThreads + threadIdx.x; i < n; i += (u64)gridDim.x * kCombineThreads) {
+        const u64 t = i / quads, c = (i % quads) * 4;
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (u64 p = t * a.topk; p < (t + 1) * a.topk; p++) {
+            if ((u32)a.ids[p] >= a.experts) continue;
+            const float w = a.weights[p];
+            const float4 o = *reinterpret_cast<const float4 *>(a.o + p * a.hidden + c);
+            y[0] += w * o.x; y[1] += w * o.y; y[2] += w * o.z; y[3] += w * o.w;
         }
+        T *out = static_cast<T *>(a.y) + t * a.hidden + c;
+#pragma unroll
+        for (int j = 0; j < 4; j++) out[j] = from_float<T>(y[j]);
+    }
+}
+
+// Workspace: offsets of its parts, each on a 256-byte boundary.
+struct Layout {
+    u64 xp, h, o, pairs, items, n_items, total;
+};
+u64 most_items(const mv_experts_desc *d)
+{
+    const u64 pairs = d->tokens * d->topk;
+    return (pairs < d->experts ? pairs : d->experts) + pairs / item_pairs(d->tokens);
+}
+Layout layout(const mv_experts_desc *d)
+{
+    const u64 pairs = d->tokens * d->topk;
+    Layout l;
+    u64 at = 0;
+    auto take = [&](u64 bytes) { const u64 here = at; at += (bytes + 255) / 256 * 256; return here; };
+    l.xp = take(d->tokens * d->hidden * 2);
+    l.h = take(pairs * d->inner * 2);
+    l.o = take(pairs * d->hidden * 4);
+    l.pairs = take(pairs * 4);
+    l.items = take(most_items(d) * sizeof(Item));
+    l.n_items = take(4);
+    l.total = at;
+    return l;
 }
 
 int check(const mv_experts_desc *d)
@@ -84,13 +400,36 @@ int check(const mv_experts_desc *d)
     return MV_OK;
 }
 
-template <class T> int run_experts(const ExpertArgs &a, cudaStream_t stream)
+template <class T, bool GATE, int MOST> int run_product(const ExpertArgs &a, u64 items, cudaStream_t stream)
 {
-    const u32 gi = (a.inner + kExpertWarps - 1) / kExpertWarps, gh = (a.hidden + kExpertWarps - 1) / kExpertWarps;
-    const u32 gp = (u32)std::fmin((double)(a.tokens * a.topk), 65535.0), gt = (u32)std::fmin((double)a.tokens, 65535.0);
-    int rc = launch(k_gate_up<T>, dim3(gi, gp), kExpertWarps * 32, 0, stream, a);
-    if (rc == MV_OK) rc = launch(k_down<T>, dim3(gh, gt), kExpertWarps * 32, 0, stream, a);
+    constexpr u32 smem = Stage<MOST>::kBudget;
+    const u32 tiles = GATE ? (a.inner + kRows / 2 - 1) / (kRows / 2) : (a.hidden + kRows - 1) / kRows;
+    const auto kernel = k_product<T, GATE, MOST>;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return MV_ECUDA;
+    return launch(kernel, dim3(tiles, (u32)std::fmin((double)items, 65535.0)), kThreads, smem, stream, a);
+}
+
+template <class T, int MOST> int run_experts(const ExpertArgs &a, u64 items, cudaStream_t stream)
+{
+    const u32 sms = sm_count();
+    if (!sms) return MV_ECUDA;
+    const u32 share = (u32)std::fmin((double)((a.tokens * (a.hidden / 8) + kPrepThreads - 1) / kPrepThreads), sms);
+    int rc = launch(k_prepare<T>, dim3(1 + share), kPrepThreads, 0, stream, a);
+    if (rc == MV_OK) rc = run_product<T, true, MOST>(a, items, stream);
+    if (rc == MV_OK) rc = run_product<T, false, MOST>(a, items, stream);
+    const u64 quads = a.tokens * (a.hidden / 4);
+    const u32 blocks = (u32)std::fmin((double)((quads + kCombineThreads - 1) / kCombineThreads), 8.0 * sms);
+    if (rc == MV_OK) rc = launch(k_combine<T>, dim3(blocks), kCombineThreads, 0, stream, a);
     return rc;
+}
+
+template <class T> int run_experts(const ExpertArgs &a, u64 items, cudaStream_t stream)
+{
+    if (a.item_pairs == 8) return run_experts<T, 1>(a, items, stream);
+    if (a.item_pairs == 16) return run_experts<T, 2>(a, items, stream);
+    return run_experts<T, 4>(a, items, stream);
 }
 
 }  // namespace mvmoe
@@ -103,7 +442,7 @@ extern "C" int mv_experts_workspace_bytes(const mv_experts_desc *d, uint64_t *by
     *bytes = 0;
     const int rc = check(d);
     if (rc != MV_OK) return rc;
-    *bytes = (4 * d->tokens * d->topk * d->inner + 255) / 256 * 256;
+    *bytes = layout(d).total;
     return MV_OK;
 }
 
@@ -128,7 +467,14 @@ extern "C" int mv_experts(const mv_experts_desc *d, void *workspace, uint64_t ws
     a.w2 = d->w2;
     a.s2 = d->s2;
     a.y = d->y;
-    a.h = static_cast<float *>(workspace);
+    const Layout l = layout(d);
+    char *ws = static_cast<char *>(workspace);
+    a.xp = ws + l.xp;
+    a.h = ws + l.h;
+    a.o = reinterpret_cast<float *>(ws + l.o);
+    a.pairs = reinterpret_cast<u32 *>(ws + l.pairs);
+    a.items = reinterpret_cast<Item *>(ws + l.items);
+    a.n_items = reinterpret_cast<u32 *>(ws + l.n_items);
     a.tokens = d->tokens;
     a.stride = d->row_stride;
     a.topk = d->topk;
@@ -136,6 +482,8 @@ extern "C" int mv_experts(const mv_experts_desc *d, void *workspace, uint64_t ws
     a.hidden = d->hidden;
     a.inner = d->inner;
     a.group = d->group;
+    a.item_pairs = item_pairs(d->tokens);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return d->dtype == MV_F16 ? run_experts<__half>(a, s) : run_experts<__nv_bfloat16>(a, s);
+    return d->dtype == MV_F16 ? run_experts<__half>(a, most_items(d), s)
+                              : run_experts<__nv_bfloat16>(a, most_items(d), s);
 }
