@@ -1,6 +1,7 @@
 // The routed experts' SwiGLU products with 4-bit weights (mv_experts in
 // include/mv.h).
 #include <cmath>
+#include <cstring>
 
 #include "mv_moe.cuh"
 
@@ -89,6 +90,15 @@ template <int N> __device__ __forceinline__ void copies_left()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+template <class T> __device__ __forceinline__ float shared_value(u32 at)
+{
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+    T t;
+    memcpy(&t, &v, 2);
+    return to_float(t);
+}
+
 // ---- grouping ------------------------------------------------------------
 constexpr u32 kPrepThreads = 512;
 
@@ -153,7 +163,12 @@ constexpr u32 kStep = 128;                      // columns a stage
 constexpr u32 kWPitch = kStep / 2 + 16;         // bytes; 16-byte pieces of eight rows fall in eight bank groups
 constexpr u32 kXPitch = kStep * 2 + 64;
 
-constexpr u32 kScaleBytes = 2 * 4 * kRows * 4;  // two stages' scales: up to four groups a row
+// Scales come by epochs of 16 groups, two in shared memory.  A row's scales
+// start anywhere, so the aligned 16-byte pieces around them are copied: three
+// hold 16 groups at any offset.
+constexpr u32 kEpoch = 16;
+constexpr u32 kSPitch = kEpoch * 2 + 16;
+constexpr u32 kScaleBytes = 2 * kRows * kSPitch;
 
 // A stage that holds up to 8 NT pairs' activations, and the shared memory of
 // a block whose items hold that many.
@@ -161,7 +176,7 @@ template <int NT> struct Stage {
     static constexpr u32 kBytes = kRows * kWPitch + NT * 8 * kXPitch;
     static constexpr u32 kBudget = kScaleBytes + (NT == 4 ? 3 : 4) * kBytes;
     template <u32 BUDGET>
-    static constexpr int kCount = (BUDGET - kScaleBytes) / kBytes < 6 ? (BUDGET - kScaleBytes) / kBytes : 6;
+    static constexpr int kCount = (BUDGET - kScaleBytes) / kBytes < 5 ? (BUDGET - kScaleBytes) / kBytes : 5;
 };
 
 // One tile of weight rows against up to 8 NT pairs' activations.  A warp
@@ -173,11 +188,12 @@ template <class T, int NT, bool GATE, u32 BUDGET>
 __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 tile, unsigned char *smem)
 {
     constexpr int S = Stage<NT>::template kCount<BUDGET>;
-    static_assert(S >= 2, "at least two stages");
+    // an epoch is four steps or more, and its copy has S - 1 to arrive in
+    static_assert(S >= 2 && S <= 5, "two to five stages");
     const u32 tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const u32 K = GATE ? a.hidden : a.inner;
-    const u32 groups = K / a.group, per_stage = kStep / a.group;
-    float *scales = reinterpret_cast<float *>(smem);
+    const u32 groups = K / a.group;
+    const u32 scales = (u32)__cvta_generic_to_shared(smem);
     const u32 ring = (u32)__cvta_generic_to_shared(smem + kScaleBytes);
     // block row r: warp r / 32's operand (r / 16) & 1, row r & 15
     auto weight_row = [&](u32 r) -> int64_t {
@@ -222,18 +238,29 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         for (int j = 0; j < NT; j++)
             if (xpnt[j] && k0 + (tid & 15) * 8 < K) copy16(xd[j] + off, xpnt[j] + k0);
     };
+    // this thread copies the scales of block row tid
+    const T *all = static_cast<const T *>(GATE ? a.s13 : a.s2);
+    const char *s_end = reinterpret_cast<const char *>(all + (u64)a.experts * (GATE ? 2 * a.inner : a.hidden) * groups);
     const int64_t srow = weight_row(tid);
-    const T *sp = srow < 0 ? nullptr : static_cast<const T *>(GATE ? a.s13 : a.s2) + (base_row + (u64)srow) * groups;
-    auto scale_of = [&](u32 s, float (&v)[4]) {
-#pragma unroll
-        for (u32 i = 0; i < 4; i++)
-            v[i] = i < per_stage && sp && s * per_stage + i < groups ? to_float(sp[s * per_stage + i]) : 0.0f;
+    const char *s_row = srow < 0 ? nullptr : reinterpret_cast<const char *>(all + (base_row + (u64)srow) * groups);
+    auto fetch_scales = [&](u32 epoch) {
+        if (!s_row || epoch * kEpoch >= groups) return;
+        const char *from = s_row + epoch * kEpoch * 2, *to = s_row + min((epoch + 1) * kEpoch, groups) * 2;
+        from -= reinterpret_cast<uintptr_t>(from) & 15;
+        u32 at = scales + ((epoch & 1) * kRows + tid) * kSPitch;
+        for (; from < to; from += 16, at += 16) {
+            const u32 bytes = s_end - from < 16 ? (u32)(s_end - from) : 16u;     // the array's end
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+        }
     };
-    auto put_scales = [&](u32 s, const float (&v)[4]) {
+    // where this lane's four rows have theirs
+    u32 s_at[4];
 #pragma unroll
-        for (u32 i = 0; i < 4; i++)
-            if (i < per_stage) scales[((s & 1) * 4 + i) * kRows + tid] = v[i];
-    };
+    for (int i = 0; i < 4; i++) {
+        const u32 r = warp * 32 + g + 8 * i;
+        const int64_t row = weight_row(r);
+        s_at[i] = scales + r * kSPitch + (u32)(((base_row + (u64)(row < 0 ? 0 : row)) * groups * 2) & 15);
+    }
 
     float total[2][NT][4], part[2][NT][4];
 #pragma unroll
@@ -244,10 +271,8 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
             for (int i = 0; i < 4; i++) total[m][n][i] = part[m][n][i] = 0.0f;
 
     const u32 steps = (K + kStep - 1) / kStep, per = a.group / 32, shift = per >> 1;   // per: 1, 2 or 4
-    float next[4];
-    scale_of(0, next);
-    put_scales(0, next);
-    scale_of(1, next);
+    const u32 shift_e = 2 + shift;                          // steps an epoch: 4, 8 or 16
+    fetch_scales(0);
 #pragma unroll
     for (int s = 0; s < S - 1; s++) {
         if ((u32)s < steps) fetch(s, s);
@@ -260,9 +285,8 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         copies_left<S - 2>();
         __syncthreads();
         if (s + S - 1 < steps) fetch(s + S - 1, ahead);
+        if ((s & ((1u << shift_e) - 1)) == 0) fetch_scales((s >> shift_e) + 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
-        put_scales(s + 1, next);
-        scale_of(s + 2, next);
         const u32 off = slot * Stage<NT>::kBytes;
         const u32 blocks = min(kStep, K - s * kStep) / 32;
 #pragma unroll
@@ -286,10 +310,11 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
                     }
                 }
                 if (((b + 1) & (per - 1)) == 0) {       // the group's last columns
-                    const float *sc = scales + ((s & 1) * 4 + (b >> shift)) * kRows + warp * 32 + g;
+                    const u32 group = (s * (kStep / 32) + b) >> shift;
+                    const u32 s_off = ((group / kEpoch) & 1) * kRows * kSPitch + (group % kEpoch) * 2;
 #pragma unroll
                     for (int m = 0; m < 2; m++) {
-                        const float s0 = sc[m * 16], s1 = sc[m * 16 + 8];
+                        const float s0 = shared_value<T>(s_at[2 * m] + s_off), s1 = shared_value<T>(s_at[2 * m + 1] + s_off);
 #pragma unroll
                         for (int n = 0; n < NT; n++) {
                             total[m][n][0] += s0 * part[m][n][0];
