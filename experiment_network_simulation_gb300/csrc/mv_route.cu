@@ -1,6 +1,7 @@
 // Routing of tokens to experts, and its gradient (mv_route,
 // mv_route_backward in include/mv.h, which states the formulas).
 #include <cmath>
+#include <cstring>
 
 #include "mv_moe.cuh"
 
@@ -60,7 +61,7 @@ __device__ __forceinline__ float slot_weight(const RouteArgs &a, int id, float x
 // One row by one warp, by comparing every expert's exact order value.
 // key: the warp's own `experts` words of shared memory.
 template <class T, int ORDER>
-__device__ void route_row(const RouteArgs &a, u64 row, u32 *key)
+__device__ __noinline__ void route_row(const RouteArgs &a, u64 row, u32 *key)
 {
     const u32 lane = threadIdx.x & 31, E = a.experts;
     const T *x = static_cast<const T *>(a.logits) + row * a.stride;
@@ -130,16 +131,248 @@ __device__ void route_row(const RouteArgs &a, u64 row, u32 *key)
     __syncwarp();
 }
 
+// ---- the fast way ---------------------------------------------------------
+// L lanes share a row, V experts a lane.  Every expert becomes one unsigned
+// key that orders like its value and ends in its place, so that keys differ
+// and ties fall to the lowest index; a lane sorts its keys by a network of
+// min and max, and the row's greatest head is taken topk times.  16-bit
+// logits fit a key whole.  Longer values lose their last bits to the place
+// (and scores come from the approximate exponential and reciprocal): where
+// two neighbours in the order are closer than that, the row is done again by
+// route_row, which compares exact values.
 constexpr u32 kRouteWarps = 8;
 
-template <class T, int ORDER>
-__global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a)
+// How the lanes of a row share the experts: a group of experts takes
+// 1 << shift lanes, `per` experts each.
+struct Shares {
+    u32 shift, per, size;
+    bool wide;                      // lanes load their experts by 16 bytes
+};
+
+__device__ __forceinline__ float exp2_fast(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float reciprocal_fast(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int L> __device__ __forceinline__ u32 row_max(u32 v)
+{
+    if (L == 32) return __reduce_max_sync(kFull, v);
+#pragma unroll
+    for (int d = L / 2; d; d >>= 1) v = max(v, __shfl_xor_sync(kFull, v, d));
+    return v;
+}
+
+__device__ __forceinline__ void order_two(u32 &a, u32 &b)
+{
+    const u32 hi = max(a, b), lo = min(a, b);
+    a = hi;
+    b = lo;
+}
+// Batcher's odd-even merge sort, greatest first.
+template <int V> __device__ __forceinline__ void sort_keys(u32 (&k)[V])
+{
+#pragma unroll
+    for (int p = 1; p < V; p <<= 1)
+#pragma unroll
+        for (int d = p; d > 0; d >>= 1)
+#pragma unroll
+            for (int j = d % p; j + d < V; j += 2 * d)
+#pragma unroll
+                for (int i = 0; i < d; i++)
+                    if (i + j + d < V && (i + j) / (2 * p) == (i + j + d) / (2 * p)) order_two(k[i + j], k[i + j + d]);
+}
+
+template <class T, int V>
+__device__ __forceinline__ void load_share(const T *x, u32 n, bool wide, float (&v)[V])
+{
+    constexpr int kPer = 16 / sizeof(T);
+    if (wide && n == V) {
+#pragma unroll
+        for (int i = 0; i < V / kPer; i++) {
+            const uint4 q = reinterpret_cast<const uint4 *>(x)[i];
+            const u32 w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if (sizeof(T) == 4) {
+                    v[i * kPer + j] = __uint_as_float(w[j]);
+                } else {
+                    T pair[2];
+                    memcpy(pair, &w[j], 4);
+                    v[i * kPer + 2 * j] = to_float(pair[0]);
+                    v[i * kPer + 2 * j + 1] = to_float(pair[1]);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) v[i] = i < n ? to_float(x[i]) : -INFINITY;
+    }
+}
+
+template <class T, int ORDER, int L, int V, bool FEW>
+__global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a, const Shares sh)
 {
     extern __shared__ u32 keys[];
-    u32 *key = keys + (threadIdx.x >> 5) * a.experts;
-    const u64 step = (u64)gridDim.x * kRouteWarps;
-    for (u64 row = (u64)blockIdx.x * kRouteWarps + (threadIdx.x >> 5); row < a.tokens; row += step)
-        route_row<T, ORDER>(a, row, key);
+    constexpr bool EXACT = sizeof(T) == 2 && ORDER == kByLogit;
+    constexpr u32 kPlace = EXACT ? L * V - 1 : V - 1;        // a key's bits for the place
+    constexpr u32 kRows = 32 / L;
+    const u32 lane = threadIdx.x & 31, sub = lane & (L - 1), warp = threadIdx.x >> 5;
+    const u32 in_group = sub & ((1u << sh.shift) - 1), group = sub >> sh.shift;
+    const u32 base = group * sh.size + in_group * sh.per;
+    const u32 n = group < a.groups && in_group * sh.per < sh.size ? min(sh.per, sh.size - in_group * sh.per) : 0;
+    const bool stats = a.softmax && (ORDER == kBySoftmax || !a.renorm);
+    float bias[V];
+    if (ORDER != kByLogit) {
+#pragma unroll
+        for (int i = 0; i < V; i++) bias[i] = i < n ? (a.bias ? a.bias[base + i] : 0.0f) : -INFINITY;
+    }
+    const u64 step = (u64)gridDim.x * kRouteWarps * kRows;
+    for (u64 first = ((u64)blockIdx.x * kRouteWarps + warp) * kRows; first < a.tokens; first += step) {
+        const u64 row = first + lane / L;
+        const bool here = row < a.tokens;
+        const T *x = static_cast<const T *>(a.logits) + (here ? row : first) * a.stride;
+        float v[V];
+        load_share<T, V>(x + base, n, sh.wide, v);
+        float m = -INFINITY, sum = 0.0f;
+        if (stats) {
+#pragma unroll
+            for (int i = 0; i < V; i++) m = fmaxf(m, v[i]);          // passes NaN by
+            m = group_max<L>(m);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                sum += open(v[i]) ? (v[i] == m ? 1.0f : exp2_fast((v[i] - m) * kLog2e)) : 0.0f;
+            sum = group_sum<L>(sum);
+        }
+        u32 key[V];
+        const float inv = ORDER == kBySoftmax ? reciprocal_fast(sum) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            float by = v[i];
+            if (ORDER == kBySigmoid) by = reciprocal_fast(1.0f + exp2_fast(-v[i] * kLog2e)) + bias[i];
+            if (ORDER == kBySoftmax) by = (v[i] == m ? 1.0f : exp2_fast((v[i] - m) * kLog2e)) * inv + bias[i];
+            const bool is_open = open(v[i]) && (ORDER == kByLogit || open(bias[i]));
+            key[i] = is_open ? (ordered(by) & ~kPlace) | (kPlace - (EXACT ? base + i : i)) : 0u;
+        }
+        sort_keys<V>(key);
+        // a value's error: the bits that made room, and the approximations
+        const float rel = EXACT || ORDER == kByLogit ? 0.0f : V * 0x1p-23f;
+        const float eps = ORDER == kByLogit ? 0.0f : ORDER == kBySigmoid ? 1e-6f : 2e-6f;
+        bool close = false;
+        if (a.groups > 1) {
+            u32 f = key[0], s = key[1];
+            for (u32 d = 1; d < 1u << sh.shift; d <<= 1) {
+                const u32 f2 = __shfl_xor_sync(kFull, f, d), s2 = __shfl_xor_sync(kFull, s, d);
+                s = max(max(s, s2), min(f, f2));
+                f = max(f, f2);
+            }
+            u32 mine = f;
+            float value = 0.0f, size = 0.0f;
+            if (!EXACT) {
+                value = unordered(f & ~kPlace);
+                size = fabsf(value);
+                if (a.top_two && s) {
+                    const float v2 = unordered(s & ~kPlace);
+                    value += v2;
+                    size += fabsf(v2);
+                }
+                mine = f ? ordered(value) : 0u;
+            }
+            u32 before = 0;
+            for (u32 g = 0; g < a.groups; g++) {
+                const u32 other = __shfl_sync(kFull, mine, g << sh.shift, L);
+                before += other > mine || (other == mine && g < group);
+            }
+            const bool stays = group < a.groups && before < a.top_groups;
+            if (!EXACT) {
+                // the best that leaves against each that stays
+                const u32 out = row_max<L>(stays || group >= a.groups ? 0u : mine);
+                const float most = __uint_as_float(row_max<L>(f ? __float_as_uint(size) : 0u));
+                const float tol = 4 * eps + 4 * rel * most;
+                if (stays && mine && out)
+                    close = ORDER == kByLogit ? (mine ^ out) <= kPlace : !(value - unordered(out) > tol);
+            }
+            if (!stays)
+#pragma unroll
+                for (int i = 0; i < V; i++) key[i] = 0;
+        }
+        // lane r of the row keeps slot r; one look further tells how sure the last is
+        u32 got = 0, from = 0, after = 0;
+        auto take = [&](u32 r, int depth) {
+            const u32 top = row_max<L>(key[0]);
+            bool won = key[0] == top;
+            u32 who = 0;
+            if (!EXACT) {
+                u32 all = __ballot_sync(kFull, won);
+                if (L < 32) all = (all >> (lane & ~(L - 1))) & ((1u << L) - 1);
+                who = __ffs(all) - 1;
+                won = sub == who;
+            }
+            if (sub == r) { got = top; from = who; }
+            if (r == a.topk) after = top;
+#pragma unroll
+            for (int i = 0; i + 1 < V; i++)
+                if (i < depth) key[i] = won ? key[i + 1] : key[i];
+            if (depth >= V - 1) key[V - 1] = won ? 0u : key[V - 1];
+        };
+        const u32 looks = a.topk + (EXACT ? 0 : 1);
+        if (FEW) {                                   // topk <= 8: only what can still be reached moves up
+#pragma unroll
+            for (int r = 0; r < 9; r++)
+                if (r < looks) take(r, 8 - r);
+        } else {
+            for (u32 r = 0; r < looks; r++) take(r, V);
+        }
+        int id = -1;
+        if (sub < a.topk && got) {
+            const u32 place = kPlace - (got & kPlace);
+            id = (int)(EXACT ? place
+                             : (from >> sh.shift) * sh.size + (from & ((1u << sh.shift) - 1)) * sh.per + place);
+        }
+        if (!EXACT) {
+            u32 next = __shfl_down_sync(kFull, got, 1, L);
+            if (sub + 1 == a.topk) next = after;
+            if (id >= 0 && next) {
+                if (ORDER == kByLogit) {
+                    close = close || (got ^ next) <= kPlace;
+                } else {
+                    const float p = unordered(got & ~kPlace), q = unordered(next & ~kPlace);
+                    close = close || !(p - q > 2 * eps + 2 * rel * (fabsf(p) + fabsf(q)));
+                }
+            }
+        }
+        float logit = 0.0f;
+        if (EXACT) {
+            // a negative number's key is its complement: the place's bits were ones
+            const u32 k = (got >> 31) ? got & ~kPlace : got | kPlace;
+            if (id >= 0) logit = unordered(k);
+        } else if (id >= 0) {
+            logit = to_float(x[id]);
+        }
+        const float w = slot_weight<L>(a, id, logit, m, sum);
+        u32 again = EXACT ? 0u : __ballot_sync(kFull, close && here);
+        if (L < 32) again = (again >> (lane & ~(L - 1))) & ((1u << L) - 1);
+        if (here && !again && sub < a.topk) {
+            a.ids[row * a.topk + sub] = id;
+            a.weights[row * a.topk + sub] = w;
+        }
+        if (!EXACT) {
+            u32 rows = __ballot_sync(kFull, again != 0 && sub == 0);
+            while (rows) {
+                const u32 at = __ffs(rows) - 1;
+                rows &= rows - 1;
+                route_row<T, ORDER>(a, first + at / L, keys + warp * a.experts);
+            }
+        }
+    }
 }
 
 struct RouteGradArgs {
@@ -221,16 +454,48 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_route_grad(const RouteGradA
     }
 }
 
+template <class T, int ORDER, int L, int V, bool FEW>
+int run_route(const RouteArgs &a, const Shares &sh, cudaStream_t stream)
+{
+    constexpr u32 kRowsABlock = kRouteWarps * (32 / L);
+    const u32 blocks = (u32)std::fmin((double)((a.tokens + kRowsABlock - 1) / kRowsABlock), 8.0 * sm_count());
+    if (!blocks) return MV_ECUDA;
+    const bool exact = sizeof(T) == 2 && ORDER == kByLogit;
+    return launch(k_route<T, ORDER, L, V, FEW>, blocks, kRouteWarps * 32,
+                  exact ? 0 : kRouteWarps * a.experts * 4, stream, a, sh);
+}
+
+// The smallest of the shapes (lanes, experts a lane) that holds the experts,
+// a lane to a slot and whole lanes to a group.
+template <class T, int ORDER> int run_route(const RouteArgs &a, cudaStream_t stream)
+{
+    auto fits = [&](u32 L, u32 V, Shares &sh) {
+        if (a.topk > L || a.groups > L) return false;
+        sh.shift = 0;
+        while (a.groups << (sh.shift + 1) <= L) sh.shift++;
+        sh.size = a.experts / a.groups;
+        sh.per = a.groups == 1 ? V : (sh.size + (1u << sh.shift) - 1) >> sh.shift;
+        if (sh.per > V || sh.size > sh.per << sh.shift) return false;
+        sh.wide = sh.per == V && aligned(a.logits, 16) && a.stride * sizeof(T) % 16 == 0 &&
+                  (a.groups == 1 || sh.size * sizeof(T) % 16 == 0);
+        return true;
+    };
+    Shares sh;
+    const bool few = a.topk <= 8;
+    if (few && fits(8, 8, sh)) return run_route<T, ORDER, 8, 8, true>(a, sh, stream);
+    if (few && fits(16, 8, sh)) return run_route<T, ORDER, 16, 8, true>(a, sh, stream);
+    if (fits(32, 8, sh))
+        return few ? run_route<T, ORDER, 32, 8, true>(a, sh, stream) : run_route<T, ORDER, 32, 8, false>(a, sh, stream);
+    if (fits(32, 16, sh)) return run_route<T, ORDER, 32, 16, false>(a, sh, stream);
+    if (fits(32, 32, sh)) return run_route<T, ORDER, 32, 32, false>(a, sh, stream);
+    return MV_EOVERFLOW;
+}
+
 template <class T> int run_route(const RouteArgs &a, Order order, cudaStream_t stream)
 {
-    const u32 blocks = (u32)std::fmin((double)((a.tokens + kRouteWarps - 1) / kRouteWarps),
-                                      (double)sm_count() * 8);
-    const u32 smem = kRouteWarps * a.experts * 4;
-    if (!blocks) return MV_ECUDA;
-    if (order == kByLogit) return launch(k_route<T, kByLogit>, blocks, kRouteWarps * 32, smem, stream, a);
-    if (order == kBySigmoid)
-        return launch(k_route<T, kBySigmoid>, blocks, kRouteWarps * 32, smem, stream, a);
-    return launch(k_route<T, kBySoftmax>, blocks, kRouteWarps * 32, smem, stream, a);
+    if (order == kByLogit) return run_route<T, kByLogit>(a, stream);
+    if (order == kBySigmoid) return run_route<T, kBySigmoid>(a, stream);
+    return run_route<T, kBySoftmax>(a, stream);
 }
 
 template <class T> int run_route_grad(const RouteGradArgs &a, cudaStream_t stream)

@@ -16,8 +16,10 @@ device.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
+import struct
 
 import torch
 
@@ -29,47 +31,47 @@ _RULES = {"max": 0, "top2": 1}
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 MAX_EXPERTS, MAX_TOPK, MAX_GROUPS, MAX_RANKS = 1024, 32, 32, 8192
 
-_vp, _u32, _u64, _f32 = C.c_void_p, C.c_uint32, C.c_uint64, C.c_float
+_vp, _u64 = C.c_void_p, C.c_uint64
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-class RouteDesc(C.Structure):
-    _fields_ = [("tokens", _u64), ("row_stride", _u64), ("experts", _u32), ("topk", _u32),
-                ("groups", _u32), ("top_groups", _u32), ("dtype", _u32), ("scores", _u32),
-                ("group_rule", _u32), ("renorm", _u32), ("scale", _f32), ("logits", _vp),
-                ("bias", _vp), ("ids", _vp), ("weights", _vp)]
+def _descriptor(name: str, fields: str):
+    """A mv_*_desc of ``include/mv.h`` as a ctypes structure (Q, I, f: 64-, 32-bit
+    and float fields, P: pointers), and its packer: filling a structure field
+    by field costs a call of these microseconds."""
+    types = {"Q": _u64, "I": C.c_uint32, "f": C.c_float, "P": _vp}
+    pairs = [f.split(":") for f in fields.split()]
+    cls = type(name, (C.Structure,), {"_fields_": [(n, types[t]) for n, t in pairs]})
+    packer = struct.Struct("@" + "".join(t for _, t in pairs))
+    assert packer.size <= C.sizeof(cls) < packer.size + 8          # C pads the end
+    return cls, packer.pack
 
 
-class RouteGradDesc(C.Structure):
-    _fields_ = [("tokens", _u64), ("row_stride", _u64), ("experts", _u32), ("topk", _u32),
-                ("dtype", _u32), ("scores", _u32), ("renorm", _u32), ("scale", _f32),
-                ("logits", _vp), ("ids", _vp), ("dweights", _vp), ("dlogits", _vp)]
-
-
-class ExchangeDesc(C.Structure):
-    _fields_ = [("batches", _u64), ("tokens", _u64), ("topk", _u32), ("experts", _u32),
-                ("sources", _u32), ("ranks", _u32), ("once", _u32), ("ids", _vp), ("place", _vp),
-                ("starts", _vp), ("load", _vp), ("sent", _vp)]
-
-
-class ExpertsDesc(C.Structure):
-    _fields_ = [("tokens", _u64), ("row_stride", _u64), ("topk", _u32), ("experts", _u32),
-                ("hidden", _u32), ("inner", _u32), ("group", _u32), ("dtype", _u32), ("x", _vp),
-                ("ids", _vp), ("weights", _vp), ("w13", _vp), ("s13", _vp), ("w2", _vp),
-                ("s2", _vp), ("y", _vp)]
-
+RouteDesc, _route_desc = _descriptor(
+    "RouteDesc", "tokens:Q row_stride:Q experts:I topk:I groups:I top_groups:I dtype:I scores:I "
+    "group_rule:I renorm:I scale:f logits:P bias:P ids:P weights:P")
+RouteGradDesc, _route_grad_desc = _descriptor(
+    "RouteGradDesc", "tokens:Q row_stride:Q experts:I topk:I dtype:I scores:I renorm:I scale:f "
+    "logits:P ids:P dweights:P dlogits:P")
+ExchangeDesc, _exchange_desc = _descriptor(
+    "ExchangeDesc", "batches:Q tokens:Q topk:I experts:I sources:I ranks:I once:I ids:P place:P "
+    "starts:P load:P sent:P")
+ExpertsDesc, _experts_desc = _descriptor(
+    "ExpertsDesc", "tokens:Q row_stride:Q topk:I experts:I hidden:I inner:I group:I dtype:I x:P "
+    "ids:P weights:P w13:P s13:P w2:P s2:P y:P")
 
 _lib = None
 
 
 def _library() -> C.CDLL:
+    """libmv.so, its routed-expert calls declared (descriptors by address)."""
     global _lib
     if _lib is None:
         lib = mv.library()
-        lib.mv_route.argtypes = [C.POINTER(RouteDesc), _vp]
-        lib.mv_route_backward.argtypes = [C.POINTER(RouteGradDesc), _vp]
-        lib.mv_exchange.argtypes = [C.POINTER(ExchangeDesc), _vp]
-        lib.mv_experts_workspace_bytes.argtypes = [C.POINTER(ExpertsDesc), C.POINTER(_u64)]
-        lib.mv_experts.argtypes = [C.POINTER(ExpertsDesc), _vp, _u64, _vp]
+        for f in ("mv_route", "mv_route_backward", "mv_exchange"):
+            getattr(lib, f).argtypes = [_vp, _vp]
+        lib.mv_experts_workspace_bytes.argtypes = [_vp, C.POINTER(_u64)]
+        lib.mv_experts.argtypes = [_vp, _vp, _u64, _vp]
         for f in ("mv_route", "mv_route_backward", "mv_exchange", "mv_experts_workspace_bytes",
                   "mv_experts"):
             getattr(lib, f).restype = C.c_int
@@ -84,6 +86,13 @@ def _need(ok: bool, what: str):
 
 def _tensor(name: str, t, dtype, shape, device=None, rows_apart: bool = False):
     """Check one argument: type, device, shape (None: any size), dense layout."""
+    if (t.__class__ is torch.Tensor and t.is_cuda and t.dtype in dtype and t.is_contiguous()
+            and t.dim() == len(shape) and (device is None or t.device == device)):
+        for s, n in zip(shape, t.shape):
+            if s is not None and s != n:
+                break
+        else:
+            return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} is a torch tensor, not {type(t).__name__}")
     if not t.is_cuda:
@@ -108,29 +117,35 @@ def _stride(t: torch.Tensor) -> int:
 
 
 class _On:
-    """The device and the stream of one call."""
+    """The device and the stream of one call that are not the current ones."""
 
     def __init__(self, device, stream, inputs):
-        self.stack = []
-        if device.index != torch.cuda.current_device():
-            self.stack.append(torch.cuda.device(device))
+        self.stack = [torch.cuda.device(device)]
         if stream is not None:
             _need(stream.device == device, f"the stream is on {stream.device}, not on {device}")
+            self.stack.append(torch.cuda.stream(stream))
             if stream != torch.cuda.current_stream(device):
-                self.stack.append(torch.cuda.stream(stream))
                 for t in inputs:
                     if t is not None:
                         t.record_stream(stream)
-        self.device = device
 
     def __enter__(self):
         for c in self.stack:
             c.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
 
     def __exit__(self, *exc):
         for c in reversed(self.stack):
             c.__exit__(*exc)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream, inputs):
+    """Makes the call's device and stream the current ones."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE
+    return _On(device, stream, inputs)
 
 
 def _done(rc: int, what: str):
@@ -171,14 +186,14 @@ def route(logits, topk: int, *, scores: str = "softmax", bias=None, groups: int 
     s, r = _choice("scores", scores, _SCORES), _choice("group_rule", group_rule, _RULES)
     if bias is not None:
         _tensor("bias", bias, (torch.float32,), (n,), logits.device)
-    with _On(logits.device, stream, (logits, bias)) as on:
-        ids = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
-        d = RouteDesc(tokens, _stride(logits), n, topk, groups, top_groups, _DTYPES[logits.dtype],
-                      s, r, bool(renorm), scale, logits.data_ptr(),
-                      None if bias is None else bias.data_ptr(), ids.data_ptr(),
-                      weights.data_ptr())
-        _done(_library().mv_route(C.byref(d), on), "mv_route")
+    dev = logits.device
+    with _on(dev, stream, (logits, bias)):
+        ids = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+        weights = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
+        d = _route_desc(tokens, _stride(logits), n, topk, groups, top_groups,
+                        _DTYPES[logits.dtype], s, r, bool(renorm), scale, logits.data_ptr(),
+                        0 if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr())
+        _done(_library().mv_route(d, _raw_stream(dev.index)), "mv_route")
     return ids, weights
 
 
@@ -198,12 +213,13 @@ def route_backward(logits, ids, dweights, *, scores: str = "softmax", renorm: bo
     _tensor("dweights", dweights, (torch.float32,), (tokens, topk), logits.device)
     _need(math.isfinite(scale), f"scale is {scale}")
     s = _choice("scores", scores, _SCORES)
-    with _On(logits.device, stream, (logits, ids, dweights)) as on:
-        out = torch.empty((tokens, n), dtype=logits.dtype, device=logits.device)
-        d = RouteGradDesc(tokens, _stride(logits), n, topk, _DTYPES[logits.dtype], s, bool(renorm),
-                          scale, logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(),
-                          out.data_ptr())
-        _done(_library().mv_route_backward(C.byref(d), on), "mv_route_backward")
+    dev = logits.device
+    with _on(dev, stream, (logits, ids, dweights)):
+        out = torch.empty((tokens, n), dtype=logits.dtype, device=dev)
+        d = _route_grad_desc(tokens, _stride(logits), n, topk, _DTYPES[logits.dtype], s,
+                             bool(renorm), scale, logits.data_ptr(), ids.data_ptr(),
+                             dweights.data_ptr(), out.data_ptr())
+        _done(_library().mv_route_backward(d, _raw_stream(dev.index)), "mv_route_backward")
     return out
 
 
@@ -241,13 +257,14 @@ def exchange(ids, place, ranks: int, *, sources: int | None = None, starts=None,
         sources = ranks if sources is None else sources
         _need(sources >= 1 and tokens % sources == 0,
               f"{tokens} tokens do not divide evenly over {sources} sources; give starts")
-    with _On(ids.device, stream, (ids, place, starts)) as on:
-        load = torch.empty((*lead, n), dtype=torch.int32, device=ids.device)
-        sent = torch.empty((*lead, sources, ranks), dtype=torch.int32, device=ids.device)
-        d = ExchangeDesc(batches, tokens, topk, n, sources, ranks, bool(once), ids.data_ptr(),
-                         place.data_ptr(), None if starts is None else starts.data_ptr(),
-                         load.data_ptr(), sent.data_ptr())
-        _done(_library().mv_exchange(C.byref(d), on), "mv_exchange")
+    dev = ids.device
+    with _on(dev, stream, (ids, place, starts)):
+        load = torch.empty((*lead, n), dtype=torch.int32, device=dev)
+        sent = torch.empty((*lead, sources, ranks), dtype=torch.int32, device=dev)
+        d = _exchange_desc(batches, tokens, topk, n, sources, ranks, bool(once), ids.data_ptr(),
+                           place.data_ptr(), 0 if starts is None else starts.data_ptr(),
+                           load.data_ptr(), sent.data_ptr())
+        _done(_library().mv_exchange(d, _raw_stream(dev.index)), "mv_exchange")
     return load, sent
 
 
@@ -284,13 +301,14 @@ def experts(x, ids, weights, w13, s13, w2, s2, *, stream=None):
     topk = ids.shape[1]
     _need(1 <= topk <= MAX_TOPK, f"topk is 1 to {MAX_TOPK}, not {topk}")
     _tensor("weights", weights, (torch.float32,), (tokens, topk), dev)
-    with _On(dev, stream, (x, ids, weights, w13, s13, w2, s2)) as on:
+    with _on(dev, stream, (x, ids, weights, w13, s13, w2, s2)):
         y = torch.empty((tokens, hidden), dtype=x.dtype, device=dev)
-        d = ExpertsDesc(tokens, _stride(x), topk, n, hidden, inner, group, _DTYPES[x.dtype],
-                        x.data_ptr(), ids.data_ptr(), weights.data_ptr(), w13.data_ptr(),
-                        s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr())
+        d = _experts_desc(tokens, _stride(x), topk, n, hidden, inner, group, _DTYPES[x.dtype],
+                          x.data_ptr(), ids.data_ptr(), weights.data_ptr(), w13.data_ptr(),
+                          s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr())
         need = _u64()
-        _done(_library().mv_experts_workspace_bytes(C.byref(d), C.byref(need)), "mv_experts")
+        _done(_library().mv_experts_workspace_bytes(d, C.byref(need)), "mv_experts")
         ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        _done(_library().mv_experts(C.byref(d), ws.data_ptr(), need.value, on), "mv_experts")
+        _done(_library().mv_experts(d, ws.data_ptr(), need.value, _raw_stream(dev.index)),
+              "mv_experts")
     return y
