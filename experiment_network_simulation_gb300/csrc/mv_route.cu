@@ -131,15 +131,14 @@ __device__ __noinline__ void route_row(const RouteArgs &a, u64 row, u32 *key)
     __syncwarp();
 }
 
-// ---- the fast way ---------------------------------------------------------
-// L lanes share a row, V experts a lane.  Every expert becomes one unsigned
-// key that orders like its value and ends in its place, so that keys differ
-// and ties fall to the lowest index; a lane sorts its keys by a network of
-// min and max, and the row's greatest head is taken topk times.  16-bit
-// logits fit a key whole.  Longer values lose their last bits to the place
-// (and scores come from the approximate exponential and reciprocal): where
-// two neighbours in the order are closer than that, the row is done again by
-// route_row, which compares exact values.
+// ---- the fast ways --------------------------------------------------------
+// Every expert becomes one unsigned key that orders like its value and ends
+// in its place, so that keys differ and ties fall to the lowest index.  Keys
+// are sorted by networks of min and max; the row's greatest is taken topk
+// times.  16-bit logits fit a key whole.  Longer values lose their last bits
+// to the place (and scores come from the approximate exponential and
+// reciprocal): where two neighbours in the order are closer than that, the
+// row is done again by route_row, which compares exact values.
 constexpr u32 kRouteWarps = 8;
 
 // How the lanes of a row share the experts: a group of experts takes
@@ -162,14 +161,6 @@ __device__ __forceinline__ float reciprocal_fast(float v)
     return r;
 }
 constexpr float kLog2e = 1.4426950408889634f;
-
-template <int L> __device__ __forceinline__ u32 row_max(u32 v)
-{
-    if (L == 32) return __reduce_max_sync(kFull, v);
-#pragma unroll
-    for (int d = L / 2; d; d >>= 1) v = max(v, __shfl_xor_sync(kFull, v, d));
-    return v;
-}
 
 __device__ __forceinline__ void order_two(u32 &a, u32 &b)
 {
@@ -218,15 +209,15 @@ __device__ __forceinline__ void load_share(const T *x, u32 n, bool wide, float (
     }
 }
 
-template <class T, int ORDER, int L, int V, bool FEW>
+// More than eight slots: a warp has a row, a lane V experts.
+template <class T, int ORDER, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a, const Shares sh)
 {
     extern __shared__ u32 keys[];
     constexpr bool EXACT = sizeof(T) == 2 && ORDER == kByLogit;
-    constexpr u32 kPlace = EXACT ? L * V - 1 : V - 1;        // a key's bits for the place
-    constexpr u32 kRows = 32 / L;
-    const u32 lane = threadIdx.x & 31, sub = lane & (L - 1), warp = threadIdx.x >> 5;
-    const u32 in_group = sub & ((1u << sh.shift) - 1), group = sub >> sh.shift;
+    constexpr u32 kPlace = EXACT ? 32 * V - 1 : V - 1;        // a key's bits for the place
+    const u32 lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const u32 in_group = lane & ((1u << sh.shift) - 1), group = lane >> sh.shift;
     const u32 base = group * sh.size + in_group * sh.per;
     const u32 n = group < a.groups && in_group * sh.per < sh.size ? min(sh.per, sh.size - in_group * sh.per) : 0;
     const bool stats = a.softmax && (ORDER == kBySoftmax || !a.renorm);
@@ -235,22 +226,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a, c
 #pragma unroll
         for (int i = 0; i < V; i++) bias[i] = i < n ? (a.bias ? a.bias[base + i] : 0.0f) : -INFINITY;
     }
-    const u64 step = (u64)gridDim.x * kRouteWarps * kRows;
-    for (u64 first = ((u64)blockIdx.x * kRouteWarps + warp) * kRows; first < a.tokens; first += step) {
-        const u64 row = first + lane / L;
-        const bool here = row < a.tokens;
-        const T *x = static_cast<const T *>(a.logits) + (here ? row : first) * a.stride;
+    const u64 step = (u64)gridDim.x * kRouteWarps;
+    for (u64 row = (u64)blockIdx.x * kRouteWarps + warp; row < a.tokens; row += step) {
+        const T *x = static_cast<const T *>(a.logits) + row * a.stride;
         float v[V];
         load_share<T, V>(x + base, n, sh.wide, v);
         float m = -INFINITY, sum = 0.0f;
         if (stats) {
 #pragma unroll
             for (int i = 0; i < V; i++) m = fmaxf(m, v[i]);          // passes NaN by
-            m = group_max<L>(m);
+            m = group_max<32>(m);
 #pragma unroll
             for (int i = 0; i < V; i++)
                 sum += open(v[i]) ? (v[i] == m ? 1.0f : exp2_fast((v[i] - m) * kLog2e)) : 0.0f;
-            sum = group_sum<L>(sum);
+            sum = group_sum<32>(sum);
         }
         u32 key[V];
         const float inv = ORDER == kBySoftmax ? reciprocal_fast(sum) : 0.0f;
@@ -288,14 +277,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a, c
             }
             u32 before = 0;
             for (u32 g = 0; g < a.groups; g++) {
-                const u32 other = __shfl_sync(kFull, mine, g << sh.shift, L);
+                const u32 other = __shfl_sync(kFull, mine, g << sh.shift);
                 before += other > mine || (other == mine && g < group);
             }
             const bool stays = group < a.groups && before < a.top_groups;
             if (!EXACT) {
                 // the best that leaves against each that stays
-                const u32 out = row_max<L>(stays || group >= a.groups ? 0u : mine);
-                const float most = __uint_as_float(row_max<L>(f ? __float_as_uint(size) : 0u));
+                const u32 out = __reduce_max_sync(kFull, stays || group >= a.groups ? 0u : mine);
+                const float most = __uint_as_float(__reduce_max_sync(kFull, f ? __float_as_uint(size) : 0u));
                 const float tol = 4 * eps + 4 * rel * most;
                 if (stays && mine && out)
                     close = ORDER == kByLogit ? (mine ^ out) <= kPlace : !(value - unordered(out) > tol);
@@ -306,40 +295,30 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a, c
         }
         // lane r of the row keeps slot r; one look further tells how sure the last is
         u32 got = 0, from = 0, after = 0;
-        auto take = [&](u32 r, int depth) {
-            const u32 top = row_max<L>(key[0]);
+        const u32 looks = a.topk + (EXACT ? 0 : 1);
+        for (u32 r = 0; r < looks; r++) {
+            const u32 top = __reduce_max_sync(kFull, key[0]);
             bool won = key[0] == top;
             u32 who = 0;
             if (!EXACT) {
-                u32 all = __ballot_sync(kFull, won);
-                if (L < 32) all = (all >> (lane & ~(L - 1))) & ((1u << L) - 1);
-                who = __ffs(all) - 1;
-                won = sub == who;
+                who = __ffs(__ballot_sync(kFull, won)) - 1;
+                won = lane == who;
             }
-            if (sub == r) { got = top; from = who; }
+            if (lane == r) { got = top; from = who; }
             if (r == a.topk) after = top;
 #pragma unroll
-            for (int i = 0; i + 1 < V; i++)
-                if (i < depth) key[i] = won ? key[i + 1] : key[i];
-            if (depth >= V - 1) key[V - 1] = won ? 0u : key[V - 1];
-        };
-        const u32 looks = a.topk + (EXACT ? 0 : 1);
-        if (FEW) {                                   // topk <= 8: only what can still be reached moves up
-#pragma unroll
-            for (int r = 0; r < 9; r++)
-                if (r < looks) take(r, 8 - r);
-        } else {
-            for (u32 r = 0; r < looks; r++) take(r, V);
+            for (int i = 0; i + 1 < V; i++) key[i] = won ? key[i + 1] : key[i];
+            key[V - 1] = won ? 0u : key[V - 1];
         }
         int id = -1;
-        if (sub < a.topk && got) {
+        if (lane < a.topk && got) {
             const u32 place = kPlace - (got & kPlace);
             id = (int)(EXACT ? place
                              : (from >> sh.shift) * sh.size + (from & ((1u << sh.shift) - 1)) * sh.per + place);
         }
         if (!EXACT) {
-            u32 next = __shfl_down_sync(kFull, got, 1, L);
-            if (sub + 1 == a.topk) next = after;
+            u32 next = __shfl_down_sync(kFull, got, 1);
+            if (lane + 1 == a.topk) next = after;
             if (id >= 0 && next) {
                 if (ORDER == kByLogit) {
                     close = close || (got ^ next) <= kPlace;
@@ -357,21 +336,371 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a, c
         } else if (id >= 0) {
             logit = to_float(x[id]);
         }
-        const float w = slot_weight<L>(a, id, logit, m, sum);
-        u32 again = EXACT ? 0u : __ballot_sync(kFull, close && here);
-        if (L < 32) again = (again >> (lane & ~(L - 1))) & ((1u << L) - 1);
-        if (here && !again && sub < a.topk) {
-            a.ids[row * a.topk + sub] = id;
-            a.weights[row * a.topk + sub] = w;
+        const float w = slot_weight<32>(a, id, logit, m, sum);
+        if (!EXACT && __any_sync(kFull, close)) {
+            route_row<T, ORDER>(a, row, keys + warp * a.experts);
+        } else if (lane < a.topk) {
+            a.ids[row * a.topk + lane] = id;
+            a.weights[row * a.topk + lane] = w;
         }
-        if (!EXACT) {
-            u32 rows = __ballot_sync(kFull, again != 0 && sub == 0);
-            while (rows) {
-                const u32 at = __ffs(rows) - 1;
-                rows &= rows - 1;
-                route_row<T, ORDER>(a, first + at / L, keys + warp * a.experts);
+    }
+}
+
+// Up to eight slots.  Four lanes share a row, so a warp has eight rows at a
+// time: what a row costs in cross-lane steps is shared by eight.  A lane
+// takes eight consecutive experts of every 32, sorts their keys and merges
+// them into its best eight.  With groups a first pass finds the groups'
+// values, and the second drops the keys of those that leave.
+//
+// Score keys are fixed point: score * f + bias' lies in (4, 6), where floats
+// are 2^-21 apart, and their last 22 bits move to the top of the key; 4
+// itself is closed.
+constexpr u32 kFew = 8, kPiece = 8, kBatch = 32;
+
+// f: power of two; bias' = bias * f + shift; close: units that may be an error.
+struct Scale {
+    float f, shift;
+    u32 close;
+    bool usable;                    // false: a bias range that no scale holds
+};
+
+template <class T> struct Bits16;   // ordered 16-bit patterns
+template <> struct Bits16<__nv_bfloat16> {
+    static constexpr u32 kLowest = 0xFF80FF80, kClosed = 0x007F, kInf = 0xFF80;
+    static __device__ __forceinline__ u32 plus_zero(u32 w)
+    {
+        u32 d;
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0u));
+        return d;
+    }
+    static __device__ __forceinline__ float value(u32 bits) { return __uint_as_float(bits << 16); }
+};
+template <> struct Bits16<__half> {
+    static constexpr u32 kLowest = 0xFC00FC00, kClosed = 0x03FF, kInf = 0xFC00;
+    static __device__ __forceinline__ u32 plus_zero(u32 w)
+    {
+        u32 d;
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0u));
+        return d;
+    }
+    static __device__ __forceinline__ float value(u32 bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
+};
+template <> struct Bits16<float> {   // not used: keeps the other branch well formed
+    static constexpr u32 kLowest = 0xFF800000, kClosed = 0, kInf = 0;
+    static __device__ __forceinline__ u32 plus_zero(u32 w) { return w; }
+    static __device__ __forceinline__ float value(u32) { return 0.0f; }
+};
+
+// Eight consecutive logits as they lie in memory (absent ones: -inf).
+template <class T> struct Piece {
+    static constexpr int kWords = kPiece * sizeof(T) / 4;
+    u32 w[kWords];
+    __device__ __forceinline__ void load(const T *x, u32 n, bool wide)
+    {
+        if (wide && n == kPiece) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; i++) {
+                const uint4 q = reinterpret_cast<const uint4 *>(x)[i];
+                w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; i++) w[i] = Bits16<T>::kLowest;
+#pragma unroll
+        for (int i = 0; i < (int)kPiece; i++)
+            if ((u32)i < n) {
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = __float_as_uint(x[i]);
+                } else {
+                    unsigned short v;
+                    memcpy(&v, x + i, 2);
+                    w[i / 2] = i & 1 ? (w[i / 2] & 0xFFFFu) | (u32)v << 16 : (w[i / 2] & 0xFFFF0000u) | v;
+                }
+            }
+    }
+    __device__ __forceinline__ float value(int i) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return Bits16<T>::value(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+    }
+};
+
+__device__ __forceinline__ float quad_max(float v)
+{
+    v = fmaxf(v, __shfl_xor_sync(kFull, v, 2));
+    return fmaxf(v, __shfl_xor_sync(kFull, v, 1));
+}
+__device__ __forceinline__ float quad_sum(float v)
+{
+    v += __shfl_xor_sync(kFull, v, 2);
+    return v + __shfl_xor_sync(kFull, v, 1);
+}
+
+template <class T, int ORDER>
+__global__ void __launch_bounds__(kRouteWarps * 32) k_route_few(const RouteArgs a, const bool wide)
+{
+    extern __shared__ float shared[];
+    __shared__ float lowest[kRouteWarps], highest[kRouteWarps];
+    constexpr bool EXACT = sizeof(T) == 2 && ORDER == kByLogit;
+    const u32 E = a.experts, lane = threadIdx.x & 31, q = lane & 3, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const u32 size = E / a.groups, parts = (size + kBatch - 1) / kBatch;
+    const bool grouped = a.groups > 1 && a.top_groups < a.groups;
+    const u32 scratch = max(E, grouped ? 8 * a.groups : 0);
+    float *bias = shared;
+    u32 *mine = reinterpret_cast<u32 *>(shared + (ORDER == kByLogit ? 0 : E)) + warp * scratch;
+    // bits of a key that hold the place
+    const u32 place = EXACT ? 0xFFFFu : ORDER != kByLogit ? 1023u : (2u << (31 - __clz((E - 1) | 1))) - 1;
+
+    Scale sc = {1.0f, 0.0f, 0, true};
+    if (ORDER != kByLogit) {
+        float lo = INFINITY, hi = -INFINITY;
+        for (u32 e = threadIdx.x; e < E; e += blockDim.x) {
+            const float b = a.bias ? a.bias[e] : 0.0f;
+            if (open(b)) { lo = fminf(lo, b); hi = fmaxf(hi, b); }
+        }
+        lo = -group_max<32>(-lo);
+        hi = group_max<32>(hi);
+        if (lane == 0) { lowest[warp] = lo; highest[warp] = hi; }
+        __syncthreads();
+        for (u32 i = 0; i < warps; i++) { lo = fminf(lo, lowest[i]); hi = fmaxf(hi, highest[i]); }
+        if (!(lo <= hi)) lo = hi = 0.0f;             // no expert is open
+        const float range = hi - lo + 1.0f;
+        while (range * sc.f > 1.875f && sc.f > 0x1p-20f) sc.f *= 0.5f;
+        sc.usable = range * sc.f <= 1.875f && fmaxf(fabsf(lo), fabsf(hi)) * sc.f <= 64.0f;
+        sc.shift = 4.0f + 0x1p-6f - lo * sc.f;
+        // the approximations' 2e-6, three roundings here, two of the exact value
+        sc.close = sc.usable ? 8 + (u32)(fmaxf(fabsf(lo), fabsf(hi)) * sc.f) : 0;
+        for (u32 e = threadIdx.x; e < E; e += blockDim.x) {
+            const float b = a.bias ? a.bias[e] : 0.0f;
+            bias[e] = open(b) ? fmaf(b, sc.f, sc.shift) : __int_as_float(0x7FFFFFFF);
+        }
+        __syncthreads();
+    }
+    const int zero = sc.usable ? (int)((sc.shift - 4.0f) * 0x1p21f) : 0;       // a value of 0, in units
+
+    const u64 step = (u64)gridDim.x * warps * 8;
+    for (u64 first = ((u64)blockIdx.x * warps + warp) * 8; first < a.tokens; first += step) {
+        const u64 row = first + (lane >> 2);
+        const bool here = row < a.tokens;
+        const T *x = static_cast<const T *>(a.logits) + (here ? row : first) * a.stride;
+        float m = -INFINITY, sum = 0.0f, inv = 0.0f;
+        // this lane's piece of a batch: its first expert and how many
+        auto from = [&](u32 g, u32 p) { return g * size + p * kBatch + q * kPiece; };
+        auto many = [&](u32 p) {
+            const u32 at = p * kBatch + q * kPiece;
+            return at < size ? min(kPiece, size - at) : 0u;
+        };
+        auto statistics = [&](bool with_max) {
+            Piece<T> v;
+            if (with_max) {
+                for (u32 g = 0; g < a.groups; g++)
+                    for (u32 p = 0; p < parts; p++) {
+                        v.load(x + from(g, p), many(p), wide);
+#pragma unroll
+                        for (int i = 0; i < (int)kPiece; i++) m = fmaxf(m, v.value(i));       // passes NaN by
+                    }
+                m = quad_max(m);
+            }
+            for (u32 g = 0; g < a.groups; g++)
+                for (u32 p = 0; p < parts; p++) {
+                    v.load(x + from(g, p), many(p), wide);
+#pragma unroll
+                    for (int i = 0; i < (int)kPiece; i++)
+                        sum += exp2_fast((fmaxf(v.value(i), -INFINITY) - m) * kLog2e);
+                }
+            sum = quad_sum(sum);
+        };
+        auto keys_of = [&](const Piece<T> &v, u32 e0, u32 n, u32 (&key)[kPiece]) {
+            if (EXACT) {
+                u32 tag = (0xFFFEu - e0) << 16 | (0xFFFFu - e0);
+#pragma unroll
+                for (int i = 0; i < (int)kPiece / 2; i++) {
+                    const u32 z = Bits16<T>::plus_zero(v.w[i % Piece<T>::kWords]);
+                    u32 negative;                             // each half's sign in all of its bits
+                    asm("prmt.b32 %0, %1, %1, 0xBB99;" : "=r"(negative) : "r"(z));
+                    const u32 o = z ^ (negative | 0x80008000u);
+                    key[2 * i] = __byte_perm(o, tag, 0x1054);
+                    key[2 * i + 1] = __byte_perm(o, tag, 0x3276);
+                    tag -= 0x00020002u;
+                }
+            } else if (ORDER == kByLogit) {
+#pragma unroll
+                for (int i = 0; i < (int)kPiece; i++)
+                    key[i] = (ordered(v.value(i)) & ~place) | ((place - e0 - i) & place);
+            } else {
+#pragma unroll
+                for (int i = 0; i < (int)kPiece; i++) {
+                    const float l = v.value(i);
+                    float capped, s;
+                    // NaN for -inf, NaN and closed biases; a logit of +inf is open
+                    asm("min.NaN.f32 %0, %1, %2;" : "=f"(capped) : "f"(l), "f"(1e30f));
+                    if (ORDER == kBySigmoid) s = reciprocal_fast(1.0f + exp2_fast(-l * kLog2e));
+                    else s = exp2_fast((l - m) * kLog2e) * inv;
+                    const float b = (u32)i < n ? bias[e0 + i] : 0.0f;
+                    const float y = fmaxf(fmaf(s, sc.f, fmaf(capped, 0.0f, b)), 4.0f);
+                    key[i] = __float_as_uint(y) * 1024u + ((1023u - e0 - i) & 1023u);
+                }
+            }
+        };
+        auto is_open = [&](u32 k) {
+            return EXACT ? (k >> 16) > Bits16<T>::kClosed : ORDER == kByLogit ? (k & ~place) > 0x007FFFFFu : k > 1023u;
+        };
+        // too near each other for these keys to tell
+        auto near = [&](u32 greater, u32 less) {
+            return !EXACT && (ORDER == kByLogit ? (greater ^ less) <= place : greater - less < (sc.close + 1) * 1024u);
+        };
+        bool close = ORDER != kByLogit && !sc.usable;
+        if (ORDER == kBySoftmax) {
+            statistics(true);
+            inv = reciprocal_fast(sum);
+            close = close || m == INFINITY;
+        }
+
+        u32 stays = kFull;
+        if (grouped) {
+            u32 *value = mine + (lane >> 2) * a.groups;
+            for (u32 g = 0; g < a.groups; g++) {
+                u32 f = 0, s = 0;
+                for (u32 p = 0; p < parts; p++) {
+                    Piece<T> v;
+                    u32 key[kPiece];
+                    v.load(x + from(g, p), many(p), wide);
+                    keys_of(v, from(g, p), many(p), key);
+#pragma unroll
+                    for (int i = 0; i < (int)kPiece; i++) {
+                        if (ORDER != kByLogit) s = max(s, min(f, key[i]));
+                        f = max(f, key[i]);
+                    }
+                }
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1) {
+                    const u32 f2 = __shfl_xor_sync(kFull, f, d);
+                    if (ORDER != kByLogit) s = max(max(s, __shfl_xor_sync(kFull, s, d)), min(f, f2));
+                    f = max(f, f2);
+                }
+                // scores: units, moved up so that 0 is below every open group
+                if (ORDER != kByLogit)
+                    f = !is_open(f) ? 0u
+                                    : (u32)((int)(f >> 10) + (a.top_two ? is_open(s) ? (int)(s >> 10) : zero : 0)) + (1u << 30);
+                if (q == 0) value[g] = f;
+            }
+            __syncwarp();
+            u32 mask = 0, in = kFull, out = 0;
+            for (u32 g = q; g < a.groups; g += 4) {
+                const u32 v = value[g];
+                u32 before = 0;
+                for (u32 o = 0; o < a.groups; o++) before += value[o] > v || (value[o] == v && o < g);
+                if (before < a.top_groups) {
+                    mask |= 1u << g;
+                    in = min(in, v);
+                } else {
+                    out = max(out, v);
+                }
+            }
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                mask |= __shfl_xor_sync(kFull, mask, d);
+                in = min(in, __shfl_xor_sync(kFull, in, d));
+                out = max(out, __shfl_xor_sync(kFull, out, d));
+            }
+            stays = mask;
+            // the worst that stays against the best that leaves
+            if (ORDER == kByLogit) close = close || (!EXACT && is_open(out) && (in ^ out) <= place);
+            else close = close || (out && in - out <= 2 * sc.close);
+            __syncwarp();
+        }
+
+        u32 best[kFew];
+#pragma unroll
+        for (int i = 0; i < (int)kFew; i++) best[i] = 0;
+        for (u32 g = 0; g < a.groups; g++) {
+            const bool kept = (stays >> g) & 1;
+            if (grouped && !__any_sync(kFull, kept)) continue;
+            for (u32 p = 0; p < parts; p++) {
+                Piece<T> v;
+                u32 key[kPiece];
+                v.load(x + from(g, p), many(p), wide);
+                keys_of(v, from(g, p), many(p), key);
+                if (grouped)
+#pragma unroll
+                    for (int i = 0; i < (int)kPiece; i++) key[i] = kept ? key[i] : 0u;
+                sort_keys<kPiece>(key);
+                // the eight greatest of two sorted eights, sorted again
+#pragma unroll
+                for (int i = 0; i < (int)kFew; i++) best[i] = max(best[i], key[kFew - 1 - i]);
+#pragma unroll
+                for (int d = 4; d; d >>= 1)
+#pragma unroll
+                    for (int i = 0; i < (int)kFew; i++)
+                        if (!(i & d)) order_two(best[i], best[i + d]);
             }
         }
+
+        // lane q of the four keeps slots q and q + 4; one look further tells
+        // how sure the last is
+        u32 got[2] = {0, 0}, last = 0;
+#pragma unroll
+        for (int r = 0; r <= (int)kFew; r++) {
+            if ((u32)r >= a.topk + (EXACT ? 0 : 1)) break;
+            u32 top = max(best[0], __shfl_xor_sync(kFull, best[0], 2));
+            top = max(top, __shfl_xor_sync(kFull, top, 1));
+            const bool won = best[0] == top;
+#pragma unroll
+            for (int i = 0; i + 1 < (int)kFew; i++)
+                if (i < (int)kFew - r) best[i] = won ? best[i + 1] : best[i];
+            if (r == 0) best[kFew - 1] = won ? 0u : best[kFew - 1];
+            if (r == 0 && ORDER == kByLogit)                  // a NaN sorts above infinity
+                close = EXACT ? (top >> 16) > Bits16<T>::kInf : close || (top & ~place) > 0xFF800000u;
+            if (r > 0) close = close || (near(last, top) && is_open(top));
+            last = top;
+            if ((u32)r < a.topk && q == (r & 3)) got[(r >> 2) & 1] = top;
+        }
+        int id[2];
+        float logit[2], w[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            id[i] = -1;
+            logit[i] = 0.0f;
+            if (!is_open(got[i])) continue;
+            id[i] = (int)(place - (got[i] & place));
+            if (EXACT) {
+                const u32 o = got[i] >> 16;
+                logit[i] = Bits16<T>::value(o ^ ((o & 0x8000u) ? 0x8000u : 0xFFFFu));
+            } else {
+                logit[i] = to_float(x[id[i]]);
+            }
+        }
+        if (ORDER == kByLogit && a.softmax && !a.renorm) {
+            m = __shfl_sync(kFull, id[0] >= 0 ? logit[0] : -INFINITY, 0, 4);     // slot 0 has the maximum
+            close = close || m == INFINITY;
+            statistics(false);
+        }
+        if (a.softmax && a.renorm) {
+            const float top = quad_max(fmaxf(id[0] >= 0 ? logit[0] : -INFINITY, id[1] >= 0 ? logit[1] : -INFINITY));
+#pragma unroll
+            for (int i = 0; i < 2; i++) w[i] = id[i] >= 0 ? exp_below(logit[i], top) : 0.0f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                w[i] = id[i] < 0 ? 0.0f : a.softmax ? exp_below(logit[i], m) / sum : sigmoid(logit[i]);
+        }
+        if (a.renorm) {
+            const float total = quad_sum(w[0] + w[1]);
+#pragma unroll
+            for (int i = 0; i < 2; i++) w[i] = total > 0.0f ? w[i] / total : 0.0f;
+        }
+        const u32 again = __ballot_sync(kFull, close && here);
+        const bool redo = (again >> (lane & ~3u)) & 15;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (here && !redo && q + 4 * i < a.topk) {
+                a.ids[row * a.topk + q + 4 * i] = id[i];
+                a.weights[row * a.topk + q + 4 * i] = w[i] * a.scale;
+            }
+        for (u32 rows = __ballot_sync(kFull, redo && q == 0); rows; rows &= rows - 1)
+            route_row<T, ORDER>(a, first + (__ffs(rows) - 1) / 4, mine);
+        __syncwarp();
     }
 }
 
@@ -454,25 +783,37 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_route_grad(const RouteGradA
     }
 }
 
-template <class T, int ORDER, int L, int V, bool FEW>
-int run_route(const RouteArgs &a, const Shares &sh, cudaStream_t stream)
+template <class T, int ORDER> int run_route_few(const RouteArgs &a, cudaStream_t stream)
 {
-    constexpr u32 kRowsABlock = kRouteWarps * (32 / L);
-    const u32 blocks = (u32)std::fmin((double)((a.tokens + kRowsABlock - 1) / kRowsABlock), 8.0 * sm_count());
-    if (!blocks) return MV_ECUDA;
-    const bool exact = sizeof(T) == 2 && ORDER == kByLogit;
-    return launch(k_route<T, ORDER, L, V, FEW>, blocks, kRouteWarps * 32,
-                  exact ? 0 : kRouteWarps * a.experts * 4, stream, a, sh);
+    const u32 sms = sm_count(), size = a.experts / a.groups;
+    if (!sms) return MV_ECUDA;
+    const bool wide = aligned(a.logits, 16) && a.stride * sizeof(T) % 16 == 0 && (a.groups == 1 || size % kPiece == 0);
+    // eight rows a warp: short batches spread over the SMs in small blocks
+    const u64 warps = (a.tokens + 7) / 8;
+    const u32 a_block = warps < 4ull * kRouteWarps * sms ? 2 : kRouteWarps;
+    const u32 blocks = (u32)std::fmin((double)((warps + a_block - 1) / a_block), 8.0 * sms);
+    const u32 scratch = a.groups > 1 && 8 * a.groups > a.experts ? 8 * a.groups : a.experts;
+    return launch(k_route_few<T, ORDER>, blocks, a_block * 32,
+                  4 * ((ORDER == kByLogit ? 0 : a.experts) + a_block * scratch), stream, a, wide);
 }
 
-// The smallest of the shapes (lanes, experts a lane) that holds the experts,
-// a lane to a slot and whole lanes to a group.
+template <class T, int ORDER, int V> int run_route(const RouteArgs &a, const Shares &sh, cudaStream_t stream)
+{
+    const u32 blocks = (u32)std::fmin((double)((a.tokens + kRouteWarps - 1) / kRouteWarps), 8.0 * sm_count());
+    if (!blocks) return MV_ECUDA;
+    const bool exact = sizeof(T) == 2 && ORDER == kByLogit;
+    return launch(k_route<T, ORDER, V>, blocks, kRouteWarps * 32, exact ? 0 : kRouteWarps * a.experts * 4,
+                  stream, a, sh);
+}
+
+// Up to eight slots by four lanes a row; more by a warp a row, in the
+// smallest shape that gives every group whole lanes.
 template <class T, int ORDER> int run_route(const RouteArgs &a, cudaStream_t stream)
 {
-    auto fits = [&](u32 L, u32 V, Shares &sh) {
-        if (a.topk > L || a.groups > L) return false;
+    if (a.topk <= kFew) return run_route_few<T, ORDER>(a, stream);
+    auto fits = [&](u32 V, Shares &sh) {
         sh.shift = 0;
-        while (a.groups << (sh.shift + 1) <= L) sh.shift++;
+        while (a.groups << (sh.shift + 1) <= 32) sh.shift++;
         sh.size = a.experts / a.groups;
         sh.per = a.groups == 1 ? V : (sh.size + (1u << sh.shift) - 1) >> sh.shift;
         if (sh.per > V || sh.size > sh.per << sh.shift) return false;
@@ -481,13 +822,9 @@ template <class T, int ORDER> int run_route(const RouteArgs &a, cudaStream_t str
         return true;
     };
     Shares sh;
-    const bool few = a.topk <= 8;
-    if (few && fits(8, 8, sh)) return run_route<T, ORDER, 8, 8, true>(a, sh, stream);
-    if (few && fits(16, 8, sh)) return run_route<T, ORDER, 16, 8, true>(a, sh, stream);
-    if (fits(32, 8, sh))
-        return few ? run_route<T, ORDER, 32, 8, true>(a, sh, stream) : run_route<T, ORDER, 32, 8, false>(a, sh, stream);
-    if (fits(32, 16, sh)) return run_route<T, ORDER, 32, 16, false>(a, sh, stream);
-    if (fits(32, 32, sh)) return run_route<T, ORDER, 32, 32, false>(a, sh, stream);
+    if (fits(8, sh)) return run_route<T, ORDER, 8>(a, sh, stream);
+    if (fits(16, sh)) return run_route<T, ORDER, 16>(a, sh, stream);
+    if (fits(32, sh)) return run_route<T, ORDER, 32>(a, sh, stream);
     return MV_EOVERFLOW;
 }
 

@@ -201,6 +201,33 @@ def test_close_calls_are_decided_by_32_bit_scores():
     assert torch.equal(ids.long(), v.sort(dim=1, descending=True, stable=True).indices[:, :10])
 
 
+@pytest.mark.parametrize("k", [5, 12])
+@pytest.mark.parametrize("E,G,tg", [(48, 1, 1), (256, 8, 3), (90, 5, 2), (700, 1, 1)])
+def test_biases_of_any_range(E, G, tg, k):
+    """Narrow, wide, far-off and infinite biases: the choice is that of the
+    32-bit sums, rebuilt with torch's own exp, division and stable sort."""
+    x = randn((150, E), E, F32, 3.0)
+    x[:5] = 0.25
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    u = torch.rand((E,), generator=g, device="cuda")
+    odd = u.clone()
+    odd[3], odd[7], odd[11] = np.inf, np.inf, -np.inf
+    for b in (0.01 * u, u - 0.5, 8 * u, -300 * u, 40.0 + u, 3e4 + u, 1e7 + u, 1e9 * u, odd, 0 * u):
+        s = 1.0 / (1.0 + torch.exp(-x))
+        v = (s + b).masked_fill(b == -np.inf, -np.inf)
+        if G > 1:
+            two = v.view(150, G, -1).sort(dim=2, descending=True).values[:, :, :2]
+            best = two[:, :, 0] + two[:, :, 1].masked_fill(two[:, :, 1] == -np.inf, 0.0)
+            keep = best.sort(dim=1, descending=True, stable=True).indices[:, :tg]
+            stays = torch.zeros_like(best, dtype=torch.bool).scatter_(1, keep, True)
+            v = v.view(150, G, -1).masked_fill(~stays[:, :, None], -np.inf).view(150, E)
+        want = v.sort(dim=1, descending=True, stable=True).indices[:, :k]
+        ids, w = moe.route(x, k, scores="sigmoid", bias=b.contiguous(), groups=G, top_groups=tg,
+                           group_rule="top2", renorm=False)
+        assert torch.equal(ids.long(), want)
+        assert torch.allclose(w, s.gather(1, want), rtol=64 * U, atol=0)
+
+
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("scores,renorm", [("softmax", True), ("softmax", False),
                                            ("sigmoid", True), ("sigmoid", False)])
