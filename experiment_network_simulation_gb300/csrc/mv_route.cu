@@ -395,16 +395,17 @@ template <> struct Bits16<float> {   // not used: keeps the other branch well fo
 template <class T> struct Piece {
     static constexpr int kWords = kPiece * sizeof(T) / 4;
     u32 w[kWords];
-    __device__ __forceinline__ void load(const T *x, u32 n, bool wide)
+    template <bool WHOLE> __device__ __forceinline__ void load(const T *x, u32 n, bool wide)
     {
-        if (wide && n == kPiece) {
+        if (WHOLE || (wide && n == kPiece)) {
 #pragma unroll
             for (int i = 0; i < kWords / 4; i++) {
                 const uint4 q = reinterpret_cast<const uint4 *>(x)[i];
                 w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
             }
-            return;
+            if (WHOLE) return;
         }
+        if (wide && n == kPiece) return;
 #pragma unroll
         for (int i = 0; i < kWords; i++) w[i] = Bits16<T>::kLowest;
 #pragma unroll
@@ -437,7 +438,11 @@ __device__ __forceinline__ float quad_sum(float v)
     return v + __shfl_xor_sync(kFull, v, 1);
 }
 
-template <class T, int ORDER>
+// A row's words for its groups: their values, and eight each to find them.
+__host__ __device__ constexpr u32 few_value_words(u32 groups) { return (groups + 1) / 2 * 2 + 8 * groups; }
+
+// WHOLE: groups are whole batches and loads are wide.
+template <class T, int ORDER, bool WHOLE>
 __global__ void __launch_bounds__(kRouteWarps * 32) k_route_few(const RouteArgs a, const bool wide)
 {
     extern __shared__ float shared[];
@@ -446,9 +451,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route_few(const RouteArgs 
     const u32 E = a.experts, lane = threadIdx.x & 31, q = lane & 3, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const u32 size = E / a.groups, parts = (size + kBatch - 1) / kBatch;
     const bool grouped = a.groups > 1 && a.top_groups < a.groups;
-    const u32 scratch = max(E, grouped ? 8 * a.groups : 0);
+    const u32 batches = parts * a.groups;
+    // a warp's own words: route_row's keys or the groups' values
+    const u32 value_words = few_value_words(a.groups);
+    const u32 values = (max(E, grouped ? 8 * value_words : 0) + 3) & ~3u;
     float *bias = shared;
-    u32 *mine = reinterpret_cast<u32 *>(shared + (ORDER == kByLogit ? 0 : E)) + warp * scratch;
+    u32 *mine = reinterpret_cast<u32 *>(shared + (ORDER == kByLogit ? 0 : (E + 3) & ~3u)) + warp * values;
     // bits of a key that hold the place
     const u32 place = EXACT ? 0xFFFFu : ORDER != kByLogit ? 1023u : (2u << (31 - __clz((E - 1) | 1))) - 1;
 
@@ -485,33 +493,50 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route_few(const RouteArgs 
         const bool here = row < a.tokens;
         const T *x = static_cast<const T *>(a.logits) + (here ? row : first) * a.stride;
         float m = -INFINITY, sum = 0.0f, inv = 0.0f;
-        // this lane's piece of a batch: its first expert and how many
-        auto from = [&](u32 g, u32 p) { return g * size + p * kBatch + q * kPiece; };
-        auto many = [&](u32 p) {
-            const u32 at = p * kBatch + q * kPiece;
-            return at < size ? min(kPiece, size - at) : 0u;
+        // A batch is part p of group g (WHOLE: the groups' batches follow on
+        // from one another); this lane's piece starts at expert from().
+        struct Batch {
+            u32 b, g, p;
+        };
+        auto from = [&](const Batch &i) {
+            return WHOLE ? i.b * kBatch + q * kPiece : i.g * size + i.p * kBatch + q * kPiece;
+        };
+        auto many = [&](const Batch &i) {
+            const u32 at = WHOLE ? 0 : i.p * kBatch + q * kPiece;
+            return WHOLE ? kPiece : at < size ? min(kPiece, size - at) : 0u;
+        };
+        auto after = [&](const Batch &i) {
+            return i.p + 1 == parts ? Batch{i.b + 1, i.g + 1, 0} : Batch{i.b + 1, i.g, i.p + 1};
+        };
+        // calls f(batch, piece) for every batch, the next one's loads under way
+        auto each = [&](auto f) {
+            Piece<T> now, next;
+            Batch i = {0, 0, 0};
+            now.template load<WHOLE>(x + from(i), many(i), wide);
+            while (i.b < batches) {
+                const Batch then = after(i);
+                if (then.b < batches) next.template load<WHOLE>(x + from(then), many(then), wide);
+                f(i, now);
+                now = next;
+                i = then;
+            }
         };
         auto statistics = [&](bool with_max) {
-            Piece<T> v;
             if (with_max) {
-                for (u32 g = 0; g < a.groups; g++)
-                    for (u32 p = 0; p < parts; p++) {
-                        v.load(x + from(g, p), many(p), wide);
+                each([&](const Batch &, const Piece<T> &v) {
 #pragma unroll
-                        for (int i = 0; i < (int)kPiece; i++) m = fmaxf(m, v.value(i));       // passes NaN by
-                    }
+                    for (int i = 0; i < (int)kPiece; i++) m = fmaxf(m, v.value(i));           // passes NaN by
+                });
                 m = quad_max(m);
             }
-            for (u32 g = 0; g < a.groups; g++)
-                for (u32 p = 0; p < parts; p++) {
-                    v.load(x + from(g, p), many(p), wide);
+            each([&](const Batch &, const Piece<T> &v) {
 #pragma unroll
-                    for (int i = 0; i < (int)kPiece; i++)
-                        sum += exp2_fast((fmaxf(v.value(i), -INFINITY) - m) * kLog2e);
-                }
+                for (int i = 0; i < (int)kPiece; i++) sum += exp2_fast((fmaxf(v.value(i), -INFINITY) - m) * kLog2e);
+            });
             sum = quad_sum(sum);
         };
-        auto keys_of = [&](const Piece<T> &v, u32 e0, u32 n, u32 (&key)[kPiece]) {
+        auto keys_of = [&](const Piece<T> &v, const Batch &at, u32 (&key)[kPiece]) {
+            const u32 e0 = from(at), n = many(at);
             if (EXACT) {
                 u32 tag = (0xFFFEu - e0) << 16 | (0xFFFFu - e0);
 #pragma unroll
@@ -529,6 +554,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route_few(const RouteArgs 
                 for (int i = 0; i < (int)kPiece; i++)
                     key[i] = (ordered(v.value(i)) & ~place) | ((place - e0 - i) & place);
             } else {
+                float add[kPiece];
+                if (WHOLE) {
+                    *reinterpret_cast<float4 *>(add) = *reinterpret_cast<const float4 *>(bias + e0);
+                    *reinterpret_cast<float4 *>(add + 4) = *reinterpret_cast<const float4 *>(bias + e0 + 4);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < (int)kPiece; i++) add[i] = (u32)i < n ? bias[e0 + i] : 0.0f;
+                }
+                const u32 tag = 1023u - e0;
 #pragma unroll
                 for (int i = 0; i < (int)kPiece; i++) {
                     const float l = v.value(i);
@@ -537,9 +571,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route_few(const RouteArgs 
                     asm("min.NaN.f32 %0, %1, %2;" : "=f"(capped) : "f"(l), "f"(1e30f));
                     if (ORDER == kBySigmoid) s = reciprocal_fast(1.0f + exp2_fast(-l * kLog2e));
                     else s = exp2_fast((l - m) * kLog2e) * inv;
-                    const float b = (u32)i < n ? bias[e0 + i] : 0.0f;
-                    const float y = fmaxf(fmaf(s, sc.f, fmaf(capped, 0.0f, b)), 4.0f);
-                    key[i] = __float_as_uint(y) * 1024u + ((1023u - e0 - i) & 1023u);
+                    const float y = fmaxf(fmaf(s, sc.f, fmaf(capped, 0.0f, add[i])), 4.0f);
+                    key[i] = __float_as_uint(y) * 1024u + (WHOLE ? tag - i : (tag - i) & 1023u);
                 }
             }
         };
@@ -559,31 +592,36 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route_few(const RouteArgs 
 
         u32 stays = kFull;
         if (grouped) {
-            u32 *value = mine + (lane >> 2) * a.groups;
-            for (u32 g = 0; g < a.groups; g++) {
-                u32 f = 0, s = 0;
-                for (u32 p = 0; p < parts; p++) {
-                    Piece<T> v;
-                    u32 key[kPiece];
-                    v.load(x + from(g, p), many(p), wide);
-                    keys_of(v, from(g, p), many(p), key);
+            u32 *value = mine + (lane >> 2) * value_words;
+            // a lane's two greatest of its pieces of a group, side by side with the other three's
+            uint2 *two = reinterpret_cast<uint2 *>(value + (a.groups + 1) / 2 * 2);
+            u32 f = 0, s = 0;
+            each([&](const Batch &i, const Piece<T> &v) {
+                u32 key[kPiece];
+                keys_of(v, i, key);
 #pragma unroll
-                    for (int i = 0; i < (int)kPiece; i++) {
-                        if (ORDER != kByLogit) s = max(s, min(f, key[i]));
-                        f = max(f, key[i]);
-                    }
+                for (int j = 0; j < (int)kPiece; j++) {
+                    if (ORDER != kByLogit) s = max(s, min(f, key[j]));
+                    f = max(f, key[j]);
                 }
+                if (i.p + 1 < parts) return;                 // the group goes on
+                two[i.g * 4 + q] = make_uint2(f, s);
+                f = s = 0;
+            });
+            __syncwarp();
+            for (u32 g = q; g < a.groups; g += 4) {
+                u32 f = 0, s = 0;
 #pragma unroll
-                for (int d = 1; d < 4; d <<= 1) {
-                    const u32 f2 = __shfl_xor_sync(kFull, f, d);
-                    if (ORDER != kByLogit) s = max(max(s, __shfl_xor_sync(kFull, s, d)), min(f, f2));
-                    f = max(f, f2);
+                for (int j = 0; j < 4; j++) {
+                    const uint2 o = two[g * 4 + j];
+                    if (ORDER != kByLogit) s = max(max(s, o.y), min(f, o.x));
+                    f = max(f, o.x);
                 }
                 // scores: units, moved up so that 0 is below every open group
                 if (ORDER != kByLogit)
                     f = !is_open(f) ? 0u
                                     : (u32)((int)(f >> 10) + (a.top_two ? is_open(s) ? (int)(s >> 10) : zero : 0)) + (1u << 30);
-                if (q == 0) value[g] = f;
+                value[g] = f;
             }
             __syncwarp();
             u32 mask = 0, in = kFull, out = 0;
@@ -614,27 +652,43 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route_few(const RouteArgs 
         u32 best[kFew];
 #pragma unroll
         for (int i = 0; i < (int)kFew; i++) best[i] = 0;
-        for (u32 g = 0; g < a.groups; g++) {
-            const bool kept = (stays >> g) & 1;
-            if (grouped && !__any_sync(kFull, kept)) continue;
-            for (u32 p = 0; p < parts; p++) {
-                Piece<T> v;
+        auto merge = [&](u32 (&key)[kPiece]) {
+            sort_keys<kPiece>(key);
+            // the eight greatest of two sorted eights, sorted again
+#pragma unroll
+            for (int i = 0; i < (int)kFew; i++) best[i] = max(best[i], key[kFew - 1 - i]);
+#pragma unroll
+            for (int d = 4; d; d >>= 1)
+#pragma unroll
+                for (int i = 0; i < (int)kFew; i++)
+                    if (!(i & d)) order_two(best[i], best[i + d]);
+        };
+        if (grouped) {
+            // each row goes through the groups that stay of its own
+            u32 left = stays;
+            auto lowest_of = [&](u32 set) { const u32 g = (u32)__ffs(set) - 1; return Batch{g * parts, g, 0}; };
+            Batch i = lowest_of(left);
+            Piece<T> now, next;
+            now.template load<WHOLE>(x + from(i), many(i), wide);
+            for (u32 n = a.top_groups * parts; n; n--) {
+                Batch then = {i.b + 1, i.g, i.p + 1};
+                if (then.p == parts) {
+                    left &= left - 1;
+                    then = lowest_of(left);
+                }
+                if (n > 1) next.template load<WHOLE>(x + from(then), many(then), wide);
                 u32 key[kPiece];
-                v.load(x + from(g, p), many(p), wide);
-                keys_of(v, from(g, p), many(p), key);
-                if (grouped)
-#pragma unroll
-                    for (int i = 0; i < (int)kPiece; i++) key[i] = kept ? key[i] : 0u;
-                sort_keys<kPiece>(key);
-                // the eight greatest of two sorted eights, sorted again
-#pragma unroll
-                for (int i = 0; i < (int)kFew; i++) best[i] = max(best[i], key[kFew - 1 - i]);
-#pragma unroll
-                for (int d = 4; d; d >>= 1)
-#pragma unroll
-                    for (int i = 0; i < (int)kFew; i++)
-                        if (!(i & d)) order_two(best[i], best[i + d]);
+                keys_of(now, i, key);
+                merge(key);
+                now = next;
+                i = then;
             }
+        } else {
+            each([&](const Batch &i, const Piece<T> &v) {
+                u32 key[kPiece];
+                keys_of(v, i, key);
+                merge(key);
+            });
         }
 
         // lane q of the four keeps slots q and q + 4; one look further tells
@@ -787,14 +841,19 @@ template <class T, int ORDER> int run_route_few(const RouteArgs &a, cudaStream_t
 {
     const u32 sms = sm_count(), size = a.experts / a.groups;
     if (!sms) return MV_ECUDA;
+    const bool grouped = a.groups > 1 && a.top_groups < a.groups;
     const bool wide = aligned(a.logits, 16) && a.stride * sizeof(T) % 16 == 0 && (a.groups == 1 || size % kPiece == 0);
-    // eight rows a warp: short batches spread over the SMs in small blocks
+    const u32 rows = grouped ? 8 * few_value_words(a.groups) : 0, values = ((rows > a.experts ? rows : a.experts) + 3) & ~3u;
+    // Eight rows a warp: short batches spread over the SMs in small blocks.
     const u64 warps = (a.tokens + 7) / 8;
     const u32 a_block = warps < 4ull * kRouteWarps * sms ? 2 : kRouteWarps;
+    const u32 smem = 4 * ((ORDER == kByLogit ? 0 : (a.experts + 3) & ~3u) + a_block * values);
     const u32 blocks = (u32)std::fmin((double)((warps + a_block - 1) / a_block), 8.0 * sms);
-    const u32 scratch = a.groups > 1 && 8 * a.groups > a.experts ? 8 * a.groups : a.experts;
-    return launch(k_route_few<T, ORDER>, blocks, a_block * 32,
-                  4 * ((ORDER == kByLogit ? 0 : a.experts) + a_block * scratch), stream, a, wide);
+    const auto kernel = size % kBatch == 0 && wide ? k_route_few<T, ORDER, true> : k_route_few<T, ORDER, false>;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return MV_ECUDA;
+    return launch(kernel, blocks, a_block * 32, smem, stream, a, wide);
 }
 
 template <class T, int ORDER, int V> int run_route(const RouteArgs &a, const Shares &sh, cudaStream_t stream)
