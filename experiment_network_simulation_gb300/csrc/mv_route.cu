@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a, c
 // Score keys are fixed point: score * f + bias' lies in (4, 6), where floats
 // are 2^-21 apart, and their last 22 bits move to the top of the key; 4
 // itself is closed.
-constexpr u32 kFew = 8, kPiece = 8, kBatch = 32;
+constexpr u32 kFew = 8, kPiece = 8, kBatch = 32, kFewWarps = 4;
 
 // f: power of two; bias' = bias * f + shift; close: units that may be an error.
 struct Scale {
@@ -443,10 +443,10 @@ __host__ __device__ constexpr u32 few_value_words(u32 groups) { return (groups +
 
 // WHOLE: groups are whole batches and loads are wide.
 template <class T, int ORDER, bool WHOLE>
-__global__ void __launch_bounds__(kRouteWarps * 32) k_route_few(const RouteArgs a, const bool wide)
+__global__ void __launch_bounds__(kFewWarps * 32, 8) k_route_few(const RouteArgs a, const bool wide)
 {
     extern __shared__ float shared[];
-    __shared__ float lowest[kRouteWarps], highest[kRouteWarps];
+    __shared__ float lowest[kFewWarps], highest[kFewWarps];
     constexpr bool EXACT = sizeof(T) == 2 && ORDER == kByLogit;
     const u32 E = a.experts, lane = threadIdx.x & 31, q = lane & 3, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const u32 size = E / a.groups, parts = (size + kBatch - 1) / kBatch;
@@ -846,9 +846,9 @@ template <class T, int ORDER> int run_route_few(const RouteArgs &a, cudaStream_t
     const u32 rows = grouped ? 8 * few_value_words(a.groups) : 0, values = ((rows > a.experts ? rows : a.experts) + 3) & ~3u;
     // Eight rows a warp: short batches spread over the SMs in small blocks.
     const u64 warps = (a.tokens + 7) / 8;
-    const u32 a_block = warps < 4ull * kRouteWarps * sms ? 2 : kRouteWarps;
+    const u32 a_block = warps < 16ull * sms ? 1 : kFewWarps;
     const u32 smem = 4 * ((ORDER == kByLogit ? 0 : (a.experts + 3) & ~3u) + a_block * values);
-    const u32 blocks = (u32)std::fmin((double)((warps + a_block - 1) / a_block), 8.0 * sms);
+    const u32 blocks = (u32)std::fmin((double)((warps + a_block - 1) / a_block), 64.0 * sms);
     const auto kernel = size % kBatch == 0 && wide ? k_route_few<T, ORDER, true> : k_route_few<T, ORDER, false>;
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
