@@ -769,72 +769,151 @@ struct RouteGradArgs {
     float scale;
 };
 
-// The gradient of one row by one warp.  With G the slots' gradients laid out
-// over the experts, and p the softmax: dx = scale p (G - sum G p), dense.
-// In the other forms only the chosen experts' logits matter.
+// The gradient of a row.  With G the slots' gradients laid out over the
+// experts, and p the softmax: dx = scale p (G - sum G p), dense.  In the
+// other forms only the chosen experts' logits matter and the rest is zeros.
+// L lanes share a row, V experts a lane: eight neighbours of every 8 L, whose
+// sums do not depend on how the row lies in memory.  G, or the slots' results,
+// are scattered into the row's floats in shared memory; rows that 16-byte
+// accesses do not fit (not WIDE) come and go through there too.
 constexpr u32 kGradWarps = 8;
 
-template <class T>
+template <class T, int L, int V, bool WIDE>
 __global__ void __launch_bounds__(kGradWarps * 32) k_route_grad(const RouteGradArgs a)
 {
     extern __shared__ float grads[];
-    const u32 lane = threadIdx.x & 31, E = a.experts;
-    float *G = grads + (threadIdx.x >> 5) * E;
-    const u64 step = (u64)gridDim.x * kGradWarps;
-    for (u64 row = (u64)blockIdx.x * kGradWarps + (threadIdx.x >> 5); row < a.tokens; row += step) {
-        const T *x = static_cast<const T *>(a.logits) + row * a.stride;
-        T *dx = static_cast<T *>(a.dlogits) + row * E;
-        for (u32 e = lane; e < E; e += 32) G[e] = 0.0f;
-        int id = lane < a.topk ? a.ids[row * a.topk + lane] : -1;
+    constexpr u32 kRows = 32 / L;
+    const u32 E = a.experts, pitch = (E + 7) & ~7u, lane = threadIdx.x & 31, sub = lane & (L - 1);
+    float *G = grads + (threadIdx.x / L) * pitch;
+    const bool dense = a.softmax && !a.renorm;
+    auto place = [&](int i) { return (i / 8) * (L * 8) + sub * 8 + i % 8; };
+    // this lane's experts out of the row in shared memory, whose pitch is a whole number of eights
+    auto gather = [&](float (&at)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4 *>(at + i) =
+                (u32)place(i) < pitch ? *reinterpret_cast<const float4 *>(G + place(i)) : make_float4(0, 0, 0, 0);
+    };
+    const u64 step = (u64)gridDim.x * kGradWarps * kRows;
+    for (u64 first = ((u64)blockIdx.x * kGradWarps + (threadIdx.x >> 5)) * kRows; first < a.tokens; first += step) {
+        const u64 row = first + lane / L;
+        const bool here = row < a.tokens;
+        const T *x = static_cast<const T *>(a.logits) + (here ? row : first) * a.stride;
+        alignas(16) float v[V];
+        if (dense) {
+            if (WIDE) {
+#pragma unroll
+                for (int i = 0; i < V; i += 8) {
+                    Piece<T> piece;
+                    piece.template load<false>(x + place(i), (u32)place(i) < E ? 8 : 0, true);
+#pragma unroll
+                    for (int j = 0; j < 8; j++) v[i + j] = piece.value(j);
+                }
+            } else {
+                for (u32 e = sub; e < pitch; e += L) G[e] = e < E ? to_float(x[e]) : -INFINITY;
+                __syncwarp();
+                gather(v);
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    if ((u32)place(i) >= E) v[i] = -INFINITY;
+                __syncwarp();
+            }
+        }
+        int id = here && sub < a.topk ? a.ids[row * a.topk + sub] : -1;
         if ((u32)id >= E) id = -1;
-        const float g = id >= 0 ? a.dweights[row * a.topk + lane] : 0.0f;
+        const float g = id >= 0 ? a.dweights[row * a.topk + sub] : 0.0f;
+        for (u32 e = sub * 4; e < pitch; e += L * 4) *reinterpret_cast<float4 *>(G + e) = make_float4(0, 0, 0, 0);
         __syncwarp();
-        if (a.softmax && !a.renorm) {
+        if (dense) {
             if (id >= 0) G[id] = g;
-            __syncwarp();
             float m = -INFINITY, sum = 0.0f, dot = 0.0f;
-            for (u32 e = lane; e < E; e += 32) {
-                const float v = to_float(x[e]);
-                if (open(v)) m = fmaxf(m, v);
+#pragma unroll
+            for (int i = 0; i < V; i++) m = fmaxf(m, v[i]);          // passes NaN by
+            m = group_max<L>(m);
+            __syncwarp();
+            alignas(16) float at[V];
+            gather(at);
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+                v[i] = !open(v[i]) ? 0.0f : v[i] == m ? 1.0f : exp2_fast((v[i] - m) * kLog2e);
+                sum += v[i];
+                dot += v[i] * at[i];
             }
-            m = group_max<32>(m);
-            for (u32 e = lane; e < E; e += 32) {
-                const float v = to_float(x[e]), p = open(v) ? exp_below(v, m) : 0.0f;
-                sum += p;
-                dot += p * G[e];
-            }
-            sum = group_sum<32>(sum);
-            dot = group_sum<32>(dot);
+            sum = group_sum<L>(sum);
+            dot = group_sum<L>(dot);
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
             dot *= inv;
-            for (u32 e = lane; e < E; e += 32) {
-                const float v = to_float(x[e]), p = open(v) ? exp_below(v, m) * inv : 0.0f;
-                dx[e] = from_float<T>(p * (G[e] - dot) * a.scale);
-            }
+#pragma unroll
+            for (int i = 0; i < V; i++) v[i] = v[i] * inv * (at[i] - dot) * a.scale;
         } else {
-            const float v = id >= 0 ? to_float(x[id]) : -INFINITY;
+            const float l = id >= 0 ? to_float(x[id]) : -INFINITY;
             float d;
             if (a.softmax) {
-                const float best = group_max<32>(v);
-                float w = id >= 0 ? exp_below(v, best) : 0.0f;
-                const float sum = group_sum<32>(w);
+                const float best = group_max<L>(l);
+                float w = id >= 0 ? exp_below(l, best) : 0.0f;
+                const float sum = group_sum<L>(w);
                 w = sum > 0.0f ? w / sum : 0.0f;
-                d = w * (g - group_sum<32>(g * w));
+                d = w * (g - group_sum<L>(g * w));
             } else {
-                const float s = id >= 0 ? sigmoid(v) : 0.0f;
+                const float s = id >= 0 ? sigmoid(l) : 0.0f;
                 d = g;
                 if (a.renorm) {
-                    const float sum = group_sum<32>(s), dot = group_sum<32>(g * s);
+                    const float sum = group_sum<L>(s), dot = group_sum<L>(g * s);
                     d = sum > 0.0f ? (g - dot / sum) / sum : 0.0f;
                 }
                 d *= s * (1.0f - s);
             }
             if (id >= 0) G[id] = d * a.scale;
             __syncwarp();
-            for (u32 e = lane; e < E; e += 32) dx[e] = from_float<T>(G[e]);
+            gather(v);
         }
         __syncwarp();
+        T *dx = static_cast<T *>(a.dlogits) + row * E;
+        if (WIDE) {
+#pragma unroll
+            for (int i = 0; i < V; i += 8) {
+                if ((u32)place(i) >= E || !here) continue;
+                T out[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) out[j] = from_float<T>(v[i + j]);
+#pragma unroll
+                for (int j = 0; j < (int)sizeof(T) / 2; j++) {
+                    uint4 q;
+                    memcpy(&q, reinterpret_cast<const char *>(out) + 16 * j, 16);
+                    reinterpret_cast<uint4 *>(dx + place(i))[j] = q;
+                }
+            }
+        } else {
+            if (dense)
+#pragma unroll
+                for (int i = 0; i < V; i += 4)
+                    if ((u32)place(i) < pitch) *reinterpret_cast<float4 *>(G + place(i)) = *reinterpret_cast<float4 *>(v + i);
+            __syncwarp();
+            if (here)
+                for (u32 e = sub; e < E; e += L) dx[e] = from_float<T>(G[e]);
+            __syncwarp();
+        }
     }
+}
+
+template <class T, int L, int V> int run_route_grad(const RouteGradArgs &a, cudaStream_t stream)
+{
+    constexpr u32 kRowsABlock = kGradWarps * 32 / L;
+    const u32 sms = sm_count(), smem = kRowsABlock * ((a.experts + 7) & ~7u) * 4;
+    if (!sms) return MV_ECUDA;
+    const bool wide = a.experts % 8 == 0 && aligned(a.logits, 16) && a.stride * sizeof(T) % 16 == 0 && aligned(a.dlogits, 16);
+    const u32 blocks = (u32)std::fmin((double)((a.tokens + kRowsABlock - 1) / kRowsABlock), 8.0 * sms);
+    return launch(wide ? k_route_grad<T, L, V, true> : k_route_grad<T, L, V, false>, blocks, kGradWarps * 32, smem, stream, a);
+}
+
+// The smallest shape that holds the experts, and a lane to a slot.
+template <class T> int run_route_grad(const RouteGradArgs &a, cudaStream_t stream)
+{
+    if (a.experts <= 64 && a.topk <= 8) return run_route_grad<T, 8, 8>(a, stream);
+    if (a.experts <= 128 && a.topk <= 16) return run_route_grad<T, 16, 8>(a, stream);
+    if (a.experts <= 256) return run_route_grad<T, 32, 8>(a, stream);
+    if (a.experts <= 512) return run_route_grad<T, 32, 16>(a, stream);
+    return run_route_grad<T, 32, 32>(a, stream);
 }
 
 template <class T, int ORDER> int run_route_few(const RouteArgs &a, cudaStream_t stream)
@@ -892,14 +971,6 @@ template <class T> int run_route(const RouteArgs &a, Order order, cudaStream_t s
     if (order == kByLogit) return run_route<T, kByLogit>(a, stream);
     if (order == kBySigmoid) return run_route<T, kBySigmoid>(a, stream);
     return run_route<T, kBySoftmax>(a, stream);
-}
-
-template <class T> int run_route_grad(const RouteGradArgs &a, cudaStream_t stream)
-{
-    const u32 blocks = (u32)std::fmin((double)((a.tokens + kGradWarps - 1) / kGradWarps),
-                                      (double)sm_count() * 8);
-    if (!blocks) return MV_ECUDA;
-    return launch(k_route_grad<T>, blocks, kGradWarps * 32, kGradWarps * a.experts * 4, stream, a);
 }
 
 }  // namespace mvmoe
