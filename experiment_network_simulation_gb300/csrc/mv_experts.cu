@@ -43,6 +43,7 @@ __device__ __forceinline__ u32 column_place(u32 c) { return (c & ~7u) | ((c & 3)
 
 template <class T> struct Math;
 template <> struct Math<__half> {
+    static constexpr bool kOneShift = true;
     static constexpr u32 kPower = 0x64006400, kOffset = 0x64086408;      // 1024, 1032
     static __device__ __forceinline__ u32 sub(u32 a, u32 b)
     {
@@ -59,6 +60,7 @@ template <> struct Math<__half> {
     }
 };
 template <> struct Math<__nv_bfloat16> {
+    static constexpr bool kOneShift = false;
     static constexpr u32 kPower = 0x43004300, kOffset = 0x43084308;      // 128, 136
     static __device__ __forceinline__ u32 sub(u32 a, u32 b)
     {
@@ -76,9 +78,20 @@ template <> struct Math<__nv_bfloat16> {
 };
 template <class T> __device__ __forceinline__ void widen(u32 word, u32 (&p)[4])
 {
+    if constexpr (Math<T>::kOneShift) {
+        // half's ten bits hold a nibble in place: 1024 + 16 q, over 16, less 72
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-        p[i] = Math<T>::sub(((word >> (4 * i)) & 0x000F000Fu) | Math<T>::kPower, Math<T>::kOffset);
+        for (int i = 0; i < 4; i += 2) {
+            const u32 w = word >> (4 * i);
+            p[i] = Math<T>::sub((w & 0x000F000Fu) | Math<T>::kPower, Math<T>::kOffset);
+            const u32 v = (w & 0x00F000F0u) | Math<T>::kPower;
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[i + 1]) : "r"(v), "r"(0x2C002C00u), "r"(0xD480D480u));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            p[i] = Math<T>::sub(((word >> (4 * i)) & 0x000F000Fu) | Math<T>::kPower, Math<T>::kOffset);
+    }
 }
 
 __device__ __forceinline__ void copy16(u32 to, const void *from)
@@ -157,44 +170,42 @@ template <class T> __global__ void __launch_bounds__(kPrepThreads) k_prepare(con
 }
 
 // ---- products ------------------------------------------------------------
-constexpr u32 kWarps = 4, kThreads = kWarps * 32;
-constexpr u32 kRows = kWarps * 32;              // weight rows a block
-constexpr u32 kStep = 128;                      // columns a stage
+constexpr u32 kWarps = 8, kThreads = kWarps * 32;
+constexpr u32 kRows = kWarps / 2 * 32;          // weight rows a block: 32 to each of four pairs of warps
+constexpr u32 kStep = 256;                      // columns a stage: half of them to each warp of a pair
 constexpr u32 kWPitch = kStep / 2 + 16;         // bytes; 16-byte pieces of eight rows fall in eight bank groups
 constexpr u32 kXPitch = kStep * 2 + 64;
 
 // Scales come by epochs of 16 groups, two in shared memory.  A row's scales
 // start anywhere, so the aligned 16-byte pieces around them are copied: three
-// hold 16 groups at any offset.
+// hold 16 groups at any offset.  An epoch is two steps or more, and its copy
+// has one step less than there are stages to arrive in.
 constexpr u32 kEpoch = 16;
 constexpr u32 kSPitch = kEpoch * 2 + 16;
 constexpr u32 kScaleBytes = 2 * kRows * kSPitch;
 
-// A stage that holds up to 8 NT pairs' activations, and the shared memory of
-// a block whose items hold that many.
-template <int NT> struct Stage {
-    static constexpr u32 kBytes = kRows * kWPitch + NT * 8 * kXPitch;
-    static constexpr u32 kBudget = kScaleBytes + (NT == 4 ? 3 : 4) * kBytes;
-    template <u32 BUDGET>
-    static constexpr int kCount = (BUDGET - kScaleBytes) / kBytes < 5 ? (BUDGET - kScaleBytes) / kBytes : 5;
-};
+// Stages of up to 8 NT pairs, and the shared memory of a block whose items
+// hold that many: two blocks fit on an SM.
+template <int NT> constexpr u32 kStageBytes = kRows * kWPitch + NT * 8 * kXPitch;
+template <int NT> constexpr int kStagesOf = NT == 4 ? 2 : 3;
+template <int NT> constexpr u32 kSmem = kScaleBytes + (NT == 1 ? kStagesOf<1> * kStageBytes<1> : kStagesOf<2> * kStageBytes<2>);
+static_assert(kStagesOf<4> * kStageBytes<4> <= kStagesOf<2> * kStageBytes<2>, "four tiles fit two tiles' room");
 
 // One tile of weight rows against up to 8 NT pairs' activations.  A warp
 // holds 32 rows as two matrix operands of 16; an operand of 16 x 16 weights
 // meets 16 x 8 activations in one mma.  Sums of a group of columns start at
-// zero and are then added, times the rows' scales, in 32 bits.  The order of
-// additions depends on the sizes alone, never on the other tokens.
-template <class T, int NT, bool GATE, u32 BUDGET>
+// zero and are then added, times the rows' scales, in 32 bits; a pair of
+// warps adds its two sums at the end.  The order of additions depends on the
+// sizes alone, never on the other tokens.
+template <class T, int NT, bool GATE>
 __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 tile, unsigned char *smem)
 {
-    constexpr int S = Stage<NT>::template kCount<BUDGET>;
-    // an epoch is four steps or more, and its copy has S - 1 to arrive in
-    static_assert(S >= 2 && S <= 5, "two to five stages");
-    const u32 tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const u32 K = GATE ? a.hidden : a.inner;
-    const u32 groups = K / a.group;
-    const u32 scales = (u32)__cvta_generic_to_shared(smem);
-    const u32 ring = (u32)__cvta_generic_to_shared(smem + kScaleBytes);
+    constexpr int kStages = kStagesOf<NT>;
+    const u32 tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const u32 half = tid >> 7, warp = (tid >> 5) & 3;         // columns, rows
+    const u32 K = GATE ? a.hidden : a.inner, groups = K / a.group;
+    const u32 per = a.group / 32, shift = per >> 1;           // blocks of 32 columns a group: 1, 2 or 4
+    const u32 scales = (u32)__cvta_generic_to_shared(smem), ring = scales + kScaleBytes;
     // block row r: warp r / 32's operand (r / 16) & 1, row r & 15
     auto weight_row = [&](u32 r) -> int64_t {
         if (GATE) {
@@ -205,43 +216,43 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         return i < a.hidden ? (int64_t)i : -1;
     };
     const u64 base_row = (u64)it.expert * (GATE ? 2 * a.inner : a.hidden);
-    const uint8_t *W = (GATE ? a.w13 : a.w2) + base_row * (K / 2);
-    // this thread's pieces of a stage
+    // this thread's pieces of a stage: weights, activations, scales
     const uint8_t *wp[4];
-    u32 wd[4];
+    u32 w_valid = 0;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        const u32 c = tid + j * kThreads, r = c >> 2;
-        const int64_t row = weight_row(r);
-        wp[j] = row < 0 ? nullptr : W + (u64)row * (K / 2) + (c & 3) * 16;
-        wd[j] = ring + r * kWPitch + (c & 3) * 16;
+        const int64_t row = weight_row((tid >> 3) + j * 32);
+        wp[j] = (GATE ? a.w13 : a.w2) + (base_row + (u64)(row < 0 ? 0 : row)) * (K / 2) + (tid & 7) * 16;
+        w_valid |= (row < 0 ? 0u : 1u) << j;
     }
-    const T *xpnt[NT];
-    u32 xd[NT];
+    const u32 w_to = ring + (tid >> 3) * kWPitch + (tid & 7) * 16;
+    const T *xp[NT];
+    u32 x_valid = 0;
 #pragma unroll
     for (int j = 0; j < NT; j++) {
-        const u32 c = tid + j * kThreads, r = c >> 4;
-        xpnt[j] = nullptr;
-        if (r < it.count) {
-            const u32 p = a.pairs[it.first + r];
-            xpnt[j] = (GATE ? static_cast<const T *>(a.xp) + (u64)(p / a.topk) * K
-                            : static_cast<const T *>(a.h) + (u64)p * K) + (c & 15) * 8;
-        }
-        xd[j] = ring + kRows * kWPitch + r * kXPitch + (c & 15) * 16;
+        const u32 r = (tid >> 5) + j * 8;
+        const u64 p = r < it.count ? a.pairs[it.first + r] : 0;
+        x_valid |= (r < it.count ? 1u : 0u) << j;
+        xp[j] = (GATE ? static_cast<const T *>(a.xp) + p / a.topk * K : static_cast<const T *>(a.h) + p * K) + lane * 8;
     }
-    auto fetch = [&](u32 s, u32 slot) {
-        const u32 k0 = s * kStep, off = slot * Stage<NT>::kBytes;
+    const u32 x_to = ring + kRows * kWPitch + (tid >> 5) * kXPitch + lane * 16;
+    auto fetch = [&](u32 s, u32 slot) {                       // pointers advance: called for s = 0, 1, ...
+        const u32 off = slot * kStageBytes<NT>;
+        const bool w_in = s * kStep + (tid & 7) * 32 < K, x_in = s * kStep + lane * 8 < K;
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (wp[j] && k0 + (tid & 3) * 32 < K) copy16(wd[j] + off, wp[j] + k0 / 2);
+        for (int j = 0; j < 4; j++) {
+            if (w_in && ((w_valid >> j) & 1)) copy16(w_to + off + j * 32 * kWPitch, wp[j]);
+            wp[j] += kStep / 2;
+        }
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-            if (xpnt[j] && k0 + (tid & 15) * 8 < K) copy16(xd[j] + off, xpnt[j] + k0);
+        for (int j = 0; j < NT; j++) {
+            if (x_in && ((x_valid >> j) & 1)) copy16(x_to + off + j * 8 * kXPitch, xp[j]);
+            xp[j] += kStep;
+        }
     };
-    // this thread copies the scales of block row tid
     const T *all = static_cast<const T *>(GATE ? a.s13 : a.s2);
     const char *s_end = reinterpret_cast<const char *>(all + (u64)a.experts * (GATE ? 2 * a.inner : a.hidden) * groups);
-    const int64_t srow = weight_row(tid);
+    const int64_t srow = tid < kRows ? weight_row(tid) : -1;
     const char *s_row = srow < 0 ? nullptr : reinterpret_cast<const char *>(all + (base_row + (u64)srow) * groups);
     auto fetch_scales = [&](u32 epoch) {
         if (!s_row || epoch * kEpoch >= groups) return;
@@ -270,67 +281,92 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
 #pragma unroll
             for (int i = 0; i < 4; i++) total[m][n][i] = part[m][n][i] = 0.0f;
 
-    const u32 steps = (K + kStep - 1) / kStep, per = a.group / 32, shift = per >> 1;   // per: 1, 2 or 4
-    const u32 shift_e = 2 + shift;                          // steps an epoch: 4, 8 or 16
+    const u32 steps = (K + kStep - 1) / kStep;
     fetch_scales(0);
 #pragma unroll
-    for (int s = 0; s < S - 1; s++) {
+    for (int s = 0; s < kStages - 1; s++) {
         if ((u32)s < steps) fetch(s, s);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    const u32 a_at = ring + (warp * 32 + (lane & 7) + ((lane >> 3) & 1) * 8 + (lane >> 4) * 16) * kWPitch;
-    const u32 x_at = ring + kRows * kWPitch + g * kXPitch + t * 16;
-    u32 slot = 0, ahead = S - 1;
-    for (u32 s = 0; s < steps; s++) {
-        copies_left<S - 2>();
-        __syncthreads();
-        if (s + S - 1 < steps) fetch(s + S - 1, ahead);
-        if ((s & ((1u << shift_e) - 1)) == 0) fetch_scales((s >> shift_e) + 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        const u32 off = slot * Stage<NT>::kBytes;
-        const u32 blocks = min(kStep, K - s * kStep) / 32;
+    const u32 a_at = ring + (warp * 32 + (lane & 7) + ((lane >> 3) & 1) * 8 + (lane >> 4) * 16) * kWPitch + half * 64;
+    const u32 x_at = ring + kRows * kWPitch + g * kXPitch + t * 16 + half * 256;
+    // this half's blocks of 32 columns of a step, those below `blocks`
+    auto multiply = [&](u32 s, u32 off, u32 blocks) {
 #pragma unroll
-        for (u32 b = 0; b < kStep / 32; b++) {
-            if (b < blocks) {
-                u32 w[4];
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a_at + off + b * 16));
-                u32 q[4][4];
+        for (u32 b = 0; b < kStep / 64; b++) {
+            if (b >= blocks) break;
+            u32 w[4], q[4][4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a_at + off + b * 16));
 #pragma unroll
-                for (int i = 0; i < 4; i++) widen<T>(w[i], q[i]);
+            for (int i = 0; i < 4; i++) widen<T>(w[i], q[i]);
 #pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    u32 x0, x1, x2, x3;
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
-                                 : "r"(x_at + off + n * 8 * kXPitch + b * 64));
+            for (int n = 0; n < NT; n++) {
+                u32 x0, x1, x2, x3;
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                             : "r"(x_at + off + n * 8 * kXPitch + b * 64));
 #pragma unroll
-                    for (int m = 0; m < 2; m++) {
-                        Math<T>::mma(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], x0, x1);
-                        Math<T>::mma(part[m][n], q[2 * m][2], q[2 * m + 1][2], q[2 * m][3], q[2 * m + 1][3], x2, x3);
-                    }
+                for (int m = 0; m < 2; m++) {
+                    Math<T>::mma(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], x0, x1);
+                    Math<T>::mma(part[m][n], q[2 * m][2], q[2 * m + 1][2], q[2 * m][3], q[2 * m + 1][3], x2, x3);
                 }
-                if (((b + 1) & (per - 1)) == 0) {       // the group's last columns
-                    const u32 group = (s * (kStep / 32) + b) >> shift;
-                    const u32 s_off = ((group / kEpoch) & 1) * kRows * kSPitch + (group % kEpoch) * 2;
+            }
+            if (((b + 1) & (per - 1)) == 0) {                 // the group's last columns
+                const u32 group = (s * (kStep / 32) + half * (kStep / 64) + b) >> shift;
+                const u32 s_off = ((group / kEpoch) & 1) * kRows * kSPitch + (group % kEpoch) * 2;
 #pragma unroll
-                    for (int m = 0; m < 2; m++) {
-                        const float s0 = shared_value<T>(s_at[2 * m] + s_off), s1 = shared_value<T>(s_at[2 * m + 1] + s_off);
+                for (int m = 0; m < 2; m++) {
+                    const float s0 = shared_value<T>(s_at[2 * m] + s_off), s1 = shared_value<T>(s_at[2 * m + 1] + s_off);
 #pragma unroll
-                        for (int n = 0; n < NT; n++) {
-                            total[m][n][0] += s0 * part[m][n][0];
-                            total[m][n][1] += s0 * part[m][n][1];
-                            total[m][n][2] += s1 * part[m][n][2];
-                            total[m][n][3] += s1 * part[m][n][3];
-                            part[m][n][0] = part[m][n][1] = part[m][n][2] = part[m][n][3] = 0.0f;
-                        }
+                    for (int n = 0; n < NT; n++) {
+                        total[m][n][0] += s0 * part[m][n][0];
+                        total[m][n][1] += s0 * part[m][n][1];
+                        total[m][n][2] += s1 * part[m][n][2];
+                        total[m][n][3] += s1 * part[m][n][3];
+                        part[m][n][0] = part[m][n][1] = part[m][n][2] = part[m][n][3] = 0.0f;
                     }
                 }
             }
         }
-        slot = slot + 1 == S ? 0 : slot + 1;
-        ahead = ahead + 1 == S ? 0 : ahead + 1;
+    };
+    u32 slot = 0, ahead = kStages - 1;
+    const u32 epoch_steps = 2u << shift;                      // 2, 4 or 8
+    for (u32 s = 0; s < steps; s++) {
+        copies_left<kStages - 2>();
+        __syncthreads();
+        if (s + kStages - 1 < steps) fetch(s + kStages - 1, ahead);
+        if ((s & (epoch_steps - 1)) == 0) fetch_scales(s / epoch_steps + 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const u32 off = slot * kStageBytes<NT>;
+        if ((s + 1) * kStep <= K) {
+            multiply(s, off, kStep / 64);
+        } else {
+            const u32 left = (K - s * kStep) / 32, mine = half * (kStep / 64);
+            multiply(s, off, left > mine ? left - mine : 0);
+        }
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+        ahead = ahead + 1 == kStages ? 0 : ahead + 1;
     }
     copies_left<0>();
+    // the second half's sums to the first, through the ring
+    __syncthreads();
+    float4 *sums = reinterpret_cast<float4 *>(smem + kScaleBytes) + (warp * 32 + lane);
+    if (half) {
+#pragma unroll
+        for (int m = 0; m < 2; m++)
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+                sums[(m * NT + n) * 128] = make_float4(total[m][n][0], total[m][n][1], total[m][n][2], total[m][n][3]);
+    }
+    __syncthreads();
+    if (half) return;
+#pragma unroll
+    for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const float4 v = sums[(m * NT + n) * 128];
+            total[m][n][0] += v.x; total[m][n][1] += v.y; total[m][n][2] += v.z; total[m][n][3] += v.w;
+        }
     // element i of operand m, tile n: row g + 8 (i / 2), pair 8 n + 2 t + (i & 1)
 #pragma unroll
     for (int n = 0; n < NT; n++)
@@ -354,15 +390,14 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         }
 }
 
-template <class T, bool GATE, int MOST> __global__ void __launch_bounds__(kThreads) k_product(const ExpertArgs a)
+template <class T, bool GATE, int MOST> __global__ void __launch_bounds__(kThreads, 2) k_product(const ExpertArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    constexpr u32 B = Stage<MOST>::kBudget;
     for (u32 i = blockIdx.y; i < *a.n_items; i += gridDim.y) {
         const Item it = a.items[i];
-        if (MOST == 1 || it.count <= 8) product<T, 1, GATE, B>(a, it, blockIdx.x, smem);
-        else if (MOST == 2 || it.count <= 16) product<T, 2, GATE, B>(a, it, blockIdx.x, smem);
-        else product<T, MOST < 4 ? 1 : 4, GATE, B>(a, it, blockIdx.x, smem);
+        if (MOST == 1 || it.count <= 8) product<T, 1, GATE>(a, it, blockIdx.x, smem);
+        else if (MOST == 2 || it.count <= 16) product<T, 2, GATE>(a, it, blockIdx.x, smem);
+        else product<T, MOST < 4 ? 1 : 4, GATE>(a, it, blockIdx.x, smem);
         __syncthreads();
     }
 }
@@ -427,7 +462,7 @@ int check(const mv_experts_desc *d)
 
 template <class T, bool GATE, int MOST> int run_product(const ExpertArgs &a, u64 items, cudaStream_t stream)
 {
-    constexpr u32 smem = Stage<MOST>::kBudget;
+    constexpr u32 smem = kSmem<MOST>;
     const u32 tiles = GATE ? (a.inner + kRows / 2 - 1) / (kRows / 2) : (a.hidden + kRows - 1) / kRows;
     const auto kernel = k_product<T, GATE, MOST>;
     if (smem > 48 * 1024 &&
