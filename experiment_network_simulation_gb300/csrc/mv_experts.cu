@@ -2,6 +2,7 @@
 // include/mv.h).
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "mv_moe.cuh"
 
@@ -25,7 +26,8 @@ struct ExpertArgs {
     u64 tokens, stride;
     u32 topk, experts, hidden, inner, group, item_pairs;
     // workspace
-    void *xp;                       // x, permuted               [tokens, hidden]
+    __half *xp;                     // x / x_unit, permuted      [tokens, hidden]
+    float *x_unit;                  // powers of two             [tokens]
     void *h;                        // silu(W1 x) (W3 x), permuted [pairs, inner]
     float *o;                       // W2 h                      [pairs, hidden]
     u32 *pairs;                     // pairs by expert
@@ -76,6 +78,13 @@ template <> struct Math<__nv_bfloat16> {
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     }
 };
+// The first product of a sum starts it.
+template <class T>
+__device__ __forceinline__ void mma_from_zero(float (&c)[4], u32 a0, u32 a1, u32 a2, u32 a3, u32 b0, u32 b1)
+{
+    c[0] = c[1] = c[2] = c[3] = 0.0f;
+    Math<T>::mma(c, a0, a1, a2, a3, b0, b1);
+}
 template <class T> __device__ __forceinline__ void widen(u32 word, u32 (&p)[4])
 {
     if constexpr (Math<T>::kOneShift) {
@@ -119,17 +128,57 @@ constexpr u32 kPrepThreads = 512;
 // expert); the other blocks write x in the products' column order.  The order
 // of an expert's pairs may differ from run to run: a pair's result does not
 // depend on its place.
+//
+// x is kept as half, whose products take fewer instructions to feed than
+// bfloat16's.  A bfloat16 row is divided by a power of two first, so that its
+// greatest magnitude lies in [2^14, 2^15): its eight bits fit half's eleven
+// exactly down to 2^-28 of the greatest, and below that the error is under
+// 2^-39 of it, less than the 32-bit sums' own.
 template <class T> __global__ void __launch_bounds__(kPrepThreads) k_prepare(const ExpertArgs a)
 {
     const u32 tid = threadIdx.x;
     if (blockIdx.x) {
-        const u64 eights = a.hidden / 8, n = a.tokens * eights;
-        for (u64 i = (u64)(blockIdx.x - 1) * kPrepThreads + tid; i < n; i += (u64)(gridDim.x - 1) * kPrepThreads) {
-            const u64 t = i / eights, c = (i % eights) * 8;
-            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + t * a.stride + c);
-            const uint4 w = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                       __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-            *reinterpret_cast<uint4 *>(static_cast<T *>(a.xp) + t * a.hidden + c) = w;
+        __shared__ float greatest[kPrepThreads / 32];
+        const u32 eights = a.hidden / 8;
+        for (u64 t = blockIdx.x - 1; t < a.tokens; t += gridDim.x - 1) {
+            const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + t * a.stride);
+            uint4 *to = reinterpret_cast<uint4 *>(a.xp + t * a.hidden);
+            float unit = 1.0f, inverse = 1.0f;
+            if constexpr (sizeof(T) == 2 && !Math<T>::kOneShift) {
+                float m = 0.0f;
+                for (u32 i = tid; i < eights; i += kPrepThreads) {
+                    const uint4 v = x[i];
+                    const u32 w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+                }
+                m = group_max<32>(m);
+                __syncthreads();                              // the last token's maxima are read
+                if ((tid & 31) == 0) greatest[tid >> 5] = m;
+                __syncthreads();
+                for (u32 i = 0; i < kPrepThreads / 32; i++) m = fmaxf(m, greatest[i]);
+                if (m > 0.0f && m < INFINITY) {
+                    const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100) - 14;
+                    unit = __uint_as_float((u32)(e + 127) << 23);
+                    inverse = __uint_as_float((u32)(127 - e) << 23);
+                }
+            }
+            for (u32 i = tid; i < eights; i += kPrepThreads) {
+                uint4 v = x[i];
+                if constexpr (!Math<T>::kOneShift) {
+                    u32 *w = reinterpret_cast<u32 *>(&v);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const __half2 h = __floats2half2_rn(__uint_as_float(w[j] << 16) * inverse,
+                                                            __uint_as_float(w[j] & 0xFFFF0000u) * inverse);
+                        memcpy(&w[j], &h, 4);
+                    }
+                }
+                to[i] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                   __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+            }
+            if (tid == 0) a.x_unit[t] = unit;
         }
         return;
     }
@@ -197,14 +246,17 @@ static_assert(kStagesOf<4> * kStageBytes<4> <= kStagesOf<2> * kStageBytes<2>, "f
 // zero and are then added, times the rows' scales, in 32 bits; a pair of
 // warps adds its two sums at the end.  The order of additions depends on the
 // sizes alone, never on the other tokens.
-template <class T, int NT, bool GATE>
+//
+// T: the type of the scales and of the result; C: of the activations; PER:
+// blocks of 32 columns a group.
+template <class T, class C, int NT, bool GATE, u32 PER>
 __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 tile, unsigned char *smem)
 {
     constexpr int kStages = kStagesOf<NT>;
+    constexpr u32 kGroup = PER * 32, kEpochSteps = kEpoch * kGroup / kStep;
     const u32 tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const u32 half = tid >> 7, warp = (tid >> 5) & 3;         // columns, rows
-    const u32 K = GATE ? a.hidden : a.inner, groups = K / a.group;
-    const u32 per = a.group / 32, shift = per >> 1;           // blocks of 32 columns a group: 1, 2 or 4
+    const u32 K = GATE ? a.hidden : a.inner, groups = K / kGroup;
     const u32 scales = (u32)__cvta_generic_to_shared(smem), ring = scales + kScaleBytes;
     // block row r: warp r / 32's operand (r / 16) & 1, row r & 15
     auto weight_row = [&](u32 r) -> int64_t {
@@ -216,39 +268,40 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         return i < a.hidden ? (int64_t)i : -1;
     };
     const u64 base_row = (u64)it.expert * (GATE ? 2 * a.inner : a.hidden);
-    // this thread's pieces of a stage: weights, activations, scales
+    // This thread's pieces of a stage: weights, activations, scales.  Rows
+    // beyond the matrix are copied from its first one and not used.
     const uint8_t *wp[4];
-    u32 w_valid = 0;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         const int64_t row = weight_row((tid >> 3) + j * 32);
         wp[j] = (GATE ? a.w13 : a.w2) + (base_row + (u64)(row < 0 ? 0 : row)) * (K / 2) + (tid & 7) * 16;
-        w_valid |= (row < 0 ? 0u : 1u) << j;
     }
     const u32 w_to = ring + (tid >> 3) * kWPitch + (tid & 7) * 16;
-    const T *xp[NT];
-    u32 x_valid = 0;
+    const C *xp[NT];
 #pragma unroll
-    for (int j = 0; j < NT; j++) {
+    for (int j = 0; j < NT; j++) {                            // a warp copies whole rows
         const u32 r = (tid >> 5) + j * 8;
-        const u64 p = r < it.count ? a.pairs[it.first + r] : 0;
-        x_valid |= (r < it.count ? 1u : 0u) << j;
-        xp[j] = (GATE ? static_cast<const T *>(a.xp) + p / a.topk * K : static_cast<const T *>(a.h) + p * K) + lane * 8;
+        xp[j] = nullptr;
+        if (r >= it.count) continue;
+        const u64 p = a.pairs[it.first + r];
+        xp[j] = (GATE ? reinterpret_cast<const C *>(a.xp) + p / a.topk * K : static_cast<const C *>(a.h) + p * K) + lane * 8;
     }
     const u32 x_to = ring + kRows * kWPitch + (tid >> 5) * kXPitch + lane * 16;
     auto fetch = [&](u32 s, u32 slot) {                       // pointers advance: called for s = 0, 1, ...
         const u32 off = slot * kStageBytes<NT>;
-        const bool w_in = s * kStep + (tid & 7) * 32 < K, x_in = s * kStep + lane * 8 < K;
+        const bool whole = (s + 1) * kStep <= K;
+        if (whole || s * kStep + (tid & 7) * 32 < K)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            if (w_in && ((w_valid >> j) & 1)) copy16(w_to + off + j * 32 * kWPitch, wp[j]);
-            wp[j] += kStep / 2;
-        }
+            for (int j = 0; j < 4; j++) copy16(w_to + off + j * 32 * kWPitch, wp[j]);
+        if (whole || s * kStep + lane * 8 < K)
 #pragma unroll
-        for (int j = 0; j < NT; j++) {
-            if (x_in && ((x_valid >> j) & 1)) copy16(x_to + off + j * 8 * kXPitch, xp[j]);
-            xp[j] += kStep;
-        }
+            for (int j = 0; j < NT; j++)
+                if (xp[j]) copy16(x_to + off + j * 8 * kXPitch, xp[j]);
+#pragma unroll
+        for (int j = 0; j < 4; j++) wp[j] += kStep / 2;
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+            if (xp[j]) xp[j] += kStep;
     };
     const T *all = static_cast<const T *>(GATE ? a.s13 : a.s2);
     const char *s_end = reinterpret_cast<const char *>(all + (u64)a.experts * (GATE ? 2 * a.inner : a.hidden) * groups);
@@ -279,7 +332,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) total[m][n][i] = part[m][n][i] = 0.0f;
+            for (int i = 0; i < 4; i++) total[m][n][i] = 0.0f;
 
     const u32 steps = (K + kStep - 1) / kStep;
     fetch_scales(0);
@@ -299,7 +352,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a_at + off + b * 16));
 #pragma unroll
-            for (int i = 0; i < 4; i++) widen<T>(w[i], q[i]);
+            for (int i = 0; i < 4; i++) widen<C>(w[i], q[i]);
 #pragma unroll
             for (int n = 0; n < NT; n++) {
                 u32 x0, x1, x2, x3;
@@ -307,12 +360,13 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
                              : "r"(x_at + off + n * 8 * kXPitch + b * 64));
 #pragma unroll
                 for (int m = 0; m < 2; m++) {
-                    Math<T>::mma(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], x0, x1);
-                    Math<T>::mma(part[m][n], q[2 * m][2], q[2 * m + 1][2], q[2 * m][3], q[2 * m + 1][3], x2, x3);
+                    if (b % PER == 0) mma_from_zero<C>(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], x0, x1);
+                    else Math<C>::mma(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], x0, x1);
+                    Math<C>::mma(part[m][n], q[2 * m][2], q[2 * m + 1][2], q[2 * m][3], q[2 * m + 1][3], x2, x3);
                 }
             }
-            if (((b + 1) & (per - 1)) == 0) {                 // the group's last columns
-                const u32 group = (s * (kStep / 32) + half * (kStep / 64) + b) >> shift;
+            if (b % PER == PER - 1) {                         // the group's last columns
+                const u32 group = s * (kStep / kGroup) + half * (kStep / 2 / kGroup) + b / PER;
                 const u32 s_off = ((group / kEpoch) & 1) * kRows * kSPitch + (group % kEpoch) * 2;
 #pragma unroll
                 for (int m = 0; m < 2; m++) {
@@ -323,19 +377,17 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
                         total[m][n][1] += s0 * part[m][n][1];
                         total[m][n][2] += s1 * part[m][n][2];
                         total[m][n][3] += s1 * part[m][n][3];
-                        part[m][n][0] = part[m][n][1] = part[m][n][2] = part[m][n][3] = 0.0f;
                     }
                 }
             }
         }
     };
     u32 slot = 0, ahead = kStages - 1;
-    const u32 epoch_steps = 2u << shift;                      // 2, 4 or 8
     for (u32 s = 0; s < steps; s++) {
         copies_left<kStages - 2>();
         __syncthreads();
         if (s + kStages - 1 < steps) fetch(s + kStages - 1, ahead);
-        if ((s & (epoch_steps - 1)) == 0) fetch_scales(s / epoch_steps + 1);
+        if (s % kEpochSteps == 0) fetch_scales(s / kEpochSteps + 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
         const u32 off = slot * kStageBytes<NT>;
         if ((s + 1) * kStep <= K) {
@@ -377,7 +429,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
             const u64 p = a.pairs[it.first + c];
             if (GATE) {
                 const u32 row = tile * (kRows / 2) + warp * 16 + r;
-                const float z = total[0][n][i], up = total[1][n][i];
+                const float unit = a.x_unit[p / a.topk], z = total[0][n][i] * unit, up = total[1][n][i] * unit;
                 if (row < a.inner)
                     static_cast<T *>(a.h)[p * a.inner + column_place(row)] = from_float<T>(z / (1.0f + expf(-z)) * up);
             } else {
@@ -390,14 +442,15 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         }
 }
 
-template <class T, bool GATE, int MOST> __global__ void __launch_bounds__(kThreads, 2) k_product(const ExpertArgs a)
+template <class T, bool GATE, int MOST, u32 PER> __global__ void __launch_bounds__(kThreads, 2) k_product(const ExpertArgs a)
 {
+    using C = std::conditional_t<GATE, __half, T>;
     extern __shared__ __align__(16) unsigned char smem[];
     for (u32 i = blockIdx.y; i < *a.n_items; i += gridDim.y) {
         const Item it = a.items[i];
-        if (MOST == 1 || it.count <= 8) product<T, 1, GATE>(a, it, blockIdx.x, smem);
-        else if (MOST == 2 || it.count <= 16) product<T, 2, GATE>(a, it, blockIdx.x, smem);
-        else product<T, MOST < 4 ? 1 : 4, GATE>(a, it, blockIdx.x, smem);
+        if (MOST == 1 || it.count <= 8) product<T, C, 1, GATE, PER>(a, it, blockIdx.x, smem);
+        else if (MOST == 2 || it.count <= 16) product<T, C, 2, GATE, PER>(a, it, blockIdx.x, smem);
+        else product<T, C, MOST < 4 ? 1 : 4, GATE, PER>(a, it, blockIdx.x, smem);
         __syncthreads();
     }
 }
@@ -425,7 +478,7 @@ template <class T> __global__ void __launch_bounds__(kCombineThreads) k_combine(
 
 // Workspace: offsets of its parts, each on a 256-byte boundary.
 struct Layout {
-    u64 xp, h, o, pairs, items, n_items, total;
+    u64 xp, x_unit, h, o, pairs, items, n_items, total;
 };
 u64 most_items(const mv_experts_desc *d)
 {
@@ -439,6 +492,7 @@ Layout layout(const mv_experts_desc *d)
     u64 at = 0;
     auto take = [&](u64 bytes) { const u64 here = at; at += (bytes + 255) / 256 * 256; return here; };
     l.xp = take(d->tokens * d->hidden * 2);
+    l.x_unit = take(d->tokens * 4);
     l.h = take(pairs * d->inner * 2);
     l.o = take(pairs * d->hidden * 4);
     l.pairs = take(pairs * 4);
@@ -460,22 +514,29 @@ int check(const mv_experts_desc *d)
     return MV_OK;
 }
 
-template <class T, bool GATE, int MOST> int run_product(const ExpertArgs &a, u64 items, cudaStream_t stream)
+template <class T, bool GATE, int MOST, u32 PER> int run_product(const ExpertArgs &a, u64 items, cudaStream_t stream)
 {
     constexpr u32 smem = kSmem<MOST>;
     const u32 tiles = GATE ? (a.inner + kRows / 2 - 1) / (kRows / 2) : (a.hidden + kRows - 1) / kRows;
-    const auto kernel = k_product<T, GATE, MOST>;
+    const auto kernel = k_product<T, GATE, MOST, PER>;
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return MV_ECUDA;
     return launch(kernel, dim3(tiles, (u32)std::fmin((double)items, 65535.0)), kThreads, smem, stream, a);
 }
 
+template <class T, bool GATE, int MOST> int run_product(const ExpertArgs &a, u64 items, cudaStream_t stream)
+{
+    if (a.group == 32) return run_product<T, GATE, MOST, 1>(a, items, stream);
+    if (a.group == 64) return run_product<T, GATE, MOST, 2>(a, items, stream);
+    return run_product<T, GATE, MOST, 4>(a, items, stream);
+}
+
 template <class T, int MOST> int run_experts(const ExpertArgs &a, u64 items, cudaStream_t stream)
 {
     const u32 sms = sm_count();
     if (!sms) return MV_ECUDA;
-    const u32 share = (u32)std::fmin((double)((a.tokens * (a.hidden / 8) + kPrepThreads - 1) / kPrepThreads), sms);
+    const u32 share = (u32)std::fmin((double)a.tokens, 2.0 * sms);
     int rc = launch(k_prepare<T>, dim3(1 + share), kPrepThreads, 0, stream, a);
     if (rc == MV_OK) rc = run_product<T, true, MOST>(a, items, stream);
     if (rc == MV_OK) rc = run_product<T, false, MOST>(a, items, stream);
@@ -529,7 +590,8 @@ extern "C" int mv_experts(const mv_experts_desc *d, void *workspace, uint64_t ws
     a.y = d->y;
     const Layout l = layout(d);
     char *ws = static_cast<char *>(workspace);
-    a.xp = ws + l.xp;
+    a.xp = reinterpret_cast<__half *>(ws + l.xp);
+    a.x_unit = reinterpret_cast<float *>(ws + l.x_unit);
     a.h = ws + l.h;
     a.o = reinterpret_cast<float *>(ws + l.o);
     a.pairs = reinterpret_cast<u32 *>(ws + l.pairs);
