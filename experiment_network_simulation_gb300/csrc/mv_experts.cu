@@ -16,7 +16,16 @@ struct Item {
     u32 expert, first, count;       // pairs[first .. first + count)
 };
 
+// Bit patterns of a widening, as kernel arguments: an instruction holds one
+// constant, and two that the compiler knew would cost it another one.
+struct Patterns {
+    u32 low, high;                  // nibbles 0 and 4, 1 and 5 of a word
+    u32 power, offset;              // what they are masked into, and that plus 8
+    u32 sixteenth, offset16;        // 1 / 16 and -(power / 16 + 8)
+};
+
 struct ExpertArgs {
+    Patterns half, own;             // for half, for the type of x
     const void *x;
     const int32_t *ids;
     const float *weights;
@@ -46,7 +55,7 @@ __device__ __forceinline__ u32 column_place(u32 c) { return (c & ~7u) | ((c & 3)
 template <class T> struct Math;
 template <> struct Math<__half> {
     static constexpr bool kOneShift = true;
-    static constexpr u32 kPower = 0x64006400, kOffset = 0x64086408;      // 1024, 1032
+    static constexpr Patterns kPatterns = {0x000F000F, 0x00F000F0, 0x64006400, 0x64086408, 0x2C002C00, 0xD480D480};   // 1024
     static __device__ __forceinline__ u32 sub(u32 a, u32 b)
     {
         u32 d;
@@ -63,7 +72,7 @@ template <> struct Math<__half> {
 };
 template <> struct Math<__nv_bfloat16> {
     static constexpr bool kOneShift = false;
-    static constexpr u32 kPower = 0x43004300, kOffset = 0x43084308;      // 128, 136
+    static constexpr Patterns kPatterns = {0x000F000F, 0, 0x43004300, 0x43084308, 0, 0};                             // 128
     static __device__ __forceinline__ u32 sub(u32 a, u32 b)
     {
         u32 d;
@@ -85,21 +94,19 @@ __device__ __forceinline__ void mma_from_zero(float (&c)[4], u32 a0, u32 a1, u32
     c[0] = c[1] = c[2] = c[3] = 0.0f;
     Math<T>::mma(c, a0, a1, a2, a3, b0, b1);
 }
-template <class T> __device__ __forceinline__ void widen(u32 word, u32 (&p)[4])
+template <class T> __device__ __forceinline__ void widen(const Patterns &c, u32 word, u32 (&p)[4])
 {
     if constexpr (Math<T>::kOneShift) {
         // half's ten bits hold a nibble in place: 1024 + 16 q, over 16, less 72
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
             const u32 w = word >> (4 * i);
-            p[i] = Math<T>::sub((w & 0x000F000Fu) | Math<T>::kPower, Math<T>::kOffset);
-            const u32 v = (w & 0x00F000F0u) | Math<T>::kPower;
-            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[i + 1]) : "r"(v), "r"(0x2C002C00u), "r"(0xD480D480u));
+            p[i] = Math<T>::sub((w & c.low) | c.power, c.offset);
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[i + 1]) : "r"((w & c.high) | c.power), "r"(c.sixteenth), "r"(c.offset16));
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            p[i] = Math<T>::sub(((word >> (4 * i)) & 0x000F000Fu) | Math<T>::kPower, Math<T>::kOffset);
+        for (int i = 0; i < 4; i++) p[i] = Math<T>::sub(((word >> (4 * i)) & c.low) | c.power, c.offset);
     }
 }
 
@@ -225,20 +232,22 @@ constexpr u32 kStep = 256;                      // columns a stage: half of them
 constexpr u32 kWPitch = kStep / 2 + 16;         // bytes; 16-byte pieces of eight rows fall in eight bank groups
 constexpr u32 kXPitch = kStep * 2 + 64;
 
-// Scales come by epochs of 16 groups, two in shared memory.  A row's scales
-// start anywhere, so the aligned 16-byte pieces around them are copied: three
-// hold 16 groups at any offset.  An epoch is two steps or more, and its copy
-// has one step less than there are stages to arrive in.
-constexpr u32 kEpoch = 16;
-constexpr u32 kSPitch = kEpoch * 2 + 16;
-constexpr u32 kScaleBytes = 2 * kRows * kSPitch;
+// Scales come by epochs of 16 groups (32 of the finest), two in shared
+// memory.  A row's scales start anywhere, so the aligned 16-byte pieces around
+// them are copied.  An epoch is four steps or more, and its copy has one step
+// less than there are stages to arrive in.
+template <u32 PER> constexpr u32 kEpochOf = PER == 1 ? 32 : 16;
+template <u32 PER> constexpr u32 kSPitchOf = kEpochOf<PER> * 2 + 16;
+template <u32 PER> constexpr u32 kScaleBytes = 2 * kRows * kSPitchOf<PER>;
 
 // Stages of up to 8 NT pairs, and the shared memory of a block whose items
 // hold that many: two blocks fit on an SM.
 template <int NT> constexpr u32 kStageBytes = kRows * kWPitch + NT * 8 * kXPitch;
-template <int NT> constexpr int kStagesOf = NT == 4 ? 2 : 3;
-template <int NT> constexpr u32 kSmem = kScaleBytes + (NT == 1 ? kStagesOf<1> * kStageBytes<1> : kStagesOf<2> * kStageBytes<2>);
-static_assert(kStagesOf<4> * kStageBytes<4> <= kStagesOf<2> * kStageBytes<2>, "four tiles fit two tiles' room");
+template <int NT> constexpr int kStagesOf = NT == 4 ? 2 : NT == 2 ? 3 : 4;
+template <u32 PER> constexpr u32 kSmem = kScaleBytes<PER> + kStagesOf<1> * kStageBytes<1>;
+static_assert(kStagesOf<4> * kStageBytes<4> <= kStagesOf<1> * kStageBytes<1> &&
+              kStagesOf<2> * kStageBytes<2> <= kStagesOf<1> * kStageBytes<1>, "more tiles take fewer stages");
+static_assert(2 * (kSmem<1> + 1024) <= 227 * 1024, "two blocks an SM");
 
 // One tile of weight rows against up to 8 NT pairs' activations.  A warp
 // holds 32 rows as two matrix operands of 16; an operand of 16 x 16 weights
@@ -253,11 +262,12 @@ template <class T, class C, int NT, bool GATE, u32 PER>
 __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 tile, unsigned char *smem)
 {
     constexpr int kStages = kStagesOf<NT>;
-    constexpr u32 kGroup = PER * 32, kEpochSteps = kEpoch * kGroup / kStep;
+    constexpr u32 kGroup = PER * 32, kEpoch = kEpochOf<PER>, kSPitch = kSPitchOf<PER>, kEpochSteps = kEpoch * kGroup / kStep;
     const u32 tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const u32 half = tid >> 7, warp = (tid >> 5) & 3;         // columns, rows
     const u32 K = GATE ? a.hidden : a.inner, groups = K / kGroup;
-    const u32 scales = (u32)__cvta_generic_to_shared(smem), ring = scales + kScaleBytes;
+    const Patterns patterns = GATE ? a.half : a.own;
+    const u32 scales = (u32)__cvta_generic_to_shared(smem), ring = scales + kScaleBytes<PER>;
     // block row r: warp r / 32's operand (r / 16) & 1, row r & 15
     auto weight_row = [&](u32 r) -> int64_t {
         if (GATE) {
@@ -352,7 +362,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a_at + off + b * 16));
 #pragma unroll
-            for (int i = 0; i < 4; i++) widen<C>(w[i], q[i]);
+            for (int i = 0; i < 4; i++) widen<C>(patterns, w[i], q[i]);
 #pragma unroll
             for (int n = 0; n < NT; n++) {
                 u32 x0, x1, x2, x3;
@@ -402,7 +412,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     copies_left<0>();
     // the second half's sums to the first, through the ring
     __syncthreads();
-    float4 *sums = reinterpret_cast<float4 *>(smem + kScaleBytes) + (warp * 32 + lane);
+    float4 *sums = reinterpret_cast<float4 *>(smem + kScaleBytes<PER>) + (warp * 32 + lane);
     if (half) {
 #pragma unroll
         for (int m = 0; m < 2; m++)
@@ -516,7 +526,7 @@ int check(const mv_experts_desc *d)
 
 template <class T, bool GATE, int MOST, u32 PER> int run_product(const ExpertArgs &a, u64 items, cudaStream_t stream)
 {
-    constexpr u32 smem = kSmem<MOST>;
+    constexpr u32 smem = kSmem<PER>;
     const u32 tiles = GATE ? (a.inner + kRows / 2 - 1) / (kRows / 2) : (a.hidden + kRows - 1) / kRows;
     const auto kernel = k_product<T, GATE, MOST, PER>;
     if (smem > 48 * 1024 &&
@@ -580,6 +590,8 @@ extern "C" int mv_experts(const mv_experts_desc *d, void *workspace, uint64_t ws
         return MV_EINVAL;
     if (ws_bytes < need) return MV_ENOMEM;
     ExpertArgs a;
+    a.half = Math<__half>::kPatterns;
+    a.own = d->dtype == MV_F16 ? Math<__half>::kPatterns : Math<__nv_bfloat16>::kPatterns;
     a.x = d->x;
     a.ids = d->ids;
     a.weights = d->weights;
