@@ -8,9 +8,9 @@
 
 namespace mvmoe {
 
-// A token's slot is a pair; pairs are grouped by expert, and up to 8, 16 or 32
+// A token's slot is a pair; pairs are grouped by expert, and up to 8, 16 or 24
 // of one expert's pairs make an item: what one pass over its weights serves.
-u32 item_pairs(u64 tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : 32; }
+u32 item_pairs(u64 tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : 24; }
 
 struct Item {
     u32 expert, first, count;       // pairs[first .. first + count)
@@ -128,6 +128,11 @@ template <class T> __device__ __forceinline__ float shared_value(u32 at)
     return to_float(t);
 }
 
+// A kernel of the chain may start while the one before it ends, and waits
+// here for what that one has written.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---- grouping ------------------------------------------------------------
 constexpr u32 kPrepThreads = 512;
 
@@ -144,6 +149,7 @@ constexpr u32 kPrepThreads = 512;
 template <class T> __global__ void __launch_bounds__(kPrepThreads) k_prepare(const ExpertArgs a)
 {
     const u32 tid = threadIdx.x;
+    let_next_start();
     if (blockIdx.x) {
         __shared__ float greatest[kPrepThreads / 32];
         const u32 eights = a.hidden / 8;
@@ -243,11 +249,11 @@ template <u32 PER> constexpr u32 kScaleBytes = 2 * kRows * kSPitchOf<PER>;
 // Stages of up to 8 NT pairs, and the shared memory of a block whose items
 // hold that many: two blocks fit on an SM.
 template <int NT> constexpr u32 kStageBytes = kRows * kWPitch + NT * 8 * kXPitch;
-template <int NT> constexpr int kStagesOf = NT == 4 ? 2 : NT == 2 ? 3 : 4;
-template <u32 PER> constexpr u32 kSmem = kScaleBytes<PER> + kStagesOf<1> * kStageBytes<1>;
-static_assert(kStagesOf<4> * kStageBytes<4> <= kStagesOf<1> * kStageBytes<1> &&
-              kStagesOf<2> * kStageBytes<2> <= kStagesOf<1> * kStageBytes<1>, "more tiles take fewer stages");
-static_assert(2 * (kSmem<1> + 1024) <= 227 * 1024, "two blocks an SM");
+template <int NT> constexpr int kStagesOf = NT == 1 ? 4 : 3;
+template <int MOST, u32 PER>
+constexpr u32 kSmem = kScaleBytes<PER> + (MOST < 3 ? kStagesOf<1> * kStageBytes<1> : kStagesOf<3> * kStageBytes<3>);
+static_assert(kStagesOf<2> * kStageBytes<2> <= kStagesOf<1> * kStageBytes<1> &&
+              kStagesOf<1> * kStageBytes<1> <= kStagesOf<3> * kStageBytes<3>, "fewer tiles fit the room of more");
 
 // One tile of weight rows against up to 8 NT pairs' activations.  A warp
 // holds 32 rows as two matrix operands of 16; an operand of 16 x 16 weights
@@ -355,24 +361,38 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     const u32 x_at = ring + kRows * kWPitch + g * kXPitch + t * 16 + half * 256;
     // this half's blocks of 32 columns of a step, those below `blocks`
     auto multiply = [&](u32 s, u32 off, u32 blocks) {
+        // every operand of the step is under way before the first is used
+        u32 w[kStep / 64][4], x[kStep / 64][4];
+#pragma unroll
+        for (u32 b = 0; b < kStep / 64; b++) {
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[b][0]), "=r"(w[b][1]), "=r"(w[b][2]), "=r"(w[b][3]) : "r"(a_at + off + b * 16));
+            if (NT == 1)
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(x[b][0]), "=r"(x[b][1]), "=r"(x[b][2]), "=r"(x[b][3])
+                             : "r"(x_at + off + b * 64));
+        }
 #pragma unroll
         for (u32 b = 0; b < kStep / 64; b++) {
             if (b >= blocks) break;
-            u32 w[4], q[4][4];
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a_at + off + b * 16));
+            u32 q[4][4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) widen<C>(patterns, w[i], q[i]);
+            for (int i = 0; i < 4; i++) widen<C>(patterns, w[b][i], q[i]);
 #pragma unroll
             for (int n = 0; n < NT; n++) {
-                u32 x0, x1, x2, x3;
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
-                             : "r"(x_at + off + n * 8 * kXPitch + b * 64));
+                u32 y[4];
+                if (NT == 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) y[i] = x[b][i];
+                } else {
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                                 : "r"(x_at + off + n * 8 * kXPitch + b * 64));
+                }
 #pragma unroll
                 for (int m = 0; m < 2; m++) {
-                    if (b % PER == 0) mma_from_zero<C>(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], x0, x1);
-                    else Math<C>::mma(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], x0, x1);
-                    Math<C>::mma(part[m][n], q[2 * m][2], q[2 * m + 1][2], q[2 * m][3], q[2 * m + 1][3], x2, x3);
+                    if (b % PER == 0) mma_from_zero<C>(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], y[0], y[1]);
+                    else Math<C>::mma(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], y[0], y[1]);
+                    Math<C>::mma(part[m][n], q[2 * m][2], q[2 * m + 1][2], q[2 * m][3], q[2 * m + 1][3], y[2], y[3]);
                 }
             }
             if (b % PER == PER - 1) {                         // the group's last columns
@@ -456,33 +476,49 @@ template <class T, bool GATE, int MOST, u32 PER> __global__ void __launch_bounds
 {
     using C = std::conditional_t<GATE, __half, T>;
     extern __shared__ __align__(16) unsigned char smem[];
+    after_previous();
+    let_next_start();
     for (u32 i = blockIdx.y; i < *a.n_items; i += gridDim.y) {
         const Item it = a.items[i];
         if (MOST == 1 || it.count <= 8) product<T, C, 1, GATE, PER>(a, it, blockIdx.x, smem);
         else if (MOST == 2 || it.count <= 16) product<T, C, 2, GATE, PER>(a, it, blockIdx.x, smem);
-        else product<T, C, MOST < 4 ? 1 : 4, GATE, PER>(a, it, blockIdx.x, smem);
+        else product<T, C, MOST < 3 ? 1 : 3, GATE, PER>(a, it, blockIdx.x, smem);
         __syncthreads();
     }
 }
 
-// y = sum over the slots, in their order, of weight x (W2 h).
-constexpr u32 kCombineThreads = 256;
+// y = sum over the slots, in their order, of weight x (W2 h).  Four columns a
+// thread; a token's ids and weights are read once and its rows eight at a time.
+constexpr u32 kCombineThreads = 128;
 
 template <class T> __global__ void __launch_bounds__(kCombineThreads) k_combine(const ExpertArgs a)
 {
+    after_previous();
     const u64 quads = a.hidden / 4, n = a.tokens * quads;
     for (u64 i = (u64)blockIdx.x * kCombineThreads + threadIdx.x; i < n; i += (u64)gridDim.x * kCombineThreads) {
         const u64 t = i / quads, c = (i % quads) * 4;
         float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (u64 p = t * a.topk; p < (t + 1) * a.topk; p++) {
-            if ((u32)a.ids[p] >= a.experts) continue;
-            const float w = a.weights[p];
-            const float4 o = *reinterpret_cast<const float4 *>(a.o + p * a.hidden + c);
-            y[0] += w * o.x; y[1] += w * o.y; y[2] += w * o.z; y[3] += w * o.w;
+        for (u32 j0 = 0; j0 < a.topk; j0 += 8) {
+            float4 o[8];
+            float w[8];
+#pragma unroll
+            for (u32 j = 0; j < 8; j++) {
+                const u64 p = t * a.topk + j0 + j;
+                const bool here = j0 + j < a.topk && (u32)a.ids[p] < a.experts;
+                w[j] = here ? a.weights[p] : 0.0f;
+                o[j] = here ? *reinterpret_cast<const float4 *>(a.o + p * a.hidden + c) : make_float4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (u32 j = 0; j < 8; j++) {
+                y[0] += w[j] * o[j].x; y[1] += w[j] * o[j].y; y[2] += w[j] * o[j].z; y[3] += w[j] * o[j].w;
+            }
         }
-        T *out = static_cast<T *>(a.y) + t * a.hidden + c;
+        T out[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) out[j] = from_float<T>(y[j]);
+        uint2 v;
+        memcpy(&v, out, 8);
+        *reinterpret_cast<uint2 *>(static_cast<T *>(a.y) + t * a.hidden + c) = v;
     }
 }
 
@@ -526,13 +562,13 @@ int check(const mv_experts_desc *d)
 
 template <class T, bool GATE, int MOST, u32 PER> int run_product(const ExpertArgs &a, u64 items, cudaStream_t stream)
 {
-    constexpr u32 smem = kSmem<PER>;
+    constexpr u32 smem = kSmem<MOST, PER>;
     const u32 tiles = GATE ? (a.inner + kRows / 2 - 1) / (kRows / 2) : (a.hidden + kRows - 1) / kRows;
     const auto kernel = k_product<T, GATE, MOST, PER>;
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return MV_ECUDA;
-    return launch(kernel, dim3(tiles, (u32)std::fmin((double)items, 65535.0)), kThreads, smem, stream, a);
+    return launch_after(kernel, dim3(tiles, (u32)std::fmin((double)items, 65535.0)), kThreads, smem, stream, a);
 }
 
 template <class T, bool GATE, int MOST> int run_product(const ExpertArgs &a, u64 items, cudaStream_t stream)
@@ -551,8 +587,8 @@ template <class T, int MOST> int run_experts(const ExpertArgs &a, u64 items, cud
     if (rc == MV_OK) rc = run_product<T, true, MOST>(a, items, stream);
     if (rc == MV_OK) rc = run_product<T, false, MOST>(a, items, stream);
     const u64 quads = a.tokens * (a.hidden / 4);
-    const u32 blocks = (u32)std::fmin((double)((quads + kCombineThreads - 1) / kCombineThreads), 8.0 * sms);
-    if (rc == MV_OK) rc = launch(k_combine<T>, dim3(blocks), kCombineThreads, 0, stream, a);
+    const u32 blocks = (u32)std::fmin((double)((quads + kCombineThreads - 1) / kCombineThreads), 16.0 * sms);
+    if (rc == MV_OK) rc = launch_after(k_combine<T>, dim3(blocks), kCombineThreads, 0, stream, a);
     return rc;
 }
 
@@ -560,7 +596,7 @@ template <class T> int run_experts(const ExpertArgs &a, u64 items, cudaStream_t 
 {
     if (a.item_pairs == 8) return run_experts<T, 1>(a, items, stream);
     if (a.item_pairs == 16) return run_experts<T, 2>(a, items, stream);
-    return run_experts<T, 4>(a, items, stream);
+    return run_experts<T, 3>(a, items, stream);
 }
 
 }  // namespace mvmoe

@@ -48,16 +48,33 @@ template <int W> __device__ __forceinline__ float group_max(float v)
 inline bool aligned(const void *p, u64 bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 inline u64 dtype_size(u32 dtype) { return dtype == MV_F32 ? 4 : 2; }
 
-// One launch; its own status, whatever an earlier call left behind.
+// One launch; its own status, whatever an earlier call left behind.  With
+// `early` the kernel may start before the stream's previous one has ended: it
+// waits for that one itself (griddepcontrol.wait).
 template <class... P, class... A>
-int launch(void (*kernel)(P...), dim3 grid, u32 threads, u32 smem, cudaStream_t stream, A... args)
+int launch_as(bool early, void (*kernel)(P...), dim3 grid, u32 threads, u32 smem, cudaStream_t stream, A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? MV_OK : MV_ECUDA;
+}
+template <class... P, class... A>
+int launch(void (*kernel)(P...), dim3 grid, u32 threads, u32 smem, cudaStream_t stream, A... args)
+{
+    return launch_as(false, kernel, grid, threads, smem, stream, args...);
+}
+template <class... P, class... A>
+int launch_after(void (*kernel)(P...), dim3 grid, u32 threads, u32 smem, cudaStream_t stream, A... args)
+{
+    return launch_as(true, kernel, grid, threads, smem, stream, args...);
 }
 
 // SMs of the current device (0 if there is none).
