@@ -12,8 +12,8 @@ namespace mvmoe {
 // of one expert's pairs make an item: what one pass over its weights serves.
 u32 item_pairs(u64 tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : 24; }
 
-struct Item {
-    u32 expert, first, count;       // pairs[first .. first + count)
+struct alignas(16) Item {
+    u32 expert, first, count, none; // pairs[first .. first + count); a count of 0: none, nor any after it
 };
 
 // Bit patterns of a widening, as kernel arguments: an instruction holds one
@@ -41,7 +41,7 @@ struct ExpertArgs {
     float *o;                       // W2 h                      [pairs, hidden]
     u32 *pairs;                     // pairs by expert
     Item *items;
-    u32 *n_items;
+    u32 most_items;
 };
 
 // ---- packed weights against 16-bit activations ---------------------------
@@ -218,12 +218,12 @@ template <class T> __global__ void __launch_bounds__(kPrepThreads) k_prepare(con
             pairs += __shfl_sync(kFull, sc, 31);
             items += __shfl_sync(kFull, sk, 31);
         }
-        if (tid == 0) *a.n_items = items;
+        for (u32 i = items + tid; i < a.most_items; i += 32) a.items[i] = {0, 0, 0, 0};
     }
     __syncthreads();
     for (u32 e = tid; e < a.experts; e += kPrepThreads)
         for (u32 i = 0; i * most < count[e]; i++)
-            a.items[item[e] + i] = {e, first[e] + i * most, min(most, count[e] - i * most)};
+            a.items[item[e] + i] = {e, first[e] + i * most, min(most, count[e] - i * most), 0};
     __syncthreads();
     for (u32 p = tid; p < n; p += kPrepThreads) {
         const u32 e = (u32)a.ids[p];
@@ -249,11 +249,14 @@ template <u32 PER> constexpr u32 kScaleBytes = 2 * kRows * kSPitchOf<PER>;
 // Stages of up to 8 NT pairs, and the shared memory of a block whose items
 // hold that many: two blocks fit on an SM.
 template <int NT> constexpr u32 kStageBytes = kRows * kWPitch + NT * 8 * kXPitch;
-template <int NT> constexpr int kStagesOf = NT == 1 ? 4 : 3;
+template <int NT, u32 PER> constexpr int kStagesOf = NT == 1 ? 4 : NT == 3 && PER == 1 ? 2 : 3;
 template <int MOST, u32 PER>
-constexpr u32 kSmem = kScaleBytes<PER> + (MOST < 3 ? kStagesOf<1> * kStageBytes<1> : kStagesOf<3> * kStageBytes<3>);
-static_assert(kStagesOf<2> * kStageBytes<2> <= kStagesOf<1> * kStageBytes<1> &&
-              kStagesOf<1> * kStageBytes<1> <= kStagesOf<3> * kStageBytes<3>, "fewer tiles fit the room of more");
+constexpr u32 kRing = MOST < 3 || PER == 1 ? kStagesOf<1, PER> * kStageBytes<1> : kStagesOf<3, PER> * kStageBytes<3>;
+template <int MOST, u32 PER> constexpr u32 kSmem = kScaleBytes<PER> + kRing<MOST, PER>;
+template <u32 PER> constexpr bool kFits =
+    kStagesOf<2, PER> * kStageBytes<2> <= kRing<2, PER> && kStagesOf<1, PER> * kStageBytes<1> <= kRing<3, PER> &&
+    kStagesOf<3, PER> * kStageBytes<3> <= kRing<3, PER> && 2 * (kSmem<3, PER> + 1024) <= 227 * 1024;
+static_assert(kFits<1> && kFits<2> && kFits<4>, "every number of tiles fits its kernel's room, and two blocks an SM");
 
 // One tile of weight rows against up to 8 NT pairs' activations.  A warp
 // holds 32 rows as two matrix operands of 16; an operand of 16 x 16 weights
@@ -267,7 +270,7 @@ static_assert(kStagesOf<2> * kStageBytes<2> <= kStagesOf<1> * kStageBytes<1> &&
 template <class T, class C, int NT, bool GATE, u32 PER>
 __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 tile, unsigned char *smem)
 {
-    constexpr int kStages = kStagesOf<NT>;
+    constexpr int kStages = kStagesOf<NT, PER>;
     constexpr u32 kGroup = PER * 32, kEpoch = kEpochOf<PER>, kSPitch = kSPitchOf<PER>, kEpochSteps = kEpoch * kGroup / kStep;
     const u32 tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const u32 half = tid >> 7, warp = (tid >> 5) & 3;         // columns, rows
@@ -293,6 +296,19 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         wp[j] = (GATE ? a.w13 : a.w2) + (base_row + (u64)(row < 0 ? 0 : row)) * (K / 2) + (tid & 7) * 16;
     }
     const u32 w_to = ring + (tid >> 3) * kWPitch + (tid & 7) * 16;
+    auto fetch_weights = [&](u32 s, u32 slot) {               // pointers advance: called for s = 0, 1, ...
+        if ((s + 1) * kStep <= K || s * kStep + (tid & 7) * 32 < K)
+#pragma unroll
+            for (int j = 0; j < 4; j++) copy16(w_to + slot * kStageBytes<NT> + j * 32 * kWPitch, wp[j]);
+#pragma unroll
+        for (int j = 0; j < 4; j++) wp[j] += kStep / 2;
+    };
+    const u32 steps = (K + kStep - 1) / kStep;
+    // the weights' copies start before anything is known of the pairs
+#pragma unroll
+    for (int s = 0; s < kStages - 1; s++)
+        if ((u32)s < steps) fetch_weights(s, s);
+
     const C *xp[NT];
 #pragma unroll
     for (int j = 0; j < NT; j++) {                            // a warp copies whole rows
@@ -303,21 +319,14 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         xp[j] = (GATE ? reinterpret_cast<const C *>(a.xp) + p / a.topk * K : static_cast<const C *>(a.h) + p * K) + lane * 8;
     }
     const u32 x_to = ring + kRows * kWPitch + (tid >> 5) * kXPitch + lane * 16;
-    auto fetch = [&](u32 s, u32 slot) {                       // pointers advance: called for s = 0, 1, ...
-        const u32 off = slot * kStageBytes<NT>;
-        const bool whole = (s + 1) * kStep <= K;
-        if (whole || s * kStep + (tid & 7) * 32 < K)
-#pragma unroll
-            for (int j = 0; j < 4; j++) copy16(w_to + off + j * 32 * kWPitch, wp[j]);
-        if (whole || s * kStep + lane * 8 < K)
-#pragma unroll
-            for (int j = 0; j < NT; j++)
-                if (xp[j]) copy16(x_to + off + j * 8 * kXPitch, xp[j]);
-#pragma unroll
-        for (int j = 0; j < 4; j++) wp[j] += kStep / 2;
+    auto fetch_rows = [&](u32 s, u32 slot) {
+        const bool in = (s + 1) * kStep <= K || s * kStep + lane * 8 < K;
 #pragma unroll
         for (int j = 0; j < NT; j++)
-            if (xp[j]) xp[j] += kStep;
+            if (xp[j]) {
+                if (in) copy16(x_to + slot * kStageBytes<NT> + j * 8 * kXPitch, xp[j]);
+                xp[j] += kStep;
+            }
     };
     const T *all = static_cast<const T *>(GATE ? a.s13 : a.s2);
     const char *s_end = reinterpret_cast<const char *>(all + (u64)a.experts * (GATE ? 2 * a.inner : a.hidden) * groups);
@@ -350,11 +359,10 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
 #pragma unroll
             for (int i = 0; i < 4; i++) total[m][n][i] = 0.0f;
 
-    const u32 steps = (K + kStep - 1) / kStep;
     fetch_scales(0);
 #pragma unroll
     for (int s = 0; s < kStages - 1; s++) {
-        if ((u32)s < steps) fetch(s, s);
+        if ((u32)s < steps) fetch_rows(s, s);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     const u32 a_at = ring + (warp * 32 + (lane & 7) + ((lane >> 3) & 1) * 8 + (lane >> 4) * 16) * kWPitch + half * 64;
@@ -416,7 +424,10 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     for (u32 s = 0; s < steps; s++) {
         copies_left<kStages - 2>();
         __syncthreads();
-        if (s + kStages - 1 < steps) fetch(s + kStages - 1, ahead);
+        if (s + kStages - 1 < steps) {
+            fetch_weights(s + kStages - 1, ahead);
+            fetch_rows(s + kStages - 1, ahead);
+        }
         if (s % kEpochSteps == 0) fetch_scales(s / kEpochSteps + 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
         const u32 off = slot * kStageBytes<NT>;
@@ -478,8 +489,10 @@ template <class T, bool GATE, int MOST, u32 PER> __global__ void __launch_bounds
     extern __shared__ __align__(16) unsigned char smem[];
     after_previous();
     let_next_start();
-    for (u32 i = blockIdx.y; i < *a.n_items; i += gridDim.y) {
-        const Item it = a.items[i];
+    for (u32 i = blockIdx.y; i < a.most_items; i += gridDim.y) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(a.items + i);
+        const Item it = {v.x, v.y, v.z, 0};
+        if (!it.count) return;
         if (MOST == 1 || it.count <= 8) product<T, C, 1, GATE, PER>(a, it, blockIdx.x, smem);
         else if (MOST == 2 || it.count <= 16) product<T, C, 2, GATE, PER>(a, it, blockIdx.x, smem);
         else product<T, C, MOST < 3 ? 1 : 3, GATE, PER>(a, it, blockIdx.x, smem);
@@ -524,7 +537,7 @@ template <class T> __global__ void __launch_bounds__(kCombineThreads) k_combine(
 
 // Workspace: offsets of its parts, each on a 256-byte boundary.
 struct Layout {
-    u64 xp, x_unit, h, o, pairs, items, n_items, total;
+    u64 xp, x_unit, h, o, pairs, items, total;
 };
 u64 most_items(const mv_experts_desc *d)
 {
@@ -543,7 +556,6 @@ Layout layout(const mv_experts_desc *d)
     l.o = take(pairs * d->hidden * 4);
     l.pairs = take(pairs * 4);
     l.items = take(most_items(d) * sizeof(Item));
-    l.n_items = take(4);
     l.total = at;
     return l;
 }
@@ -644,7 +656,7 @@ extern "C" int mv_experts(const mv_experts_desc *d, void *workspace, uint64_t ws
     a.o = reinterpret_cast<float *>(ws + l.o);
     a.pairs = reinterpret_cast<u32 *>(ws + l.pairs);
     a.items = reinterpret_cast<Item *>(ws + l.items);
-    a.n_items = reinterpret_cast<u32 *>(ws + l.n_items);
+    a.most_items = (u32)most_items(d);
     a.tokens = d->tokens;
     a.stride = d->row_stride;
     a.topk = d->topk;
