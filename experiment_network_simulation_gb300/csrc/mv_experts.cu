@@ -234,29 +234,32 @@ template <class T> __global__ void __launch_bounds__(kPrepThreads) k_prepare(con
 // ---- products ------------------------------------------------------------
 constexpr u32 kWarps = 8, kThreads = kWarps * 32;
 constexpr u32 kRows = kWarps / 2 * 32;          // weight rows a block: 32 to each of four pairs of warps
-constexpr u32 kStep = 256;                      // columns a stage: half of them to each warp of a pair
-constexpr u32 kWPitch = kStep / 2 + 16;         // bytes; 16-byte pieces of eight rows fall in eight bank groups
-constexpr u32 kXPitch = kStep * 2 + 64;
+constexpr u32 kStep = 256;                      // columns a step: half of them to each warp of a pair
+constexpr u32 kWPitch = kStep / 4;              // bytes of a row of a warp's weights; piece p of row r lies at
+constexpr u32 kWarpStage = 32 * kWPitch;        // p ^ (r / 2 & 3), so that eight rows' pieces are eight bank groups
 
-// Scales come by epochs of 16 groups (32 of the finest), two in shared
-// memory.  A row's scales start anywhere, so the aligned 16-byte pieces around
-// them are copied.  An epoch is four steps or more, and its copy has one step
-// less than there are stages to arrive in.
-template <u32 PER> constexpr u32 kEpochOf = PER == 1 ? 32 : 16;
-template <u32 PER> constexpr u32 kSPitchOf = kEpochOf<PER> * 2 + 16;
-template <u32 PER> constexpr u32 kScaleBytes = 2 * kRows * kSPitchOf<PER>;
+// Scales come by epochs of 16 groups, two in shared memory.  A row's scales
+// start anywhere, so the aligned 16-byte pieces around them are copied: three
+// hold 16 groups at any offset.
+constexpr u32 kEpoch = 16;
+constexpr u32 kSPitch = kEpoch * 2 + 16;
+constexpr u32 kScaleBytes = 2 * kRows * kSPitch;
 
-// Stages of up to 8 NT pairs, and the shared memory of a block whose items
-// hold that many: two blocks fit on an SM.
-template <int NT> constexpr u32 kStageBytes = kRows * kWPitch + NT * 8 * kXPitch;
-template <int NT, u32 PER> constexpr int kStagesOf = NT == 1 ? 4 : NT == 3 && PER == 1 ? 2 : 3;
-template <int MOST, u32 PER>
-constexpr u32 kRing = MOST < 3 || PER == 1 ? kStagesOf<1, PER> * kStageBytes<1> : kStagesOf<3, PER> * kStageBytes<3>;
-template <int MOST, u32 PER> constexpr u32 kSmem = kScaleBytes<PER> + kRing<MOST, PER>;
-template <u32 PER> constexpr bool kFits =
-    kStagesOf<2, PER> * kStageBytes<2> <= kRing<2, PER> && kStagesOf<1, PER> * kStageBytes<1> <= kRing<3, PER> &&
-    kStagesOf<3, PER> * kStageBytes<3> <= kRing<3, PER> && 2 * (kSmem<3, PER> + 1024) <= 227 * 1024;
-static_assert(kFits<1> && kFits<2> && kFits<4>, "every number of tiles fits its kernel's room, and two blocks an SM");
+// Weights are copied by the warp that uses them, kStagesOf steps in flight or
+// in use, and no other warp waits for them.  Activations are the block's, in
+// chunks of kChunkOf steps, two in shared memory; the block's warps meet once
+// a chunk.  Epochs begin with a chunk.  What is copied is there kStagesOf - 1
+// steps later: a chunk or an epoch at most.
+template <int NT, u32 PER> constexpr int kStagesOf = NT == 1 && PER > 1 ? 4 : 3;
+template <int NT, u32 PER> constexpr u32 kChunkOf = NT == 1 && PER > 1 ? 4 : 2;
+template <int NT, u32 PER> constexpr u32 kXPitch = kChunkOf<NT, PER> * kStep * 2;      // odd rows' 64-byte halves are swapped
+template <int NT, u32 PER> constexpr u32 kRing = kStagesOf<NT, PER> * kWarps * kWarpStage;
+template <int NT, u32 PER> constexpr u32 kRoom = kScaleBytes + kRing<NT, PER> + 2 * NT * 8 * kXPitch<NT, PER>;
+template <u32 A, u32 B> constexpr u32 kLarger = A > B ? A : B;
+// Shared memory of a block whose items hold up to 8 MOST pairs.
+template <int MOST, u32 PER> constexpr u32 kSmem =
+    MOST == 1 ? kRoom<1, PER> : kLarger<kRoom<1, PER>, MOST == 2 ? kRoom<2, PER> : kLarger<kRoom<2, PER>, kRoom<3, PER>>>;
+static_assert(2 * (kSmem<3, 1> + 1024) <= 227 * 1024 && 2 * (kSmem<3, 4> + 1024) <= 227 * 1024, "two blocks an SM");
 
 // One tile of weight rows against up to 8 NT pairs' activations.  A warp
 // holds 32 rows as two matrix operands of 16; an operand of 16 x 16 weights
@@ -271,12 +274,13 @@ template <class T, class C, int NT, bool GATE, u32 PER>
 __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 tile, unsigned char *smem)
 {
     constexpr int kStages = kStagesOf<NT, PER>;
-    constexpr u32 kGroup = PER * 32, kEpoch = kEpochOf<PER>, kSPitch = kSPitchOf<PER>, kEpochSteps = kEpoch * kGroup / kStep;
+    constexpr u32 kGroup = PER * 32, kEpochSteps = kEpoch * kGroup / kStep, kChunk = kChunkOf<NT, PER>, kPitch = kXPitch<NT, PER>;
+    static_assert(kEpochSteps % kChunk == 0 && kStages - 1 <= (int)kChunk, "copies arrive in time");
     const u32 tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const u32 half = tid >> 7, warp = (tid >> 5) & 3;         // columns, rows
     const u32 K = GATE ? a.hidden : a.inner, groups = K / kGroup;
     const Patterns patterns = GATE ? a.half : a.own;
-    const u32 scales = (u32)__cvta_generic_to_shared(smem), ring = scales + kScaleBytes<PER>;
+    const u32 scales = (u32)__cvta_generic_to_shared(smem), ring = scales + kScaleBytes, rows = ring + kRing<NT, PER>;
     // block row r: warp r / 32's operand (r / 16) & 1, row r & 15
     auto weight_row = [&](u32 r) -> int64_t {
         if (GATE) {
@@ -287,19 +291,19 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         return i < a.hidden ? (int64_t)i : -1;
     };
     const u64 base_row = (u64)it.expert * (GATE ? 2 * a.inner : a.hidden);
-    // This thread's pieces of a stage: weights, activations, scales.  Rows
+    // This thread's pieces of a step: weights, activations, scales.  Rows
     // beyond the matrix are copied from its first one and not used.
     const uint8_t *wp[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        const int64_t row = weight_row((tid >> 3) + j * 32);
-        wp[j] = (GATE ? a.w13 : a.w2) + (base_row + (u64)(row < 0 ? 0 : row)) * (K / 2) + (tid & 7) * 16;
+        const int64_t row = weight_row(warp * 32 + j * 8 + (lane >> 2));
+        wp[j] = (GATE ? a.w13 : a.w2) + (base_row + (u64)(row < 0 ? 0 : row)) * (K / 2) + half * (kStep / 4) + (lane & 3) * 16;
     }
-    const u32 w_to = ring + (tid >> 3) * kWPitch + (tid & 7) * 16;
+    const u32 my_ring = ring + (tid >> 5) * kWarpStage, w_to = my_ring + (lane >> 2) * kWPitch + ((lane & 3) ^ (lane >> 3)) * 16;
     auto fetch_weights = [&](u32 s, u32 slot) {               // pointers advance: called for s = 0, 1, ...
-        if ((s + 1) * kStep <= K || s * kStep + (tid & 7) * 32 < K)
+        if ((s + 1) * kStep <= K || s * kStep + half * (kStep / 2) + (lane & 3) * 32 < K)
 #pragma unroll
-            for (int j = 0; j < 4; j++) copy16(w_to + slot * kStageBytes<NT> + j * 32 * kWPitch, wp[j]);
+            for (int j = 0; j < 4; j++) copy16(w_to + slot * (kWarps * kWarpStage) + j * 8 * kWPitch, wp[j]);
 #pragma unroll
         for (int j = 0; j < 4; j++) wp[j] += kStep / 2;
     };
@@ -318,15 +322,16 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         const u64 p = a.pairs[it.first + r];
         xp[j] = (GATE ? reinterpret_cast<const C *>(a.xp) + p / a.topk * K : static_cast<const C *>(a.h) + p * K) + lane * 8;
     }
-    const u32 x_to = ring + kRows * kWPitch + (tid >> 5) * kXPitch + lane * 16;
-    auto fetch_rows = [&](u32 s, u32 slot) {
-        const bool in = (s + 1) * kStep <= K || s * kStep + lane * 8 < K;
+    const u32 x_to = rows + (tid >> 5) * kPitch + ((lane * 16) ^ ((tid & 32) * 2));
+    auto fetch_rows = [&](u32 chunk) {
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-            if (xp[j]) {
-                if (in) copy16(x_to + slot * kStageBytes<NT> + j * 8 * kXPitch, xp[j]);
-                xp[j] += kStep;
-            }
+        for (u32 i = 0; i < kChunk; i++) {
+            const u32 c = (chunk * kChunk + i) * kStep;
+            if (c + lane * 8 >= K) break;
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+                if (xp[j]) copy16(x_to + ((chunk & 1) * NT + j) * 8 * kPitch + i * kStep * 2, xp[j] + c);
+        }
     };
     const T *all = static_cast<const T *>(GATE ? a.s13 : a.s2);
     const char *s_end = reinterpret_cast<const char *>(all + (u64)a.experts * (GATE ? 2 * a.inner : a.hidden) * groups);
@@ -362,23 +367,23 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     fetch_scales(0);
 #pragma unroll
     for (int s = 0; s < kStages - 1; s++) {
-        if ((u32)s < steps) fetch_rows(s, s);
+        if (s == 0) fetch_rows(0);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    const u32 a_at = ring + (warp * 32 + (lane & 7) + ((lane >> 3) & 1) * 8 + (lane >> 4) * 16) * kWPitch + half * 64;
-    const u32 x_at = ring + kRows * kWPitch + g * kXPitch + t * 16 + half * 256;
+    const u32 a_row = my_ring + ((lane & 7) + ((lane >> 3) & 1) * 8 + (lane >> 4) * 16) * kWPitch, a_turn = (lane >> 1) & 3;
+    const u32 x_row = rows + g * kPitch + half * kStep, x_turn = (t * 16) ^ ((g & 1) * 64);
     // this half's blocks of 32 columns of a step, those below `blocks`
-    auto multiply = [&](u32 s, u32 off, u32 blocks) {
+    auto multiply = [&](u32 s, u32 off, u32 x_off, u32 blocks) {
         // every operand of the step is under way before the first is used
         u32 w[kStep / 64][4], x[kStep / 64][4];
 #pragma unroll
         for (u32 b = 0; b < kStep / 64; b++) {
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[b][0]), "=r"(w[b][1]), "=r"(w[b][2]), "=r"(w[b][3]) : "r"(a_at + off + b * 16));
+                         : "=r"(w[b][0]), "=r"(w[b][1]), "=r"(w[b][2]), "=r"(w[b][3]) : "r"(a_row + off + (b ^ a_turn) * 16));
             if (NT == 1)
                 asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                              : "=r"(x[b][0]), "=r"(x[b][1]), "=r"(x[b][2]), "=r"(x[b][3])
-                             : "r"(x_at + off + b * 64));
+                             : "r"(x_row + x_off + ((b * 64) ^ x_turn)));
         }
 #pragma unroll
         for (u32 b = 0; b < kStep / 64; b++) {
@@ -394,7 +399,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
                     for (int i = 0; i < 4; i++) y[i] = x[b][i];
                 } else {
                     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                                 : "r"(x_at + off + n * 8 * kXPitch + b * 64));
+                                 : "r"(x_row + x_off + n * 8 * kPitch + ((b * 64) ^ x_turn)));
                 }
 #pragma unroll
                 for (int m = 0; m < 2; m++) {
@@ -423,19 +428,19 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     u32 slot = 0, ahead = kStages - 1;
     for (u32 s = 0; s < steps; s++) {
         copies_left<kStages - 2>();
-        __syncthreads();
-        if (s + kStages - 1 < steps) {
-            fetch_weights(s + kStages - 1, ahead);
-            fetch_rows(s + kStages - 1, ahead);
-        }
+        if (s % kChunk == 0) __syncthreads();
+        else __syncwarp();
+        if (s + kStages - 1 < steps) fetch_weights(s + kStages - 1, ahead);
+        if (s % kChunk == 0) fetch_rows(s / kChunk + 1);
         if (s % kEpochSteps == 0) fetch_scales(s / kEpochSteps + 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
-        const u32 off = slot * kStageBytes<NT>;
+        const u32 off = slot * (kWarps * kWarpStage);
+        const u32 x_off = (s / kChunk & 1) * NT * 8 * kPitch + s % kChunk * kStep * 2;
         if ((s + 1) * kStep <= K) {
-            multiply(s, off, kStep / 64);
+            multiply(s, off, x_off, kStep / 64);
         } else {
             const u32 left = (K - s * kStep) / 32, mine = half * (kStep / 64);
-            multiply(s, off, left > mine ? left - mine : 0);
+            multiply(s, off, x_off, left > mine ? left - mine : 0);
         }
         slot = slot + 1 == kStages ? 0 : slot + 1;
         ahead = ahead + 1 == kStages ? 0 : ahead + 1;
@@ -443,7 +448,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     copies_left<0>();
     // the second half's sums to the first, through the ring
     __syncthreads();
-    float4 *sums = reinterpret_cast<float4 *>(smem + kScaleBytes<PER>) + (warp * 32 + lane);
+    float4 *sums = reinterpret_cast<float4 *>(smem + kScaleBytes) + (warp * 32 + lane);
     if (half) {
 #pragma unroll
         for (int m = 0; m < 2; m++)
