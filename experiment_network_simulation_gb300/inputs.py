@@ -795,11 +795,14 @@ def moe_traffic(seed: int, n_ranks: int = 512, tokens: int = 128, experts: int =
     return byte
 
 
-def moe_workload(byte: np.ndarray, gpus: int, alpha: int, beta=(1, 36_864)) -> Workload:
+def moe_workload(byte: np.ndarray, gpus: int, alpha: int, beta=(1, 36_864),
+                 compute_ns=None) -> Workload:
     """Dispatch then combine.  Same GPU: no traffic; same server: one analytic
     intra-server exchange per server (the largest per-GPU share); else network
     all-to-all.  A rank's combine (reverse sizes) starts once its dispatch
-    parts are done (the combine-receive barrier of the MoE kernels)."""
+    parts are done (the combine-receive barrier of the MoE kernels), and with
+    ``compute_ns`` (one duration a rank: its experts' work on what it
+    received) a compute node of that length lies between the two."""
     R = byte.shape[0]
     w = Workload(R, "moe")
     srv = np.arange(R) // gpus
@@ -819,8 +822,14 @@ def moe_workload(byte: np.ndarray, gpus: int, alpha: int, beta=(1, 36_864)) -> W
                 ids_in[r] = u
         stages.append((ids_net, ids_in))
     for r in range(R):
-        for a in (stages[0][0][r], stages[0][1][r]):
-            for b in (stages[1][0][r], stages[1][1][r]):
+        first, then = [s[r] for s in stages[0]], [s[r] for s in stages[1]]
+        if compute_ns is not None:
+            work = w.compute(r, int(compute_ns[r]))
+            for a in first:
+                w.edge(a, work)
+            first = [work]
+        for a in first:
+            for b in then:
                 w.edge(a, b)
     return w
 

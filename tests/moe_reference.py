@@ -49,7 +49,7 @@ def route(logits, topk, scores="softmax", bias=None, groups=1, top_groups=1, gro
             left = [e for e in left if e // size in order[:top_groups]]
         order = sorted(left, key=lambda e: (-v[e], e))
         for a, c in zip(order[:topk], order[1:]):
-            d = v[a] - v[c]
+            d = 0.0 if v[a] == v[c] else v[a] - v[c]
             gaps[t] = min(gaps[t], d if d > 0 else np.inf)
         order = order[:topk]
         ids[t, :len(order)] = order

@@ -201,3 +201,30 @@ def test_gpt_1f1b_schedule_and_branches():
         (u,) = c.nodes                                # DP 1: one member
         preds = [a for a, b in w.edges if b == u]
         assert len(preds) == 1 and nk[preds[0]] == I.INTRA   # after the last backward's TP step
+
+
+def test_moe_workload_with_expert_compute():
+    """With durations, a rank's combine parts wait on its compute node alone,
+    which waits on both of its dispatch parts and lasts what was given; without
+    them the workload is what it was."""
+    R, gpus = 16, 8
+    byte = np.random.default_rng(6).integers(0, 4, (R, R)) * 14_336
+    ns = [1000 * (r + 1) for r in range(R)]
+    w = I.moe_workload(byte, gpus, alpha=3, compute_ns=ns)
+    plain = I.moe_workload(byte, gpus, alpha=3)
+    assert [c.a2a for c in w.colls] == [c.a2a for c in plain.colls]
+    assert len(w.edges) == 4 * R and len(plain.edges) == 4 * R
+    preds, succs = collections.defaultdict(set), collections.defaultdict(set)
+    for u, v in w.edges:
+        preds[v].add(u)
+        succs[u].add(v)
+    per = R // gpus
+    for r in range(R):
+        part = [[c.nodes[list(c.ranks).index(r)] for c in w.colls if r in c.ranks][i] for i in range(4)]
+        work = succs[part[0]]
+        assert len(work) == 1 and succs[part[1]] == work and preds[next(iter(work))] == set(part[:2])
+        assert succs[next(iter(work))] == set(part[2:])
+    a, b = w.arrays(), plain.arrays()
+    lo = a["node_dur_lo"][a["node_kind"] == I.COMPUTE]
+    assert lo.tolist() == ns and per == 2
+    assert not (b["node_kind"] == I.COMPUTE).any()
