@@ -79,11 +79,6 @@ def _library() -> C.CDLL:
     return _lib
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
 def _tensor(name: str, t, dtype, shape, device=None, rows_apart: bool = False):
     """Check one argument: type, device, shape (None: any size), dense layout."""
     if (t.__class__ is torch.Tensor and t.is_cuda and t.dtype in dtype and t.is_contiguous()
@@ -122,7 +117,8 @@ class _On:
     def __init__(self, device, stream, inputs):
         self.stack = [torch.cuda.device(device)]
         if stream is not None:
-            _need(stream.device == device, f"the stream is on {stream.device}, not on {device}")
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, not on {device}")
             self.stack.append(torch.cuda.stream(stream))
             if stream != torch.cuda.current_stream(device):
                 for t in inputs:
@@ -176,13 +172,17 @@ def route(logits, topk: int, *, scores: str = "softmax", bias=None, groups: int 
     """
     _tensor("logits", logits, _DTYPES, (None, None), rows_apart=True)
     tokens, n = logits.shape
-    _need(1 <= n <= MAX_EXPERTS, f"{n} experts: 1 to {MAX_EXPERTS} are taken")
-    _need(1 <= groups <= MAX_GROUPS and n % groups == 0,
-          f"{groups} groups: at most {MAX_GROUPS}, and {n} experts divide into them evenly")
-    _need(1 <= top_groups <= groups, f"top_groups is 1 to {groups}, not {top_groups}")
+    if not 1 <= n <= MAX_EXPERTS:
+        raise ValueError(f"{n} experts: 1 to {MAX_EXPERTS} are taken")
+    if not 1 <= groups <= MAX_GROUPS or n % groups:
+        raise ValueError(f"{groups} groups: at most {MAX_GROUPS}, and {n} experts divide into them evenly")
+    if not 1 <= top_groups <= groups:
+        raise ValueError(f"top_groups is 1 to {groups}, not {top_groups}")
     most = min(MAX_TOPK, top_groups * (n // groups))
-    _need(1 <= topk <= most, f"topk is 1 to {most}, not {topk}")
-    _need(math.isfinite(scale), f"scale is {scale}")
+    if not 1 <= topk <= most:
+        raise ValueError(f"topk is 1 to {most}, not {topk}")
+    if not math.isfinite(scale):
+        raise ValueError(f"scale is {scale}")
     s, r = _choice("scores", scores, _SCORES), _choice("group_rule", group_rule, _RULES)
     if bias is not None:
         _tensor("bias", bias, (torch.float32,), (n,), logits.device)
@@ -206,12 +206,15 @@ def route_backward(logits, ids, dweights, *, scores: str = "softmax", renorm: bo
     """
     _tensor("logits", logits, _DTYPES, (None, None), rows_apart=True)
     tokens, n = logits.shape
-    _need(1 <= n <= MAX_EXPERTS, f"{n} experts: 1 to {MAX_EXPERTS} are taken")
+    if not 1 <= n <= MAX_EXPERTS:
+        raise ValueError(f"{n} experts: 1 to {MAX_EXPERTS} are taken")
     _tensor("ids", ids, (torch.int32,), (tokens, None), logits.device)
     topk = ids.shape[1]
-    _need(1 <= topk <= min(MAX_TOPK, n), f"topk is 1 to {min(MAX_TOPK, n)}, not {topk}")
+    if not 1 <= topk <= min(MAX_TOPK, n):
+        raise ValueError(f"topk is 1 to {min(MAX_TOPK, n)}, not {topk}")
     _tensor("dweights", dweights, (torch.float32,), (tokens, topk), logits.device)
-    _need(math.isfinite(scale), f"scale is {scale}")
+    if not math.isfinite(scale):
+        raise ValueError(f"scale is {scale}")
     s = _choice("scores", scores, _SCORES)
     dev = logits.device
     with _on(dev, stream, (logits, ids, dweights)):
@@ -245,18 +248,21 @@ def exchange(ids, place, ranks: int, *, sources: int | None = None, starts=None,
         lead = (batches,)
     _tensor("place", place, (torch.int32,), (None,), ids.device)
     n = place.shape[0]
-    _need(1 <= n <= MAX_EXPERTS, f"{n} experts: 1 to {MAX_EXPERTS} are taken")
-    _need(1 <= topk <= MAX_TOPK, f"topk is 1 to {MAX_TOPK}, not {topk}")
-    _need(1 <= ranks <= MAX_RANKS, f"ranks is 1 to {MAX_RANKS}, not {ranks}")
+    if not 1 <= n <= MAX_EXPERTS:
+        raise ValueError(f"{n} experts: 1 to {MAX_EXPERTS} are taken")
+    if not 1 <= topk <= MAX_TOPK:
+        raise ValueError(f"topk is 1 to {MAX_TOPK}, not {topk}")
+    if not 1 <= ranks <= MAX_RANKS:
+        raise ValueError(f"ranks is 1 to {MAX_RANKS}, not {ranks}")
     if starts is not None:
         _tensor("starts", starts, (torch.int64,), (None,), ids.device)
-        _need(starts.shape[0] >= 2 and sources in (None, starts.shape[0] - 1),
-              f"starts holds {starts.shape[0]} offsets, not one more than the sources")
+        if not (starts.shape[0] >= 2 and sources in (None, starts.shape[0] - 1)):
+            raise ValueError(f"starts holds {starts.shape[0]} offsets, not one more than the sources")
         sources = starts.shape[0] - 1
     else:
         sources = ranks if sources is None else sources
-        _need(sources >= 1 and tokens % sources == 0,
-              f"{tokens} tokens do not divide evenly over {sources} sources; give starts")
+        if not (sources >= 1 and tokens % sources == 0):
+            raise ValueError(f"{tokens} tokens do not divide evenly over {sources} sources; give starts")
     dev = ids.device
     with _on(dev, stream, (ids, place, starts)):
         load = torch.empty((*lead, n), dtype=torch.int32, device=dev)
@@ -287,19 +293,21 @@ def experts(x, ids, weights, w13, s13, w2, s2, *, stream=None):
     _tensor("w13", w13, (torch.uint8,), (None, None, None), dev)
     n, inner2 = w13.shape[0], w13.shape[1]
     inner = inner2 // 2
-    _need(1 <= n <= MAX_EXPERTS, f"{n} experts: 1 to {MAX_EXPERTS} are taken")
-    _need(hidden >= 32 and inner2 >= 64 and inner2 % 2 == 0 and 2 * w13.shape[2] == hidden,
-          f"w13 has shape {tuple(w13.shape)}, not [experts, 2 * inner, {hidden} / 2]")
+    if not 1 <= n <= MAX_EXPERTS:
+        raise ValueError(f"{n} experts: 1 to {MAX_EXPERTS} are taken")
+    if not (hidden >= 32 and inner2 >= 64 and inner2 % 2 == 0 and 2 * w13.shape[2] == hidden):
+        raise ValueError(f"w13 has shape {tuple(w13.shape)}, not [experts, 2 * inner, {hidden} / 2]")
     _tensor("s13", s13, (x.dtype,), (n, inner2, None), dev)
     group = hidden // s13.shape[2] if s13.shape[2] else 0
-    _need(group in (32, 64, 128) and hidden == group * s13.shape[2] and inner % group == 0,
-          f"s13 has shape {tuple(s13.shape)}: a scale stands for 32, 64 or 128 of {hidden} columns, "
-          f"and {inner} inner rows divide by that too")
+    if not (group in (32, 64, 128) and hidden == group * s13.shape[2] and inner % group == 0):
+        raise ValueError(f"s13 has shape {tuple(s13.shape)}: a scale stands for 32, 64 or 128 of {hidden} columns, "
+                         f"and {inner} inner rows divide by that too")
     _tensor("w2", w2, (torch.uint8,), (n, hidden, inner // 2), dev)
     _tensor("s2", s2, (x.dtype,), (n, hidden, inner // group), dev)
     _tensor("ids", ids, (torch.int32,), (tokens, None), dev)
     topk = ids.shape[1]
-    _need(1 <= topk <= MAX_TOPK, f"topk is 1 to {MAX_TOPK}, not {topk}")
+    if not 1 <= topk <= MAX_TOPK:
+        raise ValueError(f"topk is 1 to {MAX_TOPK}, not {topk}")
     _tensor("weights", weights, (torch.float32,), (tokens, topk), dev)
     with _on(dev, stream, (x, ids, weights, w13, s13, w2, s2)):
         y = torch.empty((tokens, hidden), dtype=x.dtype, device=dev)
