@@ -44,7 +44,8 @@ def route(logits, topk, scores="softmax", bias=None, groups=1, top_groups=1, gro
                     value[g] = sum(best[:2]) if two else best[0]
             order = sorted(value, key=lambda g: (-value[g], g))
             if len(order) > top_groups:
-                d = value[order[top_groups - 1]] - value[order[top_groups]]
+                a, c = value[order[top_groups - 1]], value[order[top_groups]]
+                d = 0.0 if a == c else a - c
                 gaps[t] = min(gaps[t], d if d > 0 else np.inf)
             left = [e for e in left if e // size in order[:top_groups]]
         order = sorted(left, key=lambda e: (-v[e], e))

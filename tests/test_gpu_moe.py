@@ -185,6 +185,50 @@ def test_route_many_rows_equal_each_alone():
             x[7_777:7_778], ids[7_777:7_778], d[7_777:7_778], scores=scores, renorm=kw["renorm"]))
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("E,k,G,tg", [(256, 8, 8, 4), (256, 8, 1, 1), (60, 4, 1, 1), (160, 6, 8, 3), (96, 1, 3, 1),
+                                      (250, 7, 5, 5), (33, 8, 11, 5), (8, 2, 1, 1), (64, 8, 32, 9), (224, 5, 7, 2)])
+def test_long_batches_choose_as_short_ones(E, k, G, tg, dtype):
+    """Long and short batches are worked by different kernels: ids and weights
+    are the same bits, in ordinary rows, rows of ties, closed, infinite and
+    not-a-number logits, near and far biases."""
+    T = 9_001
+    x = randn((T, E), E + k, dtype, 1.5)
+    g = torch.Generator(device="cuda").manual_seed(E)
+    kind = torch.randint(0, 24, (T,), generator=g, device="cuda")
+    hole = torch.rand((T, E), generator=g, device="cuda") < 0.6
+    x[kind == 1] = 0.5                                         # ties
+    x[kind == 2] = (x[kind == 2] * 2).round() / 2              # many ties, -0 among them
+    x[(kind == 3)[:, None] & hole] = -np.inf
+    x[kind == 4] = -np.inf
+    x[(kind == 5)[:, None] & hole] = float("nan")
+    x[(kind == 6)[:, None] & hole] = np.inf
+    x[(kind == 7)[:, None] & hole] = torch.finfo(dtype).min
+    x[kind == 8] = torch.finfo(dtype).max
+    x[kind == 9] *= 30
+    x[kind == 10] -= 200
+    u = torch.rand((E,), generator=g, device="cuda")
+    shut = u.clone()
+    shut[::3], shut[1] = -np.inf, float("nan")
+    for scores, rule, renorm, bias in [
+            ("softmax", "max", True, None), ("softmax", "max", False, None), ("sigmoid", "max", False, None),
+            ("sigmoid", "top2", True, 0.1 * u), ("sigmoid", "max", True, 50 * u), ("sigmoid", "top2", False, 1000 + u),
+            ("sigmoid", "top2", True, None), ("sigmoid", "max", True, shut), ("softmax", "top2", False, 0.01 * u),
+            ("softmax", "max", True, shut), ("sigmoid", "max", True, -3e5 * u)]:
+        kw = dict(scores=scores, group_rule=rule, renorm=renorm, bias=bias, groups=G, top_groups=tg)
+        ids, w = moe.route(x, k, **kw)
+        parts = [moe.route(x[a:a + 1500], k, **kw) for a in range(0, T, 1500)]
+        assert torch.equal(ids, torch.cat([p[0] for p in parts]))
+        assert torch.equal(w, torch.cat([p[1] for p in parts]))
+        assert torch.isfinite(w).all()
+        some = torch.arange(0, T, 97, device="cuda")
+        want, _, gaps = R.route(host(x[some]), k, scores, None if bias is None else host(bias), G, tg, rule, renorm)
+        sure = gaps > 2.0 ** -18 * max(1.0, 0.0 if bias is None else float(bias[bias.isfinite()].abs().max()) / 8)
+        got = ids[some].cpu().numpy()
+        ordinary = kind[some].cpu().numpy() > 10
+        assert np.array_equal(got[sure & ordinary], want[sure & ordinary])
+
+
 def test_close_calls_are_decided_by_32_bit_scores():
     """Orders closer than any shortcut could tell: float32 logits one unit
     apart, and biased scores rebuilt with torch's own exp and division."""
