@@ -39,7 +39,7 @@ struct ExpertArgs {
     float *x_unit;                  // powers of two             [tokens]
     void *h;                        // silu(W1 x) (W3 x), permuted [pairs, inner]
     float *o;                       // W2 h                      [pairs, hidden]
-    u32 *pairs;                     // pairs by expert
+    uint2 *pairs;                   // pairs by expert, each with its token
     Item *items;
     u32 most_items;
 };
@@ -227,7 +227,7 @@ template <class T> __global__ void __launch_bounds__(kPrepThreads) k_prepare(con
     __syncthreads();
     for (u32 p = tid; p < n; p += kPrepThreads) {
         const u32 e = (u32)a.ids[p];
-        if (e < a.experts) a.pairs[atomicAdd(&first[e], 1u)] = p;
+        if (e < a.experts) a.pairs[atomicAdd(&first[e], 1u)] = make_uint2(p, p / a.topk);
     }
 }
 
@@ -254,7 +254,8 @@ template <int NT, u32 PER> constexpr int kStagesOf = NT == 1 && PER > 1 ? 4 : 3;
 template <int NT, u32 PER> constexpr u32 kChunkOf = NT == 1 && PER > 1 ? 4 : 2;
 template <int NT, u32 PER> constexpr u32 kXPitch = kChunkOf<NT, PER> * kStep * 2;      // odd rows' 64-byte halves are swapped
 template <int NT, u32 PER> constexpr u32 kRing = kStagesOf<NT, PER> * kWarps * kWarpStage;
-template <int NT, u32 PER> constexpr u32 kRoom = kScaleBytes + kRing<NT, PER> + 2 * NT * 8 * kXPitch<NT, PER>;
+constexpr u32 kTable = 3 * 8 * 8;               // an item's pairs: where they go, and what x was divided by
+template <int NT, u32 PER> constexpr u32 kRoom = kTable + kScaleBytes + kRing<NT, PER> + 2 * NT * 8 * kXPitch<NT, PER>;
 template <u32 A, u32 B> constexpr u32 kLarger = A > B ? A : B;
 // Shared memory of a block whose items hold up to 8 MOST pairs.
 template <int MOST, u32 PER> constexpr u32 kSmem =
@@ -280,7 +281,8 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     const u32 half = tid >> 7, warp = (tid >> 5) & 3;         // columns, rows
     const u32 K = GATE ? a.hidden : a.inner, groups = K / kGroup;
     const Patterns patterns = GATE ? a.half : a.own;
-    const u32 scales = (u32)__cvta_generic_to_shared(smem), ring = scales + kScaleBytes, rows = ring + kRing<NT, PER>;
+    uint2 *table = reinterpret_cast<uint2 *>(smem);
+    const u32 scales = (u32)__cvta_generic_to_shared(smem) + kTable, ring = scales + kScaleBytes, rows = ring + kRing<NT, PER>;
     // block row r: warp r / 32's operand (r / 16) & 1, row r & 15
     auto weight_row = [&](u32 r) -> int64_t {
         if (GATE) {
@@ -300,8 +302,8 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         wp[j] = (GATE ? a.w13 : a.w2) + (base_row + (u64)(row < 0 ? 0 : row)) * (K / 2) + half * (kStep / 4) + (lane & 3) * 16;
     }
     const u32 my_ring = ring + (tid >> 5) * kWarpStage, w_to = my_ring + (lane >> 2) * kWPitch + ((lane & 3) ^ (lane >> 3)) * 16;
-    auto fetch_weights = [&](u32 s, u32 slot) {               // pointers advance: called for s = 0, 1, ...
-        if ((s + 1) * kStep <= K || s * kStep + half * (kStep / 2) + (lane & 3) * 32 < K)
+    auto fetch_weights = [&](u32 s, u32 slot, bool whole) {   // pointers advance: called for s = 0, 1, ...
+        if (whole || s * kStep + half * (kStep / 2) + (lane & 3) * 32 < K)
 #pragma unroll
             for (int j = 0; j < 4; j++) copy16(w_to + slot * (kWarps * kWarpStage) + j * 8 * kWPitch, wp[j]);
 #pragma unroll
@@ -311,7 +313,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     // the weights' copies start before anything is known of the pairs
 #pragma unroll
     for (int s = 0; s < kStages - 1; s++)
-        if ((u32)s < steps) fetch_weights(s, s);
+        if ((u32)s < steps) fetch_weights(s, s, false);
 
     const C *xp[NT];
 #pragma unroll
@@ -319,15 +321,16 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         const u32 r = (tid >> 5) + j * 8;
         xp[j] = nullptr;
         if (r >= it.count) continue;
-        const u64 p = a.pairs[it.first + r];
-        xp[j] = (GATE ? reinterpret_cast<const C *>(a.xp) + p / a.topk * K : static_cast<const C *>(a.h) + p * K) + lane * 8;
+        const uint2 p = a.pairs[it.first + r];
+        xp[j] = (GATE ? reinterpret_cast<const C *>(a.xp) + (u64)p.y * K : static_cast<const C *>(a.h) + (u64)p.x * K) + lane * 8;
+        if (lane == 0) table[r] = make_uint2(p.x, GATE ? __float_as_uint(a.x_unit[p.y]) : 0u);
     }
     const u32 x_to = rows + (tid >> 5) * kPitch + ((lane * 16) ^ ((tid & 32) * 2));
-    auto fetch_rows = [&](u32 chunk) {
+    auto fetch_rows = [&](u32 chunk, bool whole) {
 #pragma unroll
         for (u32 i = 0; i < kChunk; i++) {
             const u32 c = (chunk * kChunk + i) * kStep;
-            if (c + lane * 8 >= K) break;
+            if (!whole && c + lane * 8 >= K) break;
 #pragma unroll
             for (int j = 0; j < NT; j++)
                 if (xp[j]) copy16(x_to + ((chunk & 1) * NT + j) * 8 * kPitch + i * kStep * 2, xp[j] + c);
@@ -367,7 +370,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     fetch_scales(0);
 #pragma unroll
     for (int s = 0; s < kStages - 1; s++) {
-        if (s == 0) fetch_rows(0);
+        if (s == 0) fetch_rows(0, false);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     const u32 a_row = my_ring + ((lane & 7) + ((lane >> 3) & 1) * 8 + (lane >> 4) * 16) * kWPitch, a_turn = (lane >> 1) & 3;
@@ -426,17 +429,17 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         }
     };
     u32 slot = 0, ahead = kStages - 1;
-    for (u32 s = 0; s < steps; s++) {
+    // step s, number i of its chunk; whole: nothing that it multiplies or copies ends at K
+    auto step = [&](u32 s, u32 i, bool whole) {
         copies_left<kStages - 2>();
-        if (s % kChunk == 0) __syncthreads();
+        if (i == 0) __syncthreads();
         else __syncwarp();
-        if (s + kStages - 1 < steps) fetch_weights(s + kStages - 1, ahead);
-        if (s % kChunk == 0) fetch_rows(s / kChunk + 1);
-        if (s % kEpochSteps == 0) fetch_scales(s / kEpochSteps + 1);
+        if (whole || s + kStages - 1 < steps) fetch_weights(s + kStages - 1, ahead, whole);
+        if (i == 0) fetch_rows(s / kChunk + 1, whole);
+        if (i == 0 && s % kEpochSteps == 0) fetch_scales(s / kEpochSteps + 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
-        const u32 off = slot * (kWarps * kWarpStage);
-        const u32 x_off = (s / kChunk & 1) * NT * 8 * kPitch + s % kChunk * kStep * 2;
-        if ((s + 1) * kStep <= K) {
+        const u32 off = slot * (kWarps * kWarpStage), x_off = (s / kChunk & 1) * NT * 8 * kPitch + i * kStep * 2;
+        if (whole || (s + 1) * kStep <= K) {
             multiply(s, off, x_off, kStep / 64);
         } else {
             const u32 left = (K - s * kStep) / 32, mine = half * (kStep / 64);
@@ -444,48 +447,54 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         }
         slot = slot + 1 == kStages ? 0 : slot + 1;
         ahead = ahead + 1 == kStages ? 0 : ahead + 1;
-    }
+    };
+    u32 s = 0;
+    for (const u32 whole = K / kStep; s + kLarger<2 * kChunk, kChunk + kStages - 1> <= whole; s += kChunk)
+#pragma unroll
+        for (u32 i = 0; i < kChunk; i++) step(s + i, i, true);
+    for (; s < steps; s++) step(s, s % kChunk, false);
     copies_left<0>();
-    // the second half's sums to the first, through the ring
+    // The halves' sums meet through the ring: the first half finishes the
+    // operands' rows 0 to 7, the second rows 8 to 15.
     __syncthreads();
-    float4 *sums = reinterpret_cast<float4 *>(smem + kScaleBytes) + (warp * 32 + lane);
-    if (half) {
-#pragma unroll
-        for (int m = 0; m < 2; m++)
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-                sums[(m * NT + n) * 128] = make_float4(total[m][n][0], total[m][n][1], total[m][n][2], total[m][n][3]);
-    }
-    __syncthreads();
-    if (half) return;
+    float2 *sums = reinterpret_cast<float2 *>(smem + kTable + kScaleBytes) + (warp * 32 + lane);
 #pragma unroll
     for (int m = 0; m < 2; m++)
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-            const float4 v = sums[(m * NT + n) * 128];
-            total[m][n][0] += v.x; total[m][n][1] += v.y; total[m][n][2] += v.z; total[m][n][3] += v.w;
+        for (int n = 0; n < NT; n++)
+            sums[((m * NT + n) * 2 + half) * 128] =
+                half ? make_float2(total[m][n][0], total[m][n][1]) : make_float2(total[m][n][2], total[m][n][3]);
+    __syncthreads();
+    // value j of operand m, tile n: row g of the half's eight, pair 8 n + 2 t + j
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+        float v[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; m++) {
+            const float2 other = sums[((m * NT + n) * 2 + 1 - half) * 128];
+            v[m][0] = (half ? total[m][n][2] : total[m][n][0]) + other.x;
+            v[m][1] = (half ? total[m][n][3] : total[m][n][1]) + other.y;
         }
-    // element i of operand m, tile n: row g + 8 (i / 2), pair 8 n + 2 t + (i & 1)
 #pragma unroll
-    for (int n = 0; n < NT; n++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const u32 c = n * 8 + 2 * t + (i & 1), r = g + (i >> 1) * 8;
+        for (int j = 0; j < 2; j++) {
+            const u32 c = n * 8 + 2 * t + j, r = g + half * 8;
             if (c >= it.count) continue;
-            const u64 p = a.pairs[it.first + c];
+            const uint2 to = table[c];
             if (GATE) {
                 const u32 row = tile * (kRows / 2) + warp * 16 + r;
-                const float unit = a.x_unit[p / a.topk], z = total[0][n][i] * unit, up = total[1][n][i] * unit;
+                const float unit = __uint_as_float(to.y), z = v[0][j] * unit, up = v[1][j] * unit;
                 if (row < a.inner)
-                    static_cast<T *>(a.h)[p * a.inner + column_place(row)] = from_float<T>(z / (1.0f + expf(-z)) * up);
+                    static_cast<T *>(a.h)[(u64)to.x * a.inner + column_place(row)] =
+                        from_float<T>(z * reciprocal_fast(1.0f + exp2_fast(-z * kLog2e)) * up);
             } else {
 #pragma unroll
                 for (int m = 0; m < 2; m++) {
                     const u32 row = tile * kRows + warp * 32 + m * 16 + r;
-                    if (row < a.hidden) a.o[p * a.hidden + row] = total[m][n][i];
+                    if (row < a.hidden) a.o[(u64)to.x * a.hidden + row] = v[m][j];
                 }
             }
         }
+    }
 }
 
 template <class T, bool GATE, int MOST, u32 PER> __global__ void __launch_bounds__(kThreads, 2) k_product(const ExpertArgs a)
@@ -559,7 +568,7 @@ Layout layout(const mv_experts_desc *d)
     l.x_unit = take(d->tokens * 4);
     l.h = take(pairs * d->inner * 2);
     l.o = take(pairs * d->hidden * 4);
-    l.pairs = take(pairs * 4);
+    l.pairs = take(pairs * sizeof(uint2));
     l.items = take(most_items(d) * sizeof(Item));
     l.total = at;
     return l;
@@ -659,7 +668,7 @@ extern "C" int mv_experts(const mv_experts_desc *d, void *workspace, uint64_t ws
     a.x_unit = reinterpret_cast<float *>(ws + l.x_unit);
     a.h = ws + l.h;
     a.o = reinterpret_cast<float *>(ws + l.o);
-    a.pairs = reinterpret_cast<u32 *>(ws + l.pairs);
+    a.pairs = reinterpret_cast<uint2 *>(ws + l.pairs);
     a.items = reinterpret_cast<Item *>(ws + l.items);
     a.most_items = (u32)most_items(d);
     a.tokens = d->tokens;

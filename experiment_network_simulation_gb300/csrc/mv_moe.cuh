@@ -45,6 +45,21 @@ template <int W> __device__ __forceinline__ float group_max(float v)
     return v;
 }
 
+// 2^v and 1 / v to 2^-22 of their values or so.
+__device__ __forceinline__ float exp2_fast(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float reciprocal_fast(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
 inline bool aligned(const void *p, u64 bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 inline u64 dtype_size(u32 dtype) { return dtype == MV_F32 ? 4 : 2; }
 

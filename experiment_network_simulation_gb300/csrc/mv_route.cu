@@ -148,20 +148,6 @@ struct Shares {
     bool wide;                      // lanes load their experts by 16 bytes
 };
 
-__device__ __forceinline__ float exp2_fast(float v)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ float reciprocal_fast(float v)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
 __device__ __forceinline__ void order_two(u32 &a, u32 &b)
 {
     const u32 hi = max(a, b), lo = min(a, b);
