@@ -439,7 +439,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         if (i == 0 && s % kEpochSteps == 0) fetch_scales(s / kEpochSteps + 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
         const u32 off = slot * (kWarps * kWarpStage), x_off = (s / kChunk & 1) * NT * 8 * kPitch + i * kStep * 2;
-        if (whole || (s + 1) * kStep <= K) {
+        if (whole || (NT == 1 && (s + 1) * kStep <= K)) {
             multiply(s, off, x_off, kStep / 64);
         } else {
             const u32 left = (K - s * kStep) / 32, mine = half * (kStep / 64);
@@ -449,9 +449,11 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         ahead = ahead + 1 == kStages ? 0 : ahead + 1;
     };
     u32 s = 0;
-    for (const u32 whole = K / kStep; s + kLarger<2 * kChunk, kChunk + kStages - 1> <= whole; s += kChunk)
+    if (NT == 1) {                                            // more tiles leave no registers for a second copy
+        for (const u32 whole = K / kStep; s + kLarger<2 * kChunk, kChunk + kStages - 1> <= whole; s += kChunk)
 #pragma unroll
-        for (u32 i = 0; i < kChunk; i++) step(s + i, i, true);
+            for (u32 i = 0; i < kChunk; i++) step(s + i, i, true);
+    }
     for (; s < steps; s++) step(s, s % kChunk, false);
     copies_left<0>();
     // The halves' sums meet through the ring: the first half finishes the
