@@ -16,7 +16,6 @@ device.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import math
 import struct
@@ -79,6 +78,13 @@ def _library() -> C.CDLL:
     return _lib
 
 
+def _call(name: str, desc: bytes, index: int):
+    """One enqueued call on the current stream of device ``index``."""
+    rc = getattr(_lib or _library(), name)(desc, _raw_stream(index))
+    if rc != mv.MV_OK:
+        raise mv.MVError(rc, name)
+
+
 def _tensor(name: str, t, dtype, shape, device=None, rows_apart: bool = False):
     """Check one argument: type, device, shape (None: any size), dense layout."""
     if (t.__class__ is torch.Tensor and t.is_cuda and t.dtype in dtype and t.is_contiguous()
@@ -134,19 +140,9 @@ class _On:
             c.__exit__(*exc)
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on(device, stream, inputs):
-    """Makes the call's device and stream the current ones."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return _HERE
-    return _On(device, stream, inputs)
-
-
-def _done(rc: int, what: str):
-    if rc != mv.MV_OK:
-        raise mv.MVError(rc, what)
+def _elsewhere(device, stream) -> bool:
+    """Whether a call is not for the current device and stream."""
+    return stream is not None or device.index != torch.cuda.current_device()
 
 
 def _choice(what: str, value, table: dict) -> int:
@@ -187,13 +183,19 @@ def route(logits, topk: int, *, scores: str = "softmax", bias=None, groups: int 
     if bias is not None:
         _tensor("bias", bias, (torch.float32,), (n,), logits.device)
     dev = logits.device
-    with _on(dev, stream, (logits, bias)):
-        ids = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
-        weights = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
-        d = _route_desc(tokens, _stride(logits), n, topk, groups, top_groups,
-                        _DTYPES[logits.dtype], s, r, bool(renorm), scale, logits.data_ptr(),
-                        0 if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr())
-        _done(_library().mv_route(d, _raw_stream(dev.index)), "mv_route")
+    if _elsewhere(dev, stream):
+        with _On(dev, stream, (logits, bias)):
+            return _route(logits, tokens, n, topk, s, bias, groups, top_groups, r, renorm, scale, dev)
+    return _route(logits, tokens, n, topk, s, bias, groups, top_groups, r, renorm, scale, dev)
+
+
+def _route(logits, tokens, n, topk, s, bias, groups, top_groups, r, renorm, scale, dev):
+    ids = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    weights = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
+    _call("mv_route", _route_desc(
+        tokens, _stride(logits), n, topk, groups, top_groups, _DTYPES[logits.dtype], s, r,
+        bool(renorm), scale, logits.data_ptr(), 0 if bias is None else bias.data_ptr(),
+        ids.data_ptr(), weights.data_ptr()), dev.index)
     return ids, weights
 
 
@@ -217,12 +219,17 @@ def route_backward(logits, ids, dweights, *, scores: str = "softmax", renorm: bo
         raise ValueError(f"scale is {scale}")
     s = _choice("scores", scores, _SCORES)
     dev = logits.device
-    with _on(dev, stream, (logits, ids, dweights)):
-        out = torch.empty((tokens, n), dtype=logits.dtype, device=dev)
-        d = _route_grad_desc(tokens, _stride(logits), n, topk, _DTYPES[logits.dtype], s,
-                             bool(renorm), scale, logits.data_ptr(), ids.data_ptr(),
-                             dweights.data_ptr(), out.data_ptr())
-        _done(_library().mv_route_backward(d, _raw_stream(dev.index)), "mv_route_backward")
+    if _elsewhere(dev, stream):
+        with _On(dev, stream, (logits, ids, dweights)):
+            return _route_backward(logits, tokens, n, topk, ids, dweights, s, renorm, scale, dev)
+    return _route_backward(logits, tokens, n, topk, ids, dweights, s, renorm, scale, dev)
+
+
+def _route_backward(logits, tokens, n, topk, ids, dweights, s, renorm, scale, dev):
+    out = torch.empty((tokens, n), dtype=logits.dtype, device=dev)
+    _call("mv_route_backward", _route_grad_desc(
+        tokens, _stride(logits), n, topk, _DTYPES[logits.dtype], s, bool(renorm), scale,
+        logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(), out.data_ptr()), dev.index)
     return out
 
 
@@ -264,13 +271,18 @@ def exchange(ids, place, ranks: int, *, sources: int | None = None, starts=None,
         if not (sources >= 1 and tokens % sources == 0):
             raise ValueError(f"{tokens} tokens do not divide evenly over {sources} sources; give starts")
     dev = ids.device
-    with _on(dev, stream, (ids, place, starts)):
-        load = torch.empty((*lead, n), dtype=torch.int32, device=dev)
-        sent = torch.empty((*lead, sources, ranks), dtype=torch.int32, device=dev)
-        d = _exchange_desc(batches, tokens, topk, n, sources, ranks, bool(once), ids.data_ptr(),
-                           place.data_ptr(), 0 if starts is None else starts.data_ptr(),
-                           load.data_ptr(), sent.data_ptr())
-        _done(_library().mv_exchange(d, _raw_stream(dev.index)), "mv_exchange")
+    if _elsewhere(dev, stream):
+        with _On(dev, stream, (ids, place, starts)):
+            return _exchange(ids, lead, batches, tokens, topk, place, n, starts, sources, ranks, once, dev)
+    return _exchange(ids, lead, batches, tokens, topk, place, n, starts, sources, ranks, once, dev)
+
+
+def _exchange(ids, lead, batches, tokens, topk, place, n, starts, sources, ranks, once, dev):
+    load = torch.empty((*lead, n), dtype=torch.int32, device=dev)
+    sent = torch.empty((*lead, sources, ranks), dtype=torch.int32, device=dev)
+    _call("mv_exchange", _exchange_desc(
+        batches, tokens, topk, n, sources, ranks, bool(once), ids.data_ptr(), place.data_ptr(),
+        0 if starts is None else starts.data_ptr(), load.data_ptr(), sent.data_ptr()), dev.index)
     return load, sent
 
 
@@ -309,14 +321,22 @@ def experts(x, ids, weights, w13, s13, w2, s2, *, stream=None):
     if not 1 <= topk <= MAX_TOPK:
         raise ValueError(f"topk is 1 to {MAX_TOPK}, not {topk}")
     _tensor("weights", weights, (torch.float32,), (tokens, topk), dev)
-    with _on(dev, stream, (x, ids, weights, w13, s13, w2, s2)):
-        y = torch.empty((tokens, hidden), dtype=x.dtype, device=dev)
-        d = _experts_desc(tokens, _stride(x), topk, n, hidden, inner, group, _DTYPES[x.dtype],
-                          x.data_ptr(), ids.data_ptr(), weights.data_ptr(), w13.data_ptr(),
-                          s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr())
-        need = _u64()
-        _done(_library().mv_experts_workspace_bytes(d, C.byref(need)), "mv_experts")
+    if _elsewhere(dev, stream):
+        with _On(dev, stream, (x, ids, weights, w13, s13, w2, s2)):
+            return _experts(x, tokens, topk, n, hidden, inner, group, ids, weights, w13, s13, w2, s2, dev)
+    return _experts(x, tokens, topk, n, hidden, inner, group, ids, weights, w13, s13, w2, s2, dev)
+
+
+def _experts(x, tokens, topk, n, hidden, inner, group, ids, weights, w13, s13, w2, s2, dev):
+    lib, need = _lib or _library(), _u64()
+    y = torch.empty((tokens, hidden), dtype=x.dtype, device=dev)
+    d = _experts_desc(tokens, _stride(x), topk, n, hidden, inner, group, _DTYPES[x.dtype],
+                      x.data_ptr(), ids.data_ptr(), weights.data_ptr(), w13.data_ptr(),
+                      s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr())
+    rc = lib.mv_experts_workspace_bytes(d, C.byref(need))
+    if rc == mv.MV_OK:
         ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        _done(_library().mv_experts(d, ws.data_ptr(), need.value, _raw_stream(dev.index)),
-              "mv_experts")
+        rc = lib.mv_experts(d, ws.data_ptr(), need.value, _raw_stream(dev.index))
+    if rc != mv.MV_OK:
+        raise mv.MVError(rc, "mv_experts")
     return y
