@@ -1,5 +1,24 @@
 // The routed experts' SwiGLU products with 4-bit weights (mv_experts in
-// include/mv.h).
+// include/mv.h), for the few tokens of a decode step.
+//
+// Bytes decide: an expert of 7168 x 2048 is 22 MB of weights and 0.7 MB of
+// scales, read for one token or for twenty.  So pairs of token and expert are
+// grouped by expert, and each visited expert's weights are streamed once, in a
+// chain of four kernels (group; W1 and W3 with silu; W2; combine), each
+// starting as the one before it ends.  With at most 24 columns of activations
+// the matrix instruction that takes its operands from registers fits: weights
+// are widened in registers and never written back, and the tensor pipe is a
+// quarter busy.  Widening is the work: about 65 instructions for 32 x 32
+// weights, of the 89 issue slots that memory speed would leave.
+//
+// 64 tokens on 32 of 256 such experts (633 MB): 139 us, 4.6 TB/s, W1/W3 at 5.1;
+// one token (182 MB): 53 us, of which W1/W3 29 (256 blocks for 152 SMs), W2 19,
+// grouping and combining 7; 200 tokens over 60 experts of 2048 x 1408 (277 MB,
+// three tiles of activations): 150 us, bound by issue and latency at 16 warps
+// an SM.  Steps on the way, us for those three: a dot product a row and pair
+// 1801, 280, 6486; matrix instructions 212, 99, 177; scales copied ahead of
+// their use 198, 84, 162; activations as half and constants as arguments 166,
+// 66, 182; kernels started early 153, 58, 154.
 #include <cmath>
 #include <cstring>
 #include <type_traits>
@@ -232,6 +251,8 @@ template <class T> __global__ void __launch_bounds__(kPrepThreads) k_prepare(con
 }
 
 // ---- products ------------------------------------------------------------
+// h is rounded to the type of x, as a layer of separate kernels would store it:
+// it is the next product's operand.  All sums are held in 32 bits.
 constexpr u32 kWarps = 8, kThreads = kWarps * 32;
 constexpr u32 kRows = kWarps / 2 * 32;          // weight rows a block: 32 to each of four pairs of warps
 constexpr u32 kStep = 256;                      // columns a step: half of them to each warp of a pair
