@@ -398,20 +398,23 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     const u32 x_row = rows + g * kPitch + half * kStep, x_turn = (t * 16) ^ ((g & 1) * 64);
     // this half's blocks of 32 columns of a step, those below `blocks`
     auto multiply = [&](u32 s, u32 off, u32 x_off, u32 blocks) {
-        // every operand of the step is under way before the first is used
+        // one tile: every operand of the step is under way before the first is used
         u32 w[kStep / 64][4], x[kStep / 64][4];
-#pragma unroll
-        for (u32 b = 0; b < kStep / 64; b++) {
+        auto load_weights = [&](u32 b) {
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[b][0]), "=r"(w[b][1]), "=r"(w[b][2]), "=r"(w[b][3]) : "r"(a_row + off + (b ^ a_turn) * 16));
-            if (NT == 1)
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(x[b][0]), "=r"(x[b][1]), "=r"(x[b][2]), "=r"(x[b][3])
-                             : "r"(x_row + x_off + ((b * 64) ^ x_turn)));
+        };
+#pragma unroll
+        for (u32 b = 0; b < kStep / 64; b++) {
+            if (NT > 1) break;
+            load_weights(b);
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[b][0]), "=r"(x[b][1]), "=r"(x[b][2]), "=r"(x[b][3])
+                         : "r"(x_row + x_off + ((b * 64) ^ x_turn)));
         }
 #pragma unroll
         for (u32 b = 0; b < kStep / 64; b++) {
             if (b >= blocks) break;
+            if (NT > 1) load_weights(b);
             u32 q[4][4];
 #pragma unroll
             for (int i = 0; i < 4; i++) widen<C>(patterns, w[b][i], q[i]);
