@@ -187,7 +187,8 @@ def test_route_many_rows_equal_each_alone():
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("E,k,G,tg", [(256, 8, 8, 4), (256, 8, 1, 1), (60, 4, 1, 1), (160, 6, 8, 3), (96, 1, 3, 1),
-                                      (250, 7, 5, 5), (33, 8, 11, 5), (8, 2, 1, 1), (64, 8, 32, 9), (224, 5, 7, 2)])
+                                      (250, 7, 5, 5), (33, 8, 11, 5), (8, 2, 1, 1), (64, 8, 32, 9), (224, 5, 7, 2), (512, 8, 1, 1), (32, 3, 1, 1), (288, 5, 1, 1),
+                                      (1024, 8, 1, 1)])
 def test_long_batches_choose_as_short_ones(E, k, G, tg, dtype):
     """Long and short batches are worked by different kernels: ids and weights
     are the same bits, in ordinary rows, rows of ties, closed, infinite and
