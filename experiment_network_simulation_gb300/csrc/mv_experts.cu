@@ -11,10 +11,10 @@
 // quarter busy.  Widening is the work: about 65 instructions for 32 x 32
 // weights, of the 89 issue slots that memory speed would leave.
 //
-// 64 tokens on 32 of 256 such experts (633 MB): 139 us, 4.6 TB/s, W1/W3 at 5.1;
+// 64 tokens on 32 of 256 such experts (633 MB): 136 us, 4.7 TB/s, W1/W3 at 5.1;
 // one token (182 MB): 53 us, of which W1/W3 29 (256 blocks for 152 SMs), W2 19,
 // grouping and combining 7; 200 tokens over 60 experts of 2048 x 1408 (277 MB,
-// three tiles of activations): 150 us, bound by issue and latency at 16 warps
+// three tiles of activations): 143 us, bound by issue and latency at 16 warps
 // an SM.  Steps on the way, us for those three: a dot product a row and pair
 // 1801, 280, 6486; matrix instructions 212, 99, 177; scales copied ahead of
 // their use 198, 84, 162; activations as half and constants as arguments 166,

@@ -340,13 +340,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a, c
 // them into its best eight.  With groups a first pass finds the groups'
 // values, and the second goes through those that stay; it computes their keys
 // again, which costs less than the shared memory to keep them (2^16 rows of 256
-// in eight groups: 41.7 us against 44.5).
+// in eight groups: 42 us against 45).
 //
 // Bound by instructions, not by memory: 2^20 rows of 256 bfloat16 take 205 us
 // (2.9 TB/s) with the half-rate min / max / logic pipe 83% busy, 160
-// instructions a row; 2^16 rows of 256 float32, sigmoid, biased, in groups 43
-// us (1.7 TB/s), 400 instructions a row.  A warp a row with its keys in 32
-// lanes took 466 and 65 us, comparing exact values alone 876 and 129 us.
+// instructions a row; 2^16 rows of 256 float32, sigmoid, biased, in groups 38
+// us (1.9 TB/s), some 380 instructions a row.  A warp a row with its keys in 32
+// lanes took 466 and 65 us, comparing exact values alone 876 and 129 us.  Seven
+// blocks an SM leave 72 registers a thread: eight (64) take 205 and 43 us, six
+// 215 and 41.
 //
 // Score keys are fixed point: score * f + bias' lies in (4, 6), where floats
 // are 2^-21 apart, and their last 22 bits move to the top of the key; 4
@@ -439,7 +441,7 @@ __host__ __device__ constexpr u32 few_value_words(u32 groups) { return (groups +
 
 // WHOLE: groups are whole batches and loads are wide.
 template <class T, int ORDER, bool WHOLE>
-__global__ void __launch_bounds__(kFewWarps * 32, 8) k_route_few(const RouteArgs a, const bool wide)
+__global__ void __launch_bounds__(kFewWarps * 32, 7) k_route_few(const RouteArgs a, const bool wide)
 {
     extern __shared__ float shared[];
     __shared__ float lowest[kFewWarps], highest[kFewWarps];
