@@ -473,6 +473,28 @@ def test_experts_extreme_nibbles_and_gates():
     assert (check_experts(x, ids, torch.ones((6, 1), device="cuda"), (w13, s13, w2, s2), group) == 0).all()
 
 
+def test_experts_rows_of_any_magnitude():
+    """bfloat16 rows far above and below half's range, alone and side by side, a
+    row that spans both, and one of zeros: each row to the precision of its own
+    size (two half units in the 2-norm; the spanning row's small entries are
+    below the 32-bit sums' resolution of its large ones)."""
+    E, H, I, group = 2, 256, 64, 64
+    mats = layer(E, H, I, group, BF16, 8)
+    x = randn((7, H), 9, BF16)
+    powers = [0, 30, -40, 50, -20, 0, 0]
+    x = (x.float() * torch.tensor([2.0 ** p for p in powers], device="cuda")[:, None]).to(BF16)
+    x[5] *= torch.where(torch.arange(H, device="cuda") % 3 == 0, 2.0 ** 24, 2.0 ** -12).to(BF16)
+    x[6] = 0
+    ids = torch.tensor([[0, 1]] * 7, device="cuda", dtype=torch.int32)
+    w = torch.full((7, 2), 0.5, device="cuda")
+    y = moe.experts(x, ids, w, *mats)
+    h = [host(m) if m.is_floating_point() else m.cpu().numpy() for m in mats]
+    want, _ = R.experts(host(x), ids.cpu().numpy(), host(w), *h, group)
+    for t in range(6):
+        assert np.linalg.norm(host(y)[t] - want[t]) <= 2 * HALF_ULP[BF16] * np.linalg.norm(want[t]), t
+    assert (y[6] == 0).all()
+
+
 def test_experts_rows_apart_repeat_and_absent_experts_unread():
     E, H, I, group = 5, 320, 96, 32
     mats = layer(E, H, I, group, BF16, 4)
