@@ -197,7 +197,8 @@ __device__ __forceinline__ void load_share(const T *x, u32 n, bool wide, float (
     }
 }
 
-// More than eight slots: a warp has a row, a lane V experts.
+// More than eight slots, and short batches: a warp has a row, a lane V experts,
+// all of them sorted.
 template <class T, int ORDER, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a, const Shares sh)
 {
