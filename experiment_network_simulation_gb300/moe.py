@@ -10,9 +10,9 @@ mv_route_backward, mv_exchange and mv_experts (``include/mv.h``).
 :func:`.inputs.moe_workload` makes an all-to-all of.  Every call is enqueued
 on ``stream`` (default: the current one of the inputs' device) and returns
 without waiting; outputs and workspaces come from torch's allocator on that
-stream.  They record nothing for autograd.  Malformed arguments raise ValueError, what the library refuses
-:class:`.mv.MVError`.  There is no CPU fallback: tensors have to be on a CUDA
-device.
+stream, and nothing is recorded for autograd.  Malformed arguments raise
+ValueError, what the library refuses :class:`.mv.MVError`.  There is no CPU
+fallback: tensors have to be on a CUDA device.
 """
 from __future__ import annotations
 
