@@ -44,7 +44,7 @@ struct Patterns {
 };
 
 struct ExpertArgs {
-    Patterns half, own;             // for half, for the type of x
+    Patterns half, brain;           // for half, for bfloat16
     const void *x;
     const int32_t *ids;
     const float *weights;
@@ -56,7 +56,7 @@ struct ExpertArgs {
     // workspace
     __half *xp;                     // x / x_unit, permuted      [tokens, hidden]
     float *x_unit;                  // powers of two             [tokens]
-    void *h;                        // silu(W1 x) (W3 x), permuted [pairs, inner]
+    __nv_bfloat16 *h;               // silu(W1 x) (W3 x) in two parts, permuted [pairs, 2, inner]
     float *o;                       // W2 h                      [pairs, hidden]
     uint2 *pairs;                   // pairs by expert, each with its token
     Item *items;
@@ -251,8 +251,12 @@ template <class T> __global__ void __launch_bounds__(kPrepThreads) k_prepare(con
 }
 
 // ---- products ------------------------------------------------------------
-// h is rounded to the type of x, as a layer of separate kernels would store it:
-// it is the next product's operand.  All sums are held in 32 bits.
+// The inner activations h = silu(W1 x) (W3 x) are the next product's operand:
+// two bfloat16, the nearest to h and the nearest to what that leaves, together
+// within 2^-18 of h at any magnitude that 32 bits hold (float16 would end at
+// 65504).  Both parts meet the same widened weights and add to the same sums,
+// so the second costs matrix instructions and shared-memory loads, not
+// widening.  All sums are held in 32 bits, and only y is rounded to x's type.
 constexpr u32 kWarps = 8, kThreads = kWarps * 32;
 constexpr u32 kRows = kWarps / 2 * 32;          // weight rows a block: 32 to each of four pairs of warps
 constexpr u32 kStep = 256;                      // columns a step: half of them to each warp of a pair
@@ -270,18 +274,22 @@ constexpr u32 kScaleBytes = 2 * kRows * kSPitch;
 // in use, and no other warp waits for them.  Activations are the block's, in
 // chunks of kChunkOf steps, two in shared memory; the block's warps meet once
 // a chunk.  Epochs begin with a chunk.  What is copied is there kStagesOf - 1
-// steps later: a chunk or an epoch at most.
-template <int NT, u32 PER> constexpr int kStagesOf = NT == 1 && PER > 1 ? 4 : 3;
-template <int NT, u32 PER> constexpr u32 kChunkOf = NT == 1 && PER > 1 ? 4 : 2;
-template <int NT, u32 PER> constexpr u32 kXPitch = kChunkOf<NT, PER> * kStep * 2;      // odd rows' 64-byte halves are swapped
-template <int NT, u32 PER> constexpr u32 kRing = kStagesOf<NT, PER> * kWarps * kWarpStage;
+// steps later: a chunk or an epoch at most.  NB: tiles of activations, 8 rows each;
+// many of them leave room for less ahead.
+template <int NB, u32 PER> constexpr int kStagesOf = NB == 1 && PER > 1 ? 4 : NB <= 3 ? 3 : 2;
+template <int NB, u32 PER> constexpr u32 kChunkOf = NB == 1 && PER > 1 ? 4 : NB <= 3 ? 2 : 1;
+template <int NB, u32 PER> constexpr u32 kXPitch = kChunkOf<NB, PER> * kStep * 2;      // odd rows' 64-byte halves are swapped
+template <int NB, u32 PER> constexpr u32 kRing = kStagesOf<NB, PER> * kWarps * kWarpStage;
 constexpr u32 kTable = 3 * 8 * 8;               // an item's pairs: where they go, and what x was divided by
-template <int NT, u32 PER> constexpr u32 kRoom = kTable + kScaleBytes + kRing<NT, PER> + 2 * NT * 8 * kXPitch<NT, PER>;
+template <int NB, u32 PER> constexpr u32 kRoom = kTable + kScaleBytes + kRing<NB, PER> + 2 * NB * 8 * kXPitch<NB, PER>;
 template <u32 A, u32 B> constexpr u32 kLarger = A > B ? A : B;
+// Parts of the activations: x is one half, h two bfloat16.
+template <bool GATE> constexpr int kParts = GATE ? 1 : 2;
 // Shared memory of a block whose items hold up to 8 MOST pairs.
-template <int MOST, u32 PER> constexpr u32 kSmem =
-    MOST == 1 ? kRoom<1, PER> : kLarger<kRoom<1, PER>, MOST == 2 ? kRoom<2, PER> : kLarger<kRoom<2, PER>, kRoom<3, PER>>>;
-static_assert(2 * (kSmem<3, 1> + 1024) <= 227 * 1024 && 2 * (kSmem<3, 4> + 1024) <= 227 * 1024, "two blocks an SM");
+template <bool GATE, int MOST, u32 PER, int P = kParts<GATE>> constexpr u32 kSmem =
+    MOST == 1 ? kRoom<P, PER> : kLarger<kRoom<P, PER>, MOST == 2 ? kRoom<2 * P, PER> : kLarger<kRoom<2 * P, PER>, kRoom<3 * P, PER>>>;
+template <bool GATE> constexpr u32 kMostSmem = kLarger<kSmem<GATE, 3, 1>, kSmem<GATE, 3, 4>>;
+static_assert(2 * (kLarger<kMostSmem<true>, kMostSmem<false>> + 1024) <= 227 * 1024, "two blocks an SM");
 
 // One tile of weight rows against up to 8 NT pairs' activations.  A warp
 // holds 32 rows as two matrix operands of 16; an operand of 16 x 16 weights
@@ -290,20 +298,20 @@ static_assert(2 * (kSmem<3, 1> + 1024) <= 227 * 1024 && 2 * (kSmem<3, 4> + 1024)
 // warps adds its two sums at the end.  The order of additions depends on the
 // sizes alone, never on the other tokens.
 //
-// T: the type of the scales and of the result; C: of the activations; PER:
-// blocks of 32 columns a group.
+// T: the type of the scales and of the result; C: of the activations' parts;
+// PER: blocks of 32 columns a group.
 template <class T, class C, int NT, bool GATE, u32 PER>
 __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 tile, unsigned char *smem)
 {
-    constexpr int kStages = kStagesOf<NT, PER>;
-    constexpr u32 kGroup = PER * 32, kEpochSteps = kEpoch * kGroup / kStep, kChunk = kChunkOf<NT, PER>, kPitch = kXPitch<NT, PER>;
+    constexpr int kP = kParts<GATE>, kTiles = NT * kP, kStages = kStagesOf<kTiles, PER>;
+    constexpr u32 kGroup = PER * 32, kEpochSteps = kEpoch * kGroup / kStep, kChunk = kChunkOf<kTiles, PER>, kPitch = kXPitch<kTiles, PER>;
     static_assert(kEpochSteps % kChunk == 0 && kStages - 1 <= (int)kChunk, "copies arrive in time");
     const u32 tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const u32 half = tid >> 7, warp = (tid >> 5) & 3;         // columns, rows
     const u32 K = GATE ? a.hidden : a.inner, groups = K / kGroup;
-    const Patterns patterns = GATE ? a.half : a.own;
+    const Patterns patterns = GATE ? a.half : a.brain;
     uint2 *table = reinterpret_cast<uint2 *>(smem);
-    const u32 scales = (u32)__cvta_generic_to_shared(smem) + kTable, ring = scales + kScaleBytes, rows = ring + kRing<NT, PER>;
+    const u32 scales = (u32)__cvta_generic_to_shared(smem) + kTable, ring = scales + kScaleBytes, rows = ring + kRing<kTiles, PER>;
     // block row r: warp r / 32's operand (r / 16) & 1, row r & 15
     auto weight_row = [&](u32 r) -> int64_t {
         if (GATE) {
@@ -343,7 +351,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         xp[j] = nullptr;
         if (r >= it.count) continue;
         const uint2 p = a.pairs[it.first + r];
-        xp[j] = (GATE ? reinterpret_cast<const C *>(a.xp) + (u64)p.y * K : static_cast<const C *>(a.h) + (u64)p.x * K) + lane * 8;
+        xp[j] = (GATE ? reinterpret_cast<const C *>(a.xp) + (u64)p.y * K : reinterpret_cast<const C *>(a.h) + (u64)p.x * kP * K) + lane * 8;
         if (lane == 0) table[r] = make_uint2(p.x, GATE ? __float_as_uint(a.x_unit[p.y]) : 0u);
     }
     const u32 x_to = rows + (tid >> 5) * kPitch + ((lane * 16) ^ ((tid & 32) * 2));
@@ -354,7 +362,9 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
             if (!whole && c + lane * 8 >= K) break;
 #pragma unroll
             for (int j = 0; j < NT; j++)
-                if (xp[j]) copy16(x_to + ((chunk & 1) * NT + j) * 8 * kPitch + i * kStep * 2, xp[j] + c);
+#pragma unroll
+                for (int part = 0; part < kP; part++)
+                    if (xp[j]) copy16(x_to + ((chunk & 1) * kTiles + part * NT + j) * 8 * kPitch + i * kStep * 2, xp[j] + part * K + c);
         }
     };
     const T *all = static_cast<const T *>(GATE ? a.s13 : a.s2);
@@ -380,7 +390,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         s_at[i] = scales + r * kSPitch + (u32)(((base_row + (u64)(row < 0 ? 0 : row)) * groups * 2) & 15);
     }
 
-    float total[2][NT][4], part[2][NT][4];
+    float total[2][NT][4], sum[2][NT][4];
 #pragma unroll
     for (int m = 0; m < 2; m++)
 #pragma unroll
@@ -399,17 +409,21 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
     // this half's blocks of 32 columns of a step, those below `blocks`
     auto multiply = [&](u32 s, u32 off, u32 x_off, u32 blocks) {
         // one tile: every operand of the step is under way before the first is used
-        u32 w[kStep / 64][4], x[kStep / 64][4];
+        u32 w[kStep / 64][4], x[kStep / 64][kP][4];
         auto load_weights = [&](u32 b) {
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[b][0]), "=r"(w[b][1]), "=r"(w[b][2]), "=r"(w[b][3]) : "r"(a_row + off + (b ^ a_turn) * 16));
+        };
+        auto load_rows = [&](int part, int n, u32 b, u32 (&y)[4]) {
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                         : "r"(x_row + x_off + (part * NT + n) * 8 * kPitch + ((b * 64) ^ x_turn)));
         };
 #pragma unroll
         for (u32 b = 0; b < kStep / 64; b++) {
             if (NT > 1) break;
             load_weights(b);
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[b][0]), "=r"(x[b][1]), "=r"(x[b][2]), "=r"(x[b][3])
-                         : "r"(x_row + x_off + ((b * 64) ^ x_turn)));
+#pragma unroll
+            for (int part = 0; part < kP; part++) load_rows(part, 0, b, x[b][part]);
         }
 #pragma unroll
         for (u32 b = 0; b < kStep / 64; b++) {
@@ -419,22 +433,23 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
 #pragma unroll
             for (int i = 0; i < 4; i++) widen<C>(patterns, w[b][i], q[i]);
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
-                u32 y[4];
-                if (NT == 1) {
+            for (int n = 0; n < NT; n++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) y[i] = x[b][i];
-                } else {
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                                 : "r"(x_row + x_off + n * 8 * kPitch + ((b * 64) ^ x_turn)));
-                }
+                for (int part = 0; part < kP; part++) {
+                    u32 y[4];
+                    if (NT == 1) {
 #pragma unroll
-                for (int m = 0; m < 2; m++) {
-                    if (b % PER == 0) mma_from_zero<C>(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], y[0], y[1]);
-                    else Math<C>::mma(part[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], y[0], y[1]);
-                    Math<C>::mma(part[m][n], q[2 * m][2], q[2 * m + 1][2], q[2 * m][3], q[2 * m + 1][3], y[2], y[3]);
+                        for (int i = 0; i < 4; i++) y[i] = x[b][part][i];
+                    } else {
+                        load_rows(part, n, b, y);
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        if (b % PER == 0 && part == 0) mma_from_zero<C>(sum[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], y[0], y[1]);
+                        else Math<C>::mma(sum[m][n], q[2 * m][0], q[2 * m + 1][0], q[2 * m][1], q[2 * m + 1][1], y[0], y[1]);
+                        Math<C>::mma(sum[m][n], q[2 * m][2], q[2 * m + 1][2], q[2 * m][3], q[2 * m + 1][3], y[2], y[3]);
+                    }
                 }
-            }
             if (b % PER == PER - 1) {                         // the group's last columns
                 const u32 group = s * (kStep / kGroup) + half * (kStep / 2 / kGroup) + b / PER;
                 const u32 s_off = ((group / kEpoch) & 1) * kRows * kSPitch + (group % kEpoch) * 2;
@@ -443,10 +458,10 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
                     const float s0 = shared_value<T>(s_at[2 * m] + s_off), s1 = shared_value<T>(s_at[2 * m + 1] + s_off);
 #pragma unroll
                     for (int n = 0; n < NT; n++) {
-                        total[m][n][0] += s0 * part[m][n][0];
-                        total[m][n][1] += s0 * part[m][n][1];
-                        total[m][n][2] += s1 * part[m][n][2];
-                        total[m][n][3] += s1 * part[m][n][3];
+                        total[m][n][0] += s0 * sum[m][n][0];
+                        total[m][n][1] += s0 * sum[m][n][1];
+                        total[m][n][2] += s1 * sum[m][n][2];
+                        total[m][n][3] += s1 * sum[m][n][3];
                     }
                 }
             }
@@ -462,7 +477,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
         if (i == 0) fetch_rows(s / kChunk + 1, whole);
         if (i == 0 && s % kEpochSteps == 0) fetch_scales(s / kEpochSteps + 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
-        const u32 off = slot * (kWarps * kWarpStage), x_off = (s / kChunk & 1) * NT * 8 * kPitch + i * kStep * 2;
+        const u32 off = slot * (kWarps * kWarpStage), x_off = (s / kChunk & 1) * kTiles * 8 * kPitch + i * kStep * 2;
         if (whole || (NT == 1 && (s + 1) * kStep <= K)) {
             multiply(s, off, x_off, kStep / 64);
         } else {
@@ -509,9 +524,14 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
             if (GATE) {
                 const u32 row = tile * (kRows / 2) + warp * 16 + r;
                 const float unit = __uint_as_float(to.y), z = v[0][j] * unit, up = v[1][j] * unit;
-                if (row < a.inner)
-                    static_cast<T *>(a.h)[(u64)to.x * a.inner + column_place(row)] =
-                        from_float<T>(z * reciprocal_fast(1.0f + exp2_fast(-z * kLog2e)) * up);
+                if (row < a.inner) {
+                    const float h = z * reciprocal_fast(1.0f + exp2_fast(-z * kLog2e)) * up;
+                    const __nv_bfloat16 most = __float2bfloat16_rn(h);
+                    __nv_bfloat16 *at = a.h + (u64)to.x * 2 * a.inner + column_place(row);
+                    at[0] = most;
+                    const float rest = h - __bfloat162float(most);
+                    at[a.inner] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);          // of infinities nothing is left
+                }
             } else {
 #pragma unroll
                 for (int m = 0; m < 2; m++) {
@@ -525,7 +545,7 @@ __device__ __forceinline__ void product(const ExpertArgs &a, const Item it, u32 
 
 template <class T, bool GATE, int MOST, u32 PER> __global__ void __launch_bounds__(kThreads, 2) k_product(const ExpertArgs a)
 {
-    using C = std::conditional_t<GATE, __half, T>;
+    using C = std::conditional_t<GATE, __half, __nv_bfloat16>;
     extern __shared__ __align__(16) unsigned char smem[];
     after_previous();
     let_next_start();
@@ -592,7 +612,7 @@ Layout layout(const mv_experts_desc *d)
     auto take = [&](u64 bytes) { const u64 here = at; at += (bytes + 255) / 256 * 256; return here; };
     l.xp = take(d->tokens * d->hidden * 2);
     l.x_unit = take(d->tokens * 4);
-    l.h = take(pairs * d->inner * 2);
+    l.h = take(pairs * d->inner * 4);
     l.o = take(pairs * d->hidden * 4);
     l.pairs = take(pairs * sizeof(uint2));
     l.items = take(most_items(d) * sizeof(Item));
@@ -614,7 +634,7 @@ int check(const mv_experts_desc *d)
 
 template <class T, bool GATE, int MOST, u32 PER> int run_product(const ExpertArgs &a, u64 items, cudaStream_t stream)
 {
-    constexpr u32 smem = kSmem<MOST, PER>;
+    constexpr u32 smem = kSmem<GATE, MOST, PER>;
     const u32 tiles = GATE ? (a.inner + kRows / 2 - 1) / (kRows / 2) : (a.hidden + kRows - 1) / kRows;
     const auto kernel = k_product<T, GATE, MOST, PER>;
     if (smem > 48 * 1024 &&
@@ -679,7 +699,7 @@ extern "C" int mv_experts(const mv_experts_desc *d, void *workspace, uint64_t ws
     if (ws_bytes < need) return MV_ENOMEM;
     ExpertArgs a;
     a.half = Math<__half>::kPatterns;
-    a.own = d->dtype == MV_F16 ? Math<__half>::kPatterns : Math<__nv_bfloat16>::kPatterns;
+    a.brain = Math<__nv_bfloat16>::kPatterns;
     a.x = d->x;
     a.ids = d->ids;
     a.weights = d->weights;
@@ -692,7 +712,7 @@ extern "C" int mv_experts(const mv_experts_desc *d, void *workspace, uint64_t ws
     char *ws = static_cast<char *>(workspace);
     a.xp = reinterpret_cast<__half *>(ws + l.xp);
     a.x_unit = reinterpret_cast<float *>(ws + l.x_unit);
-    a.h = ws + l.h;
+    a.h = reinterpret_cast<__nv_bfloat16 *>(ws + l.h);
     a.o = reinterpret_cast<float *>(ws + l.o);
     a.pairs = reinterpret_cast<uint2 *>(ws + l.pairs);
     a.items = reinterpret_cast<Item *>(ws + l.items);

@@ -448,9 +448,10 @@ int mv_exchange(const mv_exchange_desc *desc, void *stream);
  * consecutive columns: W = (q - 8) * scale, two numbers to a byte, the even
  * column in the low half.  w13 holds W1's `inner` rows, then W3's.  x, y and
  * the scales are of type `dtype` (MV_F16 or MV_BF16); sums are held in 32
- * bits, and the inner activations silu(W1 x) * (W3 x) are rounded to `dtype`
- * (beyond its range, to infinity) before W2.  A token's result does not depend
- * on the other tokens.  Meant for up to some tens of tokens an expert.  hidden and inner are multiples of group, x's rows are row_stride
+ * bits and the inner activations silu(W1 x) * (W3 x) to 2^-18 of their value,
+ * at any magnitude of 32 bits; only y is rounded to `dtype`.  A token's result
+ * does not depend on the other tokens.  Meant for up to some tens of tokens an
+ * expert.  hidden and inner are multiples of group, x's rows are row_stride
  * elements apart (a multiple of 8), arrays of `dtype` and bytes are 16-byte
  * aligned.  Ids outside [0, experts) are experts that are not here: they add
  * nothing, and their weights are not read.  A token without any gets zeros.

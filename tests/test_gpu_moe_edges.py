@@ -1,0 +1,65 @@
+"""The routed-expert operators where they can go wrong: extremes of value, size
+and shape, against plain 64-bit code."""
+import numpy as np
+import pytest
+
+import moe_reference as R
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from experiment_network_simulation_gb300 import moe  # noqa: E402
+from test_gpu_moe import BF16, F16, HALF_ULP, host, layer, randn  # noqa: E402
+
+
+# ---- experts ---------------------------------------------------------------
+def experts_of(x, ids, w, mats, group):
+    """(result, 64-bit result, magnitudes summed) of one call."""
+    y = moe.experts(x, ids, w, *mats)
+    h = [host(m) if m.is_floating_point() else m.cpu().numpy() for m in mats]
+    return (y, *R.experts(host(x), ids.cpu().numpy(), host(w), *h, group))
+
+
+def one_slot(T, E, k, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    ids = torch.rand((T, E), generator=g, device="cuda").argsort(1)[:, :k].int().contiguous()
+    return ids, torch.rand((T, k), generator=g, device="cuda") + 0.1
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T,E,k,H,I,group", [(5, 3, 1, 256, 256, 128), (12, 1, 1, 64, 320, 64),
+                                             (24, 1, 1, 128, 256, 32), (60, 6, 2, 128, 128, 32)])
+def test_experts_round_once(T, E, k, H, I, group, dtype):
+    """Nothing but the result is rounded to the type: the inner activations are
+    held to 2^-18 or so of their value, which leaves the sum off by less than
+    2^-18 of a result's usual magnitude, 2^-8 of a float16 unit there.  Where
+    terms cancel, a result 2^-j as large (2^-j as likely) has units 2^-j as
+    large: all in all a few times 2^-8 of the results land on the other side of
+    a rounding boundary; one in twenty is allowed.  (An inner rounding to the
+    type turns over a third of them.)"""
+    mats = layer(E, H, I, group, dtype, T + H)
+    x = randn((T, H), T + 1, dtype)
+    ids, w = one_slot(T, E, k, T)
+    y, want, size = experts_of(x, ids, w, mats, group)
+    once = torch.from_numpy(want).to(dtype)
+    assert (y.cpu() == once).float().mean() >= 0.95
+    # H and I additions that each may lose 2^-23 of what is summed; inner sums are 8 to 16 times their result
+    bound = HALF_ULP[dtype] * np.abs(want) + (2.0 ** -17 + (16 * H + I) * 2.0 ** -23) * size
+    assert (np.abs(host(y) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_experts_inner_activations_of_any_magnitude(dtype):
+    """Inner activations far beyond float16's range, and far below it, whose
+    products are well inside."""
+    E, H, I, group = 2, 128, 128, 64
+    w13, s13, w2, s2 = layer(E, H, I, group, dtype, 31)
+    ids = torch.tensor([[0, 1]] * 9, device="cuda", dtype=torch.int32)
+    w = torch.full((9, 2), 0.5, device="cuda")
+    for up, down in ((2.0 ** 8, 2.0 ** -7), (2.0 ** -9, 2.0 ** 8)):
+        x = (randn((9, H), 32) * up).to(dtype)
+        y, want, size = experts_of(x, ids, w, (w13, s13, w2, (s2.float() * down).to(dtype)), group)
+        bound = HALF_ULP[dtype] * np.abs(want) + (2.0 ** -17 + (16 * H + I) * 2.0 ** -23) * size + 2.0 ** -25
+        assert (np.abs(host(y) - want) <= bound).all()
