@@ -15,15 +15,21 @@ struct ExchangeArgs {
     u32 warps;                      // warps a block
 };
 
-// Token t0 .. t1 of an item: part `split` of a source's tokens.
+// Tokens t0 .. t1 of the sources first .. last.
+__device__ __forceinline__ void source_tokens(const ExchangeArgs &a, u32 first, u32 last, u64 &t0, u64 &t1)
+{
+    t0 = first * (a.tokens / a.sources);
+    t1 = (last + 1) * (a.tokens / a.sources);
+    if (a.starts) {
+        t0 = min((u64)max(a.starts[first], (int64_t)0), a.tokens);
+        t1 = max(t0, min((u64)max(a.starts[last + 1], (int64_t)0), a.tokens));
+    }
+}
+
+// Those of an item: part `split` of a source's tokens.
 __device__ __forceinline__ void item_tokens(const ExchangeArgs &a, u32 source, u32 split, u64 &t0, u64 &t1)
 {
-    t0 = source * (a.tokens / a.sources);
-    t1 = t0 + a.tokens / a.sources;
-    if (a.starts) {
-        t0 = min((u64)max(a.starts[source], (int64_t)0), a.tokens);
-        t1 = max(t0, min((u64)max(a.starts[source + 1], (int64_t)0), a.tokens));
-    }
+    source_tokens(a, source, source, t0, t1);
     const u64 n = t1 - t0;
     t1 = t0 + n * (split + 1) / a.splits;
     t0 += n * split / a.splits;
@@ -136,8 +142,9 @@ template <bool ONCE> __global__ void __launch_bounds__(kTogether) k_exchange_tog
     int32_t *place = shared, *hist = place + E, *row = hist + E;
     const bool load_only = blockIdx.x < a.count_blocks, loads = load_only || a.count_blocks == 0;
     const u64 item = blockIdx.x - a.count_blocks, pair = item / a.splits, b = load_only ? blockIdx.x : pair / a.sources;
-    u64 t0 = 0, t1 = a.tokens;
-    if (!load_only) item_tokens(a, (u32)(pair % a.sources), (u32)(item % a.splits), t0, t1);
+    u64 t0, t1;
+    if (load_only) source_tokens(a, 0, a.sources - 1, t0, t1);      // tokens of no source count nowhere
+    else item_tokens(a, (u32)(pair % a.sources), (u32)(item % a.splits), t0, t1);
     for (u32 e = threadIdx.x; e < E; e += kTogether) {
         place[e] = a.place[e];
         hist[e] = 0;

@@ -240,11 +240,11 @@ def exchange(ids, place, ranks: int, *, sources: int | None = None, starts=None,
     ``ids`` int32 [tokens, topk], or [batches, tokens, topk] for as many
     independent exchanges (both results then get that dimension).  Tokens lie
     by source rank: equal shares of ``sources`` (default: ``ranks``), or
-    ``starts`` (int64 [sources + 1], on the device).  ``place`` int32
-    [experts] is the rank an expert lives on.  ``sent[s, d]`` counts the
-    tokens of s with an expert on d, or without ``once`` every one of their
-    experts there; ``load[e]`` the slots that hold e.  Ids outside [0,
-    experts) are empty slots.
+    ``starts`` (ascending int64 [sources + 1], on the device; tokens outside
+    them count nowhere).  ``place`` int32 [experts] is the rank an expert lives
+    on.  ``sent[s, d]`` counts the tokens of s with an expert on d, or without
+    ``once`` every one of their experts there; ``load[e]`` the slots that hold
+    e.  Ids outside [0, experts) are empty slots.
     """
     if isinstance(ids, torch.Tensor) and ids.dim() == 2:
         _tensor("ids", ids, (torch.int32,), (None, None))

@@ -351,7 +351,8 @@ int mv_simulate_static(const mv_batch_desc *desc, uint32_t max_ticks, void *stre
  * Returns MV_OK, MV_EINVAL (a null pointer or a malformed field),
  * MV_EOVERFLOW (a size beyond the limits below), MV_ENOMEM (mv_experts'
  * workspace), MV_ECUDA.  Nothing is written unless MV_OK or MV_ECUDA is
- * returned.  Zero tokens (zero batches) are valid and do nothing.
+ * returned.  Zero tokens and zero batches are valid: an exchange of no tokens
+ * counts zeros, everything else of size zero does nothing.
  */
 #define MV_F32 0
 #define MV_F16 1
@@ -422,8 +423,10 @@ int mv_route_backward(const mv_route_grad_desc *desc, void *stream);
  * topk ids.  A set's tokens lie by source rank: source s holds tokens
  * starts[s] to starts[s + 1] (ascending, 0 to tokens; each read is clamped to
  * that), the same in every set; with starts = NULL every source holds an equal
- * share (sources divides tokens).  Expert e lives on rank place[e].
- *   load[b, e]     slots of set b that hold e;
+ * share (sources divides tokens).  Tokens before starts[0] and from
+ * starts[sources] on belong to no source and count nowhere.  Expert e lives on
+ * rank place[e].
+ *   load[b, e]     slots of set b's sources that hold e;
  *   sent[b, s, d]  slots of source s whose expert lives on rank d, or with
  *                  `once` its tokens with at least one such slot.
  * Ids outside [0, experts) are empty slots; experts placed outside [0, ranks)

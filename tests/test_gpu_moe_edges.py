@@ -63,3 +63,28 @@ def test_experts_inner_activations_of_any_magnitude(dtype):
         y, want, size = experts_of(x, ids, w, (w13, s13, w2, (s2.float() * down).to(dtype)), group)
         bound = HALF_ULP[dtype] * np.abs(want) + (2.0 ** -17 + (16 * H + I) * 2.0 ** -23) * size + 2.0 ** -25
         assert (np.abs(host(y) - want) <= bound).all()
+
+
+# ---- exchange --------------------------------------------------------------
+def check_counts(ids, place, ranks, once, starts=None, sources=None):
+    kw = dict(starts=None if starts is None else torch.tensor(starts, device="cuda"), sources=sources, once=once)
+    load, sent = moe.exchange(ids, place, ranks, **kw)
+    want = R.exchange(ids.cpu().numpy(), place.cpu().numpy(), ranks, sources=sources, starts=starts, once=once)
+    assert np.array_equal(load.cpu().numpy(), want[0])
+    assert np.array_equal(sent.cpu().numpy(), want[1])
+
+
+def random_ids(shape, experts, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-1, experts + 1, shape, generator=g, device="cuda", dtype=torch.int32)
+
+
+@pytest.mark.parametrize("once", [True, False])
+@pytest.mark.parametrize("B,T,k", [(1, 40, 4), (3, 40, 4), (1, 9000, 4), (40, 300, 3), (300, 40, 5)])
+def test_exchange_of_tokens_that_no_source_holds(B, T, k, once):
+    """Starts that leave tokens out before the first source and behind the last:
+    they count nowhere, however large the call."""
+    ids = random_ids((B, T, k), 24, T)
+    place = (torch.arange(24, device="cuda") % 6).int()
+    for starts in ([3, 11, 11, 20, T - 7], [0, T - 1], [5, 5, 6, T], [T, T], [0, 0]):
+        check_counts(ids, place, 6, once, starts=starts)
