@@ -11,7 +11,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from experiment_network_simulation_gb300 import moe  # noqa: E402
-from test_gpu_moe import BF16, F16, HALF_ULP, host, layer, randn  # noqa: E402
+from test_gpu_moe import BF16, F16, F32, HALF_ULP, U, host, layer, randn, spread  # noqa: E402
 
 
 # ---- experts ---------------------------------------------------------------
@@ -88,3 +88,43 @@ def test_exchange_of_tokens_that_no_source_holds(B, T, k, once):
     place = (torch.arange(24, device="cuda") % 6).int()
     for starts in ([3, 11, 11, 20, T - 7], [0, T - 1], [5, 5, 6, T], [T, T], [0, 0]):
         check_counts(ids, place, 6, once, starts=starts)
+
+
+# ---- route -----------------------------------------------------------------
+# experts, groups: with more than eight slots no lane layout of a warp holds them
+UNEVEN = [(n, g) for n, g in [(960, 3), (960, 5), (960, 6), (960, 10), (960, 12), (720, 5), (720, 9), (720, 10),
+                              (720, 18), (720, 20), (561, 17), (1020, 17), (1023, 3), (1023, 31), (1023, 11)]]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("E,G", UNEVEN)
+def test_route_many_slots_of_uneven_groups(E, G, dtype):
+    x = randn((5, E), E + G, dtype, 2.0)
+    x[3, ::3] = -np.inf
+    x[4] = 0.5
+    b = randn((E,), G, F32, 0.1)
+    for n, (scores, bias, rule, renorm) in enumerate([("softmax", None, "max", True), ("softmax", b, "max", False),
+                                                      ("sigmoid", b, "top2", True), ("sigmoid", None, "top2", False)]):
+        for tg, k in ((G, 9), (max(2, G // 2), 32)):
+            k = min(k, tg * (E // G))
+            kw = dict(scores=scores, groups=G, top_groups=tg, group_rule=rule, renorm=renorm)
+            ids, w = moe.route(x, k, bias=bias, **kw)
+            want, ww, gaps = R.route(host(x), k, bias=None if bias is None else host(bias), **kw)
+            sure = gaps > 2.0 ** -18
+            assert 2 * sure.sum() >= 5
+            assert np.array_equal(ids.cpu().numpy()[sure], want[sure])
+            tol = U * (64 + 4 * spread(host(x)))
+            assert (np.abs(host(w) - ww) <= tol * np.abs(ww) + 2.0 ** -126)[sure].all()
+
+
+def test_every_documented_size_is_taken():
+    """Every way to part up to 1024 experts into groups, with 9 and 32 slots:
+    the ids are those of the logits' own stable order."""
+    for G in range(2, 33):
+        for E in range(G, 1025, G):
+            if E % (7 * G) and E + G <= 1024:        # a seventh of them, and the largest
+                continue
+            x = randn((2, E), E)
+            for k in {min(9, E), min(32, E)}:
+                ids, _ = moe.route(x, k, groups=G, top_groups=G)
+                assert torch.equal(ids.long(), x.sort(dim=1, descending=True, stable=True).indices[:, :k]), (E, G, k)
