@@ -871,13 +871,14 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_route_grad(const RouteGradA
                 w = sum > 0.0f ? w / sum : 0.0f;
                 d = w * (g - group_sum<L>(g * w));
             } else {
-                const float s = id >= 0 ? sigmoid(l) : 0.0f;
+                // the score s and its complement (1 - s would end at s's last bit) from one exponential
+                const float e = expf(-fabsf(l)), s = (l < 0.0f ? e : 1.0f) / (1.0f + e);
                 d = g;
                 if (a.renorm) {
                     const float sum = group_sum<L>(s), dot = group_sum<L>(g * s);
                     d = sum > 0.0f ? (g - dot / sum) / sum : 0.0f;
                 }
-                d *= s * (1.0f - s);
+                d *= e / ((1.0f + e) * (1.0f + e));
             }
             if (id >= 0) G[id] = d * a.scale;
             __syncwarp();

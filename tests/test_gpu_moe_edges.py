@@ -128,3 +128,26 @@ def test_every_documented_size_is_taken():
             for k in {min(9, E), min(32, E)}:
                 ids, _ = moe.route(x, k, groups=G, top_groups=G)
                 assert torch.equal(ids.long(), x.sort(dim=1, descending=True, stable=True).indices[:, :k]), (E, G, k)
+
+
+# ---- route_backward --------------------------------------------------------
+@pytest.mark.parametrize("E,k", [(11, 11), (40, 11), (200, 11)])
+def test_sigmoid_gradient_in_both_tails(E, k):
+    """To relative precision: a score and its complement are each an exponential
+    (2 units), a sum and a division, and three products follow."""
+    tail = torch.tensor([-80.0, -30.0, -20.0, -10.0, -5.0, 0.0, 5.0, 10.0, 15.0, 20.0, 80.0], device="cuda")
+    x = torch.full((3, E), -90.0, device="cuda")
+    x[:, E - 11:] = tail
+    ids = torch.arange(E - 11, E, device="cuda", dtype=torch.int32).repeat(3, 1).contiguous()
+    g = randn((3, k), 8).abs() + 0.5
+    s = 1.0 / (1.0 + torch.exp(-tail.double()))
+    c = 1.0 / (1.0 + torch.exp(tail.double()))
+    dx = moe.route_backward(x, ids, g, scores="sigmoid", renorm=False, scale=2.5)[:, E - 11:].double()
+    want = 2.5 * g.double() * s * c
+    assert ((dx - want).abs() <= 16 * U * want.abs()).all()
+    dx = moe.route_backward(x, ids, g, scores="sigmoid", renorm=True, scale=2.5)[:, E - 11:].double()
+    w = s / s.sum()
+    dot = (g.double() * w).sum(1, keepdim=True)
+    want = 2.5 * w * (g.double() - dot) * c
+    # the sums over eleven slots and the difference of g and its mean lose to their own size
+    assert ((dx - want).abs() <= 32 * U * 2.5 * w * c * (g.double() + dot) + 2.0 ** -126).all()
