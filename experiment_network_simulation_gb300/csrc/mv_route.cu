@@ -37,9 +37,15 @@ __device__ __forceinline__ bool open(float v) { return v > -INFINITY; }
 // exp(v - m) for v <= m; 1 at the maximum, an infinite one included.
 __device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.0f : expf(v - m); }
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// Renormalised sigmoids whose sum is below this lose bits, and all are 0 under
+// logits of -88 or so.  There sigmoid(v) is exp(v) to 2^-26, and what is left of
+// the ratio is a softmax of the chosen.  Under -700 (1e-304) a logit is taken for
+// what it must be, a mask by the type's lowest value, whose score is 0.
+constexpr float kTinySum = 0x1p-26f, kMasked = -700.0f;
+__device__ __forceinline__ float tiny_score(float v, float best) { return best >= kMasked ? exp_below(v, best) : 0.0f; }
 
-// Weights of a row's choices.  Lane r of the W lanes holds slot r: its
-// expert (or -1) and that expert's logit; m and sum are the row's softmax
+// Weights of a row's choices, of one row a warp (W is 32).  Lane r holds slot
+// r: its expert (or -1) and that expert's logit; m and sum are the row's softmax
 // statistics where the weights need them.
 template <int W>
 __device__ __forceinline__ float slot_weight(const RouteArgs &a, int id, float x, float m, float sum)
@@ -52,7 +58,12 @@ __device__ __forceinline__ float slot_weight(const RouteArgs &a, int id, float x
         w = a.softmax ? exp_below(x, m) / sum : sigmoid(x);
     }
     if (a.renorm) {
-        const float total = group_sum<W>(w);
+        float total = group_sum<W>(w);
+        if (!a.softmax && total < kTinySum) {        // the same in all of the warp
+            const float best = group_max<W>(id >= 0 ? x : -INFINITY);
+            w = id >= 0 ? tiny_score(x, best) : 0.0f;
+            total = group_sum<W>(w);
+        }
         w = total > 0.0f ? w / total : 0.0f;
     }
     return w * a.scale;
@@ -743,7 +754,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 7) k_route_few(const RouteArgs
                 w[i] = id[i] < 0 ? 0.0f : a.softmax ? exp_below(logit[i], m) / sum : sigmoid(logit[i]);
         }
         if (a.renorm) {
-            const float total = quad_sum(w[0] + w[1]);
+            float total = quad_sum(w[0] + w[1]);
+            const bool tiny = !a.softmax && total < kTinySum;
+            if (__any_sync(kFull, tiny)) {
+                const float top = quad_max(fmaxf(id[0] >= 0 ? logit[0] : -INFINITY, id[1] >= 0 ? logit[1] : -INFINITY));
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    if (tiny) w[i] = id[i] >= 0 ? tiny_score(logit[i], top) : 0.0f;
+                total = quad_sum(w[0] + w[1]);
+            }
 #pragma unroll
             for (int i = 0; i < 2; i++) w[i] = total > 0.0f ? w[i] / total : 0.0f;
         }
@@ -872,13 +891,21 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_route_grad(const RouteGradA
                 d = w * (g - group_sum<L>(g * w));
             } else {
                 // the score s and its complement (1 - s would end at s's last bit) from one exponential
-                const float e = expf(-fabsf(l)), s = (l < 0.0f ? e : 1.0f) / (1.0f + e);
+                const float e = expf(-fabsf(l)), n = 1.0f + e;
+                float s = (l < 0.0f ? e : 1.0f) / n;
                 d = g;
                 if (a.renorm) {
-                    const float sum = group_sum<L>(s), dot = group_sum<L>(g * s);
+                    float sum = group_sum<L>(s);
+                    const bool tiny = sum < kTinySum;
+                    if (__any_sync(kFull, tiny)) {
+                        const float best = group_max<L>(l);
+                        if (tiny) s = id >= 0 ? tiny_score(l, best) : 0.0f;
+                        sum = group_sum<L>(s);
+                    }
+                    const float dot = group_sum<L>(g * s);
                     d = sum > 0.0f ? (g - dot / sum) / sum : 0.0f;
                 }
-                d *= e / ((1.0f + e) * (1.0f + e));
+                d *= s * ((l < 0.0f ? 1.0f : e) / n);
             }
             if (id >= 0) G[id] = d * a.scale;
             __syncwarp();

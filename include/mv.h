@@ -382,7 +382,9 @@ int mv_simulate_static(const mv_batch_desc *desc, uint32_t max_ticks, void *stre
  *           equal values, of experts and of groups, go to the lowest index.
  *           Slots beyond the open experts get id -1 and weight 0;
  *   weight  weights[t, j] = scale * s, or with `renorm` scale * s / sum of
- *           the chosen s (0 where that sum is 0).  The bias is not part of it.
+ *           the chosen s (0 where that sum is 0).  The ratio holds where the s
+ *           are below what 32 bits hold, too; the sigmoids of logits all under
+ *           -700 count as 0.  The bias is not part of it.
  * An infinite logit is the limit: it has all of its row's softmax (with
  * several, each an equal share).  topk <= top_groups * experts / groups,
  * MV_MOE_MAX_EXPERTS, _TOPK, _GROUPS.

@@ -130,6 +130,35 @@ def test_every_documented_size_is_taken():
                 assert torch.equal(ids.long(), x.sort(dim=1, descending=True, stable=True).indices[:, :k]), (E, G, k)
 
 
+DEEP = [(7, 20, 4, 1, 1), (2600, 64, 4, 1, 1), (2600, 32, 6, 4, 2), (9, 300, 5, 1, 1), (11, 48, 12, 1, 1), (9, 48, 12, 4, 2)]
+
+
+@pytest.mark.parametrize("T,E,k,G,tg", DEEP)
+def test_sigmoid_of_very_negative_logits(T, E, k, G, tg):
+    """Scores down to nothing in 32 bits: renormalised weights depend on their
+    ratio alone.  Short and long batches, a few and many slots, exact ties."""
+    for shift in (-16.0, -19.0, -60.0, -88.0, -95.0, -200.0, -600.0):
+        x = (randn((T, E), E, F32, 2.0) + shift)[:T]
+        x[1] = shift                                                      # ties
+        x[2, 3] = 1.0                                                     # one that is not small
+        x[3, ::2] = -np.inf
+        kw = dict(scores="sigmoid", groups=G, top_groups=tg)
+        ids, w = moe.route(x, k, **kw)
+        some = np.unique(np.r_[0:min(T, 9), T - 1, np.arange(0, T, 199)])
+        want, ww, gaps = R.route(host(x)[some], k, **kw)
+        sure = gaps > 0                                                   # logits in order: exact
+        assert sure.all() and np.array_equal(ids.cpu().numpy()[some], want)
+        # row 2 spreads over the whole shift: what is far below its greatest rounds absolutely
+        tol = U * (64 + 4 * 20) * np.abs(ww) + 2.0 ** -100
+        assert (np.abs(host(w)[some] - ww) <= tol).all(), shift
+        g = randn((T, k), 5)
+        dx = host(moe.route_backward(x, ids, g, scores="sigmoid"))
+        assert np.isfinite(dx).all(), shift
+        dd = R.route_backward(host(x)[some], want, host(g)[some], "sigmoid", True, 1.0)
+        terms = np.abs(host(g)[some]).max(1, keepdims=True)
+        assert (np.abs(dx[some] - dd) <= U * 256 * terms).all(), shift
+
+
 # ---- route_backward --------------------------------------------------------
 @pytest.mark.parametrize("E,k", [(11, 11), (40, 11), (200, 11)])
 def test_sigmoid_gradient_in_both_tails(E, k):
