@@ -163,7 +163,8 @@ def route(logits, topk: int, *, scores: str = "softmax", bias=None, groups: int 
     the sum of their two best ("top2").  Equal values go to the lowest index.
     The weights are the chosen experts' scores, without the bias, divided by
     their sum if ``renorm``, times ``scale``.  An expert whose logit or bias is
-    -inf or NaN is closed; slots that no open expert is left for hold id -1
+    -inf or NaN is closed (by the bias: for the choice alone, its share of the
+    softmax stays its own); slots that no open expert is left for hold id -1
     and weight 0.
     """
     _tensor("logits", logits, _DTYPES, (None, None), rows_apart=True)

@@ -372,8 +372,9 @@ int mv_simulate_static(const mv_batch_desc *desc, uint32_t max_ticks, void *stre
  *   score   s_e = softmax(x)_e, or sigmoid(x_e) = 1 / (1 + exp(-x_e));
  *   order   v_e = s_e + bias_e; with no bias (NULL), and unless groups are
  *           ranked by sums of two, v_e = x_e, which orders alike;
- *   closed  an expert whose logit or bias is -inf or NaN: it is never chosen
- *           and adds nothing to the softmax;
+ *   closed  an expert whose logit or bias is -inf or NaN: it is never chosen.
+ *           A closed logit adds nothing to the softmax; an expert that only the
+ *           bias closes keeps its share, as the bias is no part of any score;
  *   groups  the `experts` in `groups` equal consecutive groups; the
  *           top_groups of greatest value stay, the others close.  A group's
  *           value is its greatest v, or the sum of its two greatest (with one
@@ -385,8 +386,8 @@ int mv_simulate_static(const mv_batch_desc *desc, uint32_t max_ticks, void *stre
  *           the chosen s (0 where that sum is 0).  The ratio holds where the s
  *           are below what 32 bits hold, too; the sigmoids of logits all under
  *           -700 count as 0.  The bias is not part of it.
- * An infinite logit is the limit: it has all of its row's softmax (with
- * several, each an equal share).  topk <= top_groups * experts / groups,
+ * An infinite logit is the limit: it has all of its row's softmax, whether its
+ * bias lets it be chosen or not (with several, each an equal share).  topk <= top_groups * experts / groups,
  * MV_MOE_MAX_EXPERTS, _TOPK, _GROUPS.
  */
 typedef struct mv_route_desc {

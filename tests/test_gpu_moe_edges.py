@@ -130,6 +130,27 @@ def test_every_documented_size_is_taken():
                 assert torch.equal(ids.long(), x.sort(dim=1, descending=True, stable=True).indices[:, :k]), (E, G, k)
 
 
+def test_a_bias_closes_the_choice_not_the_score():
+    """The bias is no part of the score: an expert that it closes is never
+    chosen, and keeps its share of the softmax."""
+    for T in (7, 3000):
+        x = randn((T, 64), 3, F32, 2.0)
+        b = torch.zeros(64, device="cuda")
+        b[5], b[9] = -np.inf, float("nan")
+        for k in (4, 12):
+            ids, w = moe.route(x, k, bias=b, renorm=False)
+            p = torch.softmax(x.double(), dim=1)
+            v = p.float()
+            v[:, [5, 9]] = -1.0
+            want = v.sort(dim=1, descending=True, stable=True).indices[:, :k]
+            assert (ids.long() == want).all(1).float().mean() > 0.99       # 32-bit scores differ in the last place
+            assert not ((ids == 5) | (ids == 9)).any()
+            assert torch.allclose(w.double(), p.gather(1, ids.long()), rtol=U * (64 + 4 * spread(host(x))), atol=0)
+        x[:, 9] = np.inf                                  # all of the softmax, and not to be chosen
+        ids, w = moe.route(x, 4, bias=b, renorm=False)
+        assert (w == 0).all() and not (ids == 9).any()
+
+
 DEEP = [(7, 20, 4, 1, 1), (2600, 64, 4, 1, 1), (2600, 32, 6, 4, 2), (9, 300, 5, 1, 1), (11, 48, 12, 1, 1), (9, 48, 12, 4, 2)]
 
 
