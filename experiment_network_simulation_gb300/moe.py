@@ -17,7 +17,6 @@ fallback: tensors have to be on a CUDA device.
 from __future__ import annotations
 
 import ctypes as C
-import math
 import struct
 
 import torch
@@ -29,6 +28,7 @@ _SCORES = {"softmax": SOFTMAX, "sigmoid": SIGMOID}
 _RULES = {"max": 0, "top2": 1}
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 MAX_EXPERTS, MAX_TOPK, MAX_GROUPS, MAX_RANKS = 1024, 32, 32, 8192
+_MAX_SCALE = torch.finfo(torch.float32).max        # the descriptors hold it in 32 bits
 
 _vp, _u64 = C.c_void_p, C.c_uint64
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -178,7 +178,7 @@ def route(logits, topk: int, *, scores: str = "softmax", bias=None, groups: int 
     most = min(MAX_TOPK, top_groups * (n // groups))
     if not 1 <= topk <= most:
         raise ValueError(f"topk is 1 to {most}, not {topk}")
-    if not math.isfinite(scale):
+    if not abs(scale) <= _MAX_SCALE:
         raise ValueError(f"scale is {scale}")
     s, r = _choice("scores", scores, _SCORES), _choice("group_rule", group_rule, _RULES)
     if bias is not None:
@@ -216,7 +216,7 @@ def route_backward(logits, ids, dweights, *, scores: str = "softmax", renorm: bo
     if not 1 <= topk <= min(MAX_TOPK, n):
         raise ValueError(f"topk is 1 to {min(MAX_TOPK, n)}, not {topk}")
     _tensor("dweights", dweights, (torch.float32,), (tokens, topk), logits.device)
-    if not math.isfinite(scale):
+    if not abs(scale) <= _MAX_SCALE:
         raise ValueError(f"scale is {scale}")
     s = _choice("scores", scores, _SCORES)
     dev = logits.device

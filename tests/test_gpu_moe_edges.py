@@ -201,3 +201,14 @@ def test_sigmoid_gradient_in_both_tails(E, k):
     want = 2.5 * w * (g.double() - dot) * c
     # the sums over eleven slots and the difference of g and its mean lose to their own size
     assert ((dx - want).abs() <= 32 * U * 2.5 * w * c * (g.double() + dot) + 2.0 ** -126).all()
+
+
+# ---- arguments and timing --------------------------------------------------
+def test_scale_beyond_32_bits_is_refused():
+    x = randn((4, 12), 1)
+    ids, w = moe.route(x, 3, scale=3.0e38)
+    for scale in (1e39, -1e300, float("inf")):
+        with pytest.raises(ValueError):
+            moe.route(x, 3, scale=scale)
+        with pytest.raises(ValueError):
+            moe.route_backward(x, ids, w, scale=scale)
