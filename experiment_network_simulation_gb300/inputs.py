@@ -804,6 +804,8 @@ def moe_workload(byte: np.ndarray, gpus: int, alpha: int, beta=(1, 36_864),
     ``compute_ns`` (one duration a rank: its experts' work on what it
     received) a compute node of that length lies between the two."""
     R = byte.shape[0]
+    if compute_ns is not None and (np.shape(compute_ns) != (R,) or min(compute_ns) < 0):
+        raise ValueError(f"compute_ns is one duration for each of {R} ranks")
     w = Workload(R, "moe")
     srv = np.arange(R) // gpus
     same = srv[:, None] == srv[None, :]

@@ -5,6 +5,7 @@ configuration text and the pages)."""
 import collections
 
 import numpy as np
+import pytest
 
 from experiment_network_simulation_gb300 import inputs as I
 
@@ -228,3 +229,11 @@ def test_moe_workload_with_expert_compute():
     lo = a["node_dur_lo"][a["node_kind"] == I.COMPUTE]
     assert lo.tolist() == ns and per == 2
     assert not (b["node_kind"] == I.COMPUTE).any()
+
+
+def test_moe_workload_wants_a_duration_a_rank():
+    byte = np.ones((16, 16), np.int64)
+    for ns in ([1000] * 15, [1000] * 17, [], [1000] * 15 + [-1], [[1000]] * 16):
+        with pytest.raises(ValueError):
+            I.moe_workload(byte, 8, alpha=3, compute_ns=ns)
+    I.moe_workload(byte, 8, alpha=3, compute_ns=np.arange(16))
