@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from experiment_network_simulation_gb300 import moe  # noqa: E402
+from experiment_network_simulation_gb300 import moe, moe_layer  # noqa: E402
 from test_gpu_moe import BF16, F16, F32, HALF_ULP, U, host, layer, randn, spread  # noqa: E402
 
 
@@ -212,3 +212,18 @@ def test_scale_beyond_32_bits_is_refused():
             moe.route(x, 3, scale=scale)
         with pytest.raises(ValueError):
             moe.route_backward(x, ids, w, scale=scale)
+
+
+def test_expert_times_leave_the_host_out(monkeypatch):
+    """A host that is slow to enqueue (2 ms here) does not lengthen the device's time."""
+    import time
+    small = moe_layer.Layer(servers=2, gpus=1, tokens=3, experts=8, topk=2, hidden=256, inner=64, group=32)
+    ids, w = moe.route(moe_layer.logits(small, 1), 2)
+    own = moe.experts
+
+    def slow(*a, **kw):
+        time.sleep(0.002)
+        return own(*a, **kw)
+
+    monkeypatch.setattr(moe, "experts", slow)
+    assert 0 < max(moe_layer.expert_ns(small, ids, w)) < 1_000_000
