@@ -65,6 +65,32 @@ def test_experts_inner_activations_of_any_magnitude(dtype):
         assert (np.abs(host(y) - want) <= bound).all()
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("H,I,group", [(4480, 2176, 128), (2240, 2112, 64), (1120, 1568, 32)])
+def test_experts_over_many_steps(H, I, group, dtype):
+    """Rows of many steps, chunks and scale epochs with an odd tail, for one, two
+    and three tiles of pairs an expert; a token in a large batch gets the bits
+    it gets alone.  Error as check_experts in test_gpu_moe derives it."""
+    E = 2
+    mats = layer(E, H, I, group, dtype, H)
+    x = randn((31, H), H + 1, dtype)
+    for n in (1, 13, 24, 31):                        # tiles: 1; 2; 3; 3 and 1
+        ids = torch.tensor([[t % 16 and 0 or 1] for t in range(n)], device="cuda", dtype=torch.int32)
+        if n == 24:
+            ids[:] = 0
+        w = torch.ones((n, 1), device="cuda")
+        y = moe.experts(x[:n], ids, w, *mats)
+        if n == 31:
+            h = [host(m) if m.is_floating_point() else m.cpu().numpy() for m in mats]
+            want, size = R.experts(host(x), ids.cpu().numpy(), host(w), *h, group)
+            half, err = HALF_ULP[dtype], np.abs(host(y) - want)
+            assert (err <= half * np.abs(want) + 2 * half * size + 2.0 ** -23).all()
+            assert np.linalg.norm(err) <= 2 * half * np.linalg.norm(want)
+        for t in sorted({0, 5 % n, n - 1}):
+            alone = moe.experts(x[t:t + 1], ids[t:t + 1], w[t:t + 1], *mats)
+            assert torch.equal(alone, y[t:t + 1]), (n, t)
+
+
 # ---- exchange --------------------------------------------------------------
 def check_counts(ids, place, ranks, once, starts=None, sources=None):
     kw = dict(starts=None if starts is None else torch.tensor(starts, device="cuda"), sources=sources, once=once)
