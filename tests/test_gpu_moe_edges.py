@@ -116,6 +116,31 @@ def test_exchange_of_tokens_that_no_source_holds(B, T, k, once):
         check_counts(ids, place, 6, once, starts=starts)
 
 
+@pytest.mark.parametrize("once", [True, False])
+@pytest.mark.parametrize("B,S,T,k,E,ranks", [(700, 37, 74, 3, 20, 10), (2, 2000, 4000, 5, 33, 7),
+                                             (40, 32, 64, 8, 1024, 8192), (1, 1300, 2600, 32, 40, 9),
+                                             (1300, 1, 3, 1, 5, 2)])
+def test_exchange_of_many_sources(B, S, T, k, E, ranks, once):
+    """Eight sources an SM and more: runs of sources that span batches, one warp
+    a block where counts are large, ids a token that do not divide a warp."""
+    ids = random_ids((B, T, k), E, S)
+    place = torch.randint(-1, ranks + 1, (E,), device="cuda", dtype=torch.int32,
+                          generator=torch.Generator(device="cuda").manual_seed(E))
+    check_counts(ids, place, ranks, once, sources=S)
+
+
+@pytest.mark.parametrize("once", [True, False])
+def test_exchange_of_many_uneven_sources(once):
+    g = np.random.default_rng(3)
+    T = 9000
+    cuts = np.sort(np.concatenate([g.integers(0, 40, 900), g.integers(6000, T + 1, 800)]))      # a long one amid short and empty ones
+    starts = [0, *cuts.tolist(), T]
+    ids = random_ids((2, T, 6), 50, 4)
+    place = (torch.arange(50, device="cuda") // 4).int()
+    check_counts(ids, place, 13, once, starts=starts)
+    check_counts(ids, place, 13, once, starts=[7, *[max(7, c) for c in cuts.tolist()]])
+
+
 # ---- route -----------------------------------------------------------------
 # experts, groups: with more than eight slots no lane layout of a warp holds them
 UNEVEN = [(n, g) for n, g in [(960, 3), (960, 5), (960, 6), (960, 10), (960, 12), (720, 5), (720, 9), (720, 10),
