@@ -202,6 +202,40 @@ def test_a_bias_closes_the_choice_not_the_score():
         assert (w == 0).all() and not (ids == 9).any()
 
 
+CLOSE = [(1024, 8, 1, 1, "softmax", 0.0, 3e-4), (512, 6, 8, 3, "softmax", 0.0, 1e-3), (256, 8, 8, 4, "sigmoid", -8.0, 1e-3),
+         (300, 10, 1, 1, "sigmoid", -9.0, 1e-4), (192, 5, 1, 1, "sigmoid", 12.0, 1e-5)]
+
+
+@pytest.mark.parametrize("T", [40, 2500])
+@pytest.mark.parametrize("E,k,G,tg,scores,shift,spread_of_bias", CLOSE)
+def test_choices_of_scores_that_nearly_meet(E, k, G, tg, scores, shift, spread_of_bias, T):
+    """Small or saturated scores, whose order turns on a few units of 2^-22: the
+    choice is within the 32-bit scores' error (2^-20 of the greatest, at most 1)
+    of the best, and the weights are those of the experts chosen."""
+    x = randn((T, E), E + k, F32, 1.0) + shift
+    b = randn((E,), k, F32, spread_of_bias)
+    ids, w = moe.route(x, k, scores=scores, bias=b, groups=G, top_groups=tg, group_rule="top2", renorm=False)
+    at = ids.long()
+    assert (at >= 0).all() and (at.sort(dim=1).values.diff(dim=1) > 0).all()
+    s = torch.softmax(x.double(), dim=1) if scores == "softmax" else torch.sigmoid(x.double())
+    assert torch.allclose(w.double(), s.gather(1, at), rtol=U * (64 + 4 * spread(host(x))), atol=0)
+    v = s + b.double()
+    err = 2.0 ** -20
+    if G > 1:
+        two = v.view(T, G, -1).topk(2, dim=2).values.sum(2)
+        used = torch.zeros_like(two, dtype=torch.bool).scatter_(1, at // (E // G), True)
+        assert (used.sum(1) <= tg).all()
+        least = two.topk(tg, dim=1).values[:, -1:]                        # no group used that is clearly worse
+        assert (two >= least - 2 * err)[used].all()
+        sure = (least[:, 0] - two.topk(tg + 1, dim=1).values[:, -1]) > 2 * err
+        keep = torch.zeros_like(two, dtype=torch.bool).scatter_(1, two.topk(tg, dim=1).indices, True)
+        v = v.view(T, G, -1).masked_fill(~keep[:, :, None], -np.inf).view(T, E)[sure]
+        at = at[sure]
+        assert len(at) > 0
+    got = v.gather(1, at)
+    assert (got - v.topk(k, dim=1).values).abs().max() <= err             # slot by slot
+
+
 DEEP = [(7, 20, 4, 1, 1), (2600, 64, 4, 1, 1), (2600, 32, 6, 4, 2), (9, 300, 5, 1, 1), (11, 48, 12, 1, 1), (9, 48, 12, 4, 2)]
 
 
