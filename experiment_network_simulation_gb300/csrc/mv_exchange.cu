@@ -73,9 +73,11 @@ __device__ __forceinline__ void count_slots(const ExchangeArgs &a, const int32_t
 
 // Many sources: a warp takes a run of items, one source's tokens at a time,
 // and counts in shared memory of its own: no warp waits for another.  64
-// batches of 512 sources x 128 tokens x 8 slots to 512 ranks: 51 us, 3.9 TB/s,
-// bound by the shared-memory atomics of popular experts (a block a source with
-// two atomics a slot took 128 us).
+// batches of 512 sources x 128 tokens x 8 slots to 512 ranks: 52 us, 3.9 TB/s.
+// A block a source with two shared-memory atomics a slot took 128 us, so they
+// are held to be the bound; no counter shows it.  With ONCE, two atomics and a
+// match a slot: 277 us.  A long source is one warp's, however many short ones
+// there are.
 template <bool ONCE> __global__ void __launch_bounds__(kExchangeWarps * 32) k_exchange(const ExchangeArgs a)
 {
     extern __shared__ int32_t shared[];
@@ -214,9 +216,13 @@ extern "C" int mv_exchange(const mv_exchange_desc *d, void *stream)
     a.splits = 1;
     a.count_blocks = 0;
     if (pairs < 8ull * sms) {
-        // sources of more than 2048 tokens are cut until every SM has two blocks
+        // Sources of more than 2048 tokens are cut until every SM has two blocks:
+        // 16 of 16384 tokens x 8 take 25 us on the device (whole: 138), of 4096 25 (40).
+        // Those of 2048 stay whole, at 23 (parts of 512 tokens: 13).
         const u64 want = (2ull * sms + pairs - 1) / pairs, can = (mean + 2047) / 2048;
         if (can > 1 && want > 1) a.splits = (u32)(want < can ? want : can);
+        // One set of 64 sources: up to 16384 slots 3 to 4 us by counting blocks (6.3
+        // with the load cleared and added up by the items), 32768 6.2 (7.1), 65536 9.9 (8.4).
         if (d->tokens * d->topk <= 32768) a.count_blocks = (u32)d->batches;
     }
     a.items = pairs * a.splits;

@@ -7,18 +7,22 @@
 // chain of four kernels (group; W1 and W3 with silu; W2; combine), each
 // starting as the one before it ends.  With at most 24 columns of activations
 // the matrix instruction that takes its operands from registers fits: weights
-// are widened in registers and never written back, and the tensor pipe is a
-// quarter busy.  Widening is the work: about 65 instructions for 32 x 32
-// weights, of the 89 issue slots that memory speed would leave.
+// are widened in registers and never written back, and the tensor pipe is 17 to
+// 46% busy.  Widening is most of the work: about 64 instructions for 32 x 32
+// weights of W1/W3 (92 of W2, whose activations are in two parts), of the 89
+// issue slots that memory speed would leave.  The issue slots are half used:
+// what is left is latency at 16 warps an SM.
 //
-// 64 tokens on 32 of 256 such experts (633 MB): 136 us, 4.7 TB/s, W1/W3 at 5.1;
-// one token (182 MB): 53 us, of which W1/W3 29 (256 blocks for 152 SMs), W2 19,
-// grouping and combining 7; 200 tokens over 60 experts of 2048 x 1408 (277 MB,
-// three tiles of activations): 143 us, bound by issue and latency at 16 warps
-// an SM.  Steps on the way, us for those three: a dot product a row and pair
-// 1801, 280, 6486; matrix instructions 212, 99, 177; scales copied ahead of
-// their use 198, 84, 162; activations as half and constants as arguments 166,
-// 66, 182; kernels started early 153, 58, 154.
+// 64 tokens on 32 of 256 such experts (633 MB): 150 us, 4.2 TB/s, W1/W3 at 5.0,
+// W2 3.5; one token (182 MB): 54 us, of which W1/W3 30 (256 blocks for 152 SMs),
+// W2 21, grouping and combining 7 (the kernels overlap); 7 tokens over 33 experts
+// of 2880 x 1440 with scales every 32 columns: 59 us; 200 tokens over 60
+// experts of 2048 x 1408 (277 MB, three tiles of activations): 156 us.  Steps on
+// the way, us for 64, 1 and 200 tokens: a dot product a row and pair 1801, 280,
+// 6486; matrix instructions 212, 99, 177; scales copied ahead of their use 198,
+// 84, 162; activations as half and constants as arguments 166, 66, 182; kernels
+// started early 153, 58, 154; steps without checks 136 to 143, 53, 139; inner
+// activations in two parts, not rounded to the type, 150, 54, 156.
 #include <cmath>
 #include <cstring>
 #include <type_traits>
@@ -64,6 +68,8 @@ struct ExpertArgs {
 };
 
 // ---- packed weights against 16-bit activations ---------------------------
+// Widening by mask and subtraction (Kim, Henry, Fahim and Hassan Awadalla, "Who
+// Says Elephants Can't Run", 2022).
 // A 32-bit word holds the 4-bit numbers of columns 0..7.  Masking nibbles i
 // and i + 4 into the halves of a word that holds a power of two makes that
 // power plus q in both halves, exactly; one subtraction leaves q - 8.  The

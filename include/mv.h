@@ -455,7 +455,8 @@ int mv_exchange(const mv_exchange_desc *desc, void *stream);
  * column in the low half.  w13 holds W1's `inner` rows, then W3's.  x, y and
  * the scales are of type `dtype` (MV_F16 or MV_BF16); sums are held in 32
  * bits and the inner activations silu(W1 x) * (W3 x) to 2^-18 of their value,
- * at any magnitude of 32 bits; only y is rounded to `dtype`.  A token's result
+ * at any magnitude of 32 bits; bfloat16 x counts to 2^-39 of its row's greatest
+ * magnitude; only y is rounded to `dtype`.  A token's result
  * does not depend on the other tokens.  Meant for up to some tens of tokens an
  * expert.  hidden and inner are multiples of group, x's rows are row_stride
  * elements apart (a multiple of 8), arrays of `dtype` and bytes are 16-byte

@@ -143,8 +143,8 @@ def test_exchange_of_many_uneven_sources(once):
 
 # ---- route -----------------------------------------------------------------
 # experts, groups: with more than eight slots no lane layout of a warp holds them
-UNEVEN = [(n, g) for n, g in [(960, 3), (960, 5), (960, 6), (960, 10), (960, 12), (720, 5), (720, 9), (720, 10),
-                              (720, 18), (720, 20), (561, 17), (1020, 17), (1023, 3), (1023, 31), (1023, 11)]]
+UNEVEN = [(960, 3), (960, 5), (960, 6), (960, 10), (960, 12), (720, 5), (720, 9), (720, 10), (720, 18), (720, 20),
+          (561, 17), (1020, 17), (1023, 3), (1023, 31), (1023, 11)]
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
@@ -154,8 +154,8 @@ def test_route_many_slots_of_uneven_groups(E, G, dtype):
     x[3, ::3] = -np.inf
     x[4] = 0.5
     b = randn((E,), G, F32, 0.1)
-    for n, (scores, bias, rule, renorm) in enumerate([("softmax", None, "max", True), ("softmax", b, "max", False),
-                                                      ("sigmoid", b, "top2", True), ("sigmoid", None, "top2", False)]):
+    for scores, bias, rule, renorm in [("softmax", None, "max", True), ("softmax", b, "max", False),
+                                       ("sigmoid", b, "top2", True), ("sigmoid", None, "top2", False)]:
         for tg, k in ((G, 9), (max(2, G // 2), 32)):
             k = min(k, tg * (E // G))
             kw = dict(scores=scores, groups=G, top_groups=tg, group_rule=rule, renorm=renorm)
