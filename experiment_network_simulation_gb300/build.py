@@ -1,7 +1,7 @@
 """Build the in-tree CUDA library ``libmv.so`` for sm_103a with nvcc.
 
 The translation units (simulator kernels and C-ABI host code, routed-expert
-operators) compile in parallel; the shared library lands next to this file so that it is loaded from the tree.
+and block operators) compile in parallel; the shared library lands next to this file so that it is loaded from the tree.
 """
 from __future__ import annotations
 
@@ -13,8 +13,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmv.so")
-SOURCES = ["mv_kernel.cu", "mv_api.cu", "mv_route.cu", "mv_exchange.cu", "mv_experts.cu"]
-HEADERS = ["mv_device.cuh", "mv_moe.cuh", os.path.join("..", "..", "include", "mv.h")]
+SOURCES = ["mv_kernel.cu", "mv_api.cu", "mv_route.cu", "mv_exchange.cu", "mv_experts.cu",
+           "mv_linear.cu", "mv_activation.cu"]
+HEADERS = ["mv_device.cuh", "mv_moe.cuh", "mv_block.cuh", os.path.join("..", "..", "include", "mv.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 

@@ -1,0 +1,55 @@
+// Shared by the block operators (mv_linear.cu, mv_activation.cu, mv_norm.cu).
+#pragma once
+
+#include "mv_moe.cuh"
+
+namespace mvblock {
+
+using namespace mvmoe;
+
+// 1 / (1 + exp(-v)) to some units of 2^-22 of its value; 0 under -88, where the exponential is infinite.
+__device__ __forceinline__ float logistic(float v) { return reciprocal_fast(1.0f + exp2_fast(-kLog2e * v)); }
+
+constexpr float kRootHalf = 0.70710678118654752f;
+constexpr float kTanhOuter = 1.5957691216057308f;       // 2 sqrt(2 / pi)
+constexpr float kTanhInner = 0.044715f;
+
+// Tanh's form of gelu is z logistic(2 v), v = sqrt(2 / pi) (z + 0.044715 z^3),
+// since (1 + tanh v) / 2 is the logistic function of 2 v: small values keep
+// their relative precision, which 1 + tanh v would lose.  erfc does the same
+// for gelu itself.  An infinite z counts as its limit.
+__device__ __forceinline__ float activation(u32 act, float z)
+{
+    switch (act) {
+    case MV_ACT_RELU: return z < 0.0f ? 0.0f : z;                      // a NaN stays one
+    case MV_ACT_GELU: return z == -INFINITY ? 0.0f : 0.5f * z * erfcf(-kRootHalf * z);
+    case MV_ACT_GELU_TANH: return z == -INFINITY ? 0.0f : z * logistic(kTanhOuter * fmaf(kTanhInner * z * z, z, z));
+    case MV_ACT_SILU: return z == -INFINITY ? 0.0f : z * logistic(z);
+    default: return z;
+    }
+}
+
+__device__ __forceinline__ float activation_slope(u32 act, float z)
+{
+    switch (act) {
+    case MV_ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
+    case MV_ACT_GELU: {
+        const float bell = 0.39894228040143268f * exp2_fast(-0.5f * kLog2e * z * z);
+        return 0.5f * erfcf(-kRootHalf * z) + (bell > 0.0f ? z * bell : 0.0f);
+    }
+    case MV_ACT_GELU_TANH: {
+        // q + z q (1 - q) dv/dz; q (1 - q) from |v|, where both factors are precise
+        const float zz = z * z, v = kTanhOuter * fmaf(kTanhInner * zz, z, z);
+        const float e = exp2_fast(-kLog2e * fabsf(v)), p = reciprocal_fast(1.0f + e);
+        const float both = e * p * p, dv = kTanhOuter * fmaf(3.0f * kTanhInner, zz, 1.0f);
+        return (v < 0.0f ? e * p : p) + (both > 0.0f ? z * both * dv : 0.0f);
+    }
+    case MV_ACT_SILU: {
+        const float e = exp2_fast(-kLog2e * fabsf(z)), p = reciprocal_fast(1.0f + e), both = e * p * p;
+        return (z < 0.0f ? e * p : p) + (both > 0.0f ? z * both : 0.0f);
+    }
+    default: return 1.0f;
+    }
+}
+
+}  // namespace mvblock

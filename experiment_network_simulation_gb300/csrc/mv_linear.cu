@@ -1,0 +1,991 @@
+// Matrix products with bias, activation and residual (mv_linear in
+// include/mv.h), and their gradients (mv_linear_backward).
+//
+// All of them are C[m, n] = sum over k of A[m, k] B[n, k]; only the side that
+// lies contiguous in memory differs:
+//   y  = x w^T     A = x,  B = w      both contiguous along k
+//   dx = dz w      A = dz,            B = w transposed: contiguous along n
+//   dw = dz^T x    A = dz transposed, B = x transposed: both along m or n
+// The tensor core takes either order from shared memory, so nothing is
+// transposed on the way.  Tiles of A and B come by TMA, the sums stay in TMEM
+// in 32 bits, and one warp each copies, multiplies and four finish tiles, the
+// next tile's products running while the last one is finished.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "mv_block.cuh"
+
+namespace mvblock {
+
+// ---- what becomes of a sum -------------------------------------------------
+struct Finish {
+    const void *bias, *residual;
+    void *y, *z;
+    u64 m, n;                       // rows and columns of the result
+    u64 y_stride, residual_stride;  // z is dense
+    u32 dtype, out, bias_type;      // of z; of y and the residual
+    u32 act, residual_wide, bias_wide, y_wide, z_wide;   // *_wide: four columns are one aligned access
+    float scale;
+};
+
+template <class T> __device__ __forceinline__ void load4(const void *p, u64 at, bool wide, u32 n, float (&v)[4])
+{
+    const T *from = static_cast<const T *>(p) + at;
+    if (wide && n == 4) {
+        T t[4];
+        if constexpr (sizeof(T) == 4) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(from);
+            memcpy(t, &w, 16);
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2 *>(from);
+            memcpy(t, &w, 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = to_float(t[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = i < (int)n ? to_float(from[i]) : 0.0f;
+    }
+}
+template <class T> __device__ __forceinline__ void store4(void *p, u64 at, bool wide, u32 n, const float (&v)[4])
+{
+    T *to = static_cast<T *>(p) + at;
+    T t[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) t[i] = from_float<T>(v[i]);
+    if (wide && n == 4) {
+        if constexpr (sizeof(T) == 4) {
+            uint4 w;
+            memcpy(&w, t, 16);
+            *reinterpret_cast<uint4 *>(to) = w;
+        } else {
+            uint2 w;
+            memcpy(&w, t, 8);
+            *reinterpret_cast<uint2 *>(to) = w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (i < (int)n) to[i] = t[i];
+    }
+}
+__device__ __forceinline__ void load4_as(u32 type, const void *p, u64 at, bool wide, u32 n, float (&v)[4])
+{
+    if (type == MV_BF16) load4<__nv_bfloat16>(p, at, wide, n, v);
+    else if (type == MV_F16) load4<__half>(p, at, wide, n, v);
+    else load4<float>(p, at, wide, n, v);
+}
+__device__ __forceinline__ void store4_as(u32 type, void *p, u64 at, bool wide, u32 n, const float (&v)[4])
+{
+    if (type == MV_BF16) store4<__nv_bfloat16>(p, at, wide, n, v);
+    else if (type == MV_F16) store4<__half>(p, at, wide, n, v);
+    else store4<float>(p, at, wide, n, v);
+}
+
+// Columns c .. c + 3 of row r (those inside the matrix), from their sums.
+__device__ __forceinline__ void finish4(const Finish &f, u64 r, u64 c, float (&v)[4])
+{
+    if (r >= f.m || c >= f.n) return;
+    const u32 n = f.n - c < 4 ? (u32)(f.n - c) : 4;
+    if (f.bias) {
+        float b[4];
+        load4_as(f.bias_type, f.bias, c, f.bias_wide, n, b);
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] += b[i];
+    }
+    if (f.z) store4_as(f.dtype, f.z, r * f.n + c, f.z_wide, n, v);
+    if (f.act != MV_ACT_NONE)
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = activation(f.act, v[i]);
+    if (f.residual) {
+        float b[4];
+        load4_as(f.out, f.residual, r * f.residual_stride + c, f.residual_wide, n, b);
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = fmaf(f.scale, v[i], b[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] *= f.scale;
+    }
+    store4_as(f.out, f.y, r * f.y_stride + c, f.y_wide, n, v);
+}
+
+// One column, where a warp's lanes hold neighbours of a row.
+__device__ __forceinline__ float value_as(u32 type, const void *p, u64 at)
+{
+    return type == MV_BF16 ? to_float(static_cast<const __nv_bfloat16 *>(p)[at])
+         : type == MV_F16 ? to_float(static_cast<const __half *>(p)[at]) : static_cast<const float *>(p)[at];
+}
+__device__ __forceinline__ void put_as(u32 type, void *p, u64 at, float v)
+{
+    if (type == MV_BF16) static_cast<__nv_bfloat16 *>(p)[at] = from_float<__nv_bfloat16>(v);
+    else if (type == MV_F16) static_cast<__half *>(p)[at] = from_float<__half>(v);
+    else static_cast<float *>(p)[at] = v;
+}
+__device__ __forceinline__ void finish1(const Finish &f, u64 r, u64 c, float v)
+{
+    if (f.bias) v += value_as(f.bias_type, f.bias, c);
+    if (f.z) put_as(f.dtype, f.z, r * f.n + c, v);
+    v = activation(f.act, v);
+    v = f.residual ? fmaf(f.scale, v, value_as(f.out, f.residual, r * f.residual_stride + c)) : f.scale * v;
+    put_as(f.out, f.y, r * f.y_stride + c, v);
+}
+
+// ---- PTX -------------------------------------------------------------------
+__device__ unsigned g_gave_up;          // blocks that ended a wait by its limit
+
+__device__ __forceinline__ u32 shared_at(const void *p) { return (u32)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ u64 nanoseconds()
+{
+    u64 t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ bool barrier_passed(u32 bar, u32 parity)
+{
+    u32 ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok;
+}
+// Waits for a phase, two seconds at most.
+__device__ __forceinline__ bool barrier_wait(u32 bar, u32 parity)
+{
+    if (barrier_passed(bar, parity)) return true;
+    const u64 end = nanoseconds() + 2000000000ull;
+    while (!barrier_passed(bar, parity))
+        if (nanoseconds() > end) return false;
+    return true;
+}
+__device__ __forceinline__ void barrier_init(u32 bar, u32 count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ u32 at_leader(u32 address)
+{
+    u32 there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(address));
+    return there;
+}
+__device__ __forceinline__ bool one_lane()
+{
+    u32 ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok;
+}
+template <int CTAS> __device__ __forceinline__ void copy_tile(u32 to, const CUtensorMap *map, int x, int y, u32 bar)
+{
+    if constexpr (CTAS == 2)
+        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%3, %4}], [%2];" ::"r"(to), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%3, %4}], [%2];" ::"r"(to), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+// A and B in shared memory, by descriptors; the sums in TMEM.
+template <int CTAS> __device__ __forceinline__ void multiply(u32 sums, u64 a, u64 b, u32 what, u32 add)
+{
+    if constexpr (CTAS == 2)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     ::"r"(sums), "l"(a), "l"(b), "r"(what), "r"(add) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     ::"r"(sums), "l"(a), "l"(b), "r"(what), "r"(add) : "memory");
+}
+// Arrives at the barrier, in every block of the pair, once all products issued so far are done.
+template <int CTAS> __device__ __forceinline__ void arrive_after_products(u32 bar)
+{
+    if constexpr (CTAS == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     ::"r"(bar), "h"((unsigned short)3) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void load_sums(u32 at, u32 (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void load_sums(u32 at, u32 (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+template <int CTAS> __device__ __forceinline__ void cluster_meet()
+{
+    if constexpr (CTAS == 2) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+}
+
+// ---- tiles -----------------------------------------------------------------
+// A block's share of a step of 64 columns of k: 128 rows of A and BN / CTAS
+// rows of B, 128 bytes each, in the 128-byte swizzle.  An operand that is
+// contiguous along k lies as rows of 64 k; one that is contiguous along its own
+// rows lies as pieces of 64 rows x 64 k, each k 128 bytes.
+constexpr u32 kStep = 64;
+constexpr u32 kWorkers = 4, kThreads = 64 + kWorkers * 32;     // a warp copies, one multiplies, four finish
+constexpr u32 kStaging = kWorkers * 32 * 128;
+
+template <int CTAS, int BN> struct Tile {
+    static constexpr u32 kRows = 128 * CTAS;
+    static constexpr u32 kA = 128 * 128, kBRows = BN / CTAS, kB = kBRows * 128, kStage = kA + kB;
+    // one block an SM where the tile is large; two where it is small
+    static constexpr u32 kRoom = (BN >= 128 ? 227 : 113) * 1024 - 2048 - kStaging;
+    static constexpr u32 kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
+    static constexpr u32 kColumns = BN < 32 ? 32 : BN;          // of TMEM, for one of two tiles
+    static constexpr u32 kSmem = 1024 + kStages * kStage + kStaging + 256;
+};
+
+struct Units {                      // what the blocks (or pairs) do, in order
+    u32 tiles_m, tiles_n;
+    u32 whole;                      // tiles done in one piece; of each one after them
+    u32 parts;                      // this many pieces along k
+    u32 total;                      // units in all
+    u32 steps;                      // steps of k of a tile
+    u32 half_steps;                 // steps after which A's second part begins (0: none)
+};
+
+struct Args {
+    Units u;
+    Finish f;
+    u32 what;                       // instruction descriptor
+    float *partial;                 // sums of tiles in pieces
+};
+
+// Tiles go in columns of eight along m, so that those under way share both operands in L2.
+__device__ __forceinline__ void tile_at(const Units &u, u32 i, u32 &m, u32 &n)
+{
+    const u32 band = 8 * u.tiles_n, b = i / band, rows = min(8u, u.tiles_m - 8 * b), j = i - b * band;
+    n = j / rows;
+    m = 8 * b + j - n * rows;
+}
+
+template <bool MN> __device__ __forceinline__ u64 operand(u32 at)
+{
+    // address / 16; distance of pieces / 16 (64 rows each) where the rows are contiguous; of eight
+    // lines / 16; version 1; 128-byte swizzle
+    const u64 pieces = MN ? 8192 / 16 : 1;
+    return (u64)(at >> 4 & 0x3FFF) | pieces << 16 | (u64)(1024 / 16) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// SWAP: A holds the result's columns and B its rows, for fewer rows than a tile of A has.
+template <int CTAS, int BN, bool A_MN, bool B_MN, bool SWAP>
+__global__ void __launch_bounds__(kThreads, 2)
+k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap a2_map,
+          const __grid_constant__ CUtensorMap b_map, const __grid_constant__ Args args)
+{
+    using S = Tile<CTAS, BN>;
+    extern __shared__ unsigned char raw[];
+    const u32 base = (shared_at(raw) + 1023) & ~1023u;
+    const u32 staging = base + S::kStages * S::kStage, bars = staging + kStaging;
+    const u32 full = bars, empty = full + 8 * S::kStages, done = empty + 8 * S::kStages, taken = done + 16,
+              drained = taken + 16, slot = drained + 8;
+    const u32 warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    u32 rank = 0;
+    if constexpr (CTAS == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const u32 worker = blockIdx.x / CTAS, workers = gridDim.x / CTAS;
+    const Units &u = args.u;
+
+    if (threadIdx.x == 0) {
+        for (u32 i = 0; i < S::kStages; i++) {
+            barrier_init(full + 8 * i, 1);
+            barrier_init(empty + 8 * i, 1);
+        }
+        for (u32 i = 0; i < 2; i++) {
+            barrier_init(done + 8 * i, 1);
+            barrier_init(taken + 8 * i, kWorkers * CTAS);
+        }
+        barrier_init(drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        if constexpr (CTAS == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(2 * S::kColumns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(2 * S::kColumns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_meet<CTAS>();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    u32 tmem;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    auto unit = [&](u32 i, u32 &m, u32 &n, u32 &first, u32 &last) {
+        u32 tile = i, part = 0, parts = 1;
+        if (i >= u.whole) {
+            tile = u.whole + (i - u.whole) / u.parts;
+            part = (i - u.whole) % u.parts;
+            parts = u.parts;
+        }
+        tile_at(u, tile, m, n);
+        first = (u32)((u64)u.steps * part / parts);
+        last = (u32)((u64)u.steps * (part + 1) / parts);
+    };
+
+    bool ok = true;
+    if (warp == 0) {
+        if (one_lane()) {                                         // copies
+            u32 s = 0, turn = 0;
+            u64 issued = 0;
+            for (u32 i = worker; i < u.total && ok; i += workers) {
+                u32 m, n, first, last;
+                unit(i, m, n, first, last);
+                const int row_a = (int)(m * S::kRows + rank * 128), row_b = (int)(n * BN + rank * S::kBRows);
+                for (u32 k = first; k < last; k++) {
+                    if (!barrier_wait(empty + 8 * s, turn ^ 1)) { ok = false; break; }
+                    const bool second = u.half_steps && k >= u.half_steps;
+                    const CUtensorMap *a = second ? &a2_map : &a_map;
+                    const int at = (int)((second ? k - u.half_steps : k) * kStep);
+                    const u32 to = base + s * S::kStage;
+                    u32 bar = full + 8 * s;
+                    if (rank == 0)
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(CTAS * S::kStage) : "memory");
+                    if constexpr (CTAS == 2) bar = at_leader(bar);
+                    if constexpr (A_MN) {
+                        copy_tile<CTAS>(to, a, row_a, at, bar);
+                        copy_tile<CTAS>(to + 8192, a, row_a + 64, at, bar);
+                    } else {
+                        copy_tile<CTAS>(to, a, at, row_a, bar);
+                    }
+                    if constexpr (B_MN) {
+#pragma unroll
+                        for (u32 j = 0; j < S::kBRows / 64; j++) copy_tile<CTAS>(to + S::kA + j * 8192, &b_map, row_b + 64 * j, at, bar);
+                    } else {
+                        copy_tile<CTAS>(to + S::kA, &b_map, at, row_b, bar);
+                    }
+                    issued++;
+                    if (++s == S::kStages) { s = 0; turn ^= 1; }
+                }
+            }
+            // After a wait that ran out: the copies under way end first, both blocks' (which
+            // the leader's barriers count), before the pair's blocks go on to their end.
+            if (!ok && rank == 0)
+                for (u32 j = 0; j < S::kStages && j < issued; j++) {
+                    s = s ? s - 1 : S::kStages - 1;
+                    if (s == S::kStages - 1) turn ^= 1;
+                    barrier_wait(full + 8 * s, turn);
+                }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && one_lane()) {                            // multiplies
+            u32 s = 0, turn = 0, buffer = 0, buffer_turn = 0;
+            for (u32 i = worker; i < u.total && ok; i += workers) {
+                u32 m, n, first, last;
+                unit(i, m, n, first, last);
+                ok = barrier_wait(taken + 8 * buffer, buffer_turn ^ 1);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const u32 sums = tmem + buffer * S::kColumns;
+                for (u32 k = first; k < last && ok; k++) {
+                    ok = barrier_wait(full + 8 * s, turn);
+                    if (!ok) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const u64 a = operand<A_MN>(base + s * S::kStage), b = operand<B_MN>(base + s * S::kStage + S::kA);
+#pragma unroll
+                    for (u32 j = 0; j < kStep / 16; j++)      // 16 k: 32 bytes along a line, or 16 lines
+                        multiply<CTAS>(sums, a + j * (A_MN ? 2048 / 16 : 32 / 16), b + j * (B_MN ? 2048 / 16 : 32 / 16),
+                                       args.what, k > first || j);
+                    arrive_after_products<CTAS>(empty + 8 * s);
+                    if (++s == S::kStages) { s = 0; turn ^= 1; }
+                }
+                if (ok) arrive_after_products<CTAS>(done + 8 * buffer);
+                buffer ^= 1;
+                if (buffer == 0) buffer_turn ^= 1;
+            }
+            if (!ok) {
+                arrive_after_products<CTAS>(drained);
+                barrier_wait(drained, 0);
+            }
+        }
+    } else {                                                      // finish
+        const u32 w = warp & 3;                                   // a warp reads its quarter of TMEM's lanes
+        const u32 mine = staging + w * 32 * 128;
+        u32 buffer = 0, buffer_turn = 0;
+        for (u32 i = worker; i < u.total; i += workers) {
+            u32 m, n, first, last;
+            unit(i, m, n, first, last);
+            ok = barrier_wait(done + 8 * buffer, buffer_turn);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const u32 sums = tmem + buffer * S::kColumns + (w << 21);
+            float *part = i < u.whole ? nullptr
+                        : args.partial + (u64)(i - u.whole) * (S::kRows * BN) + rank * 128 * BN;
+            const u64 row0 = (u64)m * S::kRows + rank * 128 + w * 32, col0 = (u64)n * BN;
+            if constexpr (SWAP) {
+                // lanes are columns of the result, TMEM's columns its rows
+                const u64 column = row0 + lane;
+                constexpr int kAtOnce = BN < 32 ? BN : 32;
+                for (u32 c = 0; c < BN && col0 + c < args.f.m; c += kAtOnce) {
+                    u32 v[kAtOnce];
+                    load_sums(sums + c, v);
+#pragma unroll
+                    for (int j = 0; j < kAtOnce; j++) {
+                        if (part) part[(c + j) * 128 + w * 32 + lane] = __uint_as_float(v[j]);
+                        else if (col0 + c + j < args.f.m && column < args.f.n) finish1(args.f, col0 + c + j, column, __uint_as_float(v[j]));
+                    }
+                }
+            } else {
+                for (u32 c = 0; c < BN && col0 + c < args.f.n; c += 32) {
+                    u32 v[32];
+                    load_sums(sums + c, v);
+                    if (part) {                                   // [columns / 4][rows][4]
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            *reinterpret_cast<uint4 *>(part + ((c / 4 + j) * 128 + w * 32 + lane) * 4) =
+                                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        continue;
+                    }
+                    // A lane holds a row: through shared memory, so that eight lanes share
+                    // one and its accesses are whole sectors.
+                    __syncwarp();
+#pragma unroll
+                    for (u32 j = 0; j < 8; j++)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 128 + ((j ^ (lane & 7)) * 16)),
+                                     "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3]) : "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (u32 j = 0; j < 8; j++) {
+                        const u32 r = j * 4 + (lane >> 3);
+                        float t[4];
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(t[0]), "=f"(t[1]), "=f"(t[2]), "=f"(t[3])
+                                     : "r"(mine + r * 128 + (((lane & 7) ^ (r & 7)) * 16)));
+                        finish4(args.f, row0 + r, col0 + c + (lane & 7) * 4, t);
+                    }
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CTAS == 2)
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_leader(taken + 8 * buffer)) : "memory");
+                else
+                    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(taken + 8 * buffer) : "memory");
+            }
+            buffer ^= 1;
+            if (buffer == 0) buffer_turn ^= 1;
+        }
+    }
+    if (!ok) atomicAdd(&g_gave_up, 1u);
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_meet<CTAS>();
+    if (warp == 1) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if constexpr (CTAS == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * S::kColumns));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * S::kColumns));
+    }
+}
+
+// Tiles done in pieces along k: the pieces' sums are added in their order.
+template <int CTAS, int BN, bool SWAP> __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args args)
+{
+    using S = Tile<CTAS, BN>;
+    const Units &u = args.u;
+    // 32 x 32 of a tile a block; with SWAP eight of its BN rows
+    constexpr u32 kDown = SWAP ? BN / 8 : S::kRows / 32, kAcross = SWAP ? 1 : BN / 32;
+    const u32 tile = blockIdx.x / (kDown * kAcross), here = blockIdx.x % (kDown * kAcross), t = threadIdx.x;
+    u32 m, n;
+    tile_at(u, u.whole + tile, m, n);
+    u64 row, column, at;
+    if constexpr (SWAP) {
+        const u32 r = here * 8 + (t >> 5), c = (t & 31) * 4;
+        row = (u64)n * BN + r;
+        column = (u64)m * 128 + c;
+        at = r * 128 + c;
+    } else {
+        const u32 r = (here / kAcross) * 32 + (t >> 3), c = (here % kAcross) * 32 + (t & 7) * 4;
+        row = (u64)m * S::kRows + r;
+        column = (u64)n * BN + c;
+        at = (r / 128) * (128 * BN) + ((c / 4) * 128 + (r & 127)) * 4;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (row >= args.f.m || column >= args.f.n) return;
+    constexpr u32 kPiece = S::kRows * BN;
+    const float *p = args.partial + (u64)tile * u.parts * kPiece + at;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (u32 i = 0; i < u.parts; i++) {
+        const float4 w = *reinterpret_cast<const float4 *>(p + (u64)i * kPiece);
+        v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
+    }
+    finish4(args.f, row, column, v);
+}
+
+// ---- operands as the copies want them ---------------------------------------
+// Rows that lie on no 16-byte boundary are copied to where they do, and 32-bit
+// values are split into two bfloat16, the nearest and the nearest to what that
+// leaves: within 2^-17 of the value together, at any magnitude.
+template <class T> __global__ void __launch_bounds__(256) k_pack(const T *from, u64 stride, u64 rows, u64 cols, T *to, u64 to_stride)
+{
+    const u64 n = rows * to_stride, step = (u64)gridDim.x * 256;
+    for (u64 i = (u64)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        const u64 r = i / to_stride, c = i - r * to_stride;
+        to[i] = c < cols ? from[r * stride + c] : T();
+    }
+}
+__global__ void __launch_bounds__(256) k_split(const float *from, u64 stride, u64 rows, u64 cols, __nv_bfloat16 *to, u64 to_stride, u64 second)
+{
+    const u64 n = rows * to_stride / 4, step = (u64)gridDim.x * 256, quads = to_stride / 4;
+    const bool wide = stride % 4 == 0 && (reinterpret_cast<uintptr_t>(from) & 15) == 0;
+    for (u64 i = (u64)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        const u64 r = i / quads, c = (i - r * quads) * 4;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rest[4];
+        if (c < cols) load4<float>(from, r * stride + c, wide, cols - c < 4 ? (u32)(cols - c) : 4, v);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            rest[j] = v[j] - __bfloat162float(__float2bfloat16_rn(v[j]));
+            if (!(fabsf(rest[j]) < INFINITY)) rest[j] = 0.0f;        // of infinities nothing is left
+        }
+        store4<__nv_bfloat16>(to, i * 4, true, 4, v);
+        store4<__nv_bfloat16>(to + second, i * 4, true, 4, rest);
+    }
+}
+
+// ---- columns' sums (dbias) --------------------------------------------------
+// A block adds a run of rows of 64 columns, eight rows at a time; the runs'
+// sums are added in their order by the second kernel.
+constexpr u32 kSumColumns = 64, kSumLanes = 8;
+template <class T> __global__ void __launch_bounds__(kSumColumns * kSumLanes)
+k_column_sums(const T *from, u64 stride, u64 rows, u64 cols, u64 run, float *sums)
+{
+    __shared__ float part[kSumLanes][kSumColumns];
+    const u32 x = threadIdx.x % kSumColumns, y = threadIdx.x / kSumColumns;
+    const u64 c = (u64)blockIdx.x * kSumColumns + x, first = blockIdx.y * run, last = min(first + run, rows);
+    float s = 0.0f;
+    if (c < cols)
+#pragma unroll 8
+        for (u64 r = first + y; r < last; r += kSumLanes) s += to_float(from[r * stride + c]);
+    part[y][x] = s;
+    __syncthreads();
+    if (y == 0 && c < cols) {
+        for (u32 i = 1; i < kSumLanes; i++) s += part[i][x];
+        sums[blockIdx.y * cols + c] = s;
+    }
+}
+template <class T> __global__ void __launch_bounds__(128) k_add_runs(const float *sums, u64 runs, u64 cols, T *to)
+{
+    const u64 c = (u64)blockIdx.x * 128 + threadIdx.x;
+    if (c >= cols) return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (u64 i = 0; i < runs; i++) s += sums[i * cols + c];
+    to[c] = from_float<T>(s);
+}
+
+// ---- host ------------------------------------------------------------------
+using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                            const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder()
+{
+    static Encode found = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess) p = nullptr;
+        return reinterpret_cast<Encode>(p);
+    }();
+    return found;
+}
+
+// One side of a product: `rows` by `k`, contiguous along k, or (mn) k by `rows`, contiguous along the rows.
+struct Side {
+    const void *p;
+    u64 rows, k, stride;
+    bool mn;
+};
+bool map_side(CUtensorMap *map, const Side &s, u32 dtype, u32 box_rows)
+{
+    const Encode encode = encoder();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {s.mn ? s.rows : s.k, s.mn ? s.k : s.rows}, strides[1] = {s.stride * 2};
+    const cuuint32_t box[2] = {kStep, s.mn ? kStep : box_rows}, each[2] = {1, 1};
+    return encode(map, dtype == MV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                  const_cast<void *>(s.p), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The kinds of tile: the result's rows and columns a tile, and what a step of
+// 64 k takes a block (cycles), from the measurements at plan().
+enum Kind { kPair256, kOne128, kOne64, kSwap64, kSwap16, kKinds };
+struct KindOf {
+    u32 rows, cols, blocks_an_sm_x2;    // rows and columns of A's and B's side
+    bool swap;
+    double step;
+};
+constexpr KindOf kKind[kKinds] = {{256, 256, 1, false, 530}, {128, 128, 2, false, 440}, {128, 64, 4, false, 660},
+                                  {128, 64, 4, true, 660}, {128, 16, 4, true, 500}};
+
+struct Plan {
+    Kind kind;
+    Units u;
+    u64 blocks, partial;                // blocks; bytes of pieces' sums
+};
+
+Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 sms, double &best)
+{
+    const KindOf &k = kKind[kind];
+    const u64 slots = std::max<u64>(1, (u64)sms * k.blocks_an_sm_x2 / 2), a = k.swap ? n : m, b = k.swap ? m : n;
+    const u64 tm = (a + k.rows - 1) / k.rows, tn = (b + k.cols - 1) / k.cols, tiles = tm * tn;
+    const u64 piece = (u64)k.rows * k.cols * 4;
+    Plan p = {};
+    best = INFINITY;
+    // whole tiles in rounds of all slots, and what is left in as many pieces as fill one to four more
+    const u64 whole = tiles / slots * slots, left = tiles - whole;
+    for (u64 round = 0; round <= (left ? 4 : 0); round++) {
+        const u64 parts = round ? std::min<u64>(steps, round * slots / left) : 1;
+        const double rounds = (double)((left * parts + slots - 1) / slots);
+        double cost = (double)(whole / slots) * steps * k.step + rounds * ((double)((steps + parts - 1) / parts) * k.step + 400) + 2000;
+        if (parts > 1) cost += 3000 + 1.0 * parts * left * piece / (sms * 24.0);
+        if (cost >= best) continue;
+        best = cost;
+        p.kind = kind;
+        p.u = {(u32)tm, (u32)tn, (u32)(parts == 1 ? tiles : whole), (u32)parts, (u32)(parts == 1 ? tiles : whole + left * parts),
+               (u32)steps, 0};
+        p.blocks = std::min<u64>(p.u.total, slots) * (kind == kPair256 ? 2 : 1);
+        p.partial = parts == 1 ? 0 : left * parts * piece;
+    }
+    return p;
+}
+
+Plan plan(u64 m, u64 n, u64 steps, bool swaps, u32 sms)
+{
+    Plan best = {};
+    double least = INFINITY;
+    for (int kind = 0; kind < kKinds; kind++) {
+        if (kKind[kind].swap && !swaps) continue;
+        double cost;
+        const Plan p = plan_kind((Kind)kind, m, n, steps, sms, cost);
+        if (cost < least) { least = cost; best = p; }
+    }
+    return best;
+}
+
+template <int CTAS, int BN, bool A_MN, bool B_MN, bool SWAP>
+int run_kind(const Side &a, const void *a2, const Side &b, u32 dtype, const Plan &p, Args &args, cudaStream_t stream)
+{
+    using S = Tile<CTAS, BN>;
+    const auto kernel = k_product<CTAS, BN, A_MN, B_MN, SWAP>;
+    CUtensorMap maps[3];
+    Side second = a;
+    second.p = a2 ? a2 : a.p;
+    if (!map_side(&maps[0], a, dtype, 128) || !map_side(&maps[1], second, dtype, 128) ||
+        !map_side(&maps[2], b, dtype, S::kBRows))
+        return MV_ECUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess) return MV_ECUDA;
+    // type of the sums: 32 bits; of both operands; which side is contiguous; the tile
+    args.what = 1u << 4 | (dtype == MV_BF16 ? 1u << 7 | 1u << 10 : 0u) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
+                (u32)(BN >> 3) << 17 | (u32)(128 * CTAS >> 4) << 24;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((u32)p.blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {CTAS, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = CTAS == 2 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], args) != cudaSuccess) return MV_ECUDA;
+    if (p.u.parts == 1) return MV_OK;
+    const u32 left = (p.u.total - p.u.whole) / p.u.parts;
+    const u32 blocks = left * (SWAP ? BN / 8 : S::kRows / 32 * (BN / 32));
+    return launch_after(k_join<CTAS, BN, SWAP>, dim3(blocks), 256, 0, stream, args);
+}
+
+// C = A B^T into args.f; with a2, A is the sum of two.
+template <bool A_MN, bool B_MN>
+int product(const Side &a, const void *a2, const Side &b, u32 dtype, Plan p, const Finish &f, float *partial, cudaStream_t stream)
+{
+    Args args = {};
+    args.u = p.u;
+    args.f = f;
+    args.partial = partial;
+    args.u.half_steps = a2 ? p.u.steps / 2 : 0;
+    switch (p.kind) {
+    case kPair256: return run_kind<2, 256, A_MN, B_MN, false>(a, a2, b, dtype, p, args, stream);
+    case kOne128: return run_kind<1, 128, A_MN, B_MN, false>(a, a2, b, dtype, p, args, stream);
+    case kOne64: return run_kind<1, 64, A_MN, B_MN, false>(a, a2, b, dtype, p, args, stream);
+    default: break;
+    }
+    if constexpr (!A_MN && !B_MN) {     // the forward product alone: A and B change places
+        if (p.kind == kSwap64) return run_kind<1, 64, false, false, true>(b, nullptr, a, dtype, p, args, stream);
+        if (p.kind == kSwap16) return run_kind<1, 16, false, false, true>(b, nullptr, a, dtype, p, args, stream);
+    }
+    return MV_EINVAL;
+}
+
+u64 up(u64 v, u64 to) { return (v + to - 1) / to * to; }
+u64 steps_of(u64 k) { return (k + kStep - 1) / kStep; }
+bool copies(const void *p, u64 stride) { return aligned(p, 16) && stride % 8 == 0; }
+bool wide(const void *p, u64 stride, u32 dtype) { return aligned(p, 4 * dtype_size(dtype)) && stride % 4 == 0; }
+constexpr u64 kMostRows = 1ull << 30, kMostTiles = 1ull << 31;
+
+int pack(const void *from, u64 stride, u64 rows, u64 cols, void *to, cudaStream_t stream)
+{
+    const u64 n = rows * up(cols, 8);
+    const u32 blocks = (u32)std::min<u64>((n + 1023) / 1024, 1u << 16);
+    return launch(k_pack<unsigned short>, dim3(blocks), 256, 0, stream, static_cast<const unsigned short *>(from), stride, rows, cols,
+                  static_cast<unsigned short *>(to), up(cols, 8));
+}
+
+struct LinearLayout {
+    u64 x, w, partial, total;
+    Plan plan;
+};
+struct GradLayout {
+    u64 x, w, dz, runs, partial, total;
+    u64 run;                            // rows of dz a block of the columns' sums adds
+    Plan dx, dw;
+};
+
+u32 planned_sms() { const u32 n = sm_count(); return n ? n : 152; }
+
+int check(const mv_linear_desc *d)
+{
+    if (!d || !d->cols || !d->rows || (d->dtype != MV_F16 && d->dtype != MV_BF16) ||
+        (d->out_dtype != d->dtype && d->out_dtype != MV_F32) || (d->bias_dtype != d->dtype && d->bias_dtype != MV_F32) ||
+        d->act > MV_ACT_SILU || !std::isfinite(d->scale) || d->x_stride < d->cols || d->w_stride < d->cols ||
+        (d->residual && d->residual_stride < d->rows))
+        return MV_EINVAL;
+    if (d->tokens > kMostRows || d->cols > kMostRows || d->rows > kMostRows || d->x_stride > 1ull << 36 ||
+        d->w_stride > 1ull << 36 || d->residual_stride > 1ull << 36 || (d->tokens / 128 + 1) * (d->rows / 16 + 1) > kMostTiles)
+        return MV_EOVERFLOW;
+    return MV_OK;
+}
+LinearLayout layout(const mv_linear_desc *d)
+{
+    LinearLayout l = {};
+    u64 at = 0;
+    auto take = [&](u64 bytes) { const u64 here = at; at += up(bytes, 256); return here; };
+    l.plan = plan(d->tokens, d->rows, steps_of(d->cols), d->tokens <= 256, planned_sms());
+    l.x = take(copies(d->x, d->x_stride) ? 0 : d->tokens * up(d->cols, 8) * 2);
+    l.w = take(copies(d->w, d->w_stride) ? 0 : d->rows * up(d->cols, 8) * 2);
+    l.partial = take(l.plan.partial);
+    l.total = at;
+    return l;
+}
+
+int check(const mv_linear_grad_desc *d)
+{
+    if (!d || !d->cols || !d->rows || (d->dtype != MV_F16 && d->dtype != MV_BF16) ||
+        (d->dz_dtype != d->dtype && !(d->dz_dtype == MV_F32 && d->dtype == MV_BF16)) || d->x_stride < d->cols ||
+        d->w_stride < d->cols || d->dz_stride < d->rows)
+        return MV_EINVAL;
+    if (d->tokens > kMostRows || d->cols > kMostRows || d->rows > kMostRows || d->x_stride > 1ull << 36 ||
+        d->w_stride > 1ull << 36 || d->dz_stride > 1ull << 36 || (d->tokens / 128 + 1) * (d->cols / 64 + 1) > kMostTiles ||
+        (d->rows / 128 + 1) * (d->cols / 64 + 1) > kMostTiles)
+        return MV_EOVERFLOW;
+    return MV_OK;
+}
+GradLayout layout(const mv_linear_grad_desc *d)
+{
+    GradLayout l = {};
+    u64 at = 0;
+    auto take = [&](u64 bytes) { const u64 here = at; at += up(bytes, 256); return here; };
+    const u64 parts = d->dz_dtype == MV_F32 ? 2 : 1, sms = planned_sms();
+    if (d->dx) l.dx = plan(d->tokens, d->cols, parts * steps_of(d->rows), false, (u32)sms);
+    if (d->dw) l.dw = plan(d->rows, d->cols, parts * steps_of(d->tokens), false, (u32)sms);
+    l.x = take(!d->dw || copies(d->x, d->x_stride) ? 0 : d->tokens * up(d->cols, 8) * 2);
+    l.w = take(!d->dx || copies(d->w, d->w_stride) ? 0 : d->rows * up(d->cols, 8) * 2);
+    l.dz = take(parts == 1 && copies(d->dz, d->dz_stride) ? 0 : parts * d->tokens * up(d->rows, 8) * 2);
+    // runs long enough to be worth adding, enough of them for all SMs
+    const u64 across = (d->rows + kSumColumns - 1) / kSumColumns;
+    u64 runs = std::max<u64>(1, 8 * sms / across);
+    l.run = std::max<u64>(128, up((d->tokens + runs - 1) / runs, kSumLanes));
+    runs = (d->tokens + l.run - 1) / l.run;
+    l.runs = take(d->dbias ? runs * d->rows * 4 : 0);
+    l.partial = take(std::max(l.dx.partial, l.dw.partial));
+    l.total = at;
+    return l;
+}
+
+}  // namespace mvblock
+
+using namespace mvblock;
+
+extern "C" int mv_linear_workspace_bytes(const mv_linear_desc *d, uint64_t *bytes)
+{
+    if (!bytes) return MV_EINVAL;
+    *bytes = 0;
+    const int rc = check(d);
+    if (rc != MV_OK || d->tokens == 0) return rc;
+    *bytes = layout(d).total;
+    return MV_OK;
+}
+
+extern "C" int mv_linear(const mv_linear_desc *d, void *workspace, uint64_t ws_bytes, void *stream)
+{
+    int rc = check(d);
+    if (rc != MV_OK || d->tokens == 0) return rc;
+    if (!d->x || !d->w || !d->y || !aligned(d->x, 2) || !aligned(d->w, 2) || !aligned(d->y, dtype_size(d->out_dtype)) ||
+        !aligned(d->z, 2) || !aligned(d->bias, dtype_size(d->bias_dtype)) || !aligned(d->residual, dtype_size(d->out_dtype)) ||
+        !aligned(workspace, 256))
+        return MV_EINVAL;
+    const LinearLayout l = layout(d);
+    if (l.total && !workspace) return MV_EINVAL;
+    if (ws_bytes < l.total) return MV_ENOMEM;
+    if (!sm_count()) return MV_ECUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    Side x = {d->x, d->tokens, d->cols, d->x_stride, false}, w = {d->w, d->rows, d->cols, d->w_stride, false};
+    if (!copies(d->x, d->x_stride)) {
+        rc = pack(d->x, d->x_stride, d->tokens, d->cols, ws + l.x, s);
+        x.p = ws + l.x;
+        x.stride = up(d->cols, 8);
+    }
+    if (rc == MV_OK && !copies(d->w, d->w_stride)) {
+        rc = pack(d->w, d->w_stride, d->rows, d->cols, ws + l.w, s);
+        w.p = ws + l.w;
+        w.stride = up(d->cols, 8);
+    }
+    if (rc != MV_OK) return rc;
+    Finish f = {};
+    f.bias = d->bias;
+    f.residual = d->residual;
+    f.y = d->y;
+    f.z = d->z;
+    f.m = d->tokens;
+    f.n = d->rows;
+    f.y_stride = d->rows;
+    f.residual_stride = d->residual_stride;
+    f.dtype = d->dtype;
+    f.out = d->out_dtype;
+    f.bias_type = d->bias_dtype;
+    f.act = d->act;
+    f.scale = d->scale;
+    f.residual_wide = wide(d->residual, d->residual_stride, d->out_dtype);
+    f.bias_wide = wide(d->bias, 0, d->bias_dtype);
+    f.y_wide = wide(d->y, d->rows, d->out_dtype);
+    f.z_wide = wide(d->z, d->rows, d->dtype);
+    return product<false, false>(x, nullptr, w, d->dtype, l.plan, f, reinterpret_cast<float *>(ws + l.partial), s);
+}
+
+extern "C" int mv_linear_backward_workspace_bytes(const mv_linear_grad_desc *d, uint64_t *bytes)
+{
+    if (!bytes) return MV_EINVAL;
+    *bytes = 0;
+    const int rc = check(d);
+    if (rc != MV_OK || d->tokens == 0) return rc;
+    *bytes = layout(d).total;
+    return MV_OK;
+}
+
+extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace, uint64_t ws_bytes, void *stream)
+{
+    int rc = check(d);
+    if (rc != MV_OK) return rc;
+    if ((d->tokens && (!d->dz || (d->dw && !d->x) || (d->dx && !d->w))) || !aligned(d->dz, dtype_size(d->dz_dtype)) ||
+        !aligned(d->x, 2) || !aligned(d->w, 2) || !aligned(d->dx, 2) || !aligned(d->dw, 2) || !aligned(d->dbias, 2) ||
+        !aligned(workspace, 256))
+        return MV_EINVAL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (d->tokens == 0) {               // sums of nothing
+        if (d->dw && cudaMemsetAsync(d->dw, 0, d->rows * d->cols * 2, s) != cudaSuccess) return MV_ECUDA;
+        if (d->dbias && cudaMemsetAsync(d->dbias, 0, d->rows * 2, s) != cudaSuccess) return MV_ECUDA;
+        return MV_OK;
+    }
+    const GradLayout l = layout(d);
+    if (l.total && !workspace) return MV_EINVAL;
+    if (ws_bytes < l.total) return MV_ENOMEM;
+    if (!sm_count()) return MV_ECUDA;
+    char *ws = static_cast<char *>(workspace);
+    const void *dz = d->dz, *dz2 = nullptr, *x = d->x, *w = d->w;
+    u64 dz_stride = d->dz_stride, x_stride = d->x_stride, w_stride = d->w_stride;
+    const u64 padded = up(d->rows, 8);
+    if ((d->dx || d->dw) && d->dz_dtype == MV_F32) {
+        const u64 n = d->tokens * padded;
+        const u32 blocks = (u32)std::min<u64>((n / 4 + 255) / 256, 1u << 16);
+        rc = launch(k_split, dim3(blocks), 256, 0, s, static_cast<const float *>(d->dz), d->dz_stride, d->tokens, d->rows,
+                    reinterpret_cast<__nv_bfloat16 *>(ws + l.dz), padded, n);
+        dz = ws + l.dz;
+        dz2 = ws + l.dz + n * 2;
+        dz_stride = padded;
+    } else if ((d->dx || d->dw) && !copies(d->dz, d->dz_stride)) {
+        rc = pack(d->dz, d->dz_stride, d->tokens, d->rows, ws + l.dz, s);
+        dz = ws + l.dz;
+        dz_stride = padded;
+    }
+    if (rc == MV_OK && d->dw && !copies(d->x, d->x_stride)) {
+        rc = pack(d->x, d->x_stride, d->tokens, d->cols, ws + l.x, s);
+        x = ws + l.x;
+        x_stride = up(d->cols, 8);
+    }
+    if (rc == MV_OK && d->dx && !copies(d->w, d->w_stride)) {
+        rc = pack(d->w, d->w_stride, d->rows, d->cols, ws + l.w, s);
+        w = ws + l.w;
+        w_stride = up(d->cols, 8);
+    }
+    Finish f = {};
+    f.n = d->cols;
+    f.y_stride = d->cols;
+    f.dtype = f.out = f.bias_type = d->dtype;
+    f.act = MV_ACT_NONE;
+    f.scale = 1.0f;
+    float *partial = reinterpret_cast<float *>(ws + l.partial);
+    if (rc == MV_OK && d->dx) {
+        f.m = d->tokens;
+        f.y = d->dx;
+        f.y_wide = wide(d->dx, d->cols, d->dtype);
+        rc = product<false, true>({dz, d->tokens, d->rows, dz_stride, false}, dz2, {w, d->cols, d->rows, w_stride, true}, d->dtype,
+                                  l.dx, f, partial, s);
+    }
+    if (rc == MV_OK && d->dw) {
+        f.m = d->rows;
+        f.y = d->dw;
+        f.y_wide = wide(d->dw, d->cols, d->dtype);
+        rc = product<true, true>({dz, d->rows, d->tokens, dz_stride, true}, dz2, {x, d->cols, d->tokens, x_stride, true}, d->dtype,
+                                 l.dw, f, partial, s);
+    }
+    if (rc == MV_OK && d->dbias) {
+        const u64 runs = (d->tokens + l.run - 1) / l.run;
+        float *sums = reinterpret_cast<float *>(ws + l.runs);
+        const dim3 grid((u32)((d->rows + kSumColumns - 1) / kSumColumns), (u32)runs);
+        const u32 threads = kSumColumns * kSumLanes, adders = (u32)((d->rows + 127) / 128);
+        if (d->dz_dtype == MV_F32)
+            rc = launch(k_column_sums<float>, grid, threads, 0, s, static_cast<const float *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, sums);
+        else if (d->dz_dtype == MV_F16)
+            rc = launch(k_column_sums<__half>, grid, threads, 0, s, static_cast<const __half *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, sums);
+        else
+            rc = launch(k_column_sums<__nv_bfloat16>, grid, threads, 0, s, static_cast<const __nv_bfloat16 *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, sums);
+        if (rc == MV_OK)
+            rc = d->dtype == MV_F16 ? launch(k_add_runs<__half>, dim3(adders), 128, 0, s, sums, runs, d->rows, static_cast<__half *>(d->dbias))
+                                    : launch(k_add_runs<__nv_bfloat16>, dim3(adders), 128, 0, s, sums, runs, d->rows, static_cast<__nv_bfloat16 *>(d->dbias));
+    }
+    return rc;
+}
+
+extern "C" int mv_block_status(uint32_t *gave_up)
+{
+    if (!gave_up) return MV_EINVAL;
+    return cudaMemcpyFromSymbol(gave_up, g_gave_up, sizeof *gave_up) == cudaSuccess ? MV_OK : MV_ECUDA;
+}

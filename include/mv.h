@@ -480,6 +480,103 @@ typedef struct mv_experts_desc {
 int mv_experts_workspace_bytes(const mv_experts_desc *desc, uint64_t *bytes);
 int mv_experts(const mv_experts_desc *desc, void *workspace, uint64_t ws_bytes, void *stream);
 
+/*
+ * ---- block operators --------------------------------------------------
+ *
+ * The dense side of a transformer block, before and after the routed experts
+ * and between the collectives of a training step: a matrix product with bias,
+ * activation and residual (mv_linear: the router's logits, a dense layer), its
+ * gradients (mv_linear_backward, mv_activation_backward), and the norms after
+ * one branch and before the next, with the branch's gate and the residual
+ * between them (mv_norm, mv_norm_backward).
+ *
+ * What holds for the routed-expert operators holds here: DEVICE pointers,
+ * row-major arrays whose columns are contiguous (rows may lie apart where a
+ * stride, in elements, is given; outputs are dense), enqueued on `stream`
+ * without waiting, nothing allocated or kept, same bits on every run, capture
+ * in a CUDA graph, the same errors.  Sums and statistics are held in 32 bits and every output
+ * is rounded once, from 32 bits.  The workspace (256-byte aligned; its contents do
+ * not matter; NULL where 0 bytes are needed) takes what the matching
+ * *_workspace_bytes says, which reads the sizes, the strides, and of the
+ * pointers only whether they are NULL and 16-byte aligned.  Two calls under way at once need two
+ * workspaces.
+ */
+#define MV_ACT_NONE 0
+#define MV_ACT_RELU 1        /* max(v, 0)                                     */
+#define MV_ACT_GELU 2        /* v (1 + erf(v / sqrt 2)) / 2                   */
+#define MV_ACT_GELU_TANH 3   /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+#define MV_ACT_SILU 4        /* v / (1 + exp(-v))                             */
+#define MV_NORM_RMS 0
+#define MV_NORM_LAYER 1
+#define MV_NORM_MAX_HIDDEN 16384
+
+/*
+ *   z = x w^T + bias,   y = residual + scale * act(z)
+ * x [tokens, cols] and w [rows, cols] are of type `dtype` (MV_F16 or MV_BF16),
+ * y and the residual [tokens, rows] of `out_dtype` (dtype or MV_F32), the bias
+ * [rows] of `bias_dtype` (dtype or MV_F32).  bias and residual may be NULL; z,
+ * where it is not NULL, gets the pre-activations in `dtype`; act sees them
+ * unrounded.  Rows of x and w that are not 16-byte aligned (an odd size, a
+ * stride that is no multiple of 8) are first copied into the workspace: right, but slower.
+ * cols is at least 1.  What a sum is made of depends on the sizes alone, but
+ * not on which row it is: equal rows of x give equal rows.
+ */
+typedef struct mv_linear_desc {
+    uint64_t tokens, cols, rows, x_stride, w_stride, residual_stride;
+    uint32_t dtype, out_dtype, bias_dtype, act;
+    float scale;
+    const void *x;                    /* [tokens, cols]                        */
+    const void *w;                    /* [rows, cols]                          */
+    const void *bias;                 /* [rows], or NULL                       */
+    const void *residual;             /* [tokens, rows], or NULL               */
+    void *y;                          /* out [tokens, rows]                    */
+    void *z;                          /* out [tokens, rows], or NULL           */
+} mv_linear_desc;
+int mv_linear_workspace_bytes(const mv_linear_desc *desc, uint64_t *bytes);
+int mv_linear(const mv_linear_desc *desc, void *workspace, uint64_t ws_bytes, void *stream);
+
+/*
+ * Gradients of z = x w^T + bias, given z's:
+ *   dx = dz w,   dw = dz^T x,   dbias[n] = sum over t of dz[t, n],
+ * each of type `dtype`, or not computed where its pointer is NULL.  dz is of
+ * type `dz_dtype`: dtype, or MV_F32 where dtype is MV_BF16 (it then counts to
+ * 2^-17 of each value in the products: two bfloat16).  No tokens: dw and dbias are zeros.
+ * x is read for dw, w for dx.
+ */
+typedef struct mv_linear_grad_desc {
+    uint64_t tokens, cols, rows, x_stride, w_stride, dz_stride;
+    uint32_t dtype, dz_dtype;
+    const void *dz;                   /* [tokens, rows]                        */
+    const void *x;                    /* [tokens, cols]                        */
+    const void *w;                    /* [rows, cols]                          */
+    void *dx;                         /* out [tokens, cols], or NULL           */
+    void *dw;                         /* out [rows, cols], or NULL             */
+    void *dbias;                      /* out [rows], or NULL                   */
+} mv_linear_grad_desc;
+int mv_linear_backward_workspace_bytes(const mv_linear_grad_desc *desc, uint64_t *bytes);
+int mv_linear_backward(const mv_linear_grad_desc *desc, void *workspace, uint64_t ws_bytes,
+                       void *stream);
+
+/*
+ * dz = scale * dy * act'(z), element by element: what mv_linear's y passes on
+ * to its z.  dy, z [tokens, cols] and dz of type `dtype`.  relu' is 0 at 0.
+ */
+typedef struct mv_act_grad_desc {
+    uint64_t tokens, cols, dy_stride, z_stride;
+    uint32_t dtype, act;
+    float scale;
+    const void *dy;                   /* [tokens, cols]                        */
+    const void *z;                    /* [tokens, cols]                        */
+    void *dz;                         /* out [tokens, cols]                    */
+} mv_act_grad_desc;
+int mv_activation_backward(const mv_act_grad_desc *desc, void *stream);
+
+/* How many times a wait within mv_linear's or mv_linear_backward's kernels has
+ * run into its limit (two seconds) since the library was loaded on the current
+ * device: their results are then incomplete.  0 unless the device is broken or
+ * stopped for that long.  Waits for the device. */
+int mv_block_status(uint32_t *gave_up);
+
 const char *mv_strerror(int code);
 
 #ifdef __cplusplus
