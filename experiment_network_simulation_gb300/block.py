@@ -19,7 +19,7 @@ arguments, :class:`.mv.MVError` for what the library refuses, no CPU fallback.
 from __future__ import annotations
 
 import ctypes as C
-import math
+from collections import namedtuple
 
 import torch
 
@@ -39,6 +39,15 @@ LinearGradDesc, _linear_grad_desc = _descriptor(
 ActGradDesc, _act_grad_desc = _descriptor(
     "ActGradDesc", "tokens:Q cols:Q dy_stride:Q z_stride:Q dtype:I act:I scale:f dy:P z:P dz:P")
 
+NormDesc, _norm_desc = _descriptor(
+    "NormDesc", "tokens:Q hidden:Q gates:Q y_stride:Q residual_stride:Q dtype:I param_dtype:I kind:I "
+    "alpha:f eps:f y:P residual:P weight:P bias:P post:P post_bias:P gate:P")
+NormGradDesc, _norm_grad_desc = _descriptor(
+    "NormGradDesc", "dn_stride:Q dr_stride:Q dn:P dr:P dy:P dresidual:P dweight:P dbias:P dpost:P dpost_bias:P dgate:P")
+
+KINDS = {"rms": 0, "layer": 1}
+MAX_HIDDEN = 16384
+NormGrads = namedtuple("NormGrads", "dy dresidual dweight dbias dpost dpost_bias dgate")
 _lib = None
 
 
@@ -51,6 +60,9 @@ def _library() -> C.CDLL:
             getattr(lib, f).argtypes = [_vp, _vp, _u64, _vp]
             getattr(lib, f + "_workspace_bytes").argtypes = [_vp, C.POINTER(_u64)]
         lib.mv_activation_backward.argtypes = [_vp, _vp]
+        lib.mv_norm.argtypes = [_vp, _vp, _vp, _vp]
+        lib.mv_norm_backward_workspace_bytes.argtypes = [_vp, _vp, C.POINTER(_u64)]
+        lib.mv_norm_backward.argtypes = [_vp, _vp, _vp, _u64, _vp]
         lib.mv_block_status.argtypes = [C.POINTER(C.c_uint32)]
         _lib = lib
     return _lib
@@ -186,6 +198,121 @@ def _activation_backward(dy, z, tokens, cols, act, scale, dev):
     if rc != mv.MV_OK:
         raise mv.MVError(rc, "mv_activation_backward")
     return dz
+
+
+def norm(y, weight, bias=None, *, residual=None, alpha: float = 1.0, post=None, post_bias=None,
+         gate=None, kind: str = "rms", eps: float = 1e-6, stream=None):
+    """The norms after a branch and before the next one: (n, r), [tokens, hidden] of ``y``'s type.
+
+        u = N(y) * post + post_bias       (y without post)
+        r = alpha * residual + gate * u   (without what is None)
+        n = N(r) * weight + bias
+
+    ``y`` [tokens, hidden] (float32, float16 or bfloat16) is what the branch
+    gave, ``residual`` the stream beside it (y's type; the rows of both may lie
+    apart).  N divides by the root mean square ("rms") or takes the mean off
+    first ("layer"); ``eps`` is added to the mean square.  The parameters
+    ``weight``, ``bias``, ``post``, ``post_bias`` [hidden] and ``gate`` are all
+    of y's type or all float32.  ``gate`` is [hidden], or [gates, hidden] where
+    gates divides tokens: each row for as many tokens in a row.  r is the new
+    stream; n is normed from r before its rounding.  Without residual, post and
+    gate there is no new stream, and r is ``y`` itself.
+    """
+    tokens, hidden, gates, k, params, dev = _norm_checks(y, weight, bias, residual, alpha, post, post_bias, gate, kind, eps)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream, (y, weight, bias, residual, post, post_bias, gate)):
+            return _norm(y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates, k, params, eps, dev)
+    return _norm(y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates, k, params, eps, dev)
+
+
+def _norm_checks(y, weight, bias, residual, alpha, post, post_bias, gate, kind, eps):
+    _tensor("y", y, _DTYPES, (None, None), rows_apart=True)
+    tokens, hidden = y.shape
+    dev = y.device
+    if not 1 <= hidden <= MAX_HIDDEN:
+        raise ValueError(f"hidden is 1 to {MAX_HIDDEN}, not {hidden}")
+    _tensor("weight", weight, (y.dtype, torch.float32), (hidden,), dev)
+    params = weight.dtype
+    if bias is not None:
+        _tensor("bias", bias, (params,), (hidden,), dev)
+    if residual is not None:
+        _tensor("residual", residual, (y.dtype,), (tokens, hidden), dev, rows_apart=True)
+    if post is not None:
+        _tensor("post", post, (params,), (hidden,), dev)
+    if post_bias is not None:
+        if post is None:
+            raise ValueError("post_bias needs post")
+        _tensor("post_bias", post_bias, (params,), (hidden,), dev)
+    gates = 1
+    if gate is not None:
+        if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+            _tensor("gate", gate, (params,), (hidden,), dev)
+        else:
+            _tensor("gate", gate, (params,), (None, hidden), dev)
+            gates = gate.shape[0]
+        if gates < 1 or tokens % gates:
+            raise ValueError(f"{gates} gates do not divide {tokens} tokens evenly")
+    _scale("alpha", alpha)
+    if not 0.0 <= eps <= _MAX_SCALE:
+        raise ValueError(f"eps is {eps}")
+    return tokens, hidden, gates, _choice("kind", kind, KINDS), params, dev
+
+
+def _norm(y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates, kind, params, eps, dev):
+    n = torch.empty((tokens, hidden), dtype=y.dtype, device=dev)
+    same = residual is None and post is None and gate is None
+    r = y if same else torch.empty((tokens, hidden), dtype=y.dtype, device=dev)
+    rc = (_lib or _library()).mv_norm(_norm_desc(
+        tokens, hidden, gates, _stride(y), 0 if residual is None else _stride(residual), _DTYPES[y.dtype],
+        _DTYPES[params], kind, alpha, eps, y.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(post),
+        _ptr(post_bias), _ptr(gate)), n.data_ptr(), 0 if same else r.data_ptr(), _raw_stream(dev.index))
+    if rc != mv.MV_OK:
+        raise mv.MVError(rc, "mv_norm")
+    return n, r
+
+
+def norm_backward(dn, y, weight, bias=None, *, dr=None, residual=None, alpha: float = 1.0, post=None,
+                  post_bias=None, gate=None, kind: str = "rms", eps: float = 1e-6, stream=None):
+    """Gradients of :func:`norm`'s n and r, given ``dn`` and (unless None) ``dr``.
+
+    The other arguments are norm's.  The result is a NormGrads (dy, dresidual,
+    dweight, dbias, dpost, dpost_bias, dgate): of y's type the first two, of the
+    parameters' type the others, each like what it is the gradient of and None
+    where that is None.  The statistics are computed again, so norm keeps none.
+    ``dn`` and ``dr`` [tokens, hidden] are of y's type; their rows may lie apart.
+    """
+    tokens, hidden, gates, k, params, dev = _norm_checks(y, weight, bias, residual, alpha, post, post_bias, gate, kind, eps)
+    _tensor("dn", dn, (y.dtype,), (tokens, hidden), dev, rows_apart=True)
+    if dr is not None:
+        _tensor("dr", dr, (y.dtype,), (tokens, hidden), dev, rows_apart=True)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream, (dn, dr, y, weight, bias, residual, post, post_bias, gate)):
+            return _norm_backward(dn, dr, y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates,
+                                  k, params, eps, dev)
+    return _norm_backward(dn, dr, y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates, k,
+                          params, eps, dev)
+
+
+def _norm_backward(dn, dr, y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates, kind, params,
+                   eps, dev):
+    def like(p, shape=(hidden,), dtype=params):
+        return None if p is None else torch.empty(shape, dtype=dtype, device=dev)
+
+    g = NormGrads(like(y, (tokens, hidden), y.dtype), like(residual, (tokens, hidden), y.dtype), like(weight), like(bias),
+                  like(post), like(post_bias), None if gate is None else like(gate, gate.shape))
+    d = _norm_desc(
+        tokens, hidden, gates, _stride(y), 0 if residual is None else _stride(residual), _DTYPES[y.dtype],
+        _DTYPES[params], kind, alpha, eps, y.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(post),
+        _ptr(post_bias), _ptr(gate))
+    e = _norm_grad_desc(_stride(dn), 0 if dr is None else _stride(dr), dn.data_ptr(), _ptr(dr), *map(_ptr, g))
+    lib, need = _lib or _library(), _u64()
+    rc = lib.mv_norm_backward_workspace_bytes(d, e, C.byref(need))
+    if rc == mv.MV_OK:
+        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+        rc = lib.mv_norm_backward(d, e, _ptr(ws), need.value, _raw_stream(dev.index))
+    if rc != mv.MV_OK:
+        raise mv.MVError(rc, "mv_norm_backward")
+    return g
 
 
 def gave_up() -> int:

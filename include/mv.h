@@ -571,6 +571,53 @@ typedef struct mv_act_grad_desc {
 } mv_act_grad_desc;
 int mv_activation_backward(const mv_act_grad_desc *desc, void *stream);
 
+/*
+ * Norms around the residual between two branches of a block: y is what a branch gave,
+ *   u = N(y) * post + post_bias          (y itself where post is NULL)
+ *   r = alpha * residual + gate * u      (without the parts that are NULL)
+ *   n = N(r) * weight + bias
+ * element by element along `hidden`; N(x) = x / sqrt(mean(x^2) + eps)
+ * (MV_NORM_RMS) or (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
+ * (MV_NORM_LAYER).  y, residual, n and r [tokens, hidden] are of type `dtype`
+ * (32 or 16 bits), the parameters weight, bias, post, post_bias [hidden] and
+ * gate [gates, hidden] of `param_dtype` (dtype or MV_F32).  gates divides tokens: each of
+ * its rows is shared by as many tokens in a row (1: by all).  post_bias needs
+ * post.  n comes from r before its rounding; r may be NULL.  hidden is 1 to
+ * MV_NORM_MAX_HIDDEN.
+ */
+typedef struct mv_norm_desc {
+    uint64_t tokens, hidden, gates, y_stride, residual_stride;
+    uint32_t dtype, param_dtype, kind;
+    float alpha, eps;
+    const void *y;                    /* [tokens, hidden]                      */
+    const void *residual;             /* [tokens, hidden], or NULL             */
+    const void *weight, *bias;        /* [hidden]; bias may be NULL            */
+    const void *post, *post_bias;     /* [hidden], or NULL                     */
+    const void *gate;                 /* [gates, hidden], or NULL              */
+} mv_norm_desc;
+int mv_norm(const mv_norm_desc *desc, void *n, void *r, void *stream);
+
+/*
+ * Gradients of n and r with respect to everything mv_norm reads, given dn and
+ * (not NULL) dr.  The statistics are computed again from y and the residual,
+ * with r unrounded.  dy and dresidual are of type `dtype`; dweight, dbias,
+ * dpost, dpost_bias and dgate of `param_dtype`, summed over the tokens that share
+ * them.  dbias, dpost, dpost_bias, dgate, dresidual: NULL exactly where what
+ * they are the gradient of is.  No tokens: the parameters' gradients are zeros.
+ */
+typedef struct mv_norm_grads {
+    uint64_t dn_stride, dr_stride;
+    const void *dn;                   /* [tokens, hidden]                      */
+    const void *dr;                   /* [tokens, hidden], or NULL             */
+    void *dy, *dresidual;             /* out [tokens, hidden]                  */
+    void *dweight, *dbias, *dpost, *dpost_bias;   /* out [hidden]              */
+    void *dgate;                      /* out [gates, hidden]                   */
+} mv_norm_grads;
+int mv_norm_backward_workspace_bytes(const mv_norm_desc *desc, const mv_norm_grads *grads,
+                                     uint64_t *bytes);
+int mv_norm_backward(const mv_norm_desc *desc, const mv_norm_grads *grads, void *workspace,
+                     uint64_t ws_bytes, void *stream);
+
 /* How many times a wait within mv_linear's or mv_linear_backward's kernels has
  * run into its limit (two seconds) since the library was loaded on the current
  * device: their results are then incomplete.  0 unless the device is broken or
