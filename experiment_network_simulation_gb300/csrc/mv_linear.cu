@@ -29,6 +29,7 @@ struct Finish {
     u32 dtype, out, bias_type;      // of z; of y and the residual
     u32 act, residual_wide, bias_wide, y_wide, z_wide;   // *_wide: four columns are one aligned access
     u32 easy;                       // all of them that matter
+    u32 by_tma;                     // y and z are stored by TMA: nothing is read but the bias, rows are 16-byte aligned
     float scale;
 };
 
@@ -302,6 +303,71 @@ template <int CTAS> __device__ __forceinline__ void cluster_meet()
     }
 }
 
+// A lane's row of a tile, 128 bytes of it at a time: to shared memory in the
+// 128-byte swizzle, and from there to the result by TMA, which leaves out what
+// lies beyond the matrix.  Fewer instructions than finish_rows(), whose lanes
+// have to change places for whole sectors: dx of 65536 x 256 by 256 x 7168
+// took 308 us that way.
+template <class T> __device__ __forceinline__ void store_tile(u32 mine, u32 lane, const CUtensorMap *map, int x, int y, const float *v)
+{
+    constexpr u32 kEach = 16 / sizeof(T);
+    // the store before this one has read the buffer
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (u32 j = 0; j < 8; j++) {
+        T t[kEach];
+#pragma unroll
+        for (u32 i = 0; i < kEach; i++) t[i] = from_float<T>(v[j * kEach + i]);
+        uint4 w;
+        memcpy(&w, t, 16);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 128 + ((j ^ (lane & 7)) * 16)), "r"(w.x), "r"(w.y),
+                     "r"(w.z), "r"(w.w) : "memory");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(mine), "r"(x), "r"(y) : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+template <u32 ACT, int N> __device__ __forceinline__ void activate_row(float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = activation(ACT, v[i]);
+}
+template <class T, int N> __device__ __forceinline__ void add_bias(const Finish &f, u64 c, float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        if (c + i >= f.n) break;
+        float b[4];
+        load4<T>(f.bias, c + i, f.bias_wide, f.n - (c + i) < 4 ? (u32)(f.n - (c + i)) : 4, b);
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[i + j] += b[j];
+    }
+}
+// Columns c .. of the lane's row, 128 bytes of OUT.
+template <class OUT, int N>
+__device__ __forceinline__ void finish_tile(const Finish &f, u32 mine, u32 lane, const CUtensorMap *y_map, const CUtensorMap *z_map,
+                                            u64 row0, u64 c, float (&v)[N])
+{
+    if (f.bias) {
+        if (f.bias_type == MV_F32) add_bias<float>(f, c, v);
+        else if (f.bias_type == MV_BF16) add_bias<__nv_bfloat16>(f, c, v);
+        else add_bias<__half>(f, c, v);
+    }
+    if (f.z) store_tile<OUT>(mine, lane, z_map, (int)c, (int)row0, v);
+    if (f.act == MV_ACT_RELU) activate_row<MV_ACT_RELU>(v);
+    else if (f.act == MV_ACT_GELU) activate_row<MV_ACT_GELU>(v);
+    else if (f.act == MV_ACT_GELU_TANH) activate_row<MV_ACT_GELU_TANH>(v);
+    else if (f.act == MV_ACT_SILU) activate_row<MV_ACT_SILU>(v);
+    if (f.scale != 1.0f)
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] *= f.scale;
+    store_tile<OUT>(mine, lane, y_map, (int)c, (int)row0, v);
+}
+
 // ---- tiles -----------------------------------------------------------------
 // A block's share of a step of 64 columns of k: 128 rows of A and BN / CTAS
 // rows of B, 128 bytes each, in the 128-byte swizzle.  An operand that is
@@ -357,7 +423,8 @@ template <bool MN> __device__ __forceinline__ u64 operand(u32 at)
 template <int CTAS, int BN, bool A_MN, bool B_MN, bool SWAP>
 __global__ void __launch_bounds__(Tile<CTAS, BN>::kThreads, BN >= 128 ? 1 : 2)
 k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap a2_map,
-          const __grid_constant__ CUtensorMap b_map, const __grid_constant__ Args args)
+          const __grid_constant__ CUtensorMap b_map, const __grid_constant__ CUtensorMap y_map,
+          const __grid_constant__ CUtensorMap z_map, const __grid_constant__ Args args)
 {
     using S = Tile<CTAS, BN>;
     extern __shared__ unsigned char raw[];
@@ -516,6 +583,20 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                         else if (col0 + c + j < args.f.m && column < args.f.n) finish1(args.f, col0 + c + j, column, __uint_as_float(v[j]));
                     }
                 }
+            } else if (args.f.by_tma && !part) {
+                const auto all = [&](auto type) {
+                    using OUT = decltype(type);
+                    constexpr int N = 128 / sizeof(OUT);
+                    for (u32 c = share * N; c < BN && col0 + c < args.f.n; c += kShares * N) {
+                        float v[N];
+#pragma unroll
+                        for (int i = 0; i < N; i += 32) load_sums(sums + c + i, *reinterpret_cast<u32(*)[32]>(&v[i]));
+                        if (row0 < args.f.m) finish_tile<OUT>(args.f, mine, lane, &y_map, &z_map, row0, col0 + c, v);
+                    }
+                };
+                if (args.f.out == MV_BF16) all(__nv_bfloat16());
+                else if (args.f.out == MV_F16) all(__half());
+                else all(0.0f);
             } else {
                 for (u32 c = share * 32; c < BN && col0 + c < args.f.n; c += kChunk) {
                     u32 v[32];
@@ -550,16 +631,19 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
+            // What it tells is that TMEM has been read (the fence above): a release would
+            // also wait for this tile's stores, which took as long as a short tile's products.
             if (lane == 0) {
                 if constexpr (CTAS == 2)
-                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_leader(taken + 8 * buffer)) : "memory");
+                    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_leader(taken + 8 * buffer)) : "memory");
                 else
-                    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(taken + 8 * buffer) : "memory");
+                    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(taken + 8 * buffer) : "memory");
             }
             buffer ^= 1;
             if (buffer == 0) buffer_turn ^= 1;
         }
     }
+    if (warp > 1 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");      // the stores have ended
     if (!ok) atomicAdd(&g_gave_up, 1u);
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -574,39 +658,55 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
     }
 }
 
-// Tiles done in pieces along k: the pieces' sums are added in their order.
-template <int CTAS, int BN, bool SWAP> __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args args)
+// Tiles done in pieces along k: the pieces' sums are added in their order, or,
+// where few tiles would leave most SMs without work, those of each of eight
+// groups of threads and then the groups' (4 tiles of 19 pieces: 10.9 us so 9.4;
+// 28 tiles of 8: 16.5 us, in groups 23.6).
+template <int CTAS, int BN, bool SWAP, u32 GROUPS> __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args args)
 {
     using S = Tile<CTAS, BN>;
+    constexpr u32 kEach = 256 / GROUPS;     // groups of so many threads
+    __shared__ float4 sums[GROUPS > 1 ? GROUPS : 1][32];
     const Units &u = args.u;
-    // 32 x 32 of a tile a block; with SWAP eight of its BN rows
-    constexpr u32 kDown = SWAP ? BN / 8 : S::kRows / 32, kAcross = SWAP ? 1 : BN / 32;
-    const u32 tile = blockIdx.x / (kDown * kAcross), here = blockIdx.x % (kDown * kAcross), t = threadIdx.x;
+    // kEach / 8 rows x 32 of a tile a block; with SWAP kEach / 32 x 128
+    constexpr u32 kDown = SWAP ? BN / (kEach / 32) : S::kRows / (kEach / 8), kAcross = SWAP ? 1 : BN / 32;
+    const u32 tile = blockIdx.x / (kDown * kAcross), here = blockIdx.x % (kDown * kAcross), t = threadIdx.x % kEach, group = threadIdx.x / kEach;
     u32 m, n;
     tile_at(u, u.whole + tile, m, n);
     u64 row, column, at;
     if constexpr (SWAP) {
-        const u32 r = here * 8 + (t >> 5), c = (t & 31) * 4;
+        const u32 r = here * (kEach / 32) + t / 32, c = t % 32 * 4;
         row = (u64)n * BN + r;
         column = (u64)m * 128 + c;
         at = r * 128 + c;
     } else {
-        const u32 r = (here / kAcross) * 32 + (t >> 3), c = (here % kAcross) * 32 + (t & 7) * 4;
+        const u32 r = (here / kAcross) * (kEach / 8) + (t >> 3), c = (here % kAcross) * 32 + (t & 7) * 4;
         row = (u64)m * S::kRows + r;
         column = (u64)n * BN + c;
         at = (r / 128) * (128 * BN) + ((c / 4) * 128 + (r & 127)) * 4;
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (row >= args.f.m || column >= args.f.n) return;
+    const bool mine = row < args.f.m && column < args.f.n;
     constexpr u32 kPiece = S::kRows * BN;
     const float *p = args.partial + (u64)tile * u.parts * kPiece + at;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (mine)
 #pragma unroll 8
-    for (u32 i = 0; i < u.parts; i++) {
-        const float4 w = *reinterpret_cast<const float4 *>(p + (u64)i * kPiece);
-        v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
+        for (u32 i = group; i < u.parts; i += GROUPS) {
+            const float4 w = *reinterpret_cast<const float4 *>(p + (u64)i * kPiece);
+            v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
+        }
+    if constexpr (GROUPS > 1) {
+        sums[group][t] = make_float4(v[0], v[1], v[2], v[3]);
+        __syncthreads();
+        if (group) return;
+#pragma unroll
+        for (u32 i = 1; i < GROUPS; i++) {
+            const float4 w = sums[i][t];
+            v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
+        }
     }
-    finish4(args.f, row, column, v);
+    if (mine) finish4(args.f, row, column, v);
 }
 
 // ---- operands as the copies want them ---------------------------------------
@@ -702,6 +802,18 @@ bool map_side(CUtensorMap *map, const Side &s, u32 dtype, u32 box_rows)
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A dense result, stored 32 rows of 128 bytes at a time.
+bool map_result(CUtensorMap *map, void *p, u64 rows, u64 cols, u32 type)
+{
+    const u32 size = (u32)dtype_size(type);
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * size};
+    const cuuint32_t box[2] = {128 / size, 32}, each[2] = {1, 1};
+    return encoder()(map, type == MV_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                        : type == MV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, each,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The kinds of tile: the result's rows and columns a tile, and what a step of
 // 64 k takes a block (cycles), from the measurements at plan().
 enum Kind { kPair256, kOne128, kOne64, kSwap64, kSwap16, kKinds };
@@ -763,12 +875,16 @@ int run_kind(const Side &a, const void *a2, const Side &b, u32 dtype, const Plan
 {
     using S = Tile<CTAS, BN>;
     const auto kernel = k_product<CTAS, BN, A_MN, B_MN, SWAP>;
-    CUtensorMap maps[3];
+    CUtensorMap maps[5];
     Side second = a;
     second.p = a2 ? a2 : a.p;
     if (!map_side(&maps[0], a, dtype, 128) || !map_side(&maps[1], second, dtype, 128) ||
         !map_side(&maps[2], b, dtype, S::kBRows))
         return MV_ECUDA;
+    maps[3] = maps[4] = maps[0];
+    Finish &f = args.f;
+    f.by_tma = !SWAP && !f.residual && f.n * dtype_size(f.out) % 16 == 0 && aligned(f.y, 16) && aligned(f.z, 16) && !(f.z && f.out == MV_F32);
+    if (f.by_tma && (!map_result(&maps[3], f.y, f.m, f.n, f.out) || (f.z && !map_result(&maps[4], f.z, f.m, f.n, f.out)))) return MV_ECUDA;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess) return MV_ECUDA;
     // type of the sums: 32 bits; of both operands; which side is contiguous; the tile
     args.what = 1u << 4 | (dtype == MV_BF16 ? 1u << 7 | 1u << 10 : 0u) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
@@ -783,11 +899,12 @@ int run_kind(const Side &a, const void *a2, const Side &b, u32 dtype, const Plan
     attr.val.clusterDim = {CTAS, 1, 1};
     cfg.attrs = &attr;
     cfg.numAttrs = CTAS == 2 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], args) != cudaSuccess) return MV_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], args) != cudaSuccess) return MV_ECUDA;
     if (p.u.parts == 1) return MV_OK;
     const u32 left = (p.u.total - p.u.whole) / p.u.parts;
-    const u32 blocks = left * (SWAP ? BN / 8 : S::kRows / 32 * (BN / 32));
-    return launch_after(k_join<CTAS, BN, SWAP>, dim3(blocks), 256, 0, stream, args);
+    const u32 blocks = left * (S::kRows * BN / 1024);
+    if (blocks >= 4 * sm_count()) return launch_after(k_join<CTAS, BN, SWAP, 1>, dim3(blocks), 256, 0, stream, args);
+    return launch_after(k_join<CTAS, BN, SWAP, 8>, dim3(8 * blocks), 256, 0, stream, args);
 }
 
 // C = A B^T into args.f; with a2, A is the sum of two.
