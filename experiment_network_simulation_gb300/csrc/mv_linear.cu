@@ -114,69 +114,6 @@ __device__ __forceinline__ void finish4(const Finish &f, u64 r, u64 c, float (&v
     store4_as(f.out, f.y, r * f.y_stride + c, f.y_wide, n, v);
 }
 
-// A warp's 32 x 32 of a tile, lane l with columns c .. c + 3 (c of its own) of
-// rows r + 4 j.  Step by step for all eight rows, so that a warp has eight
-// accesses under way: row after row, 8192 x 5120 to 20480 took 2210 us, so 916.
-// EASY: all of it inside the matrix, every access aligned.
-template <class T, bool EASY> __device__ __forceinline__ void load_rows(const Finish &f, const void *p, u64 r, u64 c, u64 stride, bool wide, u32 n, float (&v)[8][4])
-{
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-        if (EASY || r + 4 * j < f.m) load4<T>(p, (r + 4 * j) * stride + c, EASY || wide, EASY ? 4 : n, v[j]);
-}
-template <class T, bool EASY> __device__ __forceinline__ void store_rows(const Finish &f, void *p, u64 r, u64 c, u64 stride, bool wide, u32 n, const float (&v)[8][4])
-{
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-        if (EASY || r + 4 * j < f.m) store4<T>(p, (r + 4 * j) * stride + c, EASY || wide, EASY ? 4 : n, v[j]);
-}
-template <u32 ACT> __device__ __forceinline__ void activate(float (&v)[8][4])
-{
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) v[j][i] = activation(ACT, v[j][i]);
-}
-template <bool EASY> __device__ __forceinline__ void finish_rows(const Finish &f, u64 r, u64 c, float (&v)[8][4])
-{
-    if (!EASY && c >= f.n) return;
-    const u32 n = EASY || f.n - c >= 4 ? 4 : (u32)(f.n - c);
-    if (f.bias) {
-        float b[4];
-        load4_as(f.bias_type, f.bias, c, EASY || f.bias_wide, n, b);
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[j][i] += b[i];
-    }
-    if (f.z) {
-        if (f.dtype == MV_BF16) store_rows<__nv_bfloat16, EASY>(f, f.z, r, c, f.n, f.z_wide, n, v);
-        else store_rows<__half, EASY>(f, f.z, r, c, f.n, f.z_wide, n, v);
-    }
-    if (f.act == MV_ACT_RELU) activate<MV_ACT_RELU>(v);
-    else if (f.act == MV_ACT_GELU) activate<MV_ACT_GELU>(v);
-    else if (f.act == MV_ACT_GELU_TANH) activate<MV_ACT_GELU_TANH>(v);
-    else if (f.act == MV_ACT_SILU) activate<MV_ACT_SILU>(v);
-    if (f.residual) {
-        float b[8][4];
-        if (f.out == MV_BF16) load_rows<__nv_bfloat16, EASY>(f, f.residual, r, c, f.residual_stride, f.residual_wide, n, b);
-        else if (f.out == MV_F16) load_rows<__half, EASY>(f, f.residual, r, c, f.residual_stride, f.residual_wide, n, b);
-        else load_rows<float, EASY>(f, f.residual, r, c, f.residual_stride, f.residual_wide, n, b);
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[j][i] = fmaf(f.scale, v[j][i], b[j][i]);
-    } else if (f.scale != 1.0f) {
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[j][i] *= f.scale;
-    }
-    if (f.out == MV_BF16) store_rows<__nv_bfloat16, EASY>(f, f.y, r, c, f.y_stride, f.y_wide, n, v);
-    else if (f.out == MV_F16) store_rows<__half, EASY>(f, f.y, r, c, f.y_stride, f.y_wide, n, v);
-    else store_rows<float, EASY>(f, f.y, r, c, f.y_stride, f.y_wide, n, v);
-}
-
 // One column, where a warp's lanes hold neighbours of a row.
 __device__ __forceinline__ float value_as(u32 type, const void *p, u64 at)
 {
@@ -196,6 +133,118 @@ __device__ __forceinline__ void finish1(const Finish &f, u64 r, u64 c, float v)
     v = activation(f.act, v);
     v = f.residual ? fmaf(f.scale, v, value_as(f.out, f.residual, r * f.residual_stride + c)) : f.scale * v;
     put_as(f.out, f.y, r * f.y_stride + c, v);
+}
+
+// A warp's 32 x 32 of a tile, all of it inside the matrix and every access
+// aligned: the lane has columns c .. c + 3 (c its own) of rows r + 4 j.  Step by
+// step for all eight rows, so that a warp has eight accesses under way: row
+// after row, 8192 x 5120 to 20480 took 2210 us, so 916.
+template <class T> __device__ __forceinline__ void load_rows(const void *p, u64 r, u64 c, u64 stride, float (&v)[8][4])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j++) load4<T>(p, (r + 4 * j) * stride + c, true, 4, v[j]);
+}
+template <class T> __device__ __forceinline__ void store_rows(void *p, u64 r, u64 c, u64 stride, const float (&v)[8][4])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j++) store4<T>(p, (r + 4 * j) * stride + c, true, 4, v[j]);
+}
+template <u32 ACT, int N> __device__ __forceinline__ void activate(float *v)
+{
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = activation(ACT, v[i]);
+}
+template <int N> __device__ __forceinline__ void activate(u32 act, float *v)
+{
+    if (act == MV_ACT_RELU) activate<MV_ACT_RELU, N>(v);
+    else if (act == MV_ACT_GELU) activate<MV_ACT_GELU, N>(v);
+    else if (act == MV_ACT_GELU_TANH) activate<MV_ACT_GELU_TANH, N>(v);
+    else if (act == MV_ACT_SILU) activate<MV_ACT_SILU, N>(v);
+}
+__device__ __forceinline__ void finish_rows(const Finish &f, u64 r, u64 c, float (&v)[8][4])
+{
+    if (f.bias) {
+        float b[4];
+        load4_as(f.bias_type, f.bias, c, true, 4, b);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[j][i] += b[i];
+    }
+    if (f.z) {
+        if (f.dtype == MV_BF16) store_rows<__nv_bfloat16>(f.z, r, c, f.n, v);
+        else store_rows<__half>(f.z, r, c, f.n, v);
+    }
+    activate<32>(f.act, v[0]);
+    if (f.residual) {
+        float b[8][4];
+        if (f.out == MV_BF16) load_rows<__nv_bfloat16>(f.residual, r, c, f.residual_stride, b);
+        else if (f.out == MV_F16) load_rows<__half>(f.residual, r, c, f.residual_stride, b);
+        else load_rows<float>(f.residual, r, c, f.residual_stride, b);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[j][i] = fmaf(f.scale, v[j][i], b[j][i]);
+    } else if (f.scale != 1.0f) {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[j][i] *= f.scale;
+    }
+    if (f.out == MV_BF16) store_rows<__nv_bfloat16>(f.y, r, c, f.y_stride, v);
+    else if (f.out == MV_F16) store_rows<__half>(f.y, r, c, f.y_stride, v);
+    else store_rows<float>(f.y, r, c, f.y_stride, v);
+}
+
+// The same where rows lie anywhere, or end within the 32 x 32: a lane has
+// column c of the `rows` rows from r on, so that a warp's accesses are neighbours.
+template <class T> __device__ __forceinline__ void load_column(const void *p, u64 at, u64 stride, u32 rows, float (&v)[32])
+{
+    const T *from = static_cast<const T *>(p) + at;
+#pragma unroll
+    for (u32 j = 0; j < 32; j++) v[j] = j < rows ? to_float(from[j * stride]) : 0.0f;
+}
+template <class T> __device__ __forceinline__ void store_column(void *p, u64 at, u64 stride, u32 rows, const float (&v)[32])
+{
+    T *to = static_cast<T *>(p) + at;
+#pragma unroll
+    for (u32 j = 0; j < 32; j++)
+        if (j < rows) to[j * stride] = from_float<T>(v[j]);
+}
+__device__ __noinline__ void finish_column(const Finish &f, u32 mine, u32 lane, u64 r, u64 c)
+{
+    if (c >= f.n || r >= f.m) return;
+    const u32 rows = f.m - r < 32 ? (u32)(f.m - r) : 32;
+    float v[32];
+#pragma unroll
+    for (u32 j = 0; j < 32; j++)
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(mine + j * 128 + (((lane >> 2) ^ (j & 7)) * 16) + (lane & 3) * 4));
+    if (f.bias) {
+        const float b = value_as(f.bias_type, f.bias, c);
+#pragma unroll
+        for (u32 j = 0; j < 32; j++) v[j] += b;
+    }
+    if (f.z) {
+        if (f.dtype == MV_BF16) store_column<__nv_bfloat16>(f.z, r * f.n + c, f.n, rows, v);
+        else store_column<__half>(f.z, r * f.n + c, f.n, rows, v);
+    }
+    activate<32>(f.act, v);
+    if (f.residual) {
+        float b[32];
+        const u64 at = r * f.residual_stride + c;
+        if (f.out == MV_BF16) load_column<__nv_bfloat16>(f.residual, at, f.residual_stride, rows, b);
+        else if (f.out == MV_F16) load_column<__half>(f.residual, at, f.residual_stride, rows, b);
+        else load_column<float>(f.residual, at, f.residual_stride, rows, b);
+#pragma unroll
+        for (u32 j = 0; j < 32; j++) v[j] = fmaf(f.scale, v[j], b[j]);
+    } else if (f.scale != 1.0f) {
+#pragma unroll
+        for (u32 j = 0; j < 32; j++) v[j] *= f.scale;
+    }
+    const u64 at = r * f.y_stride + c;
+    if (f.out == MV_BF16) store_column<__nv_bfloat16>(f.y, at, f.y_stride, rows, v);
+    else if (f.out == MV_F16) store_column<__half>(f.y, at, f.y_stride, rows, v);
+    else store_column<float>(f.y, at, f.y_stride, rows, v);
 }
 
 // ---- PTX -------------------------------------------------------------------
@@ -331,11 +380,6 @@ template <class T> __device__ __forceinline__ void store_tile(u32 mine, u32 lane
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
 }
-template <u32 ACT, int N> __device__ __forceinline__ void activate_row(float (&v)[N])
-{
-#pragma unroll
-    for (int i = 0; i < N; i++) v[i] = activation(ACT, v[i]);
-}
 template <class T, int N> __device__ __forceinline__ void add_bias(const Finish &f, u64 c, float (&v)[N])
 {
 #pragma unroll
@@ -358,10 +402,7 @@ __device__ __forceinline__ void finish_tile(const Finish &f, u32 mine, u32 lane,
         else add_bias<__half>(f, c, v);
     }
     if (f.z) store_tile<OUT>(mine, lane, z_map, (int)c, (int)row0, v);
-    if (f.act == MV_ACT_RELU) activate_row<MV_ACT_RELU>(v);
-    else if (f.act == MV_ACT_GELU) activate_row<MV_ACT_GELU>(v);
-    else if (f.act == MV_ACT_GELU_TANH) activate_row<MV_ACT_GELU_TANH>(v);
-    else if (f.act == MV_ACT_SILU) activate_row<MV_ACT_SILU>(v);
+    activate<N>(f.act, v);
     if (f.scale != 1.0f)
 #pragma unroll
         for (int i = 0; i < N; i++) v[i] *= f.scale;
@@ -616,6 +657,10 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 128 + ((j ^ (lane & 7)) * 16)),
                                      "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3]) : "memory");
                     __syncwarp();
+                    if (!args.f.easy || row0 + 32 > args.f.m || col0 + c + 32 > args.f.n) {
+                        finish_column(args.f, mine, lane, row0, col0 + c + lane);
+                        continue;
+                    }
                     float t[8][4];
 #pragma unroll
                     for (u32 j = 0; j < 8; j++) {
@@ -623,10 +668,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(t[j][0]), "=f"(t[j][1]), "=f"(t[j][2]), "=f"(t[j][3])
                                      : "r"(mine + r * 128 + (((lane & 7) ^ (r & 7)) * 16)));
                     }
-                    if (args.f.easy && row0 + 32 <= args.f.m && col0 + c + 32 <= args.f.n)
-                        finish_rows<true>(args.f, row0 + (lane >> 3), col0 + c + (lane & 7) * 4, t);
-                    else
-                        finish_rows<false>(args.f, row0 + (lane >> 3), col0 + c + (lane & 7) * 4, t);
+                    finish_rows(args.f, row0 + (lane >> 3), col0 + c + (lane & 7) * 4, t);
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -713,12 +755,25 @@ template <int CTAS, int BN, bool SWAP, u32 GROUPS> __global__ void __launch_boun
 // Rows that lie on no 16-byte boundary are copied to where they do, and 32-bit
 // values are split into two bfloat16, the nearest and the nearest to what that
 // leaves: within 2^-17 of the value together, at any magnitude.
-template <class T> __global__ void __launch_bounds__(256) k_pack(const T *from, u64 stride, u64 rows, u64 cols, T *to, u64 to_stride)
+struct PackArgs {
+    const unsigned short *from[2];
+    unsigned short *to[2];
+    u64 stride[2], rows[2], cols[2];
+};
+// Two arrays at most (blockIdx.z), eight values a thread, a row (blockIdx.y and every gridDim.y) at a time.
+__global__ void __launch_bounds__(128) k_pack(const PackArgs a)
 {
-    const u64 n = rows * to_stride, step = (u64)gridDim.x * 256;
-    for (u64 i = (u64)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        const u64 r = i / to_stride, c = i - r * to_stride;
-        to[i] = c < cols ? from[r * stride + c] : T();
+    const u32 which = blockIdx.z;
+    const u64 cols = a.cols[which], to_stride = (cols + 7) / 8 * 8, c = ((u64)blockIdx.x * 128 + threadIdx.x) * 8;
+    if (c >= cols) return;
+    for (u64 r = blockIdx.y; r < a.rows[which]; r += gridDim.y) {
+        const unsigned short *from = a.from[which] + r * a.stride[which] + c;
+        unsigned short v[8];
+#pragma unroll
+        for (u32 i = 0; i < 8; i++) v[i] = c + i < cols ? from[i] : 0;
+        uint4 w;
+        memcpy(&w, v, 16);
+        *reinterpret_cast<uint4 *>(a.to[which] + r * to_stride + c) = w;
     }
 }
 __global__ void __launch_bounds__(256) k_split(const float *from, u64 stride, u64 rows, u64 cols, __nv_bfloat16 *to, u64 to_stride, u64 second)
@@ -740,32 +795,46 @@ __global__ void __launch_bounds__(256) k_split(const float *from, u64 stride, u6
 }
 
 // ---- columns' sums (dbias) --------------------------------------------------
-// A block adds a run of rows of 64 columns, eight rows at a time; the runs'
-// sums are added in their order by the second kernel.
-constexpr u32 kSumColumns = 64, kSumLanes = 8;
-template <class T> __global__ void __launch_bounds__(kSumColumns * kSumLanes)
-k_column_sums(const T *from, u64 stride, u64 rows, u64 cols, u64 run, float *sums)
+// A warp adds up every eighth row of a run, eight columns a lane; the block's
+// eight warps' sums are added, and the runs' by the second kernel, both in order.
+constexpr u32 kSumLanes = 8, kSumColumns = 8 * 32;
+template <class T> __global__ void __launch_bounds__(256)
+k_column_sums(const T *from, u64 stride, u64 rows, u64 cols, u64 run, u32 wide, float *sums)
 {
     __shared__ float part[kSumLanes][kSumColumns];
-    const u32 x = threadIdx.x % kSumColumns, y = threadIdx.x / kSumColumns;
-    const u64 c = (u64)blockIdx.x * kSumColumns + x, first = blockIdx.y * run, last = min(first + run, rows);
-    float s = 0.0f;
+    const u32 lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const u64 c = (u64)blockIdx.x * kSumColumns + lane * 8, first = blockIdx.y * run, last = min(first + run, rows);
+    float s[8] = {};
     if (c < cols)
-#pragma unroll 8
-        for (u64 r = first + y; r < last; r += kSumLanes) s += to_float(from[r * stride + c]);
-    part[y][x] = s;
+#pragma unroll 4
+        for (u64 r = first + warp; r < last; r += kSumLanes)
+#pragma unroll
+            for (u32 i = 0; i < 8; i += 4) {
+                float v[4];
+                load4<T>(from, r * stride + c + i, wide, c + i >= cols ? 0 : cols - (c + i) < 4 ? (u32)(cols - (c + i)) : 4, v);
+#pragma unroll
+                for (u32 j = 0; j < 4; j++) s[i + j] += v[j];
+            }
+#pragma unroll
+    for (u32 i = 0; i < 8; i++) part[warp][i * 32 + lane] = s[i];
+    // the kernel before this one may still run: what is written here is nobody's until it has ended
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
-    if (y == 0 && c < cols) {
-        for (u32 i = 1; i < kSumLanes; i++) s += part[i][x];
-        sums[blockIdx.y * cols + c] = s;
+    const u64 mine = (u64)blockIdx.x * kSumColumns + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
+    if (mine < cols) {
+        float v = part[0][threadIdx.x];
+        for (u32 i = 1; i < kSumLanes; i++) v += part[i][threadIdx.x];
+        sums[blockIdx.y * cols + mine] = v;
     }
 }
 template <class T> __global__ void __launch_bounds__(128) k_add_runs(const float *sums, u64 runs, u64 cols, T *to)
 {
     const u64 c = (u64)blockIdx.x * 128 + threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c >= cols) return;
     float s = 0.0f;
-#pragma unroll 8
+#pragma unroll 16
     for (u64 i = 0; i < runs; i++) s += sums[i * cols + c];
     to[c] = from_float<T>(s);
 }
@@ -935,13 +1004,33 @@ bool copies(const void *p, u64 stride) { return aligned(p, 16) && stride % 8 == 
 bool wide(const void *p, u64 stride, u32 dtype) { return aligned(p, 4 * dtype_size(dtype)) && stride % 4 == 0; }
 constexpr u64 kMostRows = 1ull << 30, kMostTiles = 1ull << 31;
 
-int pack(const void *from, u64 stride, u64 rows, u64 cols, void *to, cudaStream_t stream)
-{
-    const u64 n = rows * up(cols, 8);
-    const u32 blocks = (u32)std::min<u64>((n + 1023) / 1024, 1u << 16);
-    return launch(k_pack<unsigned short>, dim3(blocks), 256, 0, stream, static_cast<const unsigned short *>(from), stride, rows, cols,
-                  static_cast<unsigned short *>(to), up(cols, 8));
-}
+// Arrays to be copied, and the launch that does it.
+struct Packing {
+    PackArgs a = {};
+    u32 count = 0;
+    u64 widest = 0, most = 0;
+    const void *add(const void *from, u64 &stride, u64 rows, u64 cols, void *to)
+    {
+        a.from[count] = static_cast<const unsigned short *>(from);
+        a.to[count] = static_cast<unsigned short *>(to);
+        a.stride[count] = stride;
+        a.rows[count] = rows;
+        a.cols[count++] = cols;
+        widest = std::max(widest, cols);
+        most = std::max(most, rows);
+        stride = up(cols, 8);
+        return to;
+    }
+    int run(cudaStream_t stream)
+    {
+        const u32 pairs = count;
+        if (!pairs) return MV_OK;
+        const dim3 grid((u32)((widest + 1023) / 1024), (u32)std::min<u64>(most, 8192), pairs);
+        count = 0;
+        widest = most = 0;
+        return launch(k_pack, grid, 128, 0, stream, a);
+    }
+};
 
 struct LinearLayout {
     u64 x, w, partial, total;
@@ -1005,8 +1094,8 @@ GradLayout layout(const mv_linear_grad_desc *d)
     l.dz = take(parts == 1 && copies(d->dz, d->dz_stride) ? 0 : parts * d->tokens * up(d->rows, 8) * 2);
     // runs long enough to be worth adding, enough of them for all SMs
     const u64 across = (d->rows + kSumColumns - 1) / kSumColumns;
-    u64 runs = std::max<u64>(1, 8 * sms / across);
-    l.run = std::max<u64>(128, up((d->tokens + runs - 1) / runs, kSumLanes));
+    u64 runs = std::max<u64>(1, 4 * sms / across);
+    l.run = std::max<u64>(64, up((d->tokens + runs - 1) / runs, kSumLanes));
     runs = (d->tokens + l.run - 1) / l.run;
     l.runs = take(d->dbias ? runs * d->rows * 4 : 0);
     l.partial = take(std::max(l.dx.partial, l.dw.partial));
@@ -1043,16 +1132,10 @@ extern "C" int mv_linear(const mv_linear_desc *d, void *workspace, uint64_t ws_b
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     Side x = {d->x, d->tokens, d->cols, d->x_stride, false}, w = {d->w, d->rows, d->cols, d->w_stride, false};
-    if (!copies(d->x, d->x_stride)) {
-        rc = pack(d->x, d->x_stride, d->tokens, d->cols, ws + l.x, s);
-        x.p = ws + l.x;
-        x.stride = up(d->cols, 8);
-    }
-    if (rc == MV_OK && !copies(d->w, d->w_stride)) {
-        rc = pack(d->w, d->w_stride, d->rows, d->cols, ws + l.w, s);
-        w.p = ws + l.w;
-        w.stride = up(d->cols, 8);
-    }
+    Packing packing;
+    if (!copies(d->x, d->x_stride)) x.p = packing.add(d->x, x.stride, d->tokens, d->cols, ws + l.x);
+    if (!copies(d->w, d->w_stride)) w.p = packing.add(d->w, w.stride, d->rows, d->cols, ws + l.w);
+    rc = packing.run(s);
     if (rc != MV_OK) return rc;
     Finish f = {};
     f.bias = d->bias;
@@ -1108,6 +1191,7 @@ extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace,
     const void *dz = d->dz, *dz2 = nullptr, *x = d->x, *w = d->w;
     u64 dz_stride = d->dz_stride, x_stride = d->x_stride, w_stride = d->w_stride;
     const u64 padded = up(d->rows, 8);
+    Packing packing;
     if ((d->dx || d->dw) && d->dz_dtype == MV_F32) {
         const u64 n = d->tokens * padded;
         const u32 blocks = (u32)std::min<u64>((n / 4 + 255) / 256, 1u << 16);
@@ -1117,20 +1201,12 @@ extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace,
         dz2 = ws + l.dz + n * 2;
         dz_stride = padded;
     } else if ((d->dx || d->dw) && !copies(d->dz, d->dz_stride)) {
-        rc = pack(d->dz, d->dz_stride, d->tokens, d->rows, ws + l.dz, s);
-        dz = ws + l.dz;
-        dz_stride = padded;
+        dz = packing.add(d->dz, dz_stride, d->tokens, d->rows, ws + l.dz);
     }
-    if (rc == MV_OK && d->dw && !copies(d->x, d->x_stride)) {
-        rc = pack(d->x, d->x_stride, d->tokens, d->cols, ws + l.x, s);
-        x = ws + l.x;
-        x_stride = up(d->cols, 8);
-    }
-    if (rc == MV_OK && d->dx && !copies(d->w, d->w_stride)) {
-        rc = pack(d->w, d->w_stride, d->rows, d->cols, ws + l.w, s);
-        w = ws + l.w;
-        w_stride = up(d->cols, 8);
-    }
+    if (d->dw && !copies(d->x, d->x_stride)) x = packing.add(d->x, x_stride, d->tokens, d->cols, ws + l.x);
+    if (rc == MV_OK && packing.count == 2) rc = packing.run(s);
+    if (d->dx && !copies(d->w, d->w_stride)) w = packing.add(d->w, w_stride, d->rows, d->cols, ws + l.w);
+    if (rc == MV_OK) rc = packing.run(s);
     Finish f = {};
     f.n = d->cols;
     f.y_stride = d->cols;
@@ -1156,16 +1232,18 @@ extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace,
         const u64 runs = (d->tokens + l.run - 1) / l.run;
         float *sums = reinterpret_cast<float *>(ws + l.runs);
         const dim3 grid((u32)((d->rows + kSumColumns - 1) / kSumColumns), (u32)runs);
-        const u32 threads = kSumColumns * kSumLanes, adders = (u32)((d->rows + 127) / 128);
+        const u32 adders = (u32)((d->rows + 127) / 128), whole = wide(d->dz, d->dz_stride, d->dz_dtype);
+        // after a product they start while it ends; dz itself was there before that one
+        const bool early = d->dx || d->dw;
         if (d->dz_dtype == MV_F32)
-            rc = launch(k_column_sums<float>, grid, threads, 0, s, static_cast<const float *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, sums);
+            rc = launch_as(early, k_column_sums<float>, grid, 256, 0, s, static_cast<const float *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, whole, sums);
         else if (d->dz_dtype == MV_F16)
-            rc = launch(k_column_sums<__half>, grid, threads, 0, s, static_cast<const __half *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, sums);
+            rc = launch_as(early, k_column_sums<__half>, grid, 256, 0, s, static_cast<const __half *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, whole, sums);
         else
-            rc = launch(k_column_sums<__nv_bfloat16>, grid, threads, 0, s, static_cast<const __nv_bfloat16 *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, sums);
+            rc = launch_as(early, k_column_sums<__nv_bfloat16>, grid, 256, 0, s, static_cast<const __nv_bfloat16 *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, whole, sums);
         if (rc == MV_OK)
-            rc = d->dtype == MV_F16 ? launch(k_add_runs<__half>, dim3(adders), 128, 0, s, sums, runs, d->rows, static_cast<__half *>(d->dbias))
-                                    : launch(k_add_runs<__nv_bfloat16>, dim3(adders), 128, 0, s, sums, runs, d->rows, static_cast<__nv_bfloat16 *>(d->dbias));
+            rc = d->dtype == MV_F16 ? launch_after(k_add_runs<__half>, dim3(adders), 128, 0, s, sums, runs, d->rows, static_cast<__half *>(d->dbias))
+                                    : launch_after(k_add_runs<__nv_bfloat16>, dim3(adders), 128, 0, s, sums, runs, d->rows, static_cast<__nv_bfloat16 *>(d->dbias));
     }
     return rc;
 }
