@@ -69,12 +69,17 @@ def _library() -> C.CDLL:
 
 
 def _run(name: str, desc: bytes, dev):
-    """One enqueued call that needs a workspace, on the current stream of ``dev``."""
-    lib, need = _lib or _library(), _u64()
-    rc = getattr(lib, name + "_workspace_bytes")(desc, C.byref(need))
-    if rc == mv.MV_OK:
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-        rc = getattr(lib, name)(desc, ws.data_ptr() if need.value else 0, need.value, _raw_stream(dev.index))
+    """One enqueued call on the current stream of ``dev``; without a workspace
+    first, as small sizes need none."""
+    lib = _lib or _library()
+    call, stream = getattr(lib, name), _raw_stream(dev.index)
+    rc = call(desc, 0, 0, stream)
+    if rc == mv.MV_ENOMEM:
+        need = _u64()
+        rc = getattr(lib, name + "_workspace_bytes")(desc, C.byref(need))
+        if rc == mv.MV_OK:
+            ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+            rc = call(desc, ws.data_ptr(), need.value, stream)
     if rc != mv.MV_OK:
         raise mv.MVError(rc, name)
 

@@ -344,12 +344,10 @@ __device__ __forceinline__ void load_sums(u32 at, u32 (&v)[16])
         : "r"(at));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-template <int CTAS> __device__ __forceinline__ void cluster_meet()
+__device__ __forceinline__ void meet()          // the cluster's threads
 {
-    if constexpr (CTAS == 2) {
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // A lane's row of a tile, 128 bytes of it at a time: to shared memory in the
@@ -419,13 +417,14 @@ constexpr u32 kStep = 64;
 template <int CTAS, int BN> struct Tile {
     static constexpr u32 kRows = 128 * CTAS;
     // a warp copies, one multiplies, the others finish: two to each quarter of TMEM's lanes where tiles are large
-    static constexpr u32 kWorkers = CTAS == 2 ? 8 : 4, kThreads = 64 + kWorkers * 32, kStaging = kWorkers * 32 * 128;
+    static constexpr u32 kWorkers = BN >= 128 ? 8 : 4, kThreads = 64 + kWorkers * 32, kStaging = kWorkers * 32 * 128;
     static constexpr u32 kA = 128 * 128, kBRows = BN / CTAS, kB = kBRows * 128, kStage = kA + kB;
-    // one block an SM where the tile is large; two where it is small
-    static constexpr u32 kRoom = (BN >= 128 ? 227 : 113) * 1024 - 2048 - kStaging;
-    static constexpr u32 kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
+    // copies under way: as many as one block an SM has room for, or, where tiles are small and
+    // blocks many, half of them to each of two
+    static constexpr u32 fit(u32 room) { return (room - 2048 - kStaging) / kStage < 8 ? (room - 2048 - kStaging) / kStage : 8; }
+    static constexpr u32 kStages = fit(227 * 1024), kFewStages = BN >= 128 ? kStages : fit(113 * 1024);
     static constexpr u32 kColumns = BN < 32 ? 32 : BN;          // of TMEM, for one of two tiles
-    static constexpr u32 kSmem = 1024 + kStages * kStage + kStaging + 256;
+    static constexpr u32 smem(u32 stages) { return 1024 + stages * kStage + kStaging + 256; }
 };
 
 struct Units {                      // what the blocks (or pairs) do, in order
@@ -434,6 +433,7 @@ struct Units {                      // what the blocks (or pairs) do, in order
     u32 parts;                      // this many pieces along k
     u32 total;                      // units in all
     u32 steps;                      // steps of k of a tile
+    u32 stages;                     // copies under way a block
     u32 half_steps;                 // steps after which A's second part begins (0: none)
 };
 
@@ -470,17 +470,19 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
     using S = Tile<CTAS, BN>;
     extern __shared__ unsigned char raw[];
     const u32 base = (shared_at(raw) + 1023) & ~1023u;
-    const u32 staging = base + S::kStages * S::kStage, bars = staging + S::kStaging;
-    const u32 full = bars, empty = full + 8 * S::kStages, done = empty + 8 * S::kStages, taken = done + 16,
+    const u32 stages = S::kStages == S::kFewStages ? S::kStages : args.u.stages;
+    const u32 staging = base + stages * S::kStage, bars = staging + S::kStaging;
+    const u32 full = bars, empty = full + 8 * stages, done = empty + 8 * stages, taken = done + 16,
               drained = taken + 16, slot = drained + 8;
     const u32 warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     u32 rank = 0;
-    if constexpr (CTAS == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    const u32 worker = blockIdx.x / CTAS, workers = gridDim.x / CTAS;
+    if constexpr (CTAS == 2 || SWAP) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const Units &u = args.u;
+    const u32 cluster = SWAP ? u.parts : CTAS, worker = blockIdx.x / cluster, workers = gridDim.x / cluster;
+    const u32 pair_rank = CTAS == 2 ? rank : 0;
 
     if (threadIdx.x == 0) {
-        for (u32 i = 0; i < S::kStages; i++) {
+        for (u32 i = 0; i < stages; i++) {
             barrier_init(full + 8 * i, 1);
             barrier_init(empty + 8 * i, 1);
         }
@@ -503,15 +505,19 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    cluster_meet<CTAS>();
+    if constexpr (CTAS == 2) meet();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     u32 tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     auto unit = [&](u32 i, u32 &m, u32 &n, u32 &first, u32 &last) {
         u32 tile = i, part = 0, parts = 1;
-        if (i >= u.whole) {
+        if (SWAP) {
+            part = rank;
+            parts = u.parts;
+        } else if (i >= u.whole) {
             tile = u.whole + (i - u.whole) / u.parts;
             part = (i - u.whole) % u.parts;
             parts = u.parts;
@@ -529,7 +535,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
             for (u32 i = worker; i < u.total && ok; i += workers) {
                 u32 m, n, first, last;
                 unit(i, m, n, first, last);
-                const int row_a = (int)(m * S::kRows + rank * 128), row_b = (int)(n * BN + rank * S::kBRows);
+                const int row_a = (int)(m * S::kRows + pair_rank * 128), row_b = (int)(n * BN + pair_rank * S::kBRows);
                 for (u32 k = first; k < last; k++) {
                     if (!barrier_wait(empty + 8 * s, turn ^ 1)) { ok = false; break; }
                     const bool second = u.half_steps && k >= u.half_steps;
@@ -537,7 +543,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                     const int at = (int)((second ? k - u.half_steps : k) * kStep);
                     const u32 to = base + s * S::kStage;
                     u32 bar = full + 8 * s;
-                    if (rank == 0)
+                    if (pair_rank == 0)
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(CTAS * S::kStage) : "memory");
                     if constexpr (CTAS == 2) bar = at_leader(bar);
                     if constexpr (A_MN) {
@@ -553,20 +559,20 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                         copy_tile<CTAS>(to + S::kA, &b_map, at, row_b, bar);
                     }
                     issued++;
-                    if (++s == S::kStages) { s = 0; turn ^= 1; }
+                    if (++s == stages) { s = 0; turn ^= 1; }
                 }
             }
             // After a wait that ran out: the copies under way end first, both blocks' (which
             // the leader's barriers count), before the pair's blocks go on to their end.
-            if (!ok && rank == 0)
-                for (u32 j = 0; j < S::kStages && j < issued; j++) {
-                    s = s ? s - 1 : S::kStages - 1;
-                    if (s == S::kStages - 1) turn ^= 1;
+            if (!ok && pair_rank == 0)
+                for (u32 j = 0; j < stages && j < issued; j++) {
+                    s = s ? s - 1 : stages - 1;
+                    if (s == stages - 1) turn ^= 1;
                     barrier_wait(full + 8 * s, turn);
                 }
         }
     } else if (warp == 1) {
-        if (rank == 0 && one_lane()) {                            // multiplies
+        if (pair_rank == 0 && one_lane()) {                       // multiplies
             u32 s = 0, turn = 0, buffer = 0, buffer_turn = 0;
             for (u32 i = worker; i < u.total && ok; i += workers) {
                 u32 m, n, first, last;
@@ -584,7 +590,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                         multiply<CTAS>(sums, a + j * (A_MN ? 2048 / 16 : 32 / 16), b + j * (B_MN ? 2048 / 16 : 32 / 16),
                                        args.what, k > first || j);
                     arrive_after_products<CTAS>(empty + 8 * s);
-                    if (++s == S::kStages) { s = 0; turn ^= 1; }
+                    if (++s == stages) { s = 0; turn ^= 1; }
                 }
                 if (ok) arrive_after_products<CTAS>(done + 8 * buffer);
                 buffer ^= 1;
@@ -603,14 +609,21 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
         for (u32 i = worker; i < u.total; i += workers) {
             u32 m, n, first, last;
             unit(i, m, n, first, last);
+            if (!SWAP && args.f.residual && i < u.whole) {        // on its way while the tile is summed
+                const u64 size = args.f.out == MV_F32 ? 4 : 2, r = (u64)m * S::kRows + pair_rank * 128 + w * 32 + lane;
+                const u64 c = (u64)n * BN * size, end = min((u64)(n + 1) * BN, args.f.n) * size;
+                if (r < args.f.m)
+                    for (u64 j = c + share * 128; j < end; j += kShares * 128)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(args.f.residual) + r * args.f.residual_stride * size + j));
+            }
             ok = barrier_wait(done + 8 * buffer, buffer_turn);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const u32 sums = tmem + buffer * S::kColumns + (w << 21);
-            float *part = i < u.whole ? nullptr
-                        : args.partial + (u64)(i - u.whole) * (S::kRows * BN) + rank * 128 * BN;
-            const u64 row0 = (u64)m * S::kRows + rank * 128 + w * 32, col0 = (u64)n * BN;
+            float *part = SWAP || i < u.whole ? nullptr
+                        : args.partial + (u64)(i - u.whole) * (S::kRows * BN) + pair_rank * 128 * BN;
+            const u64 row0 = (u64)m * S::kRows + pair_rank * 128 + w * 32, col0 = (u64)n * BN;
             if constexpr (SWAP) {
                 // lanes are columns of the result, TMEM's columns its rows
                 const u64 column = row0 + lane;
@@ -620,7 +633,8 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                     load_sums(sums + c, v);
 #pragma unroll
                     for (int j = 0; j < kAtOnce; j++) {
-                        if (part) part[(c + j) * 128 + w * 32 + lane] = __uint_as_float(v[j]);
+                        if (u.parts > 1)                           // [rows][128 columns], in the copies' place
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + j) * 128 + w * 32 + lane) * 4), "r"(v[j]) : "memory");
                         else if (col0 + c + j < args.f.m && column < args.f.n) finish1(args.f, col0 + c + j, column, __uint_as_float(v[j]));
                     }
                 }
@@ -688,9 +702,31 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
     if (warp > 1 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");      // the stores have ended
     if (!ok) atomicAdd(&g_gave_up, 1u);
     __syncwarp();
+    if (SWAP && u.parts > 1) {
+        // The pieces' sums meet through the cluster's shared memory: each block finishes
+        // some of the quads of columns, adding the pieces in their order.
+        u32 m, n;
+        tile_at(u, worker, m, n);
+        const u64 row0 = (u64)n * BN, column0 = (u64)m * 128;
+        const u32 quads = (u32)min((u64)BN, args.f.m - row0) * 32;
+        meet();
+        for (u32 q = rank * S::kThreads + threadIdx.x; q < quads; q += u.parts * S::kThreads) {
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (u32 p = 0; p < u.parts; p++) {
+                float w[4];
+                u32 there;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(base + q * 16), "r"(p));
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]) : "r"(there) : "memory");
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[i] += w[i];
+            }
+            finish4(args.f, row0 + q / 32, column0 + q % 32 * 4, v);
+        }
+        meet();
+    }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    cluster_meet<CTAS>();
+    if constexpr (CTAS == 2) meet();
     if (warp == 1) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if constexpr (CTAS == 2)
@@ -704,29 +740,19 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
 // where few tiles would leave most SMs without work, those of each of eight
 // groups of threads and then the groups' (4 tiles of 19 pieces: 10.9 us so 9.4;
 // 28 tiles of 8: 16.5 us, in groups 23.6).
-template <int CTAS, int BN, bool SWAP, u32 GROUPS> __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args args)
+template <int CTAS, int BN, u32 GROUPS> __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args args)
 {
     using S = Tile<CTAS, BN>;
     constexpr u32 kEach = 256 / GROUPS;     // groups of so many threads
     __shared__ float4 sums[GROUPS > 1 ? GROUPS : 1][32];
     const Units &u = args.u;
-    // kEach / 8 rows x 32 of a tile a block; with SWAP kEach / 32 x 128
-    constexpr u32 kDown = SWAP ? BN / (kEach / 32) : S::kRows / (kEach / 8), kAcross = SWAP ? 1 : BN / 32;
+    // kEach / 8 rows x 32 of a tile a block
+    constexpr u32 kDown = S::kRows / (kEach / 8), kAcross = BN / 32;
     const u32 tile = blockIdx.x / (kDown * kAcross), here = blockIdx.x % (kDown * kAcross), t = threadIdx.x % kEach, group = threadIdx.x / kEach;
     u32 m, n;
     tile_at(u, u.whole + tile, m, n);
-    u64 row, column, at;
-    if constexpr (SWAP) {
-        const u32 r = here * (kEach / 32) + t / 32, c = t % 32 * 4;
-        row = (u64)n * BN + r;
-        column = (u64)m * 128 + c;
-        at = r * 128 + c;
-    } else {
-        const u32 r = (here / kAcross) * (kEach / 8) + (t >> 3), c = (here % kAcross) * 32 + (t & 7) * 4;
-        row = (u64)m * S::kRows + r;
-        column = (u64)n * BN + c;
-        at = (r / 128) * (128 * BN) + ((c / 4) * 128 + (r & 127)) * 4;
-    }
+    const u32 r = (here / kAcross) * (kEach / 8) + (t >> 3), c = (here % kAcross) * 32 + (t & 7) * 4;
+    const u64 row = (u64)m * S::kRows + r, column = (u64)n * BN + c, at = (r / 128) * (128 * BN) + ((c / 4) * 128 + (r & 127)) * 4;
     const bool mine = row < args.f.m && column < args.f.n;
     constexpr u32 kPiece = S::kRows * BN;
     const float *p = args.partial + (u64)tile * u.parts * kPiece + at;
@@ -883,45 +909,73 @@ bool map_result(CUtensorMap *map, void *p, u64 rows, u64 cols, u32 type)
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The kinds of tile: the result's rows and columns a tile, and what a step of
-// 64 k takes a block (cycles), from the measurements at plan().
+// The kinds of tile: A's rows and B's a tile, and whether two blocks share an SM where there are enough.
 enum Kind { kPair256, kOne128, kOne64, kSwap64, kSwap16, kKinds };
 struct KindOf {
-    u32 rows, cols, blocks_an_sm_x2;    // rows and columns of A's and B's side
-    bool swap;
-    double step;
+    u32 rows, cols;
+    bool two, swap;
 };
-constexpr KindOf kKind[kKinds] = {{256, 256, 1, false, 530}, {128, 128, 2, false, 440}, {128, 64, 4, false, 660},
-                                  {128, 64, 4, true, 660}, {128, 16, 4, true, 500}};
+constexpr KindOf kKind[kKinds] = {{256, 256, false, false}, {128, 128, false, false}, {128, 64, true, false},
+                                  {128, 64, true, true}, {128, 16, true, true}};
+constexpr u64 kCluster = 8;             // blocks that share a tile of the kinds that swap, at most
 
 struct Plan {
     Kind kind;
+    bool two;                           // two blocks an SM
     Units u;
     u64 blocks, partial;                // blocks; bytes of pieces' sums
 };
 
+// What a product would take with one kind of tile, in cycles, as measured on
+// GB300: a step of 64 k takes a pair of blocks 530 cycles (the products
+// themselves 512), a single one what its copies take, 64 bytes a cycle and SM,
+// but no less than a copy's 2000 cycles over the copies under way; memory gives 3300 bytes a cycle.
+// Checked by forcing each kind, us: 2048 x 5120 to 2560: 45.7 (pairs), 51.9
+// (128 x 128), 70.3 (128 x 64); 1 x 20480 to 5120: 39 (swapped, 16), 42
+// (swapped, 64), 50 (128 x 128), 64 (pairs); 64 x 5120 to 5120: 20 (swapped, 64),
+// 25 (swapped, 16), 23 (128 x 128).
 Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 sms, double &best)
 {
     const KindOf &k = kKind[kind];
-    const u64 slots = std::max<u64>(1, (u64)sms * k.blocks_an_sm_x2 / 2), a = k.swap ? n : m, b = k.swap ? m : n;
-    const u64 tm = (a + k.rows - 1) / k.rows, tn = (b + k.cols - 1) / k.cols, tiles = tm * tn;
-    const u64 piece = (u64)k.rows * k.cols * 4;
+    const u64 a = k.swap ? n : m, b = k.swap ? m : n, tm = (a + k.rows - 1) / k.rows, tn = (b + k.cols - 1) / k.cols, tiles = tm * tn;
+    const u64 each = kind == kPair256 ? 2 : 1;                         // blocks a unit
+    const double bytes = kind == kPair256 ? 32768 : (k.rows + k.cols) * 128;
+    const double memory = (double)(m + n) * (double)steps * 128 / (sms * 21.7);
     Plan p = {};
     best = INFINITY;
-    // whole tiles in rounds of all slots, and what is left in as many pieces as fill one to four more
-    const u64 whole = tiles / slots * slots, left = tiles - whole;
-    for (u64 round = 0; round <= (left ? 4 : 0); round++) {
-        const u64 parts = round ? std::min<u64>(steps, round * slots / left) : 1;
+    auto consider = [&](u64 whole, u64 left, u64 parts, u64 blocks, u64 slots, bool two, double join) {
+        const double step = kind == kPair256 ? 530 : std::max(bytes / 64 * (two ? 2 : 1), two || kind == kOne128 ? 400.0 : 250.0);
         const double rounds = (double)((left * parts + slots - 1) / slots);
-        double cost = (double)(whole / slots) * steps * k.step + rounds * ((double)((steps + parts - 1) / parts) * k.step + 400) + 2000;
-        if (parts > 1) cost += 3000 + 1.0 * parts * left * piece / (sms * 24.0);
-        if (cost >= best) continue;
+        const double work = ((double)whole / (double)slots) * ((double)steps * step + 400) +
+                            rounds * ((double)((steps + parts - 1) / parts) * step + 2000);
+        const double cost = std::max(work, memory) + 0.35 * std::min(work, memory) + join + 2000;
+        if (cost >= best) return;
         best = cost;
         p.kind = kind;
-        p.u = {(u32)tm, (u32)tn, (u32)(parts == 1 ? tiles : whole), (u32)parts, (u32)(parts == 1 ? tiles : whole + left * parts),
-               (u32)steps, 0};
-        p.blocks = std::min<u64>(p.u.total, slots) * (kind == kPair256 ? 2 : 1);
-        p.partial = parts == 1 ? 0 : left * parts * piece;
+        p.two = two;
+        p.u = {(u32)tm, (u32)tn, (u32)(k.swap || parts == 1 ? tiles : whole), (u32)parts,
+               (u32)(k.swap || parts == 1 ? tiles : whole + left * parts), (u32)steps, 0, 0};
+        p.blocks = blocks;
+        p.partial = k.swap || parts == 1 ? 0 : left * parts * (u64)k.rows * k.cols * 4;
+    };
+    if (k.swap) {                       // every tile in as many pieces, a block each, in one cluster
+        for (u64 parts = 1; parts <= std::min(kCluster, steps); parts++) {
+            const bool two = tiles * parts > sms;
+            // clusters of seven and eight leave SMs out: 1 x 20480 to 5120 in 6 pieces 39.4 us, in 7 49.2
+            const u64 slots = parts > 6 ? (u64)sms * (two ? 3 : 2) / (two ? 2 : 3) : (u64)sms * (two ? 2 : 1);
+            // more than one round costs its blocks' starts: 1 x 5120 to 20480 in one piece 39.6 us, in three 45.4
+            if (parts > 1 && tiles * parts > slots) continue;
+            consider(0, tiles, parts, tiles * parts, std::max<u64>(1, slots), two, parts > 1 ? 1000 : 0);
+        }
+        return p;
+    }
+    // whole tiles in rounds of all slots, and what is left in as many pieces as fill one to four more
+    const bool two = k.two && tiles > sms;
+    const u64 slots = std::max<u64>(1, (u64)sms * (two ? 2 : 1) / each), whole = tiles / slots * slots, left = tiles - whole;
+    for (u64 round = 0; round <= (left ? 4 : 0); round++) {
+        const u64 parts = round ? std::min<u64>(steps, round * slots / left) : 1;
+        const double join = parts > 1 ? 6000 + (double)(parts * left) * k.rows * k.cols * 4 / (sms * 24.0) : 0;
+        consider(whole, left, parts, std::min<u64>(whole + left * parts, slots) * each, slots, two, join);
     }
     return p;
 }
@@ -940,7 +994,7 @@ Plan plan(u64 m, u64 n, u64 steps, bool swaps, u32 sms)
 }
 
 template <int CTAS, int BN, bool A_MN, bool B_MN, bool SWAP>
-int run_kind(const Side &a, const void *a2, const Side &b, u32 dtype, const Plan &p, Args &args, cudaStream_t stream)
+int run_kind(const Side &a, const void *a2, const Side &b, u32 dtype, const Plan &p, Args &args, bool early, cudaStream_t stream)
 {
     using S = Tile<CTAS, BN>;
     const auto kernel = k_product<CTAS, BN, A_MN, B_MN, SWAP>;
@@ -954,31 +1008,40 @@ int run_kind(const Side &a, const void *a2, const Side &b, u32 dtype, const Plan
     Finish &f = args.f;
     f.by_tma = !SWAP && !f.residual && f.n * dtype_size(f.out) % 16 == 0 && aligned(f.y, 16) && aligned(f.z, 16) && !(f.z && f.out == MV_F32);
     if (f.by_tma && (!map_result(&maps[3], f.y, f.m, f.n, f.out) || (f.z && !map_result(&maps[4], f.z, f.m, f.n, f.out)))) return MV_ECUDA;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess) return MV_ECUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem(S::kStages)) != cudaSuccess) return MV_ECUDA;
     // type of the sums: 32 bits; of both operands; which side is contiguous; the tile
     args.what = 1u << 4 | (dtype == MV_BF16 ? 1u << 7 | 1u << 10 : 0u) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
                 (u32)(BN >> 3) << 17 | (u32)(128 * CTAS >> 4) << 24;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((u32)p.blocks);
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    args.u.stages = p.two ? S::kFewStages : S::kStages;
+    cfg.dynamicSmemBytes = S::smem(args.u.stages);
     cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim = {CTAS, 1, 1};
-    cfg.attrs = &attr;
-    cfg.numAttrs = CTAS == 2 ? 1 : 0;
+    cudaLaunchAttribute attr[2];
+    u32 attrs = 0;
+    if (early) {
+        attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[attrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    const u32 cluster = SWAP ? p.u.parts : CTAS;
+    if (cluster > 1) {
+        attr[attrs].id = cudaLaunchAttributeClusterDimension;
+        attr[attrs++].val.clusterDim = {cluster, 1, 1};
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = attrs;
     if (cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], args) != cudaSuccess) return MV_ECUDA;
-    if (p.u.parts == 1) return MV_OK;
+    if (SWAP || p.u.parts == 1) return MV_OK;
     const u32 left = (p.u.total - p.u.whole) / p.u.parts;
     const u32 blocks = left * (S::kRows * BN / 1024);
-    if (blocks >= 4 * sm_count()) return launch_after(k_join<CTAS, BN, SWAP, 1>, dim3(blocks), 256, 0, stream, args);
-    return launch_after(k_join<CTAS, BN, SWAP, 8>, dim3(8 * blocks), 256, 0, stream, args);
+    if (blocks >= 4 * sm_count()) return launch_after(k_join<CTAS, BN, 1>, dim3(blocks), 256, 0, stream, args);
+    return launch_after(k_join<CTAS, BN, 8>, dim3(8 * blocks), 256, 0, stream, args);
 }
 
-// C = A B^T into args.f; with a2, A is the sum of two.
+// C = A B^T into args.f; with a2, A is the sum of two.  early: after a kernel of this call.
 template <bool A_MN, bool B_MN>
-int product(const Side &a, const void *a2, const Side &b, u32 dtype, Plan p, const Finish &f, float *partial, cudaStream_t stream)
+int product(const Side &a, const void *a2, const Side &b, u32 dtype, Plan p, const Finish &f, float *partial, bool early, cudaStream_t stream)
 {
     Args args = {};
     args.u = p.u;
@@ -986,14 +1049,14 @@ int product(const Side &a, const void *a2, const Side &b, u32 dtype, Plan p, con
     args.partial = partial;
     args.u.half_steps = a2 ? p.u.steps / 2 : 0;
     switch (p.kind) {
-    case kPair256: return run_kind<2, 256, A_MN, B_MN, false>(a, a2, b, dtype, p, args, stream);
-    case kOne128: return run_kind<1, 128, A_MN, B_MN, false>(a, a2, b, dtype, p, args, stream);
-    case kOne64: return run_kind<1, 64, A_MN, B_MN, false>(a, a2, b, dtype, p, args, stream);
+    case kPair256: return run_kind<2, 256, A_MN, B_MN, false>(a, a2, b, dtype, p, args, early, stream);
+    case kOne128: return run_kind<1, 128, A_MN, B_MN, false>(a, a2, b, dtype, p, args, early, stream);
+    case kOne64: return run_kind<1, 64, A_MN, B_MN, false>(a, a2, b, dtype, p, args, early, stream);
     default: break;
     }
     if constexpr (!A_MN && !B_MN) {     // the forward product alone: A and B change places
-        if (p.kind == kSwap64) return run_kind<1, 64, false, false, true>(b, nullptr, a, dtype, p, args, stream);
-        if (p.kind == kSwap16) return run_kind<1, 16, false, false, true>(b, nullptr, a, dtype, p, args, stream);
+        if (p.kind == kSwap64) return run_kind<1, 64, false, false, true>(b, nullptr, a, dtype, p, args, early, stream);
+        if (p.kind == kSwap16) return run_kind<1, 16, false, false, true>(b, nullptr, a, dtype, p, args, early, stream);
     }
     return MV_EINVAL;
 }
@@ -1126,8 +1189,8 @@ extern "C" int mv_linear(const mv_linear_desc *d, void *workspace, uint64_t ws_b
         !aligned(workspace, 256))
         return MV_EINVAL;
     const LinearLayout l = layout(d);
-    if (l.total && !workspace) return MV_EINVAL;
     if (ws_bytes < l.total) return MV_ENOMEM;
+    if (l.total && !workspace) return MV_EINVAL;
     if (!sm_count()) return MV_ECUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
@@ -1135,6 +1198,7 @@ extern "C" int mv_linear(const mv_linear_desc *d, void *workspace, uint64_t ws_b
     Packing packing;
     if (!copies(d->x, d->x_stride)) x.p = packing.add(d->x, x.stride, d->tokens, d->cols, ws + l.x);
     if (!copies(d->w, d->w_stride)) w.p = packing.add(d->w, w.stride, d->rows, d->cols, ws + l.w);
+    const bool packed = packing.count != 0;
     rc = packing.run(s);
     if (rc != MV_OK) return rc;
     Finish f = {};
@@ -1156,7 +1220,7 @@ extern "C" int mv_linear(const mv_linear_desc *d, void *workspace, uint64_t ws_b
     f.y_wide = wide(d->y, d->rows, d->out_dtype);
     f.z_wide = wide(d->z, d->rows, d->dtype);
     f.easy = f.y_wide && (!f.z || f.z_wide) && (!f.bias || f.bias_wide) && (!f.residual || f.residual_wide);
-    return product<false, false>(x, nullptr, w, d->dtype, l.plan, f, reinterpret_cast<float *>(ws + l.partial), s);
+    return product<false, false>(x, nullptr, w, d->dtype, l.plan, f, reinterpret_cast<float *>(ws + l.partial), packed, s);
 }
 
 extern "C" int mv_linear_backward_workspace_bytes(const mv_linear_grad_desc *d, uint64_t *bytes)
@@ -1184,8 +1248,8 @@ extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace,
         return MV_OK;
     }
     const GradLayout l = layout(d);
-    if (l.total && !workspace) return MV_EINVAL;
     if (ws_bytes < l.total) return MV_ENOMEM;
+    if (l.total && !workspace) return MV_EINVAL;
     if (!sm_count()) return MV_ECUDA;
     char *ws = static_cast<char *>(workspace);
     const void *dz = d->dz, *dz2 = nullptr, *x = d->x, *w = d->w;
@@ -1206,6 +1270,7 @@ extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace,
     if (d->dw && !copies(d->x, d->x_stride)) x = packing.add(d->x, x_stride, d->tokens, d->cols, ws + l.x);
     if (rc == MV_OK && packing.count == 2) rc = packing.run(s);
     if (d->dx && !copies(d->w, d->w_stride)) w = packing.add(d->w, w_stride, d->rows, d->cols, ws + l.w);
+    bool early = dz != d->dz || x != d->x || packing.count;
     if (rc == MV_OK) rc = packing.run(s);
     Finish f = {};
     f.n = d->cols;
@@ -1219,22 +1284,23 @@ extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace,
         f.y = d->dx;
         f.easy = f.y_wide = wide(d->dx, d->cols, d->dtype);
         rc = product<false, true>({dz, d->tokens, d->rows, dz_stride, false}, dz2, {w, d->cols, d->rows, w_stride, true}, d->dtype,
-                                  l.dx, f, partial, s);
+                                  l.dx, f, partial, early, s);
+        early = true;
     }
     if (rc == MV_OK && d->dw) {
         f.m = d->rows;
         f.y = d->dw;
         f.easy = f.y_wide = wide(d->dw, d->cols, d->dtype);
         rc = product<true, true>({dz, d->rows, d->tokens, dz_stride, true}, dz2, {x, d->cols, d->tokens, x_stride, true}, d->dtype,
-                                 l.dw, f, partial, s);
+                                 l.dw, f, partial, early, s);
+        early = true;
     }
     if (rc == MV_OK && d->dbias) {
         const u64 runs = (d->tokens + l.run - 1) / l.run;
         float *sums = reinterpret_cast<float *>(ws + l.runs);
         const dim3 grid((u32)((d->rows + kSumColumns - 1) / kSumColumns), (u32)runs);
         const u32 adders = (u32)((d->rows + 127) / 128), whole = wide(d->dz, d->dz_stride, d->dz_dtype);
-        // after a product they start while it ends; dz itself was there before that one
-        const bool early = d->dx || d->dw;
+        // after another kernel of this call they start while it ends: dz itself was there before that one
         if (d->dz_dtype == MV_F32)
             rc = launch_as(early, k_column_sums<float>, grid, 256, 0, s, static_cast<const float *>(d->dz), d->dz_stride, d->tokens, d->rows, l.run, whole, sums);
         else if (d->dz_dtype == MV_F16)
