@@ -14,8 +14,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmv.so")
 SOURCES = ["mv_kernel.cu", "mv_api.cu", "mv_route.cu", "mv_exchange.cu", "mv_experts.cu",
-           "mv_linear.cu", "mv_activation.cu", "mv_norm.cu"]
-HEADERS = ["mv_device.cuh", "mv_moe.cuh", "mv_block.cuh", os.path.join("..", "..", "include", "mv.h")]
+           "mv_linear.cu", "mv_activation.cu", "mv_norm.cu", 
+           "mv_norm_grad_f32.cu", "mv_norm_grad_f16.cu", "mv_norm_grad_bf16.cu"]
+HEADERS = ["mv_device.cuh", "mv_moe.cuh", "mv_block.cuh", "mv_norm.cuh", "mv_norm_grad.cuh", os.path.join("..", "..", "include", "mv.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 

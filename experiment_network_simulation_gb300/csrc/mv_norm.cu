@@ -1,486 +1,155 @@
 // Norms after one branch and before the next, with the branch's gate and the
 // residual between them (mv_norm, mv_norm_backward in include/mv.h):
 //   u = N(y) post + post_bias,   r = alpha residual + gate u,   n = N(r) weight + bias
-// A block holds a row: it is read once, and the stream between the two norms is
-// normed from its 32-bit values.
+// A block holds a row: it is read once, the next one on its way, and the stream
+// between the two norms is normed from its 32-bit values.  Memory bounds it.
 #include <algorithm>
 #include <cmath>
-#include <cstring>
 
-#include "mv_block.cuh"
+#include "mv_norm.cuh"
 
 namespace mvblock {
 
-struct NormArgs {
-    const void *y, *residual, *dn, *dr;
-    const void *weight, *bias, *post, *post_bias, *gate;
-    void *n, *r, *dy, *dresidual, *dgate;           // dgate: where every token has a gate of its own
-    u64 tokens, y_stride, residual_stride, dn_stride, dr_stride;
-    u64 run, rows;                                  // tokens that share a gate; rows a block (backward)
-    u32 hidden, layer, params_f32, staged;
-    float alpha, eps, inv_hidden;
-    float *sums;                                    // a block's sums for weight, bias, post, post_bias  [blocks, 4, hidden]
-    float *gate_sums;                               // and for the gates of its rows                     [blocks + gates, hidden]
-};
-
-// ---- pieces of a row --------------------------------------------------------
-// A thread's elements: PIECES pieces of N neighbours, threads next to each
-// other; N = 1 where rows lie on no 16-byte boundary.
-template <class T, int N> __device__ __forceinline__ void get(const T *p, float (&v)[N])
-{
-    if constexpr (N == 1) {
-        v[0] = to_float(*p);
-    } else {
-        constexpr int kWords = N * sizeof(T) / 16;
-        uint4 w[kWords];
-        T t[N];
-#pragma unroll
-        for (int i = 0; i < kWords; i++) w[i] = reinterpret_cast<const uint4 *>(p)[i];
-        memcpy(t, w, sizeof w);
-#pragma unroll
-        for (int i = 0; i < N; i++) v[i] = to_float(t[i]);
-    }
-}
-template <class T, int N> __device__ __forceinline__ void put(T *p, const float (&v)[N])
-{
-    if constexpr (N == 1) {
-        *p = from_float<T>(v[0]);
-    } else {
-        constexpr int kWords = N * sizeof(T) / 16;
-        uint4 w[kWords];
-        T t[N];
-#pragma unroll
-        for (int i = 0; i < N; i++) t[i] = from_float<T>(v[i]);
-        memcpy(w, t, sizeof w);
-#pragma unroll
-        for (int i = 0; i < kWords; i++) reinterpret_cast<uint4 *>(p)[i] = w[i];
-    }
-}
-template <class T, int N> __device__ __forceinline__ void get_param(const NormArgs &a, const void *p, u64 at, float (&v)[N])
-{
-    if constexpr (sizeof(T) != 4)
-        if (!a.params_f32) return get<T, N>(static_cast<const T *>(p) + at, v);
-    get<float, N>(static_cast<const float *>(p) + at, v);
-}
-
-// Sums over the block of up to two values a thread, in a fixed order; the
-// two halves of `part` are used in turn, so that one barrier is enough.
-struct Reducer {
-    float2 (*part)[32];
-    u32 turn, warps;
-    __device__ __forceinline__ float2 operator()(float a, float b)
+// A row as it lies in memory, so that the next one costs few registers.
+template <class T, int N, int E> struct RawRow {
+    static constexpr int kPieces = E / N;
+    std::conditional_t<N == 1, T, uint4> piece[kPieces];
+    __device__ __forceinline__ void fetch(const T *row, u32 hidden, u32 threads)
     {
-        a = group_sum<32>(a);
-        b = group_sum<32>(b);
-        if (warps == 1) return make_float2(a, b);
-        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        const u32 lane = threadIdx.x & 31;
-        float2 v = lane < warps ? part[turn][lane] : make_float2(0.0f, 0.0f);
-        turn ^= 1;
-        return make_float2(group_sum<32>(v.x), group_sum<32>(v.y));
+#pragma unroll
+        for (int i = 0; i < kPieces; i++) {
+            const u32 c = (i * threads + threadIdx.x) * N;
+            if constexpr (N == 1) {
+                piece[i] = from_float<T>(0.0f);
+                if (c < hidden) piece[i] = row[c];
+            } else {
+                piece[i] = make_uint4(0, 0, 0, 0);
+                if (c < hidden) piece[i] = *reinterpret_cast<const uint4 *>(row + c);
+            }
+        }
     }
-    __device__ __forceinline__ float operator()(float a)
+    __device__ __forceinline__ void widen(float (&v)[E]) const
     {
-        a = group_sum<32>(a);
-        if (warps == 1) return a;
-        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5].x = a;
-        __syncthreads();
-        const u32 lane = threadIdx.x & 31;
-        const float v = lane < warps ? part[turn][lane].x : 0.0f;
-        turn ^= 1;
-        return group_sum<32>(v);
+#pragma unroll
+        for (int i = 0; i < kPieces; i++) {
+            if constexpr (N == 1) v[i] = to_float(piece[i]);
+            else widen_piece<T, N>(piece[i], &v[i * N]);
+        }
     }
 };
 
-// (mean, 1 / deviation) of a row; values beyond it are 0.  The deviation comes
-// from the differences to the mean, so a mean far from 0 costs it nothing.
-template <int N, int PIECES>
-__device__ __forceinline__ float2 moments(const NormArgs &a, Reducer &sum, const float (&v)[PIECES][N], u32 threads)
-{
-    float mean = 0.0f, s = 0.0f;
-    if (a.layer) {
-#pragma unroll
-        for (int i = 0; i < PIECES; i++)
-#pragma unroll
-            for (int j = 0; j < N; j++) s += v[i][j];
-        mean = sum(s) * a.inv_hidden;
-        s = 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < PIECES; i++)
-        if ((i * threads + threadIdx.x) * N < a.hidden)
-#pragma unroll
-            for (int j = 0; j < N; j++) s = fmaf(v[i][j] - mean, v[i][j] - mean, s);
-    return make_float2(mean, 1.0f / sqrtf(fmaf(sum(s), a.inv_hidden, a.eps)));
-}
-
-// Threads a block at most, by shape_of().
-template <class T, int N, int PIECES> constexpr u32 kMostThreads = PIECES < (N > 1 ? 4 : 16) ? 512 : MV_NORM_MAX_HIDDEN / (N * PIECES);
-
-// ---- forward ----------------------------------------------------------------
-template <class T, int N, int PIECES> __global__ void __launch_bounds__(kMostThreads<T, N, PIECES>) k_norm(const NormArgs a)
+template <class T, class P, int N, int E> __global__ void __launch_bounds__(kMostThreads, N > 1 && E <= 16 ? 2 : 1) k_norm(const NormArgs a)
 {
     __shared__ float2 part[2][32];
-    const u32 threads = blockDim.x;
+    const u32 threads = blockDim.x, hidden = a.hidden;
+    const bool layer = a.layer;
     Reducer sum = {part, 0, threads / 32};
+    const T *y = static_cast<const T *>(a.y), *residual = static_cast<const T *>(a.residual);
+    RawRow<T, N, E> next_y, next_residual;
+    auto fetch = [&](u64 t) {
+        if (t >= a.tokens) return;
+        next_y.fetch(y + t * a.y_stride, hidden, threads);
+        if (residual) next_residual.fetch(residual + t * a.residual_stride, hidden, threads);
+    };
+    fetch(blockIdx.x);
     for (u64 t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        float v[PIECES][N], res[PIECES][N];
-        const T *y = static_cast<const T *>(a.y) + t * a.y_stride, *residual = static_cast<const T *>(a.residual) + t * a.residual_stride;
-#pragma unroll
-        for (int i = 0; i < PIECES; i++) {
-            const u32 c = (i * threads + threadIdx.x) * N;
-#pragma unroll
-            for (int j = 0; j < N; j++) v[i][j] = res[i][j] = 0.0f;
-            if (c < a.hidden) {
-                get<T, N>(y + c, v[i]);
-                if (a.residual) get<T, N>(residual + c, res[i]);
-            }
-        }
+        float v[E], w[E];
+        next_y.widen(v);
+        RawRow<T, N, E> res = next_residual;
+        fetch(t + gridDim.x);
         if (a.post) {
-            const float2 m = moments<N, PIECES>(a, sum, v, threads);
-#pragma unroll
-            for (int i = 0; i < PIECES; i++) {
-                const u32 c = (i * threads + threadIdx.x) * N;
-                if (c >= a.hidden) continue;
-                float w[N], b[N];
-#pragma unroll
-                for (int j = 0; j < N; j++) b[j] = 0.0f;
-                get_param<T, N>(a, a.post, c, w);
-                if (a.post_bias) get_param<T, N>(a, a.post_bias, c, b);
-#pragma unroll
-                for (int j = 0; j < N; j++) v[i][j] = fmaf((v[i][j] - m.x) * m.y, w[j], b[j]);
+            normalise<N>(a, layer, sum, v, threads);
+            get_row<P, N>(static_cast<const P *>(a.post), hidden, threads, w);
+            mul_row(v, v, w);
+            if (a.post_bias) {
+                get_row<P, N>(static_cast<const P *>(a.post_bias), hidden, threads, w);
+                add_row(v, v, w);
             }
         }
-        const u64 gate_row = a.gate ? t / a.run * a.hidden : 0;
-#pragma unroll
-        for (int i = 0; i < PIECES; i++) {
-            const u32 c = (i * threads + threadIdx.x) * N;
-            if (c >= a.hidden) continue;
-            if (a.gate) {
-                float g[N];
-                get_param<T, N>(a, a.gate, gate_row + c, g);
-#pragma unroll
-                for (int j = 0; j < N; j++) v[i][j] *= g[j];
-            }
-            if (a.residual)
-#pragma unroll
-                for (int j = 0; j < N; j++) v[i][j] = fmaf(a.alpha, res[i][j], v[i][j]);
-            if (a.r) put<T, N>(static_cast<T *>(a.r) + t * a.hidden + c, v[i]);
+        if (a.gate) {
+            get_row<P, N>(static_cast<const P *>(a.gate) + (u64)((u32)t / (u32)a.run) * hidden, hidden, threads, w);
+            mul_row(v, v, w);
         }
-        const float2 m = moments<N, PIECES>(a, sum, v, threads);
-#pragma unroll
-        for (int i = 0; i < PIECES; i++) {
-            const u32 c = (i * threads + threadIdx.x) * N;
-            if (c >= a.hidden) continue;
-            float w[N], b[N];
-#pragma unroll
-            for (int j = 0; j < N; j++) b[j] = 0.0f;
-            get_param<T, N>(a, a.weight, c, w);
-            if (a.bias) get_param<T, N>(a, a.bias, c, b);
-#pragma unroll
-            for (int j = 0; j < N; j++) w[j] = fmaf((v[i][j] - m.x) * m.y, w[j], b[j]);
-            put<T, N>(static_cast<T *>(a.n) + t * a.hidden + c, w);
+        if (residual) {
+            res.widen(w);
+            fma_row(v, w, a.alpha, v);
         }
+        if (a.r) put_row<T, N>(static_cast<T *>(a.r) + t * hidden, hidden, threads, v);
+        normalise<N>(a, layer, sum, v, threads);
+        get_row<P, N>(static_cast<const P *>(a.weight), hidden, threads, w);
+        mul_row(v, v, w);
+        if (a.bias) {
+            get_row<P, N>(static_cast<const P *>(a.bias), hidden, threads, w);
+            add_row(v, v, w);
+        }
+        put_row<T, N>(static_cast<T *>(a.n) + t * hidden, hidden, threads, v);
     }
 }
 
-// ---- backward ---------------------------------------------------------------
-// With G = dr + the gradient through N(r), whose g = dn weight:
-//   N'(x): (g - mean(g x^) x^ - [layer] mean(g)) / deviation, x^ = N(x)
-//   dresidual = alpha G, dgate = sum G u, du = gate G, dpost = sum du y^,
-//   dpost_bias = sum du, dy = N'(y) of du post, dweight = sum dn r^, dbias = sum dn.
-// A block takes a run of rows and adds up its columns' sums in registers.  The
-// statistics are computed again from y and the residual, which costs no bytes.
-// The next row is copied to shared memory while this one is worked on, every
-// thread its own pieces, so that nothing waits for another's.
-template <class T, int N, int PIECES, bool POST, bool BIAS>
-__global__ void __launch_bounds__(kMostThreads<T, N, PIECES>) k_norm_grad(const NormArgs a)
-{
-    constexpr bool kCanStage = N * sizeof(T) >= 4;
-    constexpr u32 kBytes = N * sizeof(T);
-    extern __shared__ __align__(16) unsigned char stage[];
-    __shared__ float2 part[2][32];
-    const u32 threads = blockDim.x, tid = threadIdx.x;
-    Reducer sum = {part, 0, threads / 32};
-    const u64 first = blockIdx.x * a.rows, last = min(first + a.rows, a.tokens);
-    const void *const from[4] = {a.y, a.residual, a.dn, a.dr};
-    const u64 strides[4] = {a.y_stride, a.residual_stride, a.dn_stride, a.dr_stride};
-    const u32 stage_at = (u32)__cvta_generic_to_shared(stage);
-    auto fetch = [&](u64 t, u32 buffer) {
-        if constexpr (kCanStage) {
-            if (t < last)
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    if (from[k])
-#pragma unroll
-                        for (int i = 0; i < PIECES; i++) {
-                            const u32 c = (i * threads + tid) * N;
-                            if (c >= a.hidden) continue;
-                            const u32 to = stage_at + (((buffer * 4 + k) * PIECES + i) * threads + tid) * kBytes;
-                            const T *p = static_cast<const T *>(from[k]) + t * strides[k] + c;
-                            if constexpr (kBytes == 16)
-                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
-                            else
-                                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
-                        }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-    };
-    auto piece = [&](u64 t, u32 buffer, int k, int i, float (&v)[N]) {
-        const u32 c = (i * threads + tid) * N;
-        if (kCanStage && a.staged)
-            get<T, N>(reinterpret_cast<const T *>(stage + (((buffer * 4 + k) * PIECES + i) * threads + tid) * kBytes), v);
-        else
-            get<T, N>(static_cast<const T *>(from[k]) + t * strides[k] + c, v);
-    };
-    float dw[PIECES][N], db[BIAS ? PIECES : 1][N], dp[POST ? PIECES : 1][N], dpb[POST && BIAS ? PIECES : 1][N], dg[POST ? PIECES : 1][N];
-#pragma unroll
-    for (int i = 0; i < PIECES; i++)
-#pragma unroll
-        for (int j = 0; j < N; j++) {
-            dw[i][j] = 0.0f;
-            if constexpr (BIAS) db[i][j] = 0.0f;
-            if constexpr (POST) dp[i][j] = dg[i][j] = 0.0f;
-            if constexpr (POST && BIAS) dpb[i][j] = 0.0f;
-        }
-    auto store_gate = [&](u64 g) {
-        if constexpr (POST) {
-#pragma unroll
-            for (int i = 0; i < PIECES; i++) {
-                const u32 c = (i * threads + tid) * N;
-                if (c >= a.hidden) continue;
-                put<float, N>(a.gate_sums + (blockIdx.x + g) * a.hidden + c, dg[i]);
-#pragma unroll
-                for (int j = 0; j < N; j++) dg[i][j] = 0.0f;
-            }
-        }
-    };
-    if (a.staged) fetch(first, 0);
-    u64 gate = POST && a.gate ? first / a.run : 0;
-    u32 buffer = 0;
-    for (u64 t = first; t < last; t++, buffer ^= 1) {
-        if (a.staged) {
-            fetch(t + 1, buffer ^ 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        }
-        if (POST && a.gate && !a.dgate && t / a.run != gate) {
-            store_gate(gate);
-            gate = t / a.run;
-        }
-        const u64 gate_row = POST && a.gate ? t / a.run * a.hidden : 0;
-        float v[PIECES][N];
-#pragma unroll
-        for (int i = 0; i < PIECES; i++) {
-#pragma unroll
-            for (int j = 0; j < N; j++) v[i][j] = 0.0f;
-            if ((i * threads + tid) * N < a.hidden) piece(t, buffer, 0, i, v[i]);
-        }
-        float2 my = make_float2(0.0f, 1.0f);
-        const bool post = POST && a.post;
-        if (post) my = moments<N, PIECES>(a, sum, v, threads);
-        // y of a piece, normed where it is, and the branch before its gate
-        auto branch = [&](u32 c, float (&yn)[N], float (&u)[N]) {
-#pragma unroll
-            for (int j = 0; j < N; j++) u[j] = yn[j];
-            if (post) {
-                float w[N], b[N];
-#pragma unroll
-                for (int j = 0; j < N; j++) b[j] = 0.0f;
-                get_param<T, N>(a, a.post, c, w);
-                if (BIAS && a.post_bias) get_param<T, N>(a, a.post_bias, c, b);
-#pragma unroll
-                for (int j = 0; j < N; j++) {
-                    yn[j] = (yn[j] - my.x) * my.y;
-                    u[j] = fmaf(yn[j], w[j], b[j]);
-                }
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < PIECES; i++) {
-            const u32 c = (i * threads + tid) * N;
-            if (c >= a.hidden) continue;
-            float u[N];
-            branch(c, v[i], u);
-            if (POST && a.gate) {
-                float g[N];
-                get_param<T, N>(a, a.gate, gate_row + c, g);
-#pragma unroll
-                for (int j = 0; j < N; j++) u[j] *= g[j];
-            }
-            if (a.residual) {
-                float s[N];
-                piece(t, buffer, 1, i, s);
-#pragma unroll
-                for (int j = 0; j < N; j++) u[j] = fmaf(a.alpha, s[j], u[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < N; j++) v[i][j] = u[j];
-        }
-        const float2 mr = moments<N, PIECES>(a, sum, v, threads);
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PIECES; i++) {
-            const u32 c = (i * threads + tid) * N;
-            if (c >= a.hidden) continue;
-            float d[N], w[N];
-            piece(t, buffer, 2, i, d);
-            get_param<T, N>(a, a.weight, c, w);
-#pragma unroll
-            for (int j = 0; j < N; j++) {
-                v[i][j] = (v[i][j] - mr.x) * mr.y;
-                dw[i][j] = fmaf(d[j], v[i][j], dw[i][j]);
-                if constexpr (BIAS) db[i][j] += d[j];
-                const float g = d[j] * w[j];
-                s0 += g;
-                s1 = fmaf(g, v[i][j], s1);
-            }
-        }
-        float2 m = sum(s0, s1);
-        float mean = a.layer ? m.x * a.inv_hidden : 0.0f, slope = m.y * a.inv_hidden;
-        s0 = s1 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PIECES; i++) {
-            const u32 c = (i * threads + tid) * N;
-            if (c >= a.hidden) continue;
-            float d[N], w[N], e[N];
-            piece(t, buffer, 2, i, d);
-            get_param<T, N>(a, a.weight, c, w);
-#pragma unroll
-            for (int j = 0; j < N; j++) e[j] = 0.0f;
-            if (a.dr) piece(t, buffer, 3, i, e);
-#pragma unroll
-            for (int j = 0; j < N; j++) v[i][j] = fmaf(fmaf(-slope, v[i][j], fmaf(d[j], w[j], -mean)), mr.y, e[j]);
-            if (a.dresidual) {
-#pragma unroll
-                for (int j = 0; j < N; j++) e[j] = a.alpha * v[i][j];
-                put<T, N>(static_cast<T *>(a.dresidual) + t * a.hidden + c, e);
-            }
-            if constexpr (POST) {
-                float yn[N], u[N];
-                piece(t, buffer, 0, i, yn);
-                branch(c, yn, u);
-                if (a.gate) {
-                    float g[N];
-                    get_param<T, N>(a, a.gate, gate_row + c, g);
-                    if (a.dgate) {
-#pragma unroll
-                        for (int j = 0; j < N; j++) u[j] *= v[i][j];
-                        if (a.params_f32) put<float, N>(static_cast<float *>(a.dgate) + gate_row + c, u);
-                        else put<T, N>(static_cast<T *>(a.dgate) + gate_row + c, u);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < N; j++) dg[i][j] = fmaf(v[i][j], u[j], dg[i][j]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < N; j++) v[i][j] *= g[j];
-                }
-                if (post) {
-                    get_param<T, N>(a, a.post, c, w);
-#pragma unroll
-                    for (int j = 0; j < N; j++) {
-                        dp[i][j] = fmaf(v[i][j], yn[j], dp[i][j]);
-                        if constexpr (BIAS) dpb[i][j] += v[i][j];
-                        v[i][j] *= w[j];
-                        s0 += v[i][j];
-                        s1 = fmaf(v[i][j], yn[j], s1);
-                    }
-                }
-            }
-        }
-        if (post) {
-            m = sum(s0, s1);
-            mean = a.layer ? m.x * a.inv_hidden : 0.0f;
-            slope = m.y * a.inv_hidden;
-        }
-#pragma unroll
-        for (int i = 0; i < PIECES; i++) {
-            const u32 c = (i * threads + tid) * N;
-            if (c >= a.hidden) continue;
-            if (post) {
-                float yn[N];
-                piece(t, buffer, 0, i, yn);
-#pragma unroll
-                for (int j = 0; j < N; j++) v[i][j] = (v[i][j] - mean - slope * ((yn[j] - my.x) * my.y)) * my.y;
-            }
-            put<T, N>(static_cast<T *>(a.dy) + t * a.hidden + c, v[i]);
-        }
-    }
-    if (kCanStage && a.staged) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (POST && a.gate && !a.dgate && first < last) store_gate(gate);
-    float *to = a.sums + (u64)blockIdx.x * 4 * a.hidden;
-#pragma unroll
-    for (int i = 0; i < PIECES; i++) {
-        const u32 c = (i * threads + tid) * N;
-        if (c >= a.hidden) continue;
-        put<float, N>(to + c, dw[i]);
-        if constexpr (BIAS) put<float, N>(to + a.hidden + c, db[i]);
-        if constexpr (POST) put<float, N>(to + 2 * a.hidden + c, dp[i]);
-        if constexpr (POST && BIAS) put<float, N>(to + 3 * a.hidden + c, dpb[i]);
-    }
-}
-
-// The blocks' sums, added in their order: 32 columns a block of threads, every
-// warp the blocks w, w + 32, ..., then the warps'.
+// The blocks' sums, added in their order: four columns a lane, every eighth
+// block's a warp, then the warps'.
 struct AddArgs {
     const float *sums, *gate_sums;
     void *to[4], *dgate;
-    u64 hidden, blocks, run, rows, gates;
+    u64 hidden, pitch, blocks, run, rows, gates;
     u32 params_f32;
 };
-template <class T> __global__ void __launch_bounds__(1024) k_norm_add(const AddArgs a)
+template <class T> __global__ void __launch_bounds__(256) k_norm_add(const AddArgs a)
 {
-    __shared__ float part[32][33];
+    __shared__ float4 part[8][32];
+    const u32 lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const u64 c = ((u64)blockIdx.x * 32 + lane) * 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const u32 x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const u64 c = (u64)blockIdx.x * 32 + x;
     // what: four parameters, then the gates
     for (u64 what = blockIdx.y; what < 4 + a.gates; what += gridDim.y) {
         void *out = what < 4 ? a.to[what] : a.dgate;
         if (!out) continue;
-        const float *from = a.sums + what * a.hidden;
-        u64 pitch = 4 * a.hidden, first = 0, last = a.blocks, at = 0;
+        const float *from = a.sums + what * a.pitch;
+        u64 step = 4 * a.pitch, first = 0, last = a.blocks, at = 0;
         if (what >= 4) {
             const u64 g = what - 4;
             first = g * a.run / a.rows;
             last = ((g + 1) * a.run - 1) / a.rows + 1;
-            from = a.gate_sums + g * a.hidden;
-            pitch = a.hidden;
+            from = a.gate_sums + g * a.pitch;
+            step = a.pitch;
             at = g * a.hidden;
         }
-        float s = 0.0f;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (c < a.hidden)
-#pragma unroll 4
-            for (u64 b = first + y; b < last; b += 32) s += from[b * pitch + c];
+#pragma unroll 8
+            for (u64 b = first + warp; b < last; b += 8) {
+                const float4 w = *reinterpret_cast<const float4 *>(from + b * step + c);
+                s.x += w.x; s.y += w.y; s.z += w.z; s.w += w.w;
+            }
         __syncthreads();
-        part[y][x] = s;
+        part[warp][lane] = s;
         __syncthreads();
-        s = group_sum<32>(part[x][y]);                       // column y of the block's 32
-        const u64 mine = (u64)blockIdx.x * 32 + y;
-        if (x == 0 && mine < a.hidden) {
-            if (a.params_f32) static_cast<float *>(out)[at + mine] = s;
-            else static_cast<T *>(out)[at + mine] = from_float<T>(s);
-        }
+        if (threadIdx.x >= 128) continue;
+        const u64 mine = (u64)blockIdx.x * 128 + threadIdx.x;
+        if (mine >= a.hidden) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (u32 i = 0; i < 8; i++) v += reinterpret_cast<const float *>(part[i])[threadIdx.x];
+        if (a.params_f32) static_cast<float *>(out)[at + mine] = v;
+        else static_cast<T *>(out)[at + mine] = from_float<T>(v);
     }
 }
 
 // ---- host ---------------------------------------------------------------
-struct Shape {
-    u32 n, pieces, threads;
-};
-// Few pieces a thread where the row is short, more where a block would pass 512 threads.
-Shape shape_of(u32 hidden, u32 size, bool wide)
+// Sixteen elements a thread: fewer make the block's sums a larger part of the
+// work, more do not fit the registers of the backward pass (32, for rows
+// that 512 threads would not hold otherwise).  Short rows are one warp's.
+NormShape shape_of(u32 hidden, u32 size, bool wide)
 {
-    const u32 n = wide ? 16 / size : 1;
-    u32 pieces = wide ? 1 : 4;
-    while (pieces < (wide ? 4u : 16u) && hidden > n * pieces * 512) pieces *= wide ? 2 : 4;
-    const u32 threads = (hidden + n * pieces - 1) / (n * pieces);
-    return {n, pieces, (threads + 31) / 32 * 32};
+    const u32 n = wide ? 16 / size : 1, few = wide ? n : 4;
+    const u32 e = hidden <= 32 * few ? few : hidden <= 16 * kMostThreads ? 16 : 32;
+    const u32 threads = (hidden + e - 1) / e;
+    return {n, e / n, (threads + 31) / 32 * 32};
 }
 
 bool dense(const void *p, u64 stride, u32 n, u32 size) { return !p || (aligned(p, 16) && stride % n == 0 && (n * size == 16)); }
 
-int check(const mv_norm_desc *d, bool grad)
+int check(const mv_norm_desc *d)
 {
     if (!d || !d->hidden || d->dtype > MV_BF16 || (d->param_dtype != d->dtype && d->param_dtype != MV_F32) ||
         d->kind > MV_NORM_LAYER || !std::isfinite(d->alpha) || !(d->eps >= 0.0f) || !std::isfinite(d->eps) ||
@@ -494,7 +163,6 @@ int check(const mv_norm_desc *d, bool grad)
         !aligned(d->post_bias, param) || !aligned(d->gate, param))
         return MV_EINVAL;
     if (d->tokens && (!d->y || !d->weight)) return MV_EINVAL;
-    (void)grad;
     return MV_OK;
 }
 
@@ -528,25 +196,32 @@ NormArgs arguments(const mv_norm_desc *d)
     return a;
 }
 
-template <class T> int run_norm(const NormArgs &a, const Shape &s, u32 sms, cudaStream_t stream)
+template <class T, class P> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, cudaStream_t stream)
 {
-    const u32 an_sm = std::max(1u, 1536 / s.threads);
+    // blocks for as many threads as the registers hold
+    const u32 an_sm = std::max(1u, std::min(16u, (s.n > 1 && s.n * s.pieces <= 16 ? 1024 : 512) / s.threads));
     const dim3 grid((u32)std::min<u64>(a.tokens, (u64)sms * an_sm));
     constexpr int N = 16 / sizeof(T);
+    const u32 e = s.n * s.pieces;
     if (s.n > 1) {
-        if (s.pieces == 1) return launch(k_norm<T, N, 1>, grid, s.threads, 0, stream, a);
-        if (s.pieces == 2) return launch(k_norm<T, N, 2>, grid, s.threads, 0, stream, a);
-        return launch(k_norm<T, N, 4>, grid, s.threads, 0, stream, a);
+        if (e == N) return launch(k_norm<T, P, N, N>, grid, s.threads, 0, stream, a);
+        if (e == 16) return launch(k_norm<T, P, N, 16>, grid, s.threads, 0, stream, a);
+        return launch(k_norm<T, P, N, 32>, grid, s.threads, 0, stream, a);
     }
-    if (s.pieces == 4) return launch(k_norm<T, 1, 4>, grid, s.threads, 0, stream, a);
-    return launch(k_norm<T, 1, 16>, grid, s.threads, 0, stream, a);
+    if (e == 4) return launch(k_norm<T, P, 1, 4>, grid, s.threads, 0, stream, a);
+    if (e == 16) return launch(k_norm<T, P, 1, 16>, grid, s.threads, 0, stream, a);
+    return launch(k_norm<T, P, 1, 32>, grid, s.threads, 0, stream, a);
+}
+template <class T> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, cudaStream_t stream)
+{
+    return a.params_f32 ? run_norm<T, float>(a, s, sms, stream) : run_norm<T, T>(a, s, sms, stream);
 }
 
 struct GradPlan {
-    Shape shape;
+    NormShape shape;
     bool staged, each;                  // each: every token has a gate of its own
     u32 smem;
-    u64 blocks, rows, sums, gate_sums, total;
+    u64 blocks, rows, pitch, gate_sums, total;
 };
 GradPlan grad_plan(const mv_norm_desc *d, bool wide)
 {
@@ -558,41 +233,15 @@ GradPlan grad_plan(const mv_norm_desc *d, bool wide)
     p.smem = p.staged ? smem : 0;
     const u32 sms = std::max(1u, sm_count());
     const u32 an_sm = std::max(1u, std::min(512 / p.shape.threads, p.smem ? 220u * 1024 / (p.smem + 2048) : 16u));
+    // at least four rows a block: its sums are written and read once for all of them
     const u64 blocks = std::min<u64>((d->tokens + 3) / 4, (u64)sms * std::min(an_sm, 16u));
     p.rows = (d->tokens + blocks - 1) / blocks;
     p.blocks = (d->tokens + p.rows - 1) / p.rows;
     p.each = d->gate && d->gates == d->tokens;
-    p.sums = 0;
-    p.gate_sums = (p.blocks * 4 * d->hidden * 4 + 255) / 256 * 256;
-    p.total = p.gate_sums + (d->gate && !p.each ? (p.blocks + d->gates) * d->hidden * 4 : 0);
+    p.pitch = (d->hidden + 3) / 4 * 4;
+    p.gate_sums = (p.blocks * 4 * p.pitch * 4 + 255) / 256 * 256;
+    p.total = p.gate_sums + (d->gate && !p.each ? (p.blocks + d->gates) * p.pitch * 4 : 0);
     return p;
-}
-
-template <class T, int N, int PIECES, bool POST, bool BIAS> int run_grad(const NormArgs &a, const GradPlan &p, cudaStream_t stream)
-{
-    const auto kernel = k_norm_grad<T, N, PIECES, POST, BIAS>;
-    if (p.smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) != cudaSuccess)
-        return MV_ECUDA;
-    return launch(kernel, dim3((u32)p.blocks), p.shape.threads, p.smem, stream, a);
-}
-template <class T, int N, int PIECES> int run_grad(const NormArgs &a, const GradPlan &p, bool post, bool bias, cudaStream_t stream)
-{
-    if (post) return bias ? run_grad<T, N, PIECES, true, true>(a, p, stream) : run_grad<T, N, PIECES, true, false>(a, p, stream);
-    return bias ? run_grad<T, N, PIECES, false, true>(a, p, stream) : run_grad<T, N, PIECES, false, false>(a, p, stream);
-}
-template <class T> int run_grad(const NormArgs &a, const GradPlan &p, bool post, bool bias, const AddArgs &add, cudaStream_t stream)
-{
-    constexpr int N = 16 / sizeof(T);
-    int rc;
-    if (p.shape.n > 1) {
-        rc = p.shape.pieces == 1 ? run_grad<T, N, 1>(a, p, post, bias, stream)
-           : p.shape.pieces == 2 ? run_grad<T, N, 2>(a, p, post, bias, stream) : run_grad<T, N, 4>(a, p, post, bias, stream);
-    } else {
-        rc = p.shape.pieces == 4 ? run_grad<T, 1, 4>(a, p, post, bias, stream) : run_grad<T, 1, 16>(a, p, post, bias, stream);
-    }
-    if (rc != MV_OK) return rc;
-    const dim3 grid((u32)((add.hidden + 31) / 32), (u32)std::min<u64>(4 + add.gates, 65535));
-    return launch_after(k_norm_add<T>, grid, 1024, 0, stream, add);
 }
 
 }  // namespace mvblock
@@ -601,7 +250,7 @@ using namespace mvblock;
 
 extern "C" int mv_norm(const mv_norm_desc *d, void *n, void *r, void *stream)
 {
-    const int rc = check(d, false);
+    const int rc = check(d);
     if (rc != MV_OK || d->tokens == 0) return rc;
     const u64 size = dtype_size(d->dtype);
     if (!n || !aligned(n, size) || !aligned(r, size)) return MV_EINVAL;
@@ -610,7 +259,7 @@ extern "C" int mv_norm(const mv_norm_desc *d, void *n, void *r, void *stream)
     NormArgs a = arguments(d);
     a.n = n;
     a.r = r;
-    const Shape s = shape_of(a.hidden, (u32)size, wide_row(d) && aligned(n, 16) && aligned(r, 16));
+    const NormShape s = shape_of(a.hidden, (u32)size, wide_row(d) && aligned(n, 16) && aligned(r, 16));
     cudaStream_t on = static_cast<cudaStream_t>(stream);
     if (d->dtype == MV_F32) return run_norm<float>(a, s, sms, on);
     return d->dtype == MV_F16 ? run_norm<__half>(a, s, sms, on) : run_norm<__nv_bfloat16>(a, s, sms, on);
@@ -618,7 +267,7 @@ extern "C" int mv_norm(const mv_norm_desc *d, void *n, void *r, void *stream)
 
 static int check_grad(const mv_norm_desc *d, const mv_norm_grads *g)
 {
-    const int rc = check(d, true);
+    const int rc = check(d);
     if (rc != MV_OK) return rc;
     if (!g) return MV_EINVAL;
     const u64 size = dtype_size(d->dtype), param = dtype_size(d->param_dtype);
@@ -676,7 +325,7 @@ extern "C" int mv_norm_backward(const mv_norm_desc *d, const mv_norm_grads *g, v
     a.dgate = p.each ? g->dgate : nullptr;
     a.rows = p.rows;
     a.staged = p.staged;
-    a.sums = reinterpret_cast<float *>(ws + p.sums);
+    a.sums = reinterpret_cast<float *>(ws);
     a.gate_sums = reinterpret_cast<float *>(ws + p.gate_sums);
     AddArgs add = {};
     add.sums = a.sums;
@@ -687,12 +336,18 @@ extern "C" int mv_norm_backward(const mv_norm_desc *d, const mv_norm_grads *g, v
     add.to[3] = g->dpost_bias;
     add.dgate = d->gate && !p.each ? g->dgate : nullptr;
     add.hidden = d->hidden;
+    add.pitch = a.pitch = p.pitch;
     add.blocks = p.blocks;
     add.run = a.run;
     add.rows = p.rows;
     add.gates = add.dgate ? d->gates : 0;
     add.params_f32 = a.params_f32;
-    const bool post = d->post || d->gate, bias = d->bias || d->post_bias;
-    if (d->dtype == MV_F32) return run_grad<float>(a, p, post, bias, add, on);
-    return d->dtype == MV_F16 ? run_grad<__half>(a, p, post, bias, add, on) : run_grad<__nv_bfloat16>(a, p, post, bias, add, on);
+    const bool post = d->post || d->gate, bias = a.layer || d->bias || d->post_bias;
+    const int done = d->dtype == MV_F32 ? run_norm_grad<float>(a, p.shape, p.blocks, p.smem, post, bias, on)
+                   : d->dtype == MV_F16 ? run_norm_grad<__half>(a, p.shape, p.blocks, p.smem, post, bias, on)
+                                        : run_norm_grad<__nv_bfloat16>(a, p.shape, p.blocks, p.smem, post, bias, on);
+    if (done != MV_OK) return done;
+    const dim3 grid((u32)((d->hidden + 127) / 128), (u32)std::min<u64>(4 + add.gates, 65535));
+    return d->dtype == MV_BF16 ? launch_after(k_norm_add<__nv_bfloat16>, grid, 256, 0, on, add)
+                               : launch_after(k_norm_add<__half>, grid, 256, 0, on, add);
 }

@@ -1,0 +1,213 @@
+// Shared by mv_norm.cu and mv_norm_grad.cu: rows held by blocks.
+#pragma once
+
+#include <cstring>
+#include <type_traits>
+
+#include "mv_block.cuh"
+
+namespace mvblock {
+
+struct NormArgs {
+    const void *y, *residual, *dn, *dr;
+    const void *weight, *bias, *post, *post_bias, *gate;
+    void *n, *r, *dy, *dresidual, *dgate;           // dgate: where every token has a gate of its own
+    u64 tokens, y_stride, residual_stride, dn_stride, dr_stride;
+    u64 run, rows;                                  // tokens that share a gate; rows a block (backward)
+    u32 hidden, layer, params_f32, staged;
+    float alpha, eps, inv_hidden;
+    u64 pitch;                                      // hidden, up to whole fours
+    float *sums;                                    // a block's sums for weight, bias, post, post_bias  [blocks, 4, pitch]
+    float *gate_sums;                               // and for the gates of its rows                     [blocks + gates, pitch]
+};
+
+struct NormShape {
+    u32 n, pieces, threads;
+};
+template <class T> int run_norm_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream);
+
+// A thread's E elements of a row: pieces of N neighbours (16 bytes, or one
+// where rows lie on no 16-byte boundary), threads next to each other.  Beyond
+// the row they are 0.  Arithmetic goes by pairs, two values an instruction.
+template <class T, int N> __device__ __forceinline__ void widen_piece(const uint4 &w, float *v)
+{
+    const u32 words[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = __uint_as_float(words[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                v[2 * i] = __uint_as_float(words[i] << 16);
+                v[2 * i + 1] = __uint_as_float(words[i] & 0xFFFF0000u);
+            } else {
+                __half2 h;
+                memcpy(&h, &words[i], 4);
+                const float2 f = __half22float2(h);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+}
+template <class T, int N> __device__ __forceinline__ void get(const T *p, float *v)
+{
+    if constexpr (N == 1) {
+        v[0] = to_float(*p);
+    } else {
+        constexpr int kEach = 16 / sizeof(T);       // of a 16-byte word
+#pragma unroll
+        for (int i = 0; i < N; i += kEach) widen_piece<T, kEach>(*reinterpret_cast<const uint4 *>(p + i), v + i);
+    }
+}
+template <class T, int N> __device__ __forceinline__ void put(T *p, const float *v)
+{
+    if constexpr (N == 1) {
+        *p = from_float<T>(v[0]);
+    } else {
+        constexpr int kEach = 16 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < N; i += kEach) {
+            uint4 w;
+            if constexpr (sizeof(T) == 4) {
+                w = make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
+            } else {
+                u32 words[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+                        memcpy(&words[j], &h, 4);
+                    } else {
+                        const __half2 h = __floats2half2_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+                        memcpy(&words[j], &h, 4);
+                    }
+                }
+                w = make_uint4(words[0], words[1], words[2], words[3]);
+            }
+            *reinterpret_cast<uint4 *>(p + i) = w;
+        }
+    }
+}
+// Elements of a row (or of a parameter), 0 beyond `hidden`; to a row.
+template <class T, int N, int E> __device__ __forceinline__ void get_row(const T *row, u32 hidden, u32 threads, float (&v)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E / N; i++) {
+        const u32 c = (i * threads + threadIdx.x) * N;
+#pragma unroll
+        for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
+        if (c < hidden) get<T, N>(row + c, &v[i * N]);
+    }
+}
+template <class T, int N, int E> __device__ __forceinline__ void put_row(T *row, u32 hidden, u32 threads, const float (&v)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E / N; i++) {
+        const u32 c = (i * threads + threadIdx.x) * N;
+        if (c < hidden) put<T, N>(row + c, &v[i * N]);
+    }
+}
+
+__device__ __forceinline__ float2 two(const float *v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ void set(float *v, float2 w) { v[0] = w.x; v[1] = w.y; }
+// d = a b + c; d = a b; d = a + b, of E elements; one operand may be a number.
+template <int E> __device__ __forceinline__ void fma_row(float (&d)[E], const float (&a)[E], const float (&b)[E], const float (&c)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) set(&d[i], __ffma2_rn(two(&a[i]), two(&b[i]), two(&c[i])));
+}
+template <int E> __device__ __forceinline__ void fma_row(float (&d)[E], const float (&a)[E], float b, const float (&c)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) set(&d[i], __ffma2_rn(two(&a[i]), make_float2(b, b), two(&c[i])));
+}
+template <int E> __device__ __forceinline__ void mul_row(float (&d)[E], const float (&a)[E], const float (&b)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) set(&d[i], __fmul2_rn(two(&a[i]), two(&b[i])));
+}
+template <int E> __device__ __forceinline__ void mul_row(float (&d)[E], const float (&a)[E], float b)
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) set(&d[i], __fmul2_rn(two(&a[i]), make_float2(b, b)));
+}
+template <int E> __device__ __forceinline__ void add_row(float (&d)[E], const float (&a)[E], const float (&b)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) set(&d[i], __fadd2_rn(two(&a[i]), two(&b[i])));
+}
+template <int E> __device__ __forceinline__ void add_row(float (&d)[E], const float (&a)[E], float b)
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) set(&d[i], __fadd2_rn(two(&a[i]), make_float2(b, b)));
+}
+template <int E> __device__ __forceinline__ float sum_row(const float (&a)[E])
+{
+    float2 s = two(&a[0]);
+#pragma unroll
+    for (int i = 2; i < E; i += 2) s = __fadd2_rn(s, two(&a[i]));
+    return s.x + s.y;
+}
+template <int E> __device__ __forceinline__ float dot_row(const float (&a)[E], const float (&b)[E])
+{
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) s = __ffma2_rn(two(&a[i]), two(&b[i]), s);
+    return s.x + s.y;
+}
+
+// Sums over the block of one or two values a thread, in a fixed order; the two
+// halves of `part` are used in turn, so that one barrier is enough.
+struct Reducer {
+    float2 (*part)[32];
+    u32 turn, warps;
+    __device__ __forceinline__ float2 operator()(float a, float b)
+    {
+        a = group_sum<32>(a);
+        b = group_sum<32>(b);
+        if (warps == 1) return make_float2(a, b);
+        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        const u32 lane = threadIdx.x & 31;
+        const float2 v = lane < warps ? part[turn][lane] : make_float2(0.0f, 0.0f);
+        turn ^= 1;
+        return make_float2(group_sum<32>(v.x), group_sum<32>(v.y));
+    }
+    __device__ __forceinline__ float operator()(float a)
+    {
+        a = group_sum<32>(a);
+        if (warps == 1) return a;
+        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5].x = a;
+        __syncthreads();
+        const u32 lane = threadIdx.x & 31;
+        const float v = lane < warps ? part[turn][lane].x : 0.0f;
+        turn ^= 1;
+        return group_sum<32>(v);
+    }
+};
+
+// v becomes N(v) without its parameters; its mean (0 where that stays in) and
+// one over what it was divided by come back.  The deviation is taken from the differences to the mean, so a mean
+// far from 0 costs it nothing.
+template <int N, int E> __device__ __forceinline__ float2 normalise(const NormArgs &a, bool layer, Reducer &sum, float (&v)[E], u32 threads)
+{
+    float mean = 0.0f;
+    if (layer) {
+        mean = sum(sum_row(v)) * a.inv_hidden;
+        add_row(v, v, -mean);
+#pragma unroll
+        for (int i = 0; i < E / N; i++)
+            if ((i * threads + threadIdx.x) * N >= a.hidden)
+#pragma unroll
+                for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
+    }
+    const float inverse = rsqrtf(fmaf(sum(dot_row(v, v)), a.inv_hidden, a.eps));
+    mul_row(v, v, inverse);
+    return make_float2(mean, inverse);
+}
+
+constexpr u32 kMostThreads = MV_NORM_MAX_HIDDEN / 32;   // a block: 32 elements a thread where rows are longest
+
+}  // namespace mvblock
