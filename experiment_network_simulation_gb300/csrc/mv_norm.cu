@@ -11,7 +11,7 @@
 namespace mvblock {
 
 // A row as it lies in memory, so that the next one costs few registers.
-template <class T, int N, int E> struct RawRow {
+template <class T, int N, int E, bool WHOLE> struct RawRow {
     static constexpr int kPieces = E / N;
     std::conditional_t<N == 1, T, uint4> piece[kPieces];
     __device__ __forceinline__ void fetch(const T *row, u32 hidden, u32 threads)
@@ -20,11 +20,11 @@ template <class T, int N, int E> struct RawRow {
         for (int i = 0; i < kPieces; i++) {
             const u32 c = (i * threads + threadIdx.x) * N;
             if constexpr (N == 1) {
-                piece[i] = from_float<T>(0.0f);
-                if (c < hidden) piece[i] = row[c];
+                if constexpr (!WHOLE) piece[i] = from_float<T>(0.0f);
+                if (WHOLE || c < hidden) piece[i] = row[c];
             } else {
-                piece[i] = make_uint4(0, 0, 0, 0);
-                if (c < hidden) piece[i] = *reinterpret_cast<const uint4 *>(row + c);
+                if constexpr (!WHOLE) piece[i] = make_uint4(0, 0, 0, 0);
+                if (WHOLE || c < hidden) piece[i] = *reinterpret_cast<const uint4 *>(row + c);
             }
         }
     }
@@ -38,14 +38,15 @@ template <class T, int N, int E> struct RawRow {
     }
 };
 
-template <class T, class P, int N, int E> __global__ void __launch_bounds__(kMostThreads, N > 1 && E <= 16 ? 2 : 1) k_norm(const NormArgs a)
+template <class T, class P, int N, int E, bool WHOLE> __global__ void __launch_bounds__(kMostThreads, N > 1 && E <= 16 ? 2 : 1) k_norm(const NormArgs a)
 {
-    __shared__ float2 part[2][32];
+    __shared__ __align__(16) float part[2][2][16];
     const u32 threads = blockDim.x, hidden = a.hidden;
     const bool layer = a.layer;
     Reducer sum = {part, 0, threads / 32};
+    sum.start();
     const T *y = static_cast<const T *>(a.y), *residual = static_cast<const T *>(a.residual);
-    RawRow<T, N, E> next_y, next_residual;
+    RawRow<T, N, E, WHOLE> next_y, next_residual;
     auto fetch = [&](u64 t) {
         if (t >= a.tokens) return;
         next_y.fetch(y + t * a.y_stride, hidden, threads);
@@ -55,34 +56,34 @@ template <class T, class P, int N, int E> __global__ void __launch_bounds__(kMos
     for (u64 t = blockIdx.x; t < a.tokens; t += gridDim.x) {
         float v[E], w[E];
         next_y.widen(v);
-        RawRow<T, N, E> res = next_residual;
+        RawRow<T, N, E, WHOLE> res = next_residual;
         fetch(t + gridDim.x);
         if (a.post) {
-            normalise<N>(a, layer, sum, v, threads);
-            get_row<P, N>(static_cast<const P *>(a.post), hidden, threads, w);
+            normalise<N, WHOLE>(a, layer, sum, v, threads);
+            get_row<P, N, WHOLE>(static_cast<const P *>(a.post), hidden, threads, w);
             mul_row(v, v, w);
             if (a.post_bias) {
-                get_row<P, N>(static_cast<const P *>(a.post_bias), hidden, threads, w);
+                get_row<P, N, WHOLE>(static_cast<const P *>(a.post_bias), hidden, threads, w);
                 add_row(v, v, w);
             }
         }
         if (a.gate) {
-            get_row<P, N>(static_cast<const P *>(a.gate) + (u64)((u32)t / (u32)a.run) * hidden, hidden, threads, w);
+            get_row<P, N, WHOLE>(static_cast<const P *>(a.gate) + (u64)((u32)t / (u32)a.run) * hidden, hidden, threads, w);
             mul_row(v, v, w);
         }
         if (residual) {
             res.widen(w);
             fma_row(v, w, a.alpha, v);
         }
-        if (a.r) put_row<T, N>(static_cast<T *>(a.r) + t * hidden, hidden, threads, v);
-        normalise<N>(a, layer, sum, v, threads);
-        get_row<P, N>(static_cast<const P *>(a.weight), hidden, threads, w);
+        if (a.r) put_row<T, N, WHOLE>(static_cast<T *>(a.r) + t * hidden, hidden, threads, v);
+        normalise<N, WHOLE>(a, layer, sum, v, threads);
+        get_row<P, N, WHOLE>(static_cast<const P *>(a.weight), hidden, threads, w);
         mul_row(v, v, w);
         if (a.bias) {
-            get_row<P, N>(static_cast<const P *>(a.bias), hidden, threads, w);
+            get_row<P, N, WHOLE>(static_cast<const P *>(a.bias), hidden, threads, w);
             add_row(v, v, w);
         }
-        put_row<T, N>(static_cast<T *>(a.n) + t * hidden, hidden, threads, v);
+        put_row<T, N, WHOLE>(static_cast<T *>(a.n) + t * hidden, hidden, threads, v);
     }
 }
 
@@ -144,7 +145,7 @@ NormShape shape_of(u32 hidden, u32 size, bool wide)
     const u32 n = wide ? 16 / size : 1, few = wide ? n : 4;
     const u32 e = hidden <= 32 * few ? few : hidden <= 16 * kMostThreads ? 16 : 32;
     const u32 threads = (hidden + e - 1) / e;
-    return {n, e / n, (threads + 31) / 32 * 32};
+    return {n, e / n, (threads + 31) / 32 * 32, hidden % (32 * e) == 0};
 }
 
 bool dense(const void *p, u64 stride, u32 n, u32 size) { return !p || (aligned(p, 16) && stride % n == 0 && (n * size == 16)); }
@@ -204,13 +205,14 @@ template <class T, class P> int run_norm(const NormArgs &a, const NormShape &s, 
     constexpr int N = 16 / sizeof(T);
     const u32 e = s.n * s.pieces;
     if (s.n > 1) {
-        if (e == N) return launch(k_norm<T, P, N, N>, grid, s.threads, 0, stream, a);
-        if (e == 16) return launch(k_norm<T, P, N, 16>, grid, s.threads, 0, stream, a);
-        return launch(k_norm<T, P, N, 32>, grid, s.threads, 0, stream, a);
+        if (e == N) return launch(k_norm<T, P, N, N, false>, grid, s.threads, 0, stream, a);
+        if (e == 16 && s.whole) return launch(k_norm<T, P, N, 16, true>, grid, s.threads, 0, stream, a);
+        if (e == 16) return launch(k_norm<T, P, N, 16, false>, grid, s.threads, 0, stream, a);
+        return launch(k_norm<T, P, N, 32, false>, grid, s.threads, 0, stream, a);
     }
-    if (e == 4) return launch(k_norm<T, P, 1, 4>, grid, s.threads, 0, stream, a);
-    if (e == 16) return launch(k_norm<T, P, 1, 16>, grid, s.threads, 0, stream, a);
-    return launch(k_norm<T, P, 1, 32>, grid, s.threads, 0, stream, a);
+    if (e == 4) return launch(k_norm<T, P, 1, 4, false>, grid, s.threads, 0, stream, a);
+    if (e == 16) return launch(k_norm<T, P, 1, 16, false>, grid, s.threads, 0, stream, a);
+    return launch(k_norm<T, P, 1, 32, false>, grid, s.threads, 0, stream, a);
 }
 template <class T> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, cudaStream_t stream)
 {
@@ -227,12 +229,17 @@ GradPlan grad_plan(const mv_norm_desc *d, bool wide)
 {
     GradPlan p = {};
     const u32 size = (u32)dtype_size(d->dtype);
-    p.shape = shape_of((u32)d->hidden, size, wide);
-    const u32 smem = 2 * 4 * p.shape.pieces * p.shape.threads * p.shape.n * size;
-    p.staged = p.shape.n * size >= 4 && smem <= 200 * 1024;
+    const u32 hidden = (u32)d->hidden, n = wide ? 16 / size : 1;
+    // eight elements a thread and two rows at a time, or sixteen and one where a row is too long for that
+    const bool two = hidden <= 8 * kGradThreads<false>;
+    const u32 e = two ? 8 : 16, threads = ((hidden + e - 1) / e + 31) / 32 * 32;
+    p.shape = {n, e / n, threads, false};
+    const u32 smem = 5 * (two ? 2 : 1) * e * threads * size;
+    p.staged = n * size >= 4 && smem <= 220 * 1024;
     p.smem = p.staged ? smem : 0;
     const u32 sms = std::max(1u, sm_count());
-    const u32 an_sm = std::max(1u, std::min(512 / p.shape.threads, p.smem ? 220u * 1024 / (p.smem + 2048) : 16u));
+    const u32 held = (threads <= (u32)kGradThreads<true> ? kGradThreads<true> : kGradThreads<false>) / threads;
+    const u32 an_sm = std::max(1u, std::min(held, p.smem ? 224u * 1024 / (p.smem + 2048) : 16u));
     // at least four rows a block: its sums are written and read once for all of them
     const u64 blocks = std::min<u64>((d->tokens + 3) / 4, (u64)sms * std::min(an_sm, 16u));
     p.rows = (d->tokens + blocks - 1) / blocks;

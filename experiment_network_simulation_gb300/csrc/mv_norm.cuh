@@ -23,6 +23,7 @@ struct NormArgs {
 
 struct NormShape {
     u32 n, pieces, threads;
+    bool whole;                                     // the threads' pieces are the row, and no more
 };
 template <class T> int run_norm_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream);
 
@@ -90,24 +91,25 @@ template <class T, int N> __device__ __forceinline__ void put(T *p, const float 
         }
     }
 }
-// Elements of a row (or of a parameter), 0 beyond `hidden`; to a row.
-template <class T, int N, int E> __device__ __forceinline__ void get_row(const T *row, u32 hidden, u32 threads, float (&v)[E])
+// Elements of a row (or of a parameter), 0 beyond `hidden`; to a row.  WHOLE:
+// the threads' pieces are the row, and nothing lies beyond.
+template <class T, int N, bool WHOLE, int E> __device__ __forceinline__ void get_row(const T *row, u32 hidden, u32 threads, float (&v)[E])
 {
+    row += threadIdx.x * N;
 #pragma unroll
     for (int i = 0; i < E / N; i++) {
-        const u32 c = (i * threads + threadIdx.x) * N;
+        if constexpr (!WHOLE)
 #pragma unroll
-        for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
-        if (c < hidden) get<T, N>(row + c, &v[i * N]);
+            for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
+        if (WHOLE || (i * threads + threadIdx.x) * N < hidden) get<T, N>(row + i * threads * N, &v[i * N]);
     }
 }
-template <class T, int N, int E> __device__ __forceinline__ void put_row(T *row, u32 hidden, u32 threads, const float (&v)[E])
+template <class T, int N, bool WHOLE, int E> __device__ __forceinline__ void put_row(T *row, u32 hidden, u32 threads, const float (&v)[E])
 {
+    row += threadIdx.x * N;
 #pragma unroll
-    for (int i = 0; i < E / N; i++) {
-        const u32 c = (i * threads + threadIdx.x) * N;
-        if (c < hidden) put<T, N>(row + c, &v[i * N]);
-    }
+    for (int i = 0; i < E / N; i++)
+        if (WHOLE || (i * threads + threadIdx.x) * N < hidden) put<T, N>(row + i * threads * N, &v[i * N]);
 }
 
 __device__ __forceinline__ float2 two(const float *v) { return make_float2(v[0], v[1]); }
@@ -159,49 +161,69 @@ template <int E> __device__ __forceinline__ float dot_row(const float (&a)[E], c
 }
 
 // Sums over the block of one or two values a thread, in a fixed order; the two
-// halves of `part` are used in turn, so that one barrier is enough.
+// halves of `part` are used in turn, so that one barrier is enough.  After it
+// every thread adds the warps' sums itself: a second round of shuffles would
+// take twice as long.
 struct Reducer {
-    float2 (*part)[32];
+    float (*part)[2][16];
     u32 turn, warps;
+    __device__ __forceinline__ static float warps_sum(const float *p, u32 warps)
+    {
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (u32 i = 0; i < 16; i += 4) {
+            if (i >= warps) break;
+            const float4 w = *reinterpret_cast<const float4 *>(p + i);
+            s = __fadd2_rn(s, __fadd2_rn(make_float2(w.x, w.y), make_float2(w.z, w.w)));
+        }
+        return s.x + s.y;
+    }
+    __device__ __forceinline__ void start()         // warps that are not there add nothing
+    {
+        if (threadIdx.x < 32)
+            for (u32 i = threadIdx.x; i < 64; i += 32) part[0][0][i] = 0.0f;
+        __syncthreads();
+    }
     __device__ __forceinline__ float2 operator()(float a, float b)
     {
-        a = group_sum<32>(a);
-        b = group_sum<32>(b);
-        if (warps == 1) return make_float2(a, b);
-        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = make_float2(a, b);
+        // the first exchange leaves a to the lower half-warp, b to the upper
+        const bool upper = threadIdx.x & 16;
+        float v = (upper ? b : a) + __shfl_xor_sync(kFull, upper ? a : b, 16);
+        v = group_sum<16>(v);
+        if (warps == 1) return make_float2(__shfl_sync(kFull, v, 0), __shfl_sync(kFull, v, 16));
+        if ((threadIdx.x & 15) == 0) part[turn][upper][threadIdx.x >> 5] = v;
         __syncthreads();
-        const u32 lane = threadIdx.x & 31;
-        const float2 v = lane < warps ? part[turn][lane] : make_float2(0.0f, 0.0f);
+        const float2 s = make_float2(warps_sum(part[turn][0], warps), warps_sum(part[turn][1], warps));
         turn ^= 1;
-        return make_float2(group_sum<32>(v.x), group_sum<32>(v.y));
+        return s;
     }
     __device__ __forceinline__ float operator()(float a)
     {
         a = group_sum<32>(a);
         if (warps == 1) return a;
-        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5].x = a;
+        if ((threadIdx.x & 31) == 0) part[turn][0][threadIdx.x >> 5] = a;
         __syncthreads();
-        const u32 lane = threadIdx.x & 31;
-        const float v = lane < warps ? part[turn][lane].x : 0.0f;
+        const float s = warps_sum(part[turn][0], warps);
         turn ^= 1;
-        return group_sum<32>(v);
+        return s;
     }
 };
 
 // v becomes N(v) without its parameters; its mean (0 where that stays in) and
 // one over what it was divided by come back.  The deviation is taken from the differences to the mean, so a mean
 // far from 0 costs it nothing.
-template <int N, int E> __device__ __forceinline__ float2 normalise(const NormArgs &a, bool layer, Reducer &sum, float (&v)[E], u32 threads)
+template <int N, bool WHOLE, int E> __device__ __forceinline__ float2 normalise(const NormArgs &a, bool layer, Reducer &sum, float (&v)[E], u32 threads)
 {
     float mean = 0.0f;
     if (layer) {
         mean = sum(sum_row(v)) * a.inv_hidden;
         add_row(v, v, -mean);
+        if constexpr (!WHOLE)
 #pragma unroll
-        for (int i = 0; i < E / N; i++)
-            if ((i * threads + threadIdx.x) * N >= a.hidden)
+            for (int i = 0; i < E / N; i++)
+                if ((i * threads + threadIdx.x) * N >= a.hidden)
 #pragma unroll
-                for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
+                    for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
     }
     const float inverse = rsqrtf(fmaf(sum(dot_row(v, v)), a.inv_hidden, a.eps));
     mul_row(v, v, inverse);
@@ -209,5 +231,8 @@ template <int N, int E> __device__ __forceinline__ float2 normalise(const NormAr
 }
 
 constexpr u32 kMostThreads = MV_NORM_MAX_HIDDEN / 32;   // a block: 32 elements a thread where rows are longest
+
+// The backward pass: threads a block where each has 96 registers, and where it has 72.
+template <bool FEW> constexpr int kGradThreads = FEW ? 640 : 896;
 
 }  // namespace mvblock

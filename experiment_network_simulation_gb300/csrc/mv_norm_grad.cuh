@@ -7,59 +7,66 @@
 //   dpost_bias = sum du, dy = N'(y) of du post, dweight = sum dn r^, dbias = sum dn.
 // A block takes a run of rows and adds up its columns' sums in registers.  The
 // statistics are computed again from y and the residual, which costs no bytes.
-// The next row is copied to shared memory while this one is worked on, every
-// thread its own pieces, so that nothing waits for another's.
+// A row is a chain of four sums over the block, so two rows go through it
+// together: half the barriers, and parameters are read once for both.  The next
+// rows are copied to shared memory meanwhile, every thread its own pieces, so
+// that nothing waits for another's: each array as soon as its last use is over,
+// y, which is used to the end, in two buffers.
 #pragma once
 
 #include "mv_norm.cuh"
 
 namespace mvblock {
 
-template <class T, class P, int N, int E, bool POST, bool BIAS>
-__global__ void __launch_bounds__(kMostThreads) k_norm_grad(const NormArgs a)
+// R rows at a time; E elements a thread; MOST threads a block.
+template <class T, class P, int N, int E, int R, bool POST, bool BIAS, int MOST>
+__global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
 {
     constexpr bool kCanStage = N * sizeof(T) >= 4;
-    constexpr u32 kBytes = N * sizeof(T), kPieces = E / N;
+    constexpr u32 kBytes = N * sizeof(T), kPieces = E / N, kSlots = 5;        // y twice, residual, dn, dr
     extern __shared__ __align__(16) unsigned char stage[];
-    __shared__ float2 part[2][32];
+    __shared__ float2 part[2][R][32];
     const u32 threads = blockDim.x, tid = threadIdx.x, hidden = a.hidden;
     const bool layer = BIAS && a.layer, post = POST && a.post, gated = POST && a.gate, staged = kCanStage && a.staged;
-    Reducer sum = {part, 0, threads / 32};
+    // pieces of this thread; a piece beyond the row is taken from its start, and counts for nothing
+    auto within = [&](u32 i) { return (i * threads + tid) * N < hidden; };
+    auto column = [&](u32 i) { return within(i) ? (i * threads + tid) * N : 0; };
     const u64 first = blockIdx.x * a.rows, last = min(first + a.rows, a.tokens);
     const T *const from[4] = {static_cast<const T *>(a.y), static_cast<const T *>(a.residual), static_cast<const T *>(a.dn),
                               static_cast<const T *>(a.dr)};
     const u64 strides[4] = {a.y_stride, a.residual_stride, a.dn_stride, a.dr_stride};
     const u32 stage_at = (u32)__cvta_generic_to_shared(stage) + tid * kBytes, piece_bytes = threads * kBytes;
-    auto fetch = [&](u64 t, u32 buffer) {
+    // Rows that go together share their gate; a second one that is not there is the first again, and counts for nothing.
+    u64 gate = gated ? first / a.run : 0, gate_end = gated ? (gate + 1) * a.run : ~0ull;
+    auto end_of = [&](u64 t) {
+        u64 end = min(t + R, last);
+        if (gated) end = min(end, t < gate_end ? gate_end : gate_end + a.run);
+        return end;
+    };
+    auto fetch = [&](int k, u64 t, u32 slot) {
         if constexpr (kCanStage) {
-            if (t < last) {
+            if (staged && from[k] && t < last) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    if (!from[k]) continue;
-                    const T *row = from[k] + t * strides[k];
+                for (int r = 0; r < R; r++) {
+                    const T *row = from[k] + min(t + r, end_of(t) - 1) * strides[k];
 #pragma unroll
                     for (u32 i = 0; i < kPieces; i++) {
-                        const u32 c = (i * threads + tid) * N;
-                        const u32 to = stage_at + ((buffer * 4 + k) * kPieces + i) * piece_bytes;
-                        if (c < hidden) {
-                            if constexpr (kBytes == 16)
-                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(row + c) : "memory");
-                            else
-                                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(row + c) : "memory");
-                        }
+                        const u32 to = stage_at + ((slot * R + r) * kPieces + i) * piece_bytes;
+                        if constexpr (kBytes == 16)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(row + column(i)) : "memory");
+                        else
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(row + column(i)) : "memory");
                     }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     };
-    u64 t = first;
-    u32 buffer = 0;
-    auto load = [&](int k, float (&v)[E]) {
+    auto load = [&](int k, u64 t, int r, u32 slot, float (&v)[E]) {
         if (staged) {
 #pragma unroll
             for (u32 i = 0; i < kPieces; i++) {
-                const u32 at = stage_at + ((buffer * 4 + k) * kPieces + i) * piece_bytes;
+                const u32 at = stage_at + ((slot * R + r) * kPieces + i) * piece_bytes;
                 if constexpr (kBytes == 16) {
                     uint4 w;
                     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
@@ -69,173 +76,314 @@ __global__ void __launch_bounds__(kMostThreads) k_norm_grad(const NormArgs a)
                 }
             }
         } else {
-            get_row<T, N>(from[k] + t * strides[k], hidden, threads, v);
+            const T *row = from[k] + min(t + r, end_of(t) - 1) * strides[k];
+#pragma unroll
+            for (u32 i = 0; i < kPieces; i++) get<T, N>(row + column(i), &v[i * N]);
         }
     };
-    auto param = [&](const void *p, float (&v)[E]) { get_row<P, N>(static_cast<const P *>(p), hidden, threads, v); };
-    if (staged)                             // beyond the row nothing is ever copied
-        for (u32 i = 0; i < 8 * kPieces; i++) {
-            if constexpr (kBytes == 16) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stage_at + i * piece_bytes), "r"(0u) : "memory");
-            else asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + i * piece_bytes), "r"(0u) : "memory");
+    auto param = [&](const void *p, u64 at, float (&v)[E]) {
+#pragma unroll
+        for (u32 i = 0; i < kPieces; i++) get<P, N>(static_cast<const P *>(p) + at + column(i), &v[i * N]);
+    };
+    auto store = [&](void *p, u64 t, const float (&v)[E]) {
+#pragma unroll
+        for (u32 i = 0; i < kPieces; i++)
+            if (within(i)) put<T, N>(static_cast<T *>(p) + t * hidden + column(i), &v[i * N]);
+    };
+    auto store_sums = [&](float *p, const float (&v)[E]) {
+#pragma unroll
+        for (u32 i = 0; i < kPieces; i++)
+            if (within(i)) put<float, N>(p + column(i), &v[i * N]);
+    };
+    auto hide = [&](float (&v)[E]) {                          // what lies beyond the row
+#pragma unroll
+        for (u32 i = 0; i < kPieces; i++)
+            if (!within(i))
+#pragma unroll
+                for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
+    };
+    // Sums over the block of a value of each of R rows; or of two.
+    const u32 warps = threads / 32, lane = tid & 31;
+    u32 turn = 0;
+    auto sums2 = [&](float2 (&s)[R]) {
+        float mine[R];
+        const bool upper = lane & 16;
+#pragma unroll
+        for (int r = 0; r < R; r++) {                         // the first exchange leaves x to the lower half-warp, y to the upper
+            mine[r] = (upper ? s[r].y : s[r].x) + __shfl_xor_sync(kFull, upper ? s[r].x : s[r].y, 16);
+            mine[r] = group_sum<16>(mine[r]);
         }
+        if (warps > 1) {
+            if ((lane & 15) == 0)
+#pragma unroll
+                for (int r = 0; r < R; r++) (upper ? part[turn][r][tid >> 5].y : part[turn][r][tid >> 5].x) = mine[r];
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const float2 w = lane < warps ? part[turn][r][lane] : make_float2(0.0f, 0.0f);
+                mine[r] = (upper ? w.y : w.x) + __shfl_xor_sync(kFull, upper ? w.x : w.y, 16);
+                mine[r] = group_sum<16>(mine[r]);
+            }
+            turn ^= 1;
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++) s[r] = make_float2(__shfl_sync(kFull, mine[r], 0), __shfl_sync(kFull, mine[r], 16));
+    };
+    auto sums = [&](float (&s)[R]) {
+        if constexpr (R == 2) {                               // two rows' values as one row's two
+            const bool upper = lane & 16;
+            float mine = (upper ? s[1] : s[0]) + __shfl_xor_sync(kFull, upper ? s[0] : s[1], 16);
+            mine = group_sum<16>(mine);
+            if (warps > 1) {
+                if ((lane & 15) == 0) (upper ? part[turn][0][tid >> 5].y : part[turn][0][tid >> 5].x) = mine;
+                __syncthreads();
+                const float2 w = lane < warps ? part[turn][0][lane] : make_float2(0.0f, 0.0f);
+                mine = (upper ? w.y : w.x) + __shfl_xor_sync(kFull, upper ? w.x : w.y, 16);
+                mine = group_sum<16>(mine);
+                turn ^= 1;
+            }
+            s[0] = __shfl_sync(kFull, mine, 0);
+            s[1] = __shfl_sync(kFull, mine, 16);
+        } else {
+            float mine = group_sum<32>(s[0]);
+            if (warps > 1) {
+                if (lane == 0) part[turn][0][tid >> 5].x = mine;
+                __syncthreads();
+                mine = group_sum<32>(lane < warps ? part[turn][0][lane].x : 0.0f);
+                turn ^= 1;
+            }
+            s[0] = mine;
+        }
+    };
+    // v becomes N(v) of every row; means and what they were divided by, inverted
+    auto normalise = [&](float (&v)[R][E], float (&mean)[R], float (&inverse)[R]) {
+        float s[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) mean[r] = 0.0f;
+        if (layer) {
+#pragma unroll
+            for (int r = 0; r < R; r++) { hide(v[r]); s[r] = sum_row(v[r]); }
+            sums(s);
+#pragma unroll
+            for (int r = 0; r < R; r++) { mean[r] = s[r] * a.inv_hidden; add_row(v[r], v[r], -mean[r]); }
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++) { hide(v[r]); s[r] = dot_row(v[r], v[r]); }
+        sums(s);
+#pragma unroll
+        for (int r = 0; r < R; r++) { inverse[r] = rsqrtf(fmaf(s[r], a.inv_hidden, a.eps)); mul_row(v[r], v[r], inverse[r]); }
+    };
+    // means of g and of g x^, of every row
+    auto slopes = [&](const float (&g)[R][E], const float (&x)[R][E], float (&mean)[R], float (&slope)[R]) {
+        if (layer) {
+            float2 s[R];
+#pragma unroll
+            for (int r = 0; r < R; r++) s[r] = make_float2(sum_row(g[r]), dot_row(g[r], x[r]));
+            sums2(s);
+#pragma unroll
+            for (int r = 0; r < R; r++) { mean[r] = s[r].x * a.inv_hidden; slope[r] = s[r].y * a.inv_hidden; }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; r++) slope[r] = dot_row(g[r], x[r]);
+            sums(slope);
+#pragma unroll
+            for (int r = 0; r < R; r++) { mean[r] = 0.0f; slope[r] *= a.inv_hidden; }
+        }
+    };
+
     // the sums: of weight, bias, post, post_bias, gate
     float dw[E] = {}, db[BIAS ? E : 2] = {}, dp[POST ? E : 2] = {}, dpb[POST && BIAS ? E : 2] = {}, dg[POST ? E : 2] = {};
-    u64 gate = gated ? first / a.run : 0, gate_end = gated ? (gate + 1) * a.run : ~0ull;
-    if (staged) fetch(first, 0);
-    for (; t < last; t++, buffer ^= 1) {
-        if (staged) {
-            fetch(t + 1, buffer ^ 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        }
+    u32 buffer = 0;
+    fetch(0, first, 0);
+    fetch(1, first, 2);
+    fetch(2, first, 3);
+    fetch(3, first, 4);
+    for (u64 t = first, next; t < last; t = next, buffer ^= 1) {
         if constexpr (POST) {
             if (t == gate_end) {
-                if (!a.dgate) put_row<float, N>(a.gate_sums + (blockIdx.x + gate) * a.pitch, hidden, threads, dg);
+                if (!a.dgate) store_sums(a.gate_sums + (blockIdx.x + gate) * a.pitch, dg);
                 gate++;
                 gate_end += a.run;
 #pragma unroll
                 for (int i = 0; i < E; i++) dg[i] = 0.0f;
             }
         }
-        const P *gates = static_cast<const P *>(a.gate) + gate * hidden;
-        float v[E], w[E], g[E];
-        load(0, v);
-        // as in the forward pass; y's norm is gone back to by its mean and deviation
-        float2 my = make_float2(0.0f, 1.0f);
+        next = end_of(t);
+        const bool lone = R == 2 && next - t < 2;             // only the first of two rows counts
+        fetch(0, next, buffer ^ 1);
+        const u64 gate_row = gate * hidden;
+        float v[R][E], w[E], mean[R], inverse[R], my[R], iy[R], slope[R];
+        if (staged) asm volatile("cp.async.wait_group 4;" ::: "memory");
+#pragma unroll
+        for (int r = 0; r < R; r++) load(0, t, r, buffer, v[r]);
+        // as in the forward pass
         if (post) {
-            my = normalise<N>(a, layer, sum, v, threads);
-            param(a.post, w);
-            mul_row(v, v, w);
+            normalise(v, my, iy);
+            param(a.post, 0, w);
+#pragma unroll
+            for (int r = 0; r < R; r++) mul_row(v[r], v[r], w);
             if constexpr (BIAS) {
                 if (a.post_bias) {
-                    param(a.post_bias, w);
-                    add_row(v, v, w);
+                    param(a.post_bias, 0, w);
+#pragma unroll
+                    for (int r = 0; r < R; r++) add_row(v[r], v[r], w);
                 }
             }
         }
         if (gated) {
-            param(gates, w);
-            mul_row(v, v, w);
+            param(a.gate, gate_row, w);
+#pragma unroll
+            for (int r = 0; r < R; r++) mul_row(v[r], v[r], w);
         }
-        if (from[1]) {
-            load(1, w);
-            fma_row(v, w, a.alpha, v);
+        if (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        if (from[1])
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                load(1, t, r, 2, w);
+                fma_row(v[r], w, a.alpha, v[r]);
+            }
+        fetch(1, next, 2);
+        normalise(v, mean, inverse);
+        if (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        float g[R][E];
+#pragma unroll
+        for (int r = 0; r < R; r++) load(2, t, r, 3, g[r]);
+        fetch(2, next, 3);
+        if (R == 2 && lone)
+#pragma unroll
+            for (int i = 0; i < E; i++) g[R - 1][i] = 0.0f;
+        param(a.weight, 0, w);
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            fma_row(dw, g[r], v[r], dw);
+            if constexpr (BIAS) add_row(db, g[r], db);
+            mul_row(g[r], g[r], w);
+            hide(g[r]);
         }
-        const float inverse = normalise<N>(a, layer, sum, v, threads).y;
-        load(2, g);
-        fma_row(dw, g, v, dw);
-        if constexpr (BIAS) add_row(db, g, db);
-        param(a.weight, w);
-        mul_row(g, g, w);
-        float mean = 0.0f, slope;
-        if (layer) {
-            const float2 m = sum(sum_row(g), dot_row(g, v));
-            mean = m.x * a.inv_hidden;
-            slope = m.y * a.inv_hidden;
-        } else {
-            slope = sum(dot_row(g, v)) * a.inv_hidden;
+        slopes(g, v, mean, slope);
+        if (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            fma_row(v[r], v[r], -slope[r], g[r]);
+            if (layer) add_row(v[r], v[r], -mean[r]);
+            if (from[3]) {
+                load(3, t, r, 4, w);
+                fma_row(v[r], v[r], inverse[r], w);
+            } else {
+                mul_row(v[r], v[r], inverse[r]);
+            }
+            if (R == 2 && r && lone)
+#pragma unroll
+                for (int i = 0; i < E; i++) v[r][i] = 0.0f;
+            if (a.dresidual) {
+                mul_row(w, v[r], a.alpha);
+                if (!(R == 2 && r && lone)) store(a.dresidual, t + r, w);
+            }
         }
-        fma_row(v, v, -slope, g);
-        if (layer) add_row(v, v, -mean);
-        if (from[3]) {
-            load(3, w);
-            fma_row(v, v, inverse, w);
-        } else {
-            mul_row(v, v, inverse);
-        }
-        if (a.dresidual) {
-            mul_row(w, v, a.alpha);
-            put_row<T, N>(static_cast<T *>(a.dresidual) + t * hidden, hidden, threads, w);
-        }
+        fetch(3, next, 4);
         if constexpr (POST) {
-            load(0, g);
-            if (post) {
-                if (layer) add_row(g, g, -my.x);
-                mul_row(g, g, my.y);               // y^
-                param(a.post, w);
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                load(0, t, r, buffer, g[r]);
+                if (post) {
+                    if (layer) add_row(g[r], g[r], -my[r]);
+                    mul_row(g[r], g[r], iy[r]);               // y^
+                }
             }
             if (gated) {
                 float u[E];
-                if (post) {
-                    mul_row(u, g, w);
-                    if constexpr (BIAS) {
-                        if (a.post_bias) {
-                            float b[E];
-                            param(a.post_bias, b);
-                            add_row(u, u, b);
+                if (post) param(a.post, 0, w);
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    if (post) {
+                        mul_row(u, g[r], w);
+                        if constexpr (BIAS) {
+                            if (a.post_bias) {
+                                float b[E];
+                                param(a.post_bias, 0, b);
+                                add_row(u, u, b);
+                            }
                         }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < E; i++) u[i] = g[r][i];
                     }
-                    if (a.dgate) mul_row(u, u, v);
-                    else fma_row(dg, u, v, dg);
-                } else {
-                    if (a.dgate) mul_row(u, g, v);
-                    else fma_row(dg, g, v, dg);
+                    if (a.dgate) {                            // a gate a token: one row at a time
+                        if (r == 0) {
+                            mul_row(u, u, v[r]);
+#pragma unroll
+                            for (u32 i = 0; i < kPieces; i++)
+                                if (within(i)) put<P, N>(static_cast<P *>(a.dgate) + gate_row + column(i), &u[i * N]);
+                        }
+                    } else {
+                        fma_row(dg, u, v[r], dg);
+                    }
                 }
-                if (a.dgate) put_row<P, N>(static_cast<P *>(a.dgate) + gate * hidden, hidden, threads, u);
-                param(gates, u);
-                mul_row(v, v, u);
+                param(a.gate, gate_row, w);
+#pragma unroll
+                for (int r = 0; r < R; r++) mul_row(v[r], v[r], w);
             }
             if (post) {
-                fma_row(dp, v, g, dp);
-                if constexpr (BIAS) add_row(dpb, dpb, v);
-                mul_row(v, v, w);
-                if (layer) {
-                    const float2 m = sum(sum_row(v), dot_row(v, g));
-                    mean = m.x * a.inv_hidden;
-                    slope = m.y * a.inv_hidden;
-                } else {
-                    slope = sum(dot_row(v, g)) * a.inv_hidden;
+                param(a.post, 0, w);
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    fma_row(dp, v[r], g[r], dp);
+                    if constexpr (BIAS) add_row(dpb, dpb, v[r]);
+                    mul_row(v[r], v[r], w);
+                    hide(v[r]);
                 }
-                fma_row(v, g, -slope, v);
-                if (layer) add_row(v, v, -mean);
-                mul_row(v, v, my.y);
+                slopes(v, g, mean, slope);
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    fma_row(v[r], g[r], -slope[r], v[r]);
+                    if (layer) add_row(v[r], v[r], -mean[r]);
+                    mul_row(v[r], v[r], iy[r]);
+                }
             }
         }
-        put_row<T, N>(static_cast<T *>(a.dy) + t * hidden, hidden, threads, v);
+#pragma unroll
+        for (int r = 0; r < R; r++)
+            if (!(R == 2 && r && lone)) store(a.dy, t + r, v[r]);
     }
     if (staged) asm volatile("cp.async.wait_group 0;" ::: "memory");
     float *to = a.sums + (u64)blockIdx.x * 4 * a.pitch;
-    put_row<float, N>(to, hidden, threads, dw);
-    if constexpr (BIAS) put_row<float, N>(to + a.pitch, hidden, threads, db);
+    store_sums(to, dw);
+    if constexpr (BIAS) store_sums(to + a.pitch, db);
     if constexpr (POST) {
-        put_row<float, N>(to + 2 * a.pitch, hidden, threads, dp);
-        if (gated && !a.dgate) put_row<float, N>(a.gate_sums + (blockIdx.x + gate) * a.pitch, hidden, threads, dg);
+        store_sums(to + 2 * a.pitch, dp);
+        if (gated && !a.dgate) store_sums(a.gate_sums + (blockIdx.x + gate) * a.pitch, dg);
     }
-    if constexpr (POST && BIAS) put_row<float, N>(to + 3 * a.pitch, hidden, threads, dpb);
+    if constexpr (POST && BIAS) store_sums(to + 3 * a.pitch, dpb);
 }
 
-template <class T, class P, int N, int E, bool POST, bool BIAS>
+template <class T, class P, int N, int E, int R, bool POST, bool BIAS, int MOST>
 int run_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, cudaStream_t stream)
 {
-    const auto kernel = k_norm_grad<T, P, N, E, POST, BIAS>;
+    const auto kernel = k_norm_grad<T, P, N, E, R, POST, BIAS, MOST>;
     if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return MV_ECUDA;
     return launch(kernel, dim3((u32)blocks), s.threads, smem, stream, a);
 }
-// Rows that are rare (longest, or on no 16-byte boundary) have the kernel with
-// all the sums, as it is without work that is not there.
-template <class T, class P, int N, int E>
-int run_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream)
-{
-    if constexpr (E == 32) {
-        return run_grad<T, P, N, E, true, true>(a, s, blocks, smem, stream);
-    } else {
-        if constexpr (N > 1)
-            if (!bias) return post ? run_grad<T, P, N, E, true, false>(a, s, blocks, smem, stream) : run_grad<T, P, N, E, false, false>(a, s, blocks, smem, stream);
-        return post ? run_grad<T, P, N, E, true, true>(a, s, blocks, smem, stream) : run_grad<T, P, N, E, false, true>(a, s, blocks, smem, stream);
-    }
-}
+// Fewer threads leave more registers to each, which the kernels with the most
+// sums need.  Rarer rows (longest, or on no 16-byte boundary) have kernels with
+// more sums than they may need.
 template <class T, class P> int run_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream)
 {
-    constexpr int N = 16 / sizeof(T);
-    const u32 e = s.n * s.pieces;
-    if (s.n > 1) {
-        if (e == N) return run_grad<T, P, N, N>(a, s, blocks, smem, post, bias, stream);
-        if (e == 16) return run_grad<T, P, N, 16>(a, s, blocks, smem, post, bias, stream);
-        return run_grad<T, P, N, 32>(a, s, blocks, smem, post, bias, stream);
+    constexpr int N = 16 / sizeof(T), kFew = kGradThreads<true>, kMany = kGradThreads<false>;
+    const bool few = s.threads <= kFew;
+    if (s.pieces * s.n == 8 && s.n > 1) {
+        if (!post) return bias ? run_grad<T, P, N, 8, 2, false, true, kMany>(a, s, blocks, smem, stream)
+                               : run_grad<T, P, N, 8, 2, false, false, kMany>(a, s, blocks, smem, stream);
+        if (few) return bias ? run_grad<T, P, N, 8, 2, true, true, kFew>(a, s, blocks, smem, stream)
+                             : run_grad<T, P, N, 8, 2, true, false, kFew>(a, s, blocks, smem, stream);
+        return bias ? run_grad<T, P, N, 8, 2, true, true, kMany>(a, s, blocks, smem, stream)
+                    : run_grad<T, P, N, 8, 2, true, false, kMany>(a, s, blocks, smem, stream);
     }
-    if (e == 4) return run_grad<T, P, 1, 4>(a, s, blocks, smem, post, bias, stream);
-    if (e == 16) return run_grad<T, P, 1, 16>(a, s, blocks, smem, post, bias, stream);
-    return run_grad<T, P, 1, 32>(a, s, blocks, smem, post, bias, stream);
+    if (s.pieces * s.n == 8)
+        return post ? run_grad<T, P, 1, 8, 2, true, true, kMany>(a, s, blocks, smem, stream)
+                    : run_grad<T, P, 1, 8, 2, false, true, kMany>(a, s, blocks, smem, stream);
+    return s.n > 1 ? run_grad<T, P, N, 16, 1, true, true, 1024>(a, s, blocks, smem, stream)
+                   : run_grad<T, P, 1, 16, 1, true, true, 1024>(a, s, blocks, smem, stream);
 }
 
 template <class T> int run_norm_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream)
