@@ -29,40 +29,50 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
     const u32 threads = blockDim.x, tid = threadIdx.x, hidden = a.hidden;
     const bool layer = BIAS && a.layer, post = POST && a.post, gated = POST && a.gate, staged = kCanStage && a.staged;
     // pieces of this thread; a piece beyond the row is taken from its start, and counts for nothing
-    auto within = [&](u32 i) { return (i * threads + tid) * N < hidden; };
-    auto column = [&](u32 i) { return within(i) ? (i * threads + tid) * N : 0; };
-    const u64 first = blockIdx.x * a.rows, last = min(first + a.rows, a.tokens);
-    const T *const from[4] = {static_cast<const T *>(a.y), static_cast<const T *>(a.residual), static_cast<const T *>(a.dn),
-                              static_cast<const T *>(a.dr)};
-    const u64 strides[4] = {a.y_stride, a.residual_stride, a.dn_stride, a.dr_stride};
-    const u32 stage_at = (u32)__cvta_generic_to_shared(stage) + tid * kBytes, piece_bytes = threads * kBytes;
+    const bool ragged = threads * E != hidden;
+    bool within[kPieces];
+    u32 column[kPieces];
+#pragma unroll
+    for (u32 i = 0; i < kPieces; i++) {
+        column[i] = (i * threads + tid) * N;
+        within[i] = column[i] < hidden;
+        if (!within[i]) column[i] = 0;
+    }
+    const u32 first = blockIdx.x * (u32)a.rows, last = (u32)min((u64)first + a.rows, a.tokens), run = (u32)a.run;
     // Rows that go together share their gate; a second one that is not there is the first again, and counts for nothing.
-    u64 gate = gated ? first / a.run : 0, gate_end = gated ? (gate + 1) * a.run : ~0ull;
-    auto end_of = [&](u64 t) {
-        u64 end = min(t + R, last);
-        if (gated) end = min(end, t < gate_end ? gate_end : gate_end + a.run);
+    u32 gate = gated ? first / run : 0;
+    u64 gate_end = gated ? (u64)(gate + 1) * run : ~0ull;
+    auto end_of = [&](u32 t) {
+        u32 end = min(t + R, last);
+        if (gated) end = (u32)min((u64)end, t < gate_end ? gate_end : gate_end + run);
         return end;
     };
-    auto fetch = [&](int k, u64 t, u32 slot) {
+    const void *const from[4] = {a.y, a.residual, a.dn, a.dr};
+    auto row_of = [&](int k, u32 row) {
+        const u64 stride = k == 0 ? a.y_stride : k == 1 ? a.residual_stride : k == 2 ? a.dn_stride : a.dr_stride;
+        return static_cast<const T *>(from[k]) + row * stride;
+    };
+    const u32 stage_at = (u32)__cvta_generic_to_shared(stage) + tid * kBytes, piece_bytes = threads * kBytes;
+    auto fetch = [&](int k, u32 t, u32 end, u32 slot) {
         if constexpr (kCanStage) {
             if (staged && from[k] && t < last) {
 #pragma unroll
                 for (int r = 0; r < R; r++) {
-                    const T *row = from[k] + min(t + r, end_of(t) - 1) * strides[k];
+                    const T *row = row_of(k, r ? end - 1 : t);
 #pragma unroll
                     for (u32 i = 0; i < kPieces; i++) {
                         const u32 to = stage_at + ((slot * R + r) * kPieces + i) * piece_bytes;
                         if constexpr (kBytes == 16)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(row + column(i)) : "memory");
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(row + column[i]) : "memory");
                         else
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(row + column(i)) : "memory");
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(row + column[i]) : "memory");
                     }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     };
-    auto load = [&](int k, u64 t, int r, u32 slot, float (&v)[E]) {
+    auto load = [&](int k, u32 t, u32 end, int r, u32 slot, float (&v)[E]) {
         if (staged) {
 #pragma unroll
             for (u32 i = 0; i < kPieces; i++) {
@@ -76,29 +86,31 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
                 }
             }
         } else {
-            const T *row = from[k] + min(t + r, end_of(t) - 1) * strides[k];
+            const T *row = row_of(k, r ? end - 1 : t);
 #pragma unroll
-            for (u32 i = 0; i < kPieces; i++) get<T, N>(row + column(i), &v[i * N]);
+            for (u32 i = 0; i < kPieces; i++) get<T, N>(row + column[i], &v[i * N]);
         }
     };
-    auto param = [&](const void *p, u64 at, float (&v)[E]) {
+    auto param = [&](const void *p, float (&v)[E]) {
 #pragma unroll
-        for (u32 i = 0; i < kPieces; i++) get<P, N>(static_cast<const P *>(p) + at + column(i), &v[i * N]);
+        for (u32 i = 0; i < kPieces; i++) get<P, N>(static_cast<const P *>(p) + column[i], &v[i * N]);
     };
-    auto store = [&](void *p, u64 t, const float (&v)[E]) {
+    auto store = [&](void *p, u32 t, const float (&v)[E]) {
+        T *row = static_cast<T *>(p) + (u64)t * hidden;
 #pragma unroll
         for (u32 i = 0; i < kPieces; i++)
-            if (within(i)) put<T, N>(static_cast<T *>(p) + t * hidden + column(i), &v[i * N]);
+            if (within[i]) put<T, N>(row + column[i], &v[i * N]);
     };
     auto store_sums = [&](float *p, const float (&v)[E]) {
 #pragma unroll
         for (u32 i = 0; i < kPieces; i++)
-            if (within(i)) put<float, N>(p + column(i), &v[i * N]);
+            if (within[i]) put<float, N>(p + column[i], &v[i * N]);
     };
     auto hide = [&](float (&v)[E]) {                          // what lies beyond the row
+        if (!ragged) return;
 #pragma unroll
         for (u32 i = 0; i < kPieces; i++)
-            if (!within(i))
+            if (!within[i])
 #pragma unroll
                 for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
     };
@@ -194,44 +206,45 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
     // the sums: of weight, bias, post, post_bias, gate
     float dw[E] = {}, db[BIAS ? E : 2] = {}, dp[POST ? E : 2] = {}, dpb[POST && BIAS ? E : 2] = {}, dg[POST ? E : 2] = {};
     u32 buffer = 0;
-    fetch(0, first, 0);
-    fetch(1, first, 2);
-    fetch(2, first, 3);
-    fetch(3, first, 4);
-    for (u64 t = first, next; t < last; t = next, buffer ^= 1) {
+    u32 end = end_of(first);
+    fetch(0, first, end, 0);
+    fetch(1, first, end, 2);
+    fetch(2, first, end, 3);
+    fetch(3, first, end, 4);
+    for (u32 t = first; t < last; buffer ^= 1) {
         if constexpr (POST) {
             if (t == gate_end) {
-                if (!a.dgate) store_sums(a.gate_sums + (blockIdx.x + gate) * a.pitch, dg);
+                if (!a.dgate) store_sums(a.gate_sums + (blockIdx.x + (u64)gate) * a.pitch, dg);
                 gate++;
-                gate_end += a.run;
+                gate_end += run;
 #pragma unroll
                 for (int i = 0; i < E; i++) dg[i] = 0.0f;
             }
         }
-        next = end_of(t);
-        const bool lone = R == 2 && next - t < 2;             // only the first of two rows counts
-        fetch(0, next, buffer ^ 1);
-        const u64 gate_row = gate * hidden;
+        const u32 next = end, next_end = end_of(next);
+        const bool lone = R == 2 && end - t < 2;              // only the first of two rows counts
+        const P *const gate_row = POST ? static_cast<const P *>(a.gate) + (u64)gate * hidden : nullptr;
+        fetch(0, next, next_end, buffer ^ 1);
         float v[R][E], w[E], mean[R], inverse[R], my[R], iy[R], slope[R];
         if (staged) asm volatile("cp.async.wait_group 4;" ::: "memory");
 #pragma unroll
-        for (int r = 0; r < R; r++) load(0, t, r, buffer, v[r]);
+        for (int r = 0; r < R; r++) load(0, t, end, r, buffer, v[r]);
         // as in the forward pass
         if (post) {
             normalise(v, my, iy);
-            param(a.post, 0, w);
+            param(a.post, w);
 #pragma unroll
             for (int r = 0; r < R; r++) mul_row(v[r], v[r], w);
             if constexpr (BIAS) {
                 if (a.post_bias) {
-                    param(a.post_bias, 0, w);
+                    param(a.post_bias, w);
 #pragma unroll
                     for (int r = 0; r < R; r++) add_row(v[r], v[r], w);
                 }
             }
         }
         if (gated) {
-            param(a.gate, gate_row, w);
+            param(gate_row, w);
 #pragma unroll
             for (int r = 0; r < R; r++) mul_row(v[r], v[r], w);
         }
@@ -239,20 +252,20 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
         if (from[1])
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                load(1, t, r, 2, w);
+                load(1, t, end, r, 2, w);
                 fma_row(v[r], w, a.alpha, v[r]);
             }
-        fetch(1, next, 2);
+        fetch(1, next, next_end, 2);
         normalise(v, mean, inverse);
         if (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
         float g[R][E];
 #pragma unroll
-        for (int r = 0; r < R; r++) load(2, t, r, 3, g[r]);
-        fetch(2, next, 3);
+        for (int r = 0; r < R; r++) load(2, t, end, r, 3, g[r]);
+        fetch(2, next, next_end, 3);
         if (R == 2 && lone)
 #pragma unroll
             for (int i = 0; i < E; i++) g[R - 1][i] = 0.0f;
-        param(a.weight, 0, w);
+        param(a.weight, w);
 #pragma unroll
         for (int r = 0; r < R; r++) {
             fma_row(dw, g[r], v[r], dw);
@@ -267,7 +280,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
             fma_row(v[r], v[r], -slope[r], g[r]);
             if (layer) add_row(v[r], v[r], -mean[r]);
             if (from[3]) {
-                load(3, t, r, 4, w);
+                load(3, t, end, r, 4, w);
                 fma_row(v[r], v[r], inverse[r], w);
             } else {
                 mul_row(v[r], v[r], inverse[r]);
@@ -280,11 +293,11 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
                 if (!(R == 2 && r && lone)) store(a.dresidual, t + r, w);
             }
         }
-        fetch(3, next, 4);
+        fetch(3, next, next_end, 4);
         if constexpr (POST) {
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                load(0, t, r, buffer, g[r]);
+                load(0, t, end, r, buffer, g[r]);
                 if (post) {
                     if (layer) add_row(g[r], g[r], -my[r]);
                     mul_row(g[r], g[r], iy[r]);               // y^
@@ -292,7 +305,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
             }
             if (gated) {
                 float u[E];
-                if (post) param(a.post, 0, w);
+                if (post) param(a.post, w);
 #pragma unroll
                 for (int r = 0; r < R; r++) {
                     if (post) {
@@ -300,7 +313,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
                         if constexpr (BIAS) {
                             if (a.post_bias) {
                                 float b[E];
-                                param(a.post_bias, 0, b);
+                                param(a.post_bias, b);
                                 add_row(u, u, b);
                             }
                         }
@@ -313,18 +326,18 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
                             mul_row(u, u, v[r]);
 #pragma unroll
                             for (u32 i = 0; i < kPieces; i++)
-                                if (within(i)) put<P, N>(static_cast<P *>(a.dgate) + gate_row + column(i), &u[i * N]);
+                                if (within[i]) put<P, N>(static_cast<P *>(a.dgate) + (u64)gate * hidden + column[i], &u[i * N]);
                         }
                     } else {
                         fma_row(dg, u, v[r], dg);
                     }
                 }
-                param(a.gate, gate_row, w);
+                param(gate_row, w);
 #pragma unroll
                 for (int r = 0; r < R; r++) mul_row(v[r], v[r], w);
             }
             if (post) {
-                param(a.post, 0, w);
+                param(a.post, w);
 #pragma unroll
                 for (int r = 0; r < R; r++) {
                     fma_row(dp, v[r], g[r], dp);
@@ -344,6 +357,8 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
 #pragma unroll
         for (int r = 0; r < R; r++)
             if (!(R == 2 && r && lone)) store(a.dy, t + r, v[r]);
+        t = next;
+        end = next_end;
     }
     if (staged) asm volatile("cp.async.wait_group 0;" ::: "memory");
     float *to = a.sums + (u64)blockIdx.x * 4 * a.pitch;
@@ -351,7 +366,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
     if constexpr (BIAS) store_sums(to + a.pitch, db);
     if constexpr (POST) {
         store_sums(to + 2 * a.pitch, dp);
-        if (gated && !a.dgate) store_sums(a.gate_sums + (blockIdx.x + gate) * a.pitch, dg);
+        if (gated && !a.dgate) store_sums(a.gate_sums + (blockIdx.x + (u64)gate) * a.pitch, dg);
     }
     if constexpr (POST && BIAS) store_sums(to + 3 * a.pitch, dpb);
 }
