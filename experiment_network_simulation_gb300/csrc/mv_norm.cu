@@ -221,7 +221,7 @@ template <class T> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, 
 
 struct GradPlan {
     NormShape shape;
-    bool staged, each;                  // each: every token has a gate of its own
+    bool each;                          // every token has a gate of its own
     u32 smem;
     u64 blocks, rows, pitch, gate_sums, total;
 };
@@ -230,13 +230,16 @@ GradPlan grad_plan(const mv_norm_desc *d, bool wide)
     GradPlan p = {};
     const u32 size = (u32)dtype_size(d->dtype);
     const u32 hidden = (u32)d->hidden, n = wide ? 16 / size : 1;
-    // eight elements a thread and two rows at a time, or sixteen and one where a row is too long for that
-    const bool two = hidden <= 8 * kGradThreads<false>;
-    const u32 e = two ? 8 : 16, threads = ((hidden + e - 1) / e + 31) / 32 * 32;
-    p.shape = {n, e / n, threads, false};
-    const u32 smem = 5 * (two ? 2 : 1) * e * threads * size;
-    p.staged = n * size >= 4 && smem <= 220 * 1024;
-    p.smem = p.staged ? smem : 0;
+    // eight elements a thread and two rows at a time, copied ahead; sixteen and one where a row is too long for that
+    auto shape = [&](u32 e) { return NormShape{n, e / n, ((hidden + e - 1) / e + 31) / 32 * 32, false}; };
+    auto copies = [&](const NormShape &s) { return n * size >= 4 ? 5 * 2 * 8 * s.threads * size : 0; };
+    p.shape = shape(8);
+    p.smem = copies(p.shape);
+    if (p.shape.threads > (u32)kGradThreads<false> || p.smem > 216 * 1024) {
+        p.shape = shape(16);
+        p.smem = 0;
+    }
+    const u32 threads = p.shape.threads;
     const u32 sms = std::max(1u, sm_count());
     const u32 held = (threads <= (u32)kGradThreads<true> ? kGradThreads<true> : kGradThreads<false>) / threads;
     const u32 an_sm = std::max(1u, std::min(held, p.smem ? 224u * 1024 / (p.smem + 2048) : 16u));
@@ -331,7 +334,6 @@ extern "C" int mv_norm_backward(const mv_norm_desc *d, const mv_norm_grads *g, v
     a.dresidual = g->dresidual;
     a.dgate = p.each ? g->dgate : nullptr;
     a.rows = p.rows;
-    a.staged = p.staged;
     a.sums = reinterpret_cast<float *>(ws);
     a.gate_sums = reinterpret_cast<float *>(ws + p.gate_sums);
     AddArgs add = {};

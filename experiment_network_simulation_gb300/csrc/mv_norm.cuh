@@ -14,7 +14,7 @@ struct NormArgs {
     void *n, *r, *dy, *dresidual, *dgate;           // dgate: where every token has a gate of its own
     u64 tokens, y_stride, residual_stride, dn_stride, dr_stride;
     u64 run, rows;                                  // tokens that share a gate; rows a block (backward)
-    u32 hidden, layer, params_f32, staged;
+    u32 hidden, layer, params_f32;
     float alpha, eps, inv_hidden;
     u64 pitch;                                      // hidden, up to whole fours
     float *sums;                                    // a block's sums for weight, bias, post, post_bias  [blocks, 4, pitch]

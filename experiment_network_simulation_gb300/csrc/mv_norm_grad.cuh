@@ -22,12 +22,13 @@ namespace mvblock {
 template <class T, class P, int N, int E, int R, bool POST, bool BIAS, int MOST>
 __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
 {
-    constexpr bool kCanStage = N * sizeof(T) >= 4;
+    // pieces of 2 bytes cannot be copied, and the longest rows do not fit: they are read where they are used
+    constexpr bool staged = N * sizeof(T) >= 4 && R == 2;
     constexpr u32 kBytes = N * sizeof(T), kPieces = E / N, kSlots = 5;        // y twice, residual, dn, dr
     extern __shared__ __align__(16) unsigned char stage[];
     __shared__ float2 part[2][R][32];
     const u32 threads = blockDim.x, tid = threadIdx.x, hidden = a.hidden;
-    const bool layer = BIAS && a.layer, post = POST && a.post, gated = POST && a.gate, staged = kCanStage && a.staged;
+    const bool layer = BIAS && a.layer, post = POST && a.post, gated = POST && a.gate;
     // pieces of this thread; a piece beyond the row is taken from its start, and counts for nothing
     const bool ragged = threads * E != hidden;
     bool within[kPieces];
@@ -54,8 +55,8 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
     };
     const u32 stage_at = (u32)__cvta_generic_to_shared(stage) + tid * kBytes, piece_bytes = threads * kBytes;
     auto fetch = [&](int k, u32 t, u32 end, u32 slot) {
-        if constexpr (kCanStage) {
-            if (staged && from[k] && t < last) {
+        if constexpr (staged) {
+            if (from[k] && t < last) {
 #pragma unroll
                 for (int r = 0; r < R; r++) {
                     const T *row = row_of(k, r ? end - 1 : t);
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
         }
     };
     auto load = [&](int k, u32 t, u32 end, int r, u32 slot, float (&v)[E]) {
-        if (staged) {
+        if constexpr (staged) {
 #pragma unroll
             for (u32 i = 0; i < kPieces; i++) {
                 const u32 at = stage_at + ((slot * R + r) * kPieces + i) * piece_bytes;
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
         const P *const gate_row = POST ? static_cast<const P *>(a.gate) + (u64)gate * hidden : nullptr;
         fetch(0, next, next_end, buffer ^ 1);
         float v[R][E], w[E], mean[R], inverse[R], my[R], iy[R], slope[R];
-        if (staged) asm volatile("cp.async.wait_group 4;" ::: "memory");
+        if constexpr (staged) asm volatile("cp.async.wait_group 4;" ::: "memory");
 #pragma unroll
         for (int r = 0; r < R; r++) load(0, t, end, r, buffer, v[r]);
         // as in the forward pass
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
 #pragma unroll
             for (int r = 0; r < R; r++) mul_row(v[r], v[r], w);
         }
-        if (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        if constexpr (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
         if (from[1])
 #pragma unroll
             for (int r = 0; r < R; r++) {
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
             }
         fetch(1, next, next_end, 2);
         normalise(v, mean, inverse);
-        if (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        if constexpr (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
         float g[R][E];
 #pragma unroll
         for (int r = 0; r < R; r++) load(2, t, end, r, 3, g[r]);
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
             hide(g[r]);
         }
         slopes(g, v, mean, slope);
-        if (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        if constexpr (staged) asm volatile("cp.async.wait_group 3;" ::: "memory");
 #pragma unroll
         for (int r = 0; r < R; r++) {
             fma_row(v[r], v[r], -slope[r], g[r]);
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
         t = next;
         end = next_end;
     }
-    if (staged) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if constexpr (staged) asm volatile("cp.async.wait_group 0;" ::: "memory");
     float *to = a.sums + (u64)blockIdx.x * 4 * a.pitch;
     store_sums(to, dw);
     if constexpr (BIAS) store_sums(to + a.pitch, db);
