@@ -334,6 +334,29 @@ __device__ __forceinline__ void load_sums(u32 at, u32 (&v)[32])
         : "r"(at));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void store_sums(u32 at, const u32 (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+        ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+          "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+          "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(at)
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void store_sums(u32 at, const u32 (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+        ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(at)
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void load_sums(u32 at, u32 (&v)[16])
 {
     asm volatile(
@@ -423,7 +446,8 @@ template <int CTAS, int BN> struct Tile {
     // blocks many, half of them to each of two
     static constexpr u32 fit(u32 room) { return (room - 2048 - kStaging) / kStage < 8 ? (room - 2048 - kStaging) / kStage : 8; }
     static constexpr u32 kStages = fit(227 * 1024), kFewStages = BN >= 128 ? kStages : fit(113 * 1024);
-    static constexpr u32 kColumns = BN < 32 ? 32 : BN;          // of TMEM, for one of two tiles
+    // columns of TMEM: of one of two tiles under way, and of those and the sums of a long tile's earlier runs
+    static constexpr u32 kColumns = BN < 32 ? 32 : BN, kAllColumns = BN == 256 ? 512 : 4 * kColumns;
     static constexpr u32 smem(u32 stages) { return 1024 + stages * kStage + kStaging + 256; }
 };
 
@@ -434,6 +458,7 @@ struct Units {                      // what the blocks (or pairs) do, in order
     u32 total;                      // units in all
     u32 steps;                      // steps of k of a tile
     u32 stages;                     // copies under way a block
+    u32 chain;                      // steps that are summed in one go (below)
     u32 half_steps;                 // steps after which A's second part begins (0: none)
 };
 
@@ -496,10 +521,10 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
     }
     if (warp == 1) {
         if constexpr (CTAS == 2) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(2 * S::kColumns) : "memory");
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(S::kAllColumns) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(2 * S::kColumns) : "memory");
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(S::kAllColumns) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         }
     }
@@ -577,24 +602,26 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
             for (u32 i = worker; i < u.total && ok; i += workers) {
                 u32 m, n, first, last;
                 unit(i, m, n, first, last);
-                ok = barrier_wait(taken + 8 * buffer, buffer_turn ^ 1);
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const u32 sums = tmem + buffer * S::kColumns;
-                for (u32 k = first; k < last && ok; k++) {
-                    ok = barrier_wait(full + 8 * s, turn);
-                    if (!ok) break;
+                for (u32 k = first; k < last && ok;) {
+                    ok = barrier_wait(taken + 8 * buffer, buffer_turn ^ 1);
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const u64 a = operand<A_MN>(base + s * S::kStage), b = operand<B_MN>(base + s * S::kStage + S::kA);
+                    const u32 sums = tmem + buffer * S::kColumns, start = k, end = min(last, k + u.chain);
+                    for (; k < end && ok; k++) {
+                        ok = barrier_wait(full + 8 * s, turn);
+                        if (!ok) break;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const u64 a = operand<A_MN>(base + s * S::kStage), b = operand<B_MN>(base + s * S::kStage + S::kA);
 #pragma unroll
-                    for (u32 j = 0; j < kStep / 16; j++)      // 16 k: 32 bytes along a line, or 16 lines
-                        multiply<CTAS>(sums, a + j * (A_MN ? 2048 / 16 : 32 / 16), b + j * (B_MN ? 2048 / 16 : 32 / 16),
-                                       args.what, k > first || j);
-                    arrive_after_products<CTAS>(empty + 8 * s);
-                    if (++s == stages) { s = 0; turn ^= 1; }
+                        for (u32 j = 0; j < kStep / 16; j++)  // 16 k: 32 bytes along a line, or 16 lines
+                            multiply<CTAS>(sums, a + j * (A_MN ? 2048 / 16 : 32 / 16), b + j * (B_MN ? 2048 / 16 : 32 / 16),
+                                           args.what, k > start || j);
+                        arrive_after_products<CTAS>(empty + 8 * s);
+                        if (++s == stages) { s = 0; turn ^= 1; }
+                    }
+                    if (ok) arrive_after_products<CTAS>(done + 8 * buffer);
+                    buffer ^= 1;
+                    if (buffer == 0) buffer_turn ^= 1;
                 }
-                if (ok) arrive_after_products<CTAS>(done + 8 * buffer);
-                buffer ^= 1;
-                if (buffer == 0) buffer_turn ^= 1;
             }
             if (!ok) {
                 arrive_after_products<CTAS>(drained);
@@ -604,7 +631,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
     } else {                                                      // finish
         const u32 w = warp & 3;                                   // a warp reads its quarter of TMEM's lanes
         const u32 mine = staging + (warp - 2) * 32 * 128, share = (warp - 2) / 4;
-        constexpr u32 kShares = S::kWorkers / 4, kChunk = 32 * kShares;
+        constexpr u32 kShares = S::kWorkers / 4;
         u32 buffer = 0, buffer_turn = 0;
         for (u32 i = worker; i < u.total; i += workers) {
             u32 m, n, first, last;
@@ -616,11 +643,62 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                     for (u64 j = c + share * 128; j < end; j += kShares * 128)
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(args.f.residual) + r * args.f.residual_stride * size + j));
             }
-            ok = barrier_wait(done + 8 * buffer, buffer_turn);
-            ok = __all_sync(kFull, ok);
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            // The tensor core's additions cut what is beyond 32 bits off, so an error of a long
+            // chain grows with its length (2e-6 after 2048 products): where the result has 32 bits
+            // or the chain is very long, it is summed in runs of u.chain steps, and a run's sum is
+            // added, rounded to nearest, to the sum of those before it (in TMEM too).
+            const u32 earlier = tmem + 2 * S::kColumns + (w << 21);
+            constexpr u32 kRun = BN < 32 ? 16 : 32, kShare = BN / kShares;
+            u32 k = first;
+            const auto arrived = [&] {
+                ok = barrier_wait(done + 8 * buffer, buffer_turn);
+                ok = __all_sync(kFull, ok);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                return ok;
+            };
+            const auto taken_over = [&] {
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                // What it tells is that TMEM has been read (the fence above): a release would
+                // also wait for this tile's stores, which took as long as a short tile's products.
+                if (lane == 0) {
+                    if constexpr (CTAS == 2)
+                        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_leader(taken + 8 * buffer)) : "memory");
+                    else
+                        asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(taken + 8 * buffer) : "memory");
+                }
+                buffer ^= 1;
+                if (buffer == 0) buffer_turn ^= 1;
+            };
+            if constexpr (BN < 256) {
+                for (; last - k > u.chain; k += u.chain) {
+                    if (!arrived()) break;
+                    const u32 sums = tmem + buffer * S::kColumns + (w << 21);
+                    for (u32 c = share * kShare; c < (share + 1) * kShare; c += kRun) {
+                        u32 v[kRun], e[kRun];
+                        load_sums(sums + c, v);
+                        if (k > first) {
+                            load_sums(earlier + c, e);
+#pragma unroll
+                            for (u32 j = 0; j < kRun; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(e[j]));
+                        }
+                        store_sums(earlier + c, v);
+                    }
+                    taken_over();
+                }
+            }
+            if (!ok || !arrived()) break;
             const u32 sums = tmem + buffer * S::kColumns + (w << 21);
+            const auto load_all = [&](u32 c, auto &v) {           // the sums of columns c ..
+                load_sums(sums + c, v);
+                if constexpr (BN < 256)
+                    if (k > first) {
+                        std::remove_reference_t<decltype(v)> e;
+                        load_sums(earlier + c, e);
+#pragma unroll
+                        for (u32 j = 0; j < sizeof(v) / 4; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(e[j]));
+                    }
+            };
             float *part = SWAP || i < u.whole ? nullptr
                         : args.partial + (u64)(i - u.whole) * (S::kRows * BN) + pair_rank * 128 * BN;
             const u64 row0 = (u64)m * S::kRows + pair_rank * 128 + w * 32, col0 = (u64)n * BN;
@@ -630,7 +708,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                 constexpr int kAtOnce = BN < 32 ? BN : 32;
                 for (u32 c = 0; c < BN && col0 + c < args.f.m; c += kAtOnce) {
                     u32 v[kAtOnce];
-                    load_sums(sums + c, v);
+                    load_all(c, v);
 #pragma unroll
                     for (int j = 0; j < kAtOnce; j++) {
                         if (u.parts > 1)                           // [rows][128 columns], in the copies' place
@@ -642,10 +720,10 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                 const auto all = [&](auto type) {
                     using OUT = decltype(type);
                     constexpr int N = 128 / sizeof(OUT);
-                    for (u32 c = share * N; c < BN && col0 + c < args.f.n; c += kShares * N) {
+                    for (u32 c = share * kShare; c < (share + 1) * kShare && col0 + c < args.f.n; c += N) {
                         float v[N];
 #pragma unroll
-                        for (int i = 0; i < N; i += 32) load_sums(sums + c + i, *reinterpret_cast<u32(*)[32]>(&v[i]));
+                        for (int j = 0; j < N; j += 32) load_all(c + j, *reinterpret_cast<u32(*)[32]>(&v[j]));
                         if (row0 < args.f.m) finish_tile<OUT>(args.f, mine, lane, &y_map, &z_map, row0, col0 + c, v);
                     }
                 };
@@ -653,9 +731,9 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                 else if (args.f.out == MV_F16) all(__half());
                 else all(0.0f);
             } else {
-                for (u32 c = share * 32; c < BN && col0 + c < args.f.n; c += kChunk) {
+                for (u32 c = share * kShare; c < (share + 1) * kShare && col0 + c < args.f.n; c += 32) {
                     u32 v[32];
-                    load_sums(sums + c, v);
+                    load_all(c, v);
                     if (part) {                                   // [columns / 4][rows][4]
 #pragma unroll
                         for (int j = 0; j < 8; j++)
@@ -685,18 +763,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                     finish_rows(args.f, row0 + (lane >> 3), col0 + c + (lane & 7) * 4, t);
                 }
             }
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            // What it tells is that TMEM has been read (the fence above): a release would
-            // also wait for this tile's stores, which took as long as a short tile's products.
-            if (lane == 0) {
-                if constexpr (CTAS == 2)
-                    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_leader(taken + 8 * buffer)) : "memory");
-                else
-                    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(taken + 8 * buffer) : "memory");
-            }
-            buffer ^= 1;
-            if (buffer == 0) buffer_turn ^= 1;
+            taken_over();
         }
     }
     if (warp > 1 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");      // the stores have ended
@@ -730,9 +797,9 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
     if (warp == 1) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if constexpr (CTAS == 2)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * S::kColumns));
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kAllColumns));
         else
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * S::kColumns));
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kAllColumns));
     }
 }
 
@@ -910,12 +977,12 @@ bool map_result(CUtensorMap *map, void *p, u64 rows, u64 cols, u32 type)
 }
 
 // The kinds of tile: A's rows and B's a tile, and whether two blocks share an SM where there are enough.
-enum Kind { kPair256, kOne128, kOne64, kSwap64, kSwap16, kKinds };
+enum Kind { kPair256, kPair128, kOne128, kOne64, kSwap64, kSwap16, kKinds };
 struct KindOf {
     u32 rows, cols;
     bool two, swap;
 };
-constexpr KindOf kKind[kKinds] = {{256, 256, false, false}, {128, 128, false, false}, {128, 64, true, false},
+constexpr KindOf kKind[kKinds] = {{256, 256, false, false}, {256, 128, false, false}, {128, 128, false, false}, {128, 64, true, false},
                                   {128, 64, true, true}, {128, 16, true, true}};
 constexpr u64 kCluster = 8;             // blocks that share a tile of the kinds that swap, at most
 
@@ -934,17 +1001,20 @@ struct Plan {
 // (128 x 128), 70.3 (128 x 64); 1 x 20480 to 5120: 39 (swapped, 16), 42
 // (swapped, 64), 50 (128 x 128), 64 (pairs); 64 x 5120 to 5120: 20 (swapped, 64),
 // 25 (swapped, 16), 23 (128 x 128).
-Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 sms, double &best)
+Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 chain, u32 sms, double &best)
 {
     const KindOf &k = kKind[kind];
+    const bool pair = kind <= kPair128;
     const u64 a = k.swap ? n : m, b = k.swap ? m : n, tm = (a + k.rows - 1) / k.rows, tn = (b + k.cols - 1) / k.cols, tiles = tm * tn;
-    const u64 each = kind == kPair256 ? 2 : 1;                         // blocks a unit
-    const double bytes = kind == kPair256 ? 32768 : (k.rows + k.cols) * 128;
+    const u64 each = pair ? 2 : 1;                                     // blocks a unit
+    const double bytes = (k.rows + k.cols) * (pair ? 64 : 128);
     const double memory = (double)(m + n) * (double)steps * 128 / (sms * 21.7);
     Plan p = {};
     best = INFINITY;
     auto consider = [&](u64 whole, u64 left, u64 parts, u64 blocks, u64 slots, bool two, double join) {
-        const double step = kind == kPair256 ? 530 : std::max(bytes / 64 * (two ? 2 : 1), two || kind == kOne128 ? 400.0 : 250.0);
+        // TMEM has no room for earlier sums beside the largest tiles
+        if (kind == kPair256 && (steps + (whole ? 1 : parts) - 1) / (whole ? 1 : parts) > chain) return;
+        const double step = kind == kPair256 ? 530 : kind == kPair128 ? 400 : std::max(bytes / 64 * (two ? 2 : 1), two || kind == kOne128 ? 400.0 : 250.0);
         const double rounds = (double)((left * parts + slots - 1) / slots);
         const double work = ((double)whole / (double)slots) * ((double)steps * step + 400) +
                             rounds * ((double)((steps + parts - 1) / parts) * step + 2000);
@@ -954,7 +1024,7 @@ Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 sms, double &best)
         p.kind = kind;
         p.two = two;
         p.u = {(u32)tm, (u32)tn, (u32)(k.swap || parts == 1 ? tiles : whole), (u32)parts,
-               (u32)(k.swap || parts == 1 ? tiles : whole + left * parts), (u32)steps, 0, 0};
+               (u32)(k.swap || parts == 1 ? tiles : whole + left * parts), (u32)steps, 0, chain, 0};
         p.blocks = blocks;
         p.partial = k.swap || parts == 1 ? 0 : left * parts * (u64)k.rows * k.cols * 4;
     };
@@ -980,14 +1050,15 @@ Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 sms, double &best)
     return p;
 }
 
-Plan plan(u64 m, u64 n, u64 steps, bool swaps, u32 sms)
+// chain: the longest run of steps that may be summed in one go.
+Plan plan(u64 m, u64 n, u64 steps, u32 chain, bool swaps, u32 sms)
 {
     Plan best = {};
     double least = INFINITY;
     for (int kind = 0; kind < kKinds; kind++) {
         if (kKind[kind].swap && !swaps) continue;
         double cost;
-        const Plan p = plan_kind((Kind)kind, m, n, steps, sms, cost);
+        const Plan p = plan_kind((Kind)kind, m, n, steps, chain, sms, cost);
         if (cost < least) { least = cost; best = p; }
     }
     return best;
@@ -1050,6 +1121,7 @@ int product(const Side &a, const void *a2, const Side &b, u32 dtype, Plan p, con
     args.u.half_steps = a2 ? p.u.steps / 2 : 0;
     switch (p.kind) {
     case kPair256: return run_kind<2, 256, A_MN, B_MN, false>(a, a2, b, dtype, p, args, early, stream);
+    case kPair128: return run_kind<2, 128, A_MN, B_MN, false>(a, a2, b, dtype, p, args, early, stream);
     case kOne128: return run_kind<1, 128, A_MN, B_MN, false>(a, a2, b, dtype, p, args, early, stream);
     case kOne64: return run_kind<1, 64, A_MN, B_MN, false>(a, a2, b, dtype, p, args, early, stream);
     default: break;
@@ -1065,6 +1137,9 @@ u64 up(u64 v, u64 to) { return (v + to - 1) / to * to; }
 u64 steps_of(u64 k) { return (k + kStep - 1) / kStep; }
 bool copies(const void *p, u64 stride) { return aligned(p, 16) && stride % 8 == 0; }
 bool wide(const void *p, u64 stride, u32 dtype) { return aligned(p, 4 * dtype_size(dtype)) && stride % 4 == 0; }
+// Steps of 64 products summed in one go: 512 products (5e-7 of error) where the result has 32 bits, 32768
+// (4e-5, a fiftieth of bfloat16's rounding) where it has 16.
+constexpr u32 kChain32 = 8, kChain16 = 512;
 constexpr u64 kMostRows = 1ull << 30, kMostTiles = 1ull << 31;
 
 // Arrays to be copied, and the launch that does it.
@@ -1124,7 +1199,7 @@ LinearLayout layout(const mv_linear_desc *d)
     LinearLayout l = {};
     u64 at = 0;
     auto take = [&](u64 bytes) { const u64 here = at; at += up(bytes, 256); return here; };
-    l.plan = plan(d->tokens, d->rows, steps_of(d->cols), d->tokens <= 256, planned_sms());
+    l.plan = plan(d->tokens, d->rows, steps_of(d->cols), d->out_dtype == MV_F32 ? kChain32 : kChain16, d->tokens <= 256, planned_sms());
     l.x = take(copies(d->x, d->x_stride) ? 0 : d->tokens * up(d->cols, 8) * 2);
     l.w = take(copies(d->w, d->w_stride) ? 0 : d->rows * up(d->cols, 8) * 2);
     l.partial = take(l.plan.partial);
@@ -1150,8 +1225,8 @@ GradLayout layout(const mv_linear_grad_desc *d)
     u64 at = 0;
     auto take = [&](u64 bytes) { const u64 here = at; at += up(bytes, 256); return here; };
     const u64 parts = d->dz_dtype == MV_F32 ? 2 : 1, sms = planned_sms();
-    if (d->dx) l.dx = plan(d->tokens, d->cols, parts * steps_of(d->rows), false, (u32)sms);
-    if (d->dw) l.dw = plan(d->rows, d->cols, parts * steps_of(d->tokens), false, (u32)sms);
+    if (d->dx) l.dx = plan(d->tokens, d->cols, parts * steps_of(d->rows), kChain16, false, (u32)sms);
+    if (d->dw) l.dw = plan(d->rows, d->cols, parts * steps_of(d->tokens), kChain16, false, (u32)sms);
     l.x = take(!d->dw || copies(d->x, d->x_stride) ? 0 : d->tokens * up(d->cols, 8) * 2);
     l.w = take(!d->dx || copies(d->w, d->w_stride) ? 0 : d->rows * up(d->cols, 8) * 2);
     l.dz = take(parts == 1 && copies(d->dz, d->dz_stride) ? 0 : parts * d->tokens * up(d->rows, 8) * 2);
