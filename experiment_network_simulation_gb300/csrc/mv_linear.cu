@@ -876,13 +876,18 @@ __global__ void __launch_bounds__(256) k_split(const float *from, u64 stride, u6
     for (u64 i = (u64)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
         const u64 r = i / quads, c = (i - r * quads) * 4;
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rest[4];
+        __nv_bfloat16 most[4];
         if (c < cols) load4<float>(from, r * stride + c, wide, cols - c < 4 ? (u32)(cols - c) : 4, v);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            rest[j] = v[j] - __bfloat162float(__float2bfloat16_rn(v[j]));
+            most[j] = fabsf(v[j]) > 3.3895e38f && fabsf(v[j]) < INFINITY ? __float2bfloat16_rz(v[j])      // would round to infinity
+                                                                         : __float2bfloat16_rn(v[j]);
+            rest[j] = v[j] - __bfloat162float(most[j]);
             if (!(fabsf(rest[j]) < INFINITY)) rest[j] = 0.0f;        // of infinities nothing is left
         }
-        store4<__nv_bfloat16>(to, i * 4, true, 4, v);
+        uint2 w;
+        memcpy(&w, most, 8);
+        *reinterpret_cast<uint2 *>(to + i * 4) = w;
         store4<__nv_bfloat16>(to + second, i * 4, true, 4, rest);
     }
 }
