@@ -300,11 +300,12 @@ def norm_backward(dn, y, weight, bias=None, *, dr=None, residual=None, alpha: fl
 
 def _norm_backward(dn, dr, y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates, kind, params,
                    eps, dev):
-    def like(p, shape=(hidden,), dtype=params):
+    def like(p, dtype, *shape):
         return None if p is None else torch.empty(shape, dtype=dtype, device=dev)
 
-    g = NormGrads(like(y, (tokens, hidden), y.dtype), like(residual, (tokens, hidden), y.dtype), like(weight), like(bias),
-                  like(post), like(post_bias), None if gate is None else like(gate, gate.shape))
+    g = NormGrads(like(y, y.dtype, tokens, hidden), like(residual, y.dtype, tokens, hidden), like(weight, params, hidden),
+                  like(bias, params, hidden), like(post, params, hidden), like(post_bias, params, hidden),
+                  None if gate is None else like(gate, params, *gate.shape))
     d = _norm_desc(
         tokens, hidden, gates, _stride(y), 0 if residual is None else _stride(residual), _DTYPES[y.dtype],
         _DTYPES[params], kind, alpha, eps, y.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(post),

@@ -853,20 +853,29 @@ struct PackArgs {
     unsigned short *to[2];
     u64 stride[2], rows[2], cols[2];
 };
-// Two arrays at most (blockIdx.z), eight values a thread, a row (blockIdx.y and every gridDim.y) at a time.
-__global__ void __launch_bounds__(128) k_pack(const PackArgs a)
+// Two arrays at most (blockIdx.y), a row a warp, eight values a lane.  They are
+// read by aligned words of two values, each of which holds one of the row at least.
+__global__ void __launch_bounds__(256) k_pack(const PackArgs a)
 {
-    const u32 which = blockIdx.z;
-    const u64 cols = a.cols[which], to_stride = (cols + 7) / 8 * 8, c = ((u64)blockIdx.x * 128 + threadIdx.x) * 8;
-    if (c >= cols) return;
-    for (u64 r = blockIdx.y; r < a.rows[which]; r += gridDim.y) {
-        const unsigned short *from = a.from[which] + r * a.stride[which] + c;
-        unsigned short v[8];
+    const u32 which = blockIdx.y, lane = threadIdx.x & 31;
+    const u64 cols = a.cols[which], to_stride = (cols + 7) / 8 * 8;
+    for (u64 r = blockIdx.x * 8 + (threadIdx.x >> 5); r < a.rows[which]; r += gridDim.x * 8) {
+        const unsigned short *from = a.from[which] + r * a.stride[which];
+        const u32 odd = (u32)(reinterpret_cast<uintptr_t>(from) >> 1 & 1);
+        const u32 *words = reinterpret_cast<const u32 *>(from - odd);
+        const u64 end = (cols + odd + 1) / 2;                 // words of the row
+#pragma unroll 2
+        for (u64 c = lane * 8; c < cols; c += 256) {
+            u32 w[5], v[4];
 #pragma unroll
-        for (u32 i = 0; i < 8; i++) v[i] = c + i < cols ? from[i] : 0;
-        uint4 w;
-        memcpy(&w, v, 16);
-        *reinterpret_cast<uint4 *>(a.to[which] + r * to_stride + c) = w;
+            for (u32 i = 0; i < 5; i++) w[i] = c / 2 + i < end ? words[c / 2 + i] : 0;
+#pragma unroll
+            for (u32 i = 0; i < 4; i++) {
+                v[i] = odd ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+                if (c + 2 * i + 1 >= cols) v[i] = c + 2 * i < cols ? v[i] & 0xFFFFu : 0;
+            }
+            *reinterpret_cast<uint4 *>(a.to[which] + r * to_stride + c) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
     }
 }
 __global__ void __launch_bounds__(256) k_split(const float *from, u64 stride, u64 rows, u64 cols, __nv_bfloat16 *to, u64 to_stride, u64 second)
@@ -1151,7 +1160,7 @@ constexpr u64 kMostRows = 1ull << 30, kMostTiles = 1ull << 31;
 struct Packing {
     PackArgs a = {};
     u32 count = 0;
-    u64 widest = 0, most = 0;
+    u64 most = 0;
     const void *add(const void *from, u64 &stride, u64 rows, u64 cols, void *to)
     {
         a.from[count] = static_cast<const unsigned short *>(from);
@@ -1159,7 +1168,6 @@ struct Packing {
         a.stride[count] = stride;
         a.rows[count] = rows;
         a.cols[count++] = cols;
-        widest = std::max(widest, cols);
         most = std::max(most, rows);
         stride = up(cols, 8);
         return to;
@@ -1168,10 +1176,10 @@ struct Packing {
     {
         const u32 pairs = count;
         if (!pairs) return MV_OK;
-        const dim3 grid((u32)((widest + 1023) / 1024), (u32)std::min<u64>(most, 8192), pairs);
+        const dim3 grid((u32)std::min<u64>((most + 7) / 8, 8192), pairs);
         count = 0;
-        widest = most = 0;
-        return launch(k_pack, grid, 128, 0, stream, a);
+        most = 0;
+        return launch(k_pack, grid, 256, 0, stream, a);
     }
 };
 

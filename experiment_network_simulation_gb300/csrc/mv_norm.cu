@@ -87,19 +87,20 @@ template <class T, class P, int N, int E, bool WHOLE> __global__ void __launch_b
     }
 }
 
-// The blocks' sums, added in their order: four columns a lane, every eighth
+// The blocks' sums, added in their order: two columns a lane, every sixteenth
 // block's a warp, then the warps'.
+constexpr u32 kAddWarps = 16, kAddColumns = 64;
 struct AddArgs {
     const float *sums, *gate_sums;
     void *to[4], *dgate;
     u64 hidden, pitch, blocks, run, rows, gates;
     u32 params_f32;
 };
-template <class T> __global__ void __launch_bounds__(256) k_norm_add(const AddArgs a)
+template <class T> __global__ void __launch_bounds__(32 * kAddWarps) k_norm_add(const AddArgs a)
 {
-    __shared__ float4 part[8][32];
+    __shared__ float2 part[kAddWarps][32];
     const u32 lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const u64 c = ((u64)blockIdx.x * 32 + lane) * 4;
+    const u64 c = ((u64)blockIdx.x * 32 + lane) * 2;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // what: four parameters, then the gates
     for (u64 what = blockIdx.y; what < 4 + a.gates; what += gridDim.y) {
@@ -115,22 +116,22 @@ template <class T> __global__ void __launch_bounds__(256) k_norm_add(const AddAr
             step = a.pitch;
             at = g * a.hidden;
         }
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float2 s = make_float2(0.0f, 0.0f);
         if (c < a.hidden)
 #pragma unroll 8
-            for (u64 b = first + warp; b < last; b += 8) {
-                const float4 w = *reinterpret_cast<const float4 *>(from + b * step + c);
-                s.x += w.x; s.y += w.y; s.z += w.z; s.w += w.w;
+            for (u64 b = first + warp; b < last; b += kAddWarps) {
+                const float2 w = *reinterpret_cast<const float2 *>(from + b * step + c);
+                s.x += w.x; s.y += w.y;
             }
         __syncthreads();
         part[warp][lane] = s;
         __syncthreads();
-        if (threadIdx.x >= 128) continue;
-        const u64 mine = (u64)blockIdx.x * 128 + threadIdx.x;
+        if (threadIdx.x >= kAddColumns) continue;
+        const u64 mine = (u64)blockIdx.x * kAddColumns + threadIdx.x;
         if (mine >= a.hidden) continue;
         float v = 0.0f;
 #pragma unroll
-        for (u32 i = 0; i < 8; i++) v += reinterpret_cast<const float *>(part[i])[threadIdx.x];
+        for (u32 i = 0; i < kAddWarps; i++) v += reinterpret_cast<const float *>(part[i])[threadIdx.x];
         if (a.params_f32) static_cast<float *>(out)[at + mine] = v;
         else static_cast<T *>(out)[at + mine] = from_float<T>(v);
     }
@@ -356,7 +357,7 @@ extern "C" int mv_norm_backward(const mv_norm_desc *d, const mv_norm_grads *g, v
                    : d->dtype == MV_F16 ? run_norm_grad<__half>(a, p.shape, p.blocks, p.smem, post, bias, on)
                                         : run_norm_grad<__nv_bfloat16>(a, p.shape, p.blocks, p.smem, post, bias, on);
     if (done != MV_OK) return done;
-    const dim3 grid((u32)((d->hidden + 127) / 128), (u32)std::min<u64>(4 + add.gates, 65535));
-    return d->dtype == MV_BF16 ? launch_after(k_norm_add<__nv_bfloat16>, grid, 256, 0, on, add)
-                               : launch_after(k_norm_add<__half>, grid, 256, 0, on, add);
+    const dim3 grid((u32)((d->hidden + kAddColumns - 1) / kAddColumns), (u32)std::min<u64>(4 + add.gates, 65535));
+    return d->dtype == MV_BF16 ? launch_after(k_norm_add<__nv_bfloat16>, grid, 32 * kAddWarps, 0, on, add)
+                               : launch_after(k_norm_add<__half>, grid, 32 * kAddWarps, 0, on, add);
 }
