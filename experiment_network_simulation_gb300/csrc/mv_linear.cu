@@ -28,8 +28,7 @@ struct Finish {
     u64 y_stride, residual_stride;  // z is dense
     u32 dtype, out, bias_type;      // of z; of y and the residual
     u32 act, residual_wide, bias_wide, y_wide, z_wide;   // *_wide: four columns are one aligned access
-    u32 easy;                       // all of them that matter
-    u32 by_tma;                     // y and z are stored by TMA: nothing is read but the bias, rows are 16-byte aligned
+    u32 by_tma;                     // y and z are stored by TMA, the residual comes by it: rows are 16-byte aligned
     float scale;
 };
 
@@ -135,20 +134,6 @@ __device__ __forceinline__ void finish1(const Finish &f, u64 r, u64 c, float v)
     put_as(f.out, f.y, r * f.y_stride + c, v);
 }
 
-// A warp's 32 x 32 of a tile, all of it inside the matrix and every access
-// aligned: the lane has columns c .. c + 3 (c its own) of rows r + 4 j.  Step by
-// step for all eight rows, so that a warp has eight accesses under way: row
-// after row, 8192 x 5120 to 20480 took 2210 us, so 916.
-template <class T> __device__ __forceinline__ void load_rows(const void *p, u64 r, u64 c, u64 stride, float (&v)[8][4])
-{
-#pragma unroll
-    for (int j = 0; j < 8; j++) load4<T>(p, (r + 4 * j) * stride + c, true, 4, v[j]);
-}
-template <class T> __device__ __forceinline__ void store_rows(void *p, u64 r, u64 c, u64 stride, const float (&v)[8][4])
-{
-#pragma unroll
-    for (int j = 0; j < 8; j++) store4<T>(p, (r + 4 * j) * stride + c, true, 4, v[j]);
-}
 template <u32 ACT, int N> __device__ __forceinline__ void activate(float *v)
 {
 #pragma unroll
@@ -161,43 +146,9 @@ template <int N> __device__ __forceinline__ void activate(u32 act, float *v)
     else if (act == MV_ACT_GELU_TANH) activate<MV_ACT_GELU_TANH, N>(v);
     else if (act == MV_ACT_SILU) activate<MV_ACT_SILU, N>(v);
 }
-__device__ __forceinline__ void finish_rows(const Finish &f, u64 r, u64 c, float (&v)[8][4])
-{
-    if (f.bias) {
-        float b[4];
-        load4_as(f.bias_type, f.bias, c, true, 4, b);
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[j][i] += b[i];
-    }
-    if (f.z) {
-        if (f.dtype == MV_BF16) store_rows<__nv_bfloat16>(f.z, r, c, f.n, v);
-        else store_rows<__half>(f.z, r, c, f.n, v);
-    }
-    activate<32>(f.act, v[0]);
-    if (f.residual) {
-        float b[8][4];
-        if (f.out == MV_BF16) load_rows<__nv_bfloat16>(f.residual, r, c, f.residual_stride, b);
-        else if (f.out == MV_F16) load_rows<__half>(f.residual, r, c, f.residual_stride, b);
-        else load_rows<float>(f.residual, r, c, f.residual_stride, b);
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[j][i] = fmaf(f.scale, v[j][i], b[j][i]);
-    } else if (f.scale != 1.0f) {
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[j][i] *= f.scale;
-    }
-    if (f.out == MV_BF16) store_rows<__nv_bfloat16>(f.y, r, c, f.y_stride, v);
-    else if (f.out == MV_F16) store_rows<__half>(f.y, r, c, f.y_stride, v);
-    else store_rows<float>(f.y, r, c, f.y_stride, v);
-}
-
-// The same where rows lie anywhere, or end within the 32 x 32: a lane has
-// column c of the `rows` rows from r on, so that a warp's accesses are neighbours.
+// A warp's 32 x 32 of a tile from shared memory, where rows lie anywhere: a lane
+// has column c of the rows from r on, so that a warp's accesses are neighbours,
+// and 32 of them under way (row after row, 8192 x 5120 to 20480 took 2210 us, so 916).
 template <class T> __device__ __forceinline__ void load_column(const void *p, u64 at, u64 stride, u32 rows, float (&v)[32])
 {
     const T *from = static_cast<const T *>(p) + at;
@@ -375,31 +326,44 @@ __device__ __forceinline__ void meet()          // the cluster's threads
 
 // A lane's row of a tile, 128 bytes of it at a time: to shared memory in the
 // 128-byte swizzle, and from there to the result by TMA, which leaves out what
-// lies beyond the matrix.  Fewer instructions than finish_rows(), whose lanes
-// have to change places for whole sectors: dx of 65536 x 256 by 256 x 7168
-// took 308 us that way.
-template <class T> __device__ __forceinline__ void store_tile(u32 mine, u32 lane, const CUtensorMap *map, int x, int y, const float *v)
+// lies beyond the matrix.  Fewer instructions than by a lane's own stores,
+// which have to change places for whole sectors: dx of 65536 x 256 by 256 x 7168
+// took 308 us that way, 203 so.
+template <class T> __device__ __forceinline__ void send_tile(u32 mine, u32 lane, const CUtensorMap *map, int x, int y)
 {
-    constexpr u32 kEach = 16 / sizeof(T);
-    // the store before this one has read the buffer
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncwarp();
-#pragma unroll
-    for (u32 j = 0; j < 8; j++) {
-        T t[kEach];
-#pragma unroll
-        for (u32 i = 0; i < kEach; i++) t[i] = from_float<T>(v[j * kEach + i]);
-        uint4 w;
-        memcpy(&w, t, 16);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 128 + ((j ^ (lane & 7)) * 16)), "r"(w.x), "r"(w.y),
-                     "r"(w.z), "r"(w.w) : "memory");
-    }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) {
         asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(mine), "r"(x), "r"(y) : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
+}
+// RESIDUAL: v is added, times the scale, to what lies there.
+template <class T, bool RESIDUAL>
+__device__ __forceinline__ void store_tile(u32 mine, u32 lane, const CUtensorMap *map, int x, int y, const float *v, float scale)
+{
+    constexpr u32 kEach = 16 / sizeof(T);
+    if constexpr (!RESIDUAL) {
+        // the store before this one has read the buffer
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+    }
+#pragma unroll
+    for (u32 j = 0; j < 8; j++) {
+        const u32 at = mine + lane * 128 + ((j ^ (lane & 7)) * 16);
+        T t[kEach];
+        uint4 w;
+        if constexpr (RESIDUAL) {
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+            memcpy(t, &w, 16);
+        }
+#pragma unroll
+        for (u32 i = 0; i < kEach; i++)
+            t[i] = from_float<T>(RESIDUAL ? fmaf(scale, v[j * kEach + i], to_float(t[i])) : v[j * kEach + i]);
+        memcpy(&w, t, 16);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+    }
+    send_tile<T>(mine, lane, map, x, y);
 }
 template <class T, int N> __device__ __forceinline__ void add_bias(const Finish &f, u64 c, float (&v)[N])
 {
@@ -412,7 +376,16 @@ template <class T, int N> __device__ __forceinline__ void add_bias(const Finish 
         for (int j = 0; j < 4; j++) v[i + j] += b[j];
     }
 }
-// Columns c .. of the lane's row, 128 bytes of OUT.
+// The residual of the same 128 bytes, on its way to the same place; its arrival is at the barrier.
+__device__ __forceinline__ void fetch_residual(u32 mine, u32 lane, u32 bar, const CUtensorMap *map, int x, int y)
+{
+    if (lane == 0) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(32 * 128) : "memory");
+        copy_tile<1>(mine, map, x, y, bar);
+    }
+}
+// Columns c .. of the lane's row, 128 bytes of OUT; the residual's are in shared memory.
 template <class OUT, int N>
 __device__ __forceinline__ void finish_tile(const Finish &f, u32 mine, u32 lane, const CUtensorMap *y_map, const CUtensorMap *z_map,
                                             u64 row0, u64 c, float (&v)[N])
@@ -422,12 +395,16 @@ __device__ __forceinline__ void finish_tile(const Finish &f, u32 mine, u32 lane,
         else if (f.bias_type == MV_BF16) add_bias<__nv_bfloat16>(f, c, v);
         else add_bias<__half>(f, c, v);
     }
-    if (f.z) store_tile<OUT>(mine, lane, z_map, (int)c, (int)row0, v);
+    if (f.z) store_tile<OUT, false>(mine, lane, z_map, (int)c, (int)row0, v, 1.0f);
     activate<N>(f.act, v);
+    if (f.residual) {
+        store_tile<OUT, true>(mine, lane, y_map, (int)c, (int)row0, v, f.scale);
+        return;
+    }
     if (f.scale != 1.0f)
 #pragma unroll
         for (int i = 0; i < N; i++) v[i] *= f.scale;
-    store_tile<OUT>(mine, lane, y_map, (int)c, (int)row0, v);
+    store_tile<OUT, false>(mine, lane, y_map, (int)c, (int)row0, v, 1.0f);
 }
 
 // ---- tiles -----------------------------------------------------------------
@@ -490,7 +467,8 @@ template <int CTAS, int BN, bool A_MN, bool B_MN, bool SWAP>
 __global__ void __launch_bounds__(Tile<CTAS, BN>::kThreads, BN >= 128 ? 1 : 2)
 k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap a2_map,
           const __grid_constant__ CUtensorMap b_map, const __grid_constant__ CUtensorMap y_map,
-          const __grid_constant__ CUtensorMap z_map, const __grid_constant__ Args args)
+          const __grid_constant__ CUtensorMap z_map, const __grid_constant__ CUtensorMap residual_map,
+          const __grid_constant__ Args args)
 {
     using S = Tile<CTAS, BN>;
     extern __shared__ unsigned char raw[];
@@ -498,7 +476,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
     const u32 stages = S::kStages == S::kFewStages ? S::kStages : args.u.stages;
     const u32 staging = base + stages * S::kStage, bars = staging + S::kStaging;
     const u32 full = bars, empty = full + 8 * stages, done = empty + 8 * stages, taken = done + 16,
-              drained = taken + 16, slot = drained + 8;
+              drained = taken + 16, slot = drained + 8, residuals = slot + 8;
     const u32 warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     u32 rank = 0;
     if constexpr (CTAS == 2 || SWAP) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -516,6 +494,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
             barrier_init(taken + 8 * i, S::kWorkers * CTAS);
         }
         barrier_init(drained, 1);
+        for (u32 i = 0; i < S::kWorkers; i++) barrier_init(residuals + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -632,23 +611,23 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
         const u32 w = warp & 3;                                   // a warp reads its quarter of TMEM's lanes
         const u32 mine = staging + (warp - 2) * 32 * 128, share = (warp - 2) / 4;
         constexpr u32 kShares = S::kWorkers / 4;
-        u32 buffer = 0, buffer_turn = 0;
-        for (u32 i = worker; i < u.total; i += workers) {
+        const u32 residual_bar = residuals + (warp - 2) * 8;
+        u32 buffer = 0, buffer_turn = 0, residual_turn = 0;
+        for (u32 i = worker; i < u.total && ok; i += workers) {
             u32 m, n, first, last;
             unit(i, m, n, first, last);
-            if (!SWAP && args.f.residual && i < u.whole) {        // on its way while the tile is summed
-                const u64 size = args.f.out == MV_F32 ? 4 : 2, r = (u64)m * S::kRows + pair_rank * 128 + w * 32 + lane;
-                const u64 c = (u64)n * BN * size, end = min((u64)(n + 1) * BN, args.f.n) * size;
-                if (r < args.f.m)
-                    for (u64 j = c + share * 128; j < end; j += kShares * 128)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(args.f.residual) + r * args.f.residual_stride * size + j));
-            }
+            constexpr u32 kRun = BN < 32 ? 16 : 32, kShare = BN / kShares;
+            const u64 row0 = (u64)m * S::kRows + pair_rank * 128 + w * 32, col0 = (u64)n * BN;
+            float *part = SWAP || i < u.whole ? nullptr
+                        : args.partial + (u64)(i - u.whole) * (S::kRows * BN) + pair_rank * 128 * BN;
+            // the residual is on its way while the tile is summed
+            const bool fetched = !SWAP && !part && args.f.by_tma && args.f.residual && row0 < args.f.m && col0 + share * kShare < args.f.n;
+            if (fetched) fetch_residual(mine, lane, residual_bar, &residual_map, (int)(col0 + share * kShare), (int)row0);
             // The tensor core's additions cut what is beyond 32 bits off, so an error of a long
             // chain grows with its length (2e-6 after 2048 products): where the result has 32 bits
             // or the chain is very long, it is summed in runs of u.chain steps, and a run's sum is
             // added, rounded to nearest, to the sum of those before it (in TMEM too).
             const u32 earlier = tmem + 2 * S::kColumns + (w << 21);
-            constexpr u32 kRun = BN < 32 ? 16 : 32, kShare = BN / kShares;
             u32 k = first;
             const auto arrived = [&] {
                 ok = barrier_wait(done + 8 * buffer, buffer_turn);
@@ -687,7 +666,10 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                     taken_over();
                 }
             }
-            if (!ok || !arrived()) break;
+            if (!ok || !arrived()) {
+                if (fetched) barrier_wait(residual_bar, residual_turn);
+                break;
+            }
             const u32 sums = tmem + buffer * S::kColumns + (w << 21);
             const auto load_all = [&](u32 c, auto &v) {           // the sums of columns c ..
                 load_sums(sums + c, v);
@@ -699,9 +681,6 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                         for (u32 j = 0; j < sizeof(v) / 4; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(e[j]));
                     }
             };
-            float *part = SWAP || i < u.whole ? nullptr
-                        : args.partial + (u64)(i - u.whole) * (S::kRows * BN) + pair_rank * 128 * BN;
-            const u64 row0 = (u64)m * S::kRows + pair_rank * 128 + w * 32, col0 = (u64)n * BN;
             if constexpr (SWAP) {
                 // lanes are columns of the result, TMEM's columns its rows
                 const u64 column = row0 + lane;
@@ -724,6 +703,13 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                         float v[N];
 #pragma unroll
                         for (int j = 0; j < N; j += 32) load_all(c + j, *reinterpret_cast<u32(*)[32]>(&v[j]));
+                        if (fetched) {
+                            if (c != share * kShare) fetch_residual(mine, lane, residual_bar, &residual_map, (int)(col0 + c), (int)row0);
+                            ok = barrier_wait(residual_bar, residual_turn);
+                            ok = __all_sync(kFull, ok);
+                            if (!ok) return;
+                            residual_turn ^= 1;
+                        }
                         if (row0 < args.f.m) finish_tile<OUT>(args.f, mine, lane, &y_map, &z_map, row0, col0 + c, v);
                     }
                 };
@@ -749,18 +735,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 128 + ((j ^ (lane & 7)) * 16)),
                                      "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3]) : "memory");
                     __syncwarp();
-                    if (!args.f.easy || row0 + 32 > args.f.m || col0 + c + 32 > args.f.n) {
-                        finish_column(args.f, mine, lane, row0, col0 + c + lane);
-                        continue;
-                    }
-                    float t[8][4];
-#pragma unroll
-                    for (u32 j = 0; j < 8; j++) {
-                        const u32 r = j * 4 + (lane >> 3);
-                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(t[j][0]), "=f"(t[j][1]), "=f"(t[j][2]), "=f"(t[j][3])
-                                     : "r"(mine + r * 128 + (((lane & 7) ^ (r & 7)) * 16)));
-                    }
-                    finish_rows(args.f, row0 + (lane >> 3), col0 + c + (lane & 7) * 4, t);
+                    finish_column(args.f, mine, lane, row0, col0 + c + lane);
                 }
             }
             taken_over();
@@ -978,11 +953,11 @@ bool map_side(CUtensorMap *map, const Side &s, u32 dtype, u32 box_rows)
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A dense result, stored 32 rows of 128 bytes at a time.
-bool map_result(CUtensorMap *map, void *p, u64 rows, u64 cols, u32 type)
+// A result or residual, 32 rows of 128 bytes at a time.
+bool map_result(CUtensorMap *map, void *p, u64 rows, u64 cols, u64 stride, u32 type)
 {
     const u32 size = (u32)dtype_size(type);
-    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * size};
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride * size};
     const cuuint32_t box[2] = {128 / size, 32}, each[2] = {1, 1};
     return encoder()(map, type == MV_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                         : type == MV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, each,
@@ -1083,16 +1058,20 @@ int run_kind(const Side &a, const void *a2, const Side &b, u32 dtype, const Plan
 {
     using S = Tile<CTAS, BN>;
     const auto kernel = k_product<CTAS, BN, A_MN, B_MN, SWAP>;
-    CUtensorMap maps[5];
+    CUtensorMap maps[6];
     Side second = a;
     second.p = a2 ? a2 : a.p;
     if (!map_side(&maps[0], a, dtype, 128) || !map_side(&maps[1], second, dtype, 128) ||
         !map_side(&maps[2], b, dtype, S::kBRows))
         return MV_ECUDA;
-    maps[3] = maps[4] = maps[0];
+    maps[3] = maps[4] = maps[5] = maps[0];
     Finish &f = args.f;
-    f.by_tma = !SWAP && !f.residual && f.n * dtype_size(f.out) % 16 == 0 && aligned(f.y, 16) && aligned(f.z, 16) && !(f.z && f.out == MV_F32);
-    if (f.by_tma && (!map_result(&maps[3], f.y, f.m, f.n, f.out) || (f.z && !map_result(&maps[4], f.z, f.m, f.n, f.out)))) return MV_ECUDA;
+    const u64 size = dtype_size(f.out);
+    f.by_tma = !SWAP && f.n * size % 16 == 0 && aligned(f.y, 16) && aligned(f.z, 16) && !(f.z && (f.residual || f.out == MV_F32)) &&
+               (!f.residual || (aligned(f.residual, 16) && f.residual_stride * size % 16 == 0));
+    if (f.by_tma && (!map_result(&maps[3], f.y, f.m, f.n, f.n, f.out) || (f.z && !map_result(&maps[4], f.z, f.m, f.n, f.n, f.out)) ||
+                     (f.residual && !map_result(&maps[5], const_cast<void *>(f.residual), f.m, f.n, f.residual_stride, f.out))))
+        return MV_ECUDA;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem(S::kStages)) != cudaSuccess) return MV_ECUDA;
     // type of the sums: 32 bits; of both operands; which side is contiguous; the tile
     args.what = 1u << 4 | (dtype == MV_BF16 ? 1u << 7 | 1u << 10 : 0u) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
@@ -1116,7 +1095,7 @@ int run_kind(const Side &a, const void *a2, const Side &b, u32 dtype, const Plan
     }
     cfg.attrs = attr;
     cfg.numAttrs = attrs;
-    if (cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], args) != cudaSuccess) return MV_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], args) != cudaSuccess) return MV_ECUDA;
     if (SWAP || p.u.parts == 1) return MV_OK;
     const u32 left = (p.u.total - p.u.whole) / p.u.parts;
     const u32 blocks = left * (S::kRows * BN / 1024);
@@ -1307,7 +1286,6 @@ extern "C" int mv_linear(const mv_linear_desc *d, void *workspace, uint64_t ws_b
     f.bias_wide = wide(d->bias, 0, d->bias_dtype);
     f.y_wide = wide(d->y, d->rows, d->out_dtype);
     f.z_wide = wide(d->z, d->rows, d->dtype);
-    f.easy = f.y_wide && (!f.z || f.z_wide) && (!f.bias || f.bias_wide) && (!f.residual || f.residual_wide);
     return product<false, false>(x, nullptr, w, d->dtype, l.plan, f, reinterpret_cast<float *>(ws + l.partial), packed, s);
 }
 
@@ -1370,7 +1348,7 @@ extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace,
     if (rc == MV_OK && d->dx) {
         f.m = d->tokens;
         f.y = d->dx;
-        f.easy = f.y_wide = wide(d->dx, d->cols, d->dtype);
+        f.y_wide = wide(d->dx, d->cols, d->dtype);
         rc = product<false, true>({dz, d->tokens, d->rows, dz_stride, false}, dz2, {w, d->cols, d->rows, w_stride, true}, d->dtype,
                                   l.dx, f, partial, early, s);
         early = true;
@@ -1378,7 +1356,7 @@ extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace,
     if (rc == MV_OK && d->dw) {
         f.m = d->rows;
         f.y = d->dw;
-        f.easy = f.y_wide = wide(d->dw, d->cols, d->dtype);
+        f.y_wide = wide(d->dw, d->cols, d->dtype);
         rc = product<true, true>({dz, d->rows, d->tokens, dz_stride, true}, dz2, {x, d->cols, d->tokens, x_stride, true}, d->dtype,
                                  l.dw, f, partial, early, s);
         early = true;
