@@ -1028,14 +1028,18 @@ Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 chain, u32 sms, double &b
         }
         return p;
     }
-    // whole tiles in rounds of all slots, and what is left in as many pieces as fill one to four more
+    // whole tiles in rounds of all slots, and what is left in pieces: as many as fill one to four more rounds, or fewer
     const bool two = k.two && tiles > sms;
     const u64 slots = std::max<u64>(1, (u64)sms * (two ? 2 : 1) / each), whole = tiles / slots * slots, left = tiles - whole;
-    for (u64 round = 0; round <= (left ? 4 : 0); round++) {
-        const u64 parts = round ? std::min<u64>(steps, round * slots / left) : 1;
+    auto in_parts = [&](u64 parts) {
         const double join = parts > 1 ? 6000 + (double)(parts * left) * k.rows * k.cols * 4 / (sms * 24.0) : 0;
         consider(whole, left, parts, std::min<u64>(whole + left * parts, slots) * each, slots, two, join);
-    }
+    };
+    in_parts(1);
+    if (!left) return p;
+    for (u64 round = 1; round <= 4; round++) in_parts(std::max<u64>(1, std::min<u64>(steps, round * slots / left)));
+    for (u64 parts : {2, 4, 8, 12})
+        if (parts < slots / left && parts <= steps) in_parts(parts);
     return p;
 }
 
