@@ -11,7 +11,9 @@ simulator steps dispatch, that work, and combine over a fabric
 (:func:`.inputs.moe_workload`).  Routers are compared on the same logits:
 free choice, choice within few groups (a group's experts share a server, so a
 token's copies go to fewer servers), and a balance bias that :func:`balance`
-moves from step to step.
+moves from step to step.  Before the router stand the norm, the residual and the
+router's product of the block (:func:`dense`, :func:`block_step`), whose time a rank
+spends before its dispatch (:func:`dense_ns`).
 
     python -m experiment_network_simulation_gb300.moe_layer
 """
@@ -23,7 +25,7 @@ import numpy as np
 import torch
 
 from . import inputs as I
-from . import moe, mv
+from . import block, moe, mv
 
 
 @dataclass
@@ -97,8 +99,8 @@ def expert_ns(layer: Layer, ids: torch.Tensor, weights: torch.Tensor, repeats: i
     per = layer.experts // layer.ranks
     mats = random_experts(layer, per, device=ids.device)
     x = torch.randn((ids.shape[0], layer.hidden), device=ids.device).bfloat16()
-    flush = torch.empty(1 << 28, dtype=torch.uint8, device=ids.device)
-    out, fills = [], 1
+    timer = _Timer(ids.device, repeats)
+    out = []
     for r in range(layer.ranks):
         here = (ids >= r * per) & (ids < (r + 1) * per)
         rows = here.any(1).nonzero().flatten()
@@ -107,24 +109,69 @@ def expert_ns(layer: Layer, ids: torch.Tensor, weights: torch.Tensor, repeats: i
             continue
         local = torch.where(here, ids - r * per, -1)[rows].int().contiguous()
         mine, w = x[rows].contiguous(), weights[rows].contiguous()
+        out.append(timer(lambda: moe.experts(mine, local, w, *mats)))
+    return out
+
+
+class _Timer:
+    """Device time of a call in ns, as :func:`expert_ns` describes it."""
+
+    def __init__(self, device, repeats: int):
+        self.flush = torch.empty(1 << 28, dtype=torch.uint8, device=device)
+        self.repeats, self.fills = repeats, 1
+
+    def __call__(self, call) -> int:
         times = []
-        while len(times) < repeats + 2:
+        while len(times) < self.repeats + 2:
             a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
-            for _ in range(fills):
-                flush.zero_()
+            for _ in range(self.fills):
+                self.flush.zero_()
             a.record()
-            moe.experts(mine, local, w, *mats)
+            call()
             b.record()
             late = a.query()
             b.synchronize()
             if not late:
                 times.append(a.elapsed_time(b))
-            elif fills < 1 << 12:
-                fills *= 2
+            elif self.fills < 1 << 12:
+                self.fills *= 2
             else:
-                raise RuntimeError("the host takes too long to enqueue the experts' work")
-        out.append(int(1e6 * sorted(times[2:])[repeats // 2]))
-    return out
+                raise RuntimeError("the host takes too long to enqueue the work")
+        return int(1e6 * sorted(times[2:])[self.repeats // 2])
+
+
+def dense(layer: Layer, seed: int = 0, device="cuda") -> dict:
+    """Random weights of what a block does before its experts: the norm of the last
+    branch, that branch's gate, the norm before this one, the router's matrix and bias."""
+    g = torch.Generator(device=device).manual_seed(seed)
+
+    def near(mean, *shape):
+        return mean + 0.1 * torch.randn(shape, generator=g, device=device)
+
+    return dict(post=near(1.0, layer.hidden), gate=near(0.5, layer.hidden), weight=near(1.0, layer.hidden),
+                router=(torch.randn((layer.experts, layer.hidden), generator=g, device=device) * layer.hidden ** -0.5).bfloat16(),
+                bias=near(0.0, layer.experts))
+
+
+def choose(layer: Layer, d: dict, y: torch.Tensor, stream: torch.Tensor, **kw) -> tuple:
+    """A block up to its dispatch, [tokens, hidden] bfloat16: the last branch's output
+    ``y`` joins the ``stream``, which is normed and routed: (n, stream, ids, weights)."""
+    n, stream = block.norm(y, d["weight"], residual=stream, post=d["post"], gate=d["gate"])
+    logits = block.linear(n, d["router"], d["bias"], out_dtype=torch.float32)
+    return (n, stream, *moe.route(logits, layer.topk, scores="sigmoid", **kw))
+
+
+def block_step(layer: Layer, d: dict, mats: tuple, y: torch.Tensor, stream: torch.Tensor, **kw) -> tuple:
+    """A block's decode step on one device that has all the experts: (y, stream) of the next."""
+    n, stream, ids, weights = choose(layer, d, y, stream, **kw)
+    return moe.experts(n, ids, weights, *mats), stream
+
+
+def dense_ns(layer: Layer, repeats: int = 5, device="cuda") -> int:
+    """What a rank's tokens take up to their dispatch, in ns (:func:`choose`)."""
+    d = dense(layer, device=device)
+    y, stream = (torch.randn((layer.tokens, layer.hidden), device=device).bfloat16() for _ in range(2))
+    return _Timer(y.device, repeats)(lambda: choose(layer, d, y, stream))
 
 
 def experiment(layer: Layer, byte: np.ndarray, compute_ns, gbps: int = 400, pkt: int = 4096) -> I.Experiment:
@@ -162,6 +209,7 @@ def compare(layer: Layer, seed: int = 0, rounds: int = 40, step: float = 0.02) -
 
 
 if __name__ == "__main__":
+    print(f"norm, logits and choice of a rank's tokens before dispatch: {dense_ns(Layer()) / 1e3:.1f} us")
     for row in compare(Layer()):
         print(f"{row['router']:32s} {row['copies']:6d} copies, busiest expert {row['busiest_load']:4.1f} x "
               f"the mean, experts' work {row['busiest_ns'] / 1e3:6.1f} us at most, step {row['step_us']:8.1f} us")
