@@ -1,6 +1,9 @@
 // Shared by the block operators (mv_linear.cu, mv_activation.cu, mv_norm.cu).
 #pragma once
 
+#include <cstring>
+#include <type_traits>
+
 #include "mv_moe.cuh"
 
 namespace mvblock {
@@ -52,4 +55,66 @@ __device__ __forceinline__ float activation_slope(u32 act, float z)
     }
 }
 
+// 16 bytes of a row as 32-bit values; N neighbours (16 bytes or more, or one) from and to memory.
+template <class T, int N> __device__ __forceinline__ void widen_piece(const uint4 &w, float *v)
+{
+    const u32 words[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = __uint_as_float(words[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                v[2 * i] = __uint_as_float(words[i] << 16);
+                v[2 * i + 1] = __uint_as_float(words[i] & 0xFFFF0000u);
+            } else {
+                __half2 h;
+                memcpy(&h, &words[i], 4);
+                const float2 f = __half22float2(h);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+}
+template <class T, int N> __device__ __forceinline__ void get(const T *p, float *v)
+{
+    if constexpr (N == 1) {
+        v[0] = to_float(*p);
+    } else {
+        constexpr int kEach = 16 / sizeof(T);       // of a 16-byte word
+#pragma unroll
+        for (int i = 0; i < N; i += kEach) widen_piece<T, kEach>(*reinterpret_cast<const uint4 *>(p + i), v + i);
+    }
+}
+template <class T, int N> __device__ __forceinline__ void put(T *p, const float *v)
+{
+    if constexpr (N == 1) {
+        *p = from_float<T>(v[0]);
+    } else {
+        constexpr int kEach = 16 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < N; i += kEach) {
+            uint4 w;
+            if constexpr (sizeof(T) == 4) {
+                w = make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
+            } else {
+                u32 words[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+                        memcpy(&words[j], &h, 4);
+                    } else {
+                        const __half2 h = __floats2half2_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+                        memcpy(&words[j], &h, 4);
+                    }
+                }
+                w = make_uint4(words[0], words[1], words[2], words[3]);
+            }
+            *reinterpret_cast<uint4 *>(p + i) = w;
+        }
+    }
+}
 }  // namespace mvblock
