@@ -10,6 +10,12 @@
 
 namespace mvblock {
 
+// Rows of up to 16 elements a thread go by blocks of at most 320 threads, two an SM
+// with 96 registers a thread, or by larger ones alone: 16384 x 7168 with both norms
+// took 214 us in two blocks of 64 registers, 195 in one; 16384 x 5120 with biases
+// 152 us in one.
+constexpr u32 kFewThreads = 320;
+
 // A row as it lies in memory, so that the next one costs few registers.
 template <class T, int N, int E, bool WHOLE> struct RawRow {
     static constexpr int kPieces = E / N;
@@ -38,7 +44,7 @@ template <class T, int N, int E, bool WHOLE> struct RawRow {
     }
 };
 
-template <class T, class P, int N, int E, bool WHOLE> __global__ void __launch_bounds__(kMostThreads, N > 1 && E <= 16 ? 2 : 1) k_norm(const NormArgs a)
+template <class T, class P, int N, int E, bool WHOLE, bool FEW> __global__ void __launch_bounds__(FEW ? kFewThreads : kMostThreads, FEW ? 2 : 1) k_norm(const NormArgs a)
 {
     __shared__ __align__(16) float part[2][2][16];
     const u32 threads = blockDim.x, hidden = a.hidden;
@@ -200,20 +206,21 @@ NormArgs arguments(const mv_norm_desc *d)
 
 template <class T, class P> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, cudaStream_t stream)
 {
-    // blocks for as many threads as the registers hold
-    const u32 an_sm = std::max(1u, std::min(16u, (s.n > 1 && s.n * s.pieces <= 16 ? 1024 : 512) / s.threads));
+    const u32 e = s.n * s.pieces;
+    const bool few = s.n > 1 && e <= 16 && s.threads <= kFewThreads;          // single elements take more registers
+    const u32 an_sm = std::max(1u, std::min(16u, (few ? 2 * kFewThreads : kMostThreads) / s.threads));
     const dim3 grid((u32)std::min<u64>(a.tokens, (u64)sms * an_sm));
     constexpr int N = 16 / sizeof(T);
-    const u32 e = s.n * s.pieces;
+    auto run = [&](auto kernel) { return launch(kernel, grid, s.threads, 0, stream, a); };
     if (s.n > 1) {
-        if (e == N) return launch(k_norm<T, P, N, N, false>, grid, s.threads, 0, stream, a);
-        if (e == 16 && s.whole) return launch(k_norm<T, P, N, 16, true>, grid, s.threads, 0, stream, a);
-        if (e == 16) return launch(k_norm<T, P, N, 16, false>, grid, s.threads, 0, stream, a);
-        return launch(k_norm<T, P, N, 32, false>, grid, s.threads, 0, stream, a);
+        if (e == N) return run(k_norm<T, P, N, N, false, true>);
+        if (e == 16 && s.whole) return few ? run(k_norm<T, P, N, 16, true, true>) : run(k_norm<T, P, N, 16, true, false>);
+        if (e == 16) return few ? run(k_norm<T, P, N, 16, false, true>) : run(k_norm<T, P, N, 16, false, false>);
+        return run(k_norm<T, P, N, 32, false, false>);
     }
-    if (e == 4) return launch(k_norm<T, P, 1, 4, false>, grid, s.threads, 0, stream, a);
-    if (e == 16) return launch(k_norm<T, P, 1, 16, false>, grid, s.threads, 0, stream, a);
-    return launch(k_norm<T, P, 1, 32, false>, grid, s.threads, 0, stream, a);
+    if (e == 4) return run(k_norm<T, P, 1, 4, false, false>);
+    if (e == 16) return run(k_norm<T, P, 1, 16, false, false>);
+    return run(k_norm<T, P, 1, 32, false, false>);
 }
 template <class T> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, cudaStream_t stream)
 {
