@@ -8,7 +8,7 @@
 //   dw = dz^T x    A = dz transposed, B = x transposed: both along m or n
 // The tensor core takes either order from shared memory, so nothing is
 // transposed on the way.  Tiles of A and B come by TMA, the sums stay in TMEM
-// in 32 bits, and one warp each copies, multiplies and four finish tiles, the
+// in 32 bits; one warp copies, one multiplies and four or eight finish tiles, the
 // next tile's products running while the last one is finished.
 #include <cuda.h>
 
@@ -199,7 +199,7 @@ __device__ __noinline__ void finish_column(const Finish &f, u32 mine, u32 lane, 
 }
 
 // ---- PTX -------------------------------------------------------------------
-__device__ unsigned g_gave_up;          // blocks that ended a wait by its limit
+__device__ unsigned g_gave_up;          // warps that ended a wait by its limit
 
 __device__ __forceinline__ u32 shared_at(const void *p) { return (u32)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ u64 nanoseconds()
@@ -566,13 +566,14 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                     if (++s == stages) { s = 0; turn ^= 1; }
                 }
             }
-            // After a wait that ran out: the copies under way end first, both blocks' (which
-            // the leader's barriers count), before the pair's blocks go on to their end.
-            if (!ok && pair_rank == 0)
+            // The copies under way end before the block does, and so do the arrivals that tell
+            // that they were used.  After a wait that ran out the former are waited for, both
+            // blocks' of a pair, which the leader's barriers count; else the latter.
+            if (ok || pair_rank == 0)
                 for (u32 j = 0; j < stages && j < issued; j++) {
                     s = s ? s - 1 : stages - 1;
                     if (s == stages - 1) turn ^= 1;
-                    barrier_wait(full + 8 * s, turn);
+                    barrier_wait((ok ? empty : full) + 8 * s, turn);
                 }
         }
     } else if (warp == 1) {
@@ -742,7 +743,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
         }
     }
     if (warp > 1 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");      // the stores have ended
-    if (!ok) atomicAdd(&g_gave_up, 1u);
+    if (!ok && (warp < 2 || lane == 0)) atomicAdd(&g_gave_up, 1u);
     __syncwarp();
     if (SWAP && u.parts > 1) {
         // The pieces' sums meet through the cluster's shared memory: each block finishes

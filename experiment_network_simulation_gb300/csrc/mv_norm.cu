@@ -99,8 +99,8 @@ constexpr u32 kAddWarps = 16, kAddColumns = 64;
 struct AddArgs {
     const float *sums, *gate_sums;
     void *to[4], *dgate;
-    u64 hidden, pitch, blocks, run, rows, gates;
-    u32 params_f32;
+    u64 tokens, hidden, pitch, blocks, run, rows;
+    u32 shared, gates_first, params_f32;
 };
 template <class T> __global__ void __launch_bounds__(32 * kAddWarps) k_norm_add(const AddArgs a)
 {
@@ -108,27 +108,42 @@ template <class T> __global__ void __launch_bounds__(32 * kAddWarps) k_norm_add(
     const u32 lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const u64 c = ((u64)blockIdx.x * 32 + lane) * 2;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // what: four parameters, then the gates
-    for (u64 what = blockIdx.y; what < 4 + a.gates; what += gridDim.y) {
+    // what: four parameters, then the gates that more than one block has a part of: one of every gate
+    // or, where those are more, of every block, the gate that begins in it and goes on after it
+    for (u32 what = blockIdx.y; what < 4 + a.shared; what += gridDim.y) {
         void *out = what < 4 ? a.to[what] : a.dgate;
         if (!out) continue;
         const float *from = a.sums + what * a.pitch;
-        u64 step = 4 * a.pitch, first = 0, last = a.blocks, at = 0;
+        u64 step = 4 * a.pitch, first = 0, last = a.blocks, at = 0, own = 0;
         if (what >= 4) {
-            const u64 g = what - 4;
-            first = g * a.run / a.rows;
+            const u32 i = what - 4, g = a.gates_first ? i : (u32)(min((i + 1) * a.rows, a.tokens) - 1) / (u32)a.run;
+            const u32 b = a.gates_first ? (u32)(g * a.run) / (u32)a.rows : i;
+            const u64 begin = b * a.rows, end = min(begin + a.rows, a.tokens);
+            if (g * a.run < begin || (g + 1) * a.run <= end) continue;
+            // this block's part, and as their first gates' those of the blocks up to its end
+            first = b;
             last = ((g + 1) * a.run - 1) / a.rows + 1;
-            from = a.gate_sums + g * a.pitch;
-            step = a.pitch;
+            from = a.gate_sums;
+            step = 2 * a.pitch;
             at = g * a.hidden;
+            own = g != (u32)begin / (u32)a.run ? a.pitch : 0;
         }
         float2 s = make_float2(0.0f, 0.0f);
-        if (c < a.hidden)
+        if (c < a.hidden) {
+            const float *p = from + (first + warp) * step + c;
+            u32 left = (u32)(last - first);
+            left = left > warp ? (left - warp + kAddWarps - 1) / kAddWarps : 0;
+            if (own && warp == 0) {
+                s = *reinterpret_cast<const float2 *>(p + own);
+                p += kAddWarps * step;
+                left--;
+            }
 #pragma unroll 8
-            for (u64 b = first + warp; b < last; b += kAddWarps) {
-                const float2 w = *reinterpret_cast<const float2 *>(from + b * step + c);
+            for (; left; left--, p += kAddWarps * step) {
+                const float2 w = *reinterpret_cast<const float2 *>(p);
                 s.x += w.x; s.y += w.y;
             }
+        }
         __syncthreads();
         part[warp][lane] = s;
         __syncthreads();
@@ -229,7 +244,6 @@ template <class T> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, 
 
 struct GradPlan {
     NormShape shape;
-    bool each;                          // every token has a gate of its own
     u32 smem;
     u64 blocks, rows, pitch, gate_sums, total;
 };
@@ -255,10 +269,9 @@ GradPlan grad_plan(const mv_norm_desc *d, bool wide)
     const u64 blocks = std::min<u64>((d->tokens + 3) / 4, (u64)sms * std::min(an_sm, 16u));
     p.rows = (d->tokens + blocks - 1) / blocks;
     p.blocks = (d->tokens + p.rows - 1) / p.rows;
-    p.each = d->gate && d->gates == d->tokens;
     p.pitch = (d->hidden + 3) / 4 * 4;
     p.gate_sums = (p.blocks * 4 * p.pitch * 4 + 255) / 256 * 256;
-    p.total = p.gate_sums + (d->gate && !p.each ? (p.blocks + d->gates) * p.pitch * 4 : 0);
+    p.total = p.gate_sums + (d->gate ? p.blocks * 2 * p.pitch * 4 : 0);
     return p;
 }
 
@@ -340,7 +353,7 @@ extern "C" int mv_norm_backward(const mv_norm_desc *d, const mv_norm_grads *g, v
     a.dr_stride = g->dr_stride;
     a.dy = g->dy;
     a.dresidual = g->dresidual;
-    a.dgate = p.each ? g->dgate : nullptr;
+    a.dgate = g->dgate;
     a.rows = p.rows;
     a.sums = reinterpret_cast<float *>(ws);
     a.gate_sums = reinterpret_cast<float *>(ws + p.gate_sums);
@@ -351,20 +364,22 @@ extern "C" int mv_norm_backward(const mv_norm_desc *d, const mv_norm_grads *g, v
     add.to[1] = g->dbias;
     add.to[2] = g->dpost;
     add.to[3] = g->dpost_bias;
-    add.dgate = d->gate && !p.each ? g->dgate : nullptr;
+    add.dgate = g->dgate;
+    add.tokens = d->tokens;
+    add.gates_first = d->gates <= p.blocks;
+    add.shared = add.dgate ? (u32)std::min<u64>(d->gates, p.blocks) : 0;
     add.hidden = d->hidden;
     add.pitch = a.pitch = p.pitch;
     add.blocks = p.blocks;
     add.run = a.run;
     add.rows = p.rows;
-    add.gates = add.dgate ? d->gates : 0;
     add.params_f32 = a.params_f32;
     const bool post = d->post || d->gate, bias = a.layer || d->bias || d->post_bias;
     const int done = d->dtype == MV_F32 ? run_norm_grad<float>(a, p.shape, p.blocks, p.smem, post, bias, on)
                    : d->dtype == MV_F16 ? run_norm_grad<__half>(a, p.shape, p.blocks, p.smem, post, bias, on)
                                         : run_norm_grad<__nv_bfloat16>(a, p.shape, p.blocks, p.smem, post, bias, on);
     if (done != MV_OK) return done;
-    const dim3 grid((u32)((d->hidden + kAddColumns - 1) / kAddColumns), (u32)std::min<u64>(4 + add.gates, 65535));
+    const dim3 grid((u32)((d->hidden + kAddColumns - 1) / kAddColumns), 4 + std::min(add.shared, 16u));
     return d->dtype == MV_BF16 ? launch_after(k_norm_add<__nv_bfloat16>, grid, 32 * kAddWarps, 0, on, add)
                                : launch_after(k_norm_add<__half>, grid, 32 * kAddWarps, 0, on, add);
 }

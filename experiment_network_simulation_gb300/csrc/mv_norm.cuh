@@ -8,14 +8,14 @@ namespace mvblock {
 struct NormArgs {
     const void *y, *residual, *dn, *dr;
     const void *weight, *bias, *post, *post_bias, *gate;
-    void *n, *r, *dy, *dresidual, *dgate;           // dgate: where every token has a gate of its own
+    void *n, *r, *dy, *dresidual, *dgate;
     u64 tokens, y_stride, residual_stride, dn_stride, dr_stride;
     u64 run, rows;                                  // tokens that share a gate; rows a block (backward)
     u32 hidden, layer, params_f32;
     float alpha, eps, inv_hidden;
     u64 pitch;                                      // hidden, up to whole fours
     float *sums;                                    // a block's sums for weight, bias, post, post_bias  [blocks, 4, pitch]
-    float *gate_sums;                               // and for the gates of its rows                     [blocks + gates, pitch]
+    float *gate_sums;                               // and for its first and last gates                  [blocks, 2, pitch]
 };
 
 struct NormShape {

@@ -206,6 +206,20 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
 
     // the sums: of weight, bias, post, post_bias, gate
     float dw[E] = {}, db[BIAS ? E : 2] = {}, dp[POST ? E : 2] = {}, dpb[POST && BIAS ? E : 2] = {}, dg[POST ? E : 2] = {};
+    // A gate whose rows are all this block's is done with them; of another the block has a
+    // part, in one of two places: its first gate's, or another's, which goes on after it.
+    auto store_gate = [&] {
+        if constexpr (POST) {
+            if ((u64)gate * run >= first && gate_end <= last) {
+                P *to = static_cast<P *>(a.dgate) + (u64)gate * hidden;
+#pragma unroll
+                for (u32 i = 0; i < kPieces; i++)
+                    if (within[i]) put<P, N>(to + column[i], &dg[i * N]);
+            } else {
+                store_sums(a.gate_sums + (blockIdx.x * 2ull + (gate != first / run)) * a.pitch, dg);
+            }
+        }
+    };
     u32 buffer = 0;
     u32 end = end_of(first);
     fetch(0, first, end, 0);
@@ -215,7 +229,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
     for (u32 t = first; t < last; buffer ^= 1) {
         if constexpr (POST) {
             if (t == gate_end) {
-                if (!a.dgate) store_sums(a.gate_sums + (blockIdx.x + (u64)gate) * a.pitch, dg);
+                store_gate();
                 gate++;
                 gate_end += run;
 #pragma unroll
@@ -322,16 +336,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
 #pragma unroll
                         for (int i = 0; i < E; i++) u[i] = g[r][i];
                     }
-                    if (a.dgate) {                            // a gate a token: one row at a time
-                        if (r == 0) {
-                            mul_row(u, u, v[r]);
-#pragma unroll
-                            for (u32 i = 0; i < kPieces; i++)
-                                if (within[i]) put<P, N>(static_cast<P *>(a.dgate) + (u64)gate * hidden + column[i], &u[i * N]);
-                        }
-                    } else {
-                        fma_row(dg, u, v[r], dg);
-                    }
+                    fma_row(dg, u, v[r], dg);
                 }
                 param(gate_row, w);
 #pragma unroll
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
     if constexpr (BIAS) store_sums(to + a.pitch, db);
     if constexpr (POST) {
         store_sums(to + 2 * a.pitch, dp);
-        if (gated && !a.dgate) store_sums(a.gate_sums + (blockIdx.x + (u64)gate) * a.pitch, dg);
+        if (gated) store_gate();
     }
     if constexpr (POST && BIAS) store_sums(to + 3 * a.pitch, dpb);
 }

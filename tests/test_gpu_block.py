@@ -317,7 +317,7 @@ def test_norm_longest_rows(hidden):
         check_norm(norm_inputs(6, hidden, dtype, "rms", F32, True, True, 2, False), "rms")
 
 
-@pytest.mark.parametrize("tokens,gates", [(1, 1), (2, 2), (3, 1), (600, 1), (600, 600), (600, 4), (605, 5), (1300, 26), (2500, 500), (2002, 1001)])
+@pytest.mark.parametrize("tokens,gates", [(1, 1), (2, 2), (3, 1), (600, 1), (600, 600), (600, 4), (605, 5), (1300, 26), (2500, 500), (2002, 1001), (4000, 8), (3999, 3), (6000, 40), (9001, 1)])
 def test_norm_gates(tokens, gates):
     """Runs of tokens that share a gate, across blocks and within, of odd and even lengths."""
     check_norm(norm_inputs(tokens, 72, F32, "layer", F32, True, True, gates, True), "layer", 0.5)
