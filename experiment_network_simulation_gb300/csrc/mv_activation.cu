@@ -19,7 +19,8 @@ constexpr u32 kSlopeThreads = 256;
 
 // scale * dy * act'(z) of two neighbours: the formulas of activation_slope(),
 // two values an instruction where there is one, as one value at a time it is
-// instructions, not memory, that bound 16-bit arrays (gelu_tanh of 8192 x 20480: 172 us).
+// instructions, not memory, that bound 16-bit arrays (8192 x 20480: gelu_tanh 172 us,
+// so 163; gelu 316, so 171).
 // SHORT: for a 16-bit result.
 template <u32 ACT, bool SHORT> __device__ __forceinline__ float2 slope2(float2 z, float2 dy, float scale)
 {
@@ -42,22 +43,9 @@ template <u32 ACT, bool SHORT> __device__ __forceinline__ float2 slope2(float2 z
         more = make_float2(both.x > 0.0f ? more.x : 0.0f, both.y > 0.0f ? more.y : 0.0f);
         return __fmul2_rn(__fmul2_rn(dy, __fadd2_rn(q, more)), s);
     } else if constexpr (ACT == MV_ACT_GELU && SHORT) {
-        // Phi(z) + z phi(z).  With a = |z| and t = 1 / (1 + 0.4 a) the normal distribution's tail
-        // is t 2^(p(t) - a^2 log2(e) / 2); p is a Chebyshev fit (degree 8, to 1.3e-7) of what that
-        // leaves of its logarithm.  2e-7 of 1, less than a hundredth of a 16-bit result's rounding,
-        // and a fraction of erfc's instructions (8192 x 20480: 316 us so far).
-        constexpr float kTail[9] = {0.275790244f, -1.41183841f, 2.81971717f, -2.53615332f, 0.788428247f, -0.264325142f, 0.537471354f, 1.43842268f, -2.64751267f};
-        auto all = [](float v) { return make_float2(v, v); };
-        const float2 a = make_float2(fabsf(z.x), fabsf(z.y)), below = __ffma2_rn(a, all(0.4f), all(1.0f));
-        const float2 t = make_float2(reciprocal_fast(below.x), reciprocal_fast(below.y));
-        float2 p = all(kTail[0]);
-#pragma unroll
-        for (int i = 1; i < 9; i++) p = __ffma2_rn(p, t, all(kTail[i]));
-        const float2 square = __fmul2_rn(__fmul2_rn(a, a), all(-0.5f * kLog2e));
-        p = __fadd2_rn(p, square);
-        const float2 tail = __fmul2_rn(t, make_float2(exp2_fast(p.x), exp2_fast(p.y)));
-        const float2 bell = __fmul2_rn(make_float2(exp2_fast(square.x), exp2_fast(square.y)), all(0.39894228040143268f));
-        const float2 q = make_float2(z.x > 0.0f ? 1.0f - tail.x : tail.x, z.y > 0.0f ? 1.0f - tail.y : tail.y);
+        // Phi(z) + z phi(z)
+        float2 bell;
+        const float2 q = normal2(z, bell);
         float2 more = __fmul2_rn(z, bell);
         more = make_float2(bell.x > 0.0f ? more.x : 0.0f, bell.y > 0.0f ? more.y : 0.0f);
         return __fmul2_rn(__fmul2_rn(dy, __fadd2_rn(q, more)), s);

@@ -134,38 +134,18 @@ __device__ __forceinline__ void finish1(const Finish &f, u64 r, u64 c, float v)
     put_as(f.out, f.y, r * f.y_stride + c, v);
 }
 
-template <u32 ACT, int N> __device__ __forceinline__ void activate(float *v)
-{
-#pragma unroll
-    for (int i = 0; i < N; i++) v[i] = activation(ACT, v[i]);
-}
-template <int N> __device__ __forceinline__ void activate(u32 act, float *v)
-{
-    if (act == MV_ACT_RELU) activate<MV_ACT_RELU, N>(v);
-    else if (act == MV_ACT_GELU) activate<MV_ACT_GELU, N>(v);
-    else if (act == MV_ACT_GELU_TANH) activate<MV_ACT_GELU_TANH, N>(v);
-    else if (act == MV_ACT_SILU) activate<MV_ACT_SILU, N>(v);
-}
 // A warp's 32 x 32 of a tile from shared memory, where rows lie anywhere: a lane
-// has column c of the rows from r on, so that a warp's accesses are neighbours,
-// and 32 of them under way (row after row, 8192 x 5120 to 20480 took 2210 us, so 916).
-template <class T> __device__ __forceinline__ void load_column(const void *p, u64 at, u64 stride, u32 rows, float (&v)[32])
+// has column c of the rows from r on, so that a warp's accesses are neighbours.
+// ALL: of 32 rows.  Residuals are read first and all at once (each in its turn,
+// 3604 x 80 to 2448 with residual and pre-activations took 70 us, so 42).
+template <class OUT, bool ALL> __device__ __forceinline__ void finish_column(const Finish &f, u32 mine, u32 lane, u64 r, u64 c, u32 rows)
 {
-    const T *from = static_cast<const T *>(p) + at;
+    OUT residual[32];
+    if (f.residual) {
+        const OUT *from = static_cast<const OUT *>(f.residual) + r * f.residual_stride + c;
 #pragma unroll
-    for (u32 j = 0; j < 32; j++) v[j] = j < rows ? to_float(from[j * stride]) : 0.0f;
-}
-template <class T> __device__ __forceinline__ void store_column(void *p, u64 at, u64 stride, u32 rows, const float (&v)[32])
-{
-    T *to = static_cast<T *>(p) + at;
-#pragma unroll
-    for (u32 j = 0; j < 32; j++)
-        if (j < rows) to[j * stride] = from_float<T>(v[j]);
-}
-__device__ __noinline__ void finish_column(const Finish &f, u32 mine, u32 lane, u64 r, u64 c)
-{
-    if (c >= f.n || r >= f.m) return;
-    const u32 rows = f.m - r < 32 ? (u32)(f.m - r) : 32;
+        for (u32 j = 0; j < 32; j++) residual[j] = ALL || j < rows ? from[j * f.residual_stride] : from_float<OUT>(0.0f);
+    }
     float v[32];
 #pragma unroll
     for (u32 j = 0; j < 32; j++)
@@ -176,26 +156,34 @@ __device__ __noinline__ void finish_column(const Finish &f, u32 mine, u32 lane, 
         for (u32 j = 0; j < 32; j++) v[j] += b;
     }
     if (f.z) {
-        if (f.dtype == MV_BF16) store_column<__nv_bfloat16>(f.z, r * f.n + c, f.n, rows, v);
-        else store_column<__half>(f.z, r * f.n + c, f.n, rows, v);
-    }
-    activate<32>(f.act, v);
-    if (f.residual) {
-        float b[32];
-        const u64 at = r * f.residual_stride + c;
-        if (f.out == MV_BF16) load_column<__nv_bfloat16>(f.residual, at, f.residual_stride, rows, b);
-        else if (f.out == MV_F16) load_column<__half>(f.residual, at, f.residual_stride, rows, b);
-        else load_column<float>(f.residual, at, f.residual_stride, rows, b);
+        unsigned short *z = static_cast<unsigned short *>(f.z) + r * f.n + c;
 #pragma unroll
-        for (u32 j = 0; j < 32; j++) v[j] = fmaf(f.scale, v[j], b[j]);
-    } else if (f.scale != 1.0f) {
-#pragma unroll
-        for (u32 j = 0; j < 32; j++) v[j] *= f.scale;
+        for (u32 j = 0; j < 32; j++) {
+            unsigned short w;
+            if (f.dtype == MV_BF16) {
+                const __nv_bfloat16 t = from_float<__nv_bfloat16>(v[j]);
+                memcpy(&w, &t, 2);
+            } else {
+                const __half t = from_float<__half>(v[j]);
+                memcpy(&w, &t, 2);
+            }
+            if (ALL || j < rows) z[j * f.n] = w;
+        }
     }
-    const u64 at = r * f.y_stride + c;
-    if (f.out == MV_BF16) store_column<__nv_bfloat16>(f.y, at, f.y_stride, rows, v);
-    else if (f.out == MV_F16) store_column<__half>(f.y, at, f.y_stride, rows, v);
-    else store_column<float>(f.y, at, f.y_stride, rows, v);
+    activate<32, sizeof(OUT) == 2>(f.act, v);
+    OUT *y = static_cast<OUT *>(f.y) + r * f.y_stride + c;
+#pragma unroll
+    for (u32 j = 0; j < 32; j++) {
+        const float t = f.residual ? fmaf(f.scale, v[j], to_float(residual[j])) : f.scale * v[j];
+        if (ALL || j < rows) y[j * f.y_stride] = from_float<OUT>(t);
+    }
+}
+template <class OUT> __device__ __noinline__ void finish_column(const Finish &from, u32 mine, u32 lane, u64 r, u64 c)
+{
+    const Finish f = from;              // in registers: through the reference each would be read again after every store
+    if (c >= f.n || r >= f.m) return;
+    if (f.m - r >= 32) finish_column<OUT, true>(f, mine, lane, r, c, 32);
+    else finish_column<OUT, false>(f, mine, lane, r, c, (u32)(f.m - r));
 }
 
 // ---- PTX -------------------------------------------------------------------
@@ -396,7 +384,7 @@ __device__ __forceinline__ void finish_tile(const Finish &f, u32 mine, u32 lane,
         else add_bias<__half>(f, c, v);
     }
     if (f.z) store_tile<OUT, false>(mine, lane, z_map, (int)c, (int)row0, v, 1.0f);
-    activate<N>(f.act, v);
+    activate<N, sizeof(OUT) == 2>(f.act, v);
     if (f.residual) {
         store_tile<OUT, true>(mine, lane, y_map, (int)c, (int)row0, v, f.scale);
         return;
@@ -736,7 +724,9 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 128 + ((j ^ (lane & 7)) * 16)),
                                      "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3]) : "memory");
                     __syncwarp();
-                    finish_column(args.f, mine, lane, row0, col0 + c + lane);
+                    if (args.f.out == MV_BF16) finish_column<__nv_bfloat16>(args.f, mine, lane, row0, col0 + c + lane);
+                    else if (args.f.out == MV_F16) finish_column<__half>(args.f, mine, lane, row0, col0 + c + lane);
+                    else finish_column<float>(args.f, mine, lane, row0, col0 + c + lane);
                 }
             }
             taken_over();
@@ -829,28 +819,42 @@ struct PackArgs {
     unsigned short *to[2];
     u64 stride[2], rows[2], cols[2];
 };
-// Two arrays at most (blockIdx.y), a row a warp, eight values a lane.  They are
-// read by aligned words of two values, each of which holds one of the row at least.
-__global__ void __launch_bounds__(256) k_pack(const PackArgs a)
+// Two arrays at most (blockIdx.y), eight values a thread and four such under way.
+// They are read by aligned words of two values, each of which holds one of the row at least.
+constexpr u32 kPackThreads = 256, kPackAhead = 4;
+__global__ void __launch_bounds__(kPackThreads) k_pack(const PackArgs a)
 {
-    const u32 which = blockIdx.y, lane = threadIdx.x & 31;
-    const u64 cols = a.cols[which], to_stride = (cols + 7) / 8 * 8;
-    for (u64 r = blockIdx.x * 8 + (threadIdx.x >> 5); r < a.rows[which]; r += gridDim.x * 8) {
-        const unsigned short *from = a.from[which] + r * a.stride[which];
-        const u32 odd = (u32)(reinterpret_cast<uintptr_t>(from) >> 1 & 1);
-        const u32 *words = reinterpret_cast<const u32 *>(from - odd);
-        const u64 end = (cols + odd + 1) / 2;                 // words of the row
-#pragma unroll 2
-        for (u64 c = lane * 8; c < cols; c += 256) {
-            u32 w[5], v[4];
+    const u32 which = blockIdx.y;
+    const u64 cols = a.cols[which], stride = a.stride[which], pieces = (cols + 7) / 8, n = a.rows[which] * pieces;
+    const unsigned short *all = a.from[which];
+    uint4 *to = reinterpret_cast<uint4 *>(a.to[which]);
+    for (u64 i0 = (u64)blockIdx.x * (kPackThreads * kPackAhead) + threadIdx.x; i0 < n; i0 += (u64)gridDim.x * (kPackThreads * kPackAhead)) {
+        u32 w[kPackAhead][5], odd[kPackAhead];
+        u64 c[kPackAhead];
 #pragma unroll
-            for (u32 i = 0; i < 5; i++) w[i] = c / 2 + i < end ? words[c / 2 + i] : 0;
+        for (u32 j = 0; j < kPackAhead; j++) {
+            const u64 i = i0 + j * kPackThreads;
+            if (i >= n) break;
+            const u64 r = n >> 32 ? i / pieces : (u32)i / (u32)pieces;
+            c[j] = (i - r * pieces) * 8;
+            const unsigned short *from = all + r * stride;
+            odd[j] = (u32)(reinterpret_cast<uintptr_t>(from) >> 1 & 1);
+            const u32 *words = reinterpret_cast<const u32 *>(from - odd[j]) + c[j] / 2;
+            const u64 left = (cols + odd[j] + 1) / 2 - c[j] / 2;           // words of the row from here on
 #pragma unroll
-            for (u32 i = 0; i < 4; i++) {
-                v[i] = odd ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
-                if (c + 2 * i + 1 >= cols) v[i] = c + 2 * i < cols ? v[i] & 0xFFFFu : 0;
+            for (u32 k = 0; k < 5; k++) w[j][k] = k < left ? words[k] : 0;
+        }
+#pragma unroll
+        for (u32 j = 0; j < kPackAhead; j++) {
+            const u64 i = i0 + j * kPackThreads;
+            if (i >= n) break;
+            u32 v[4];
+#pragma unroll
+            for (u32 k = 0; k < 4; k++) {
+                v[k] = odd[j] ? __funnelshift_r(w[j][k], w[j][k + 1], 16) : w[j][k];
+                if (c[j] + 2 * k + 1 >= cols) v[k] = c[j] + 2 * k < cols ? v[k] & 0xFFFFu : 0;
             }
-            *reinterpret_cast<uint4 *>(a.to[which] + r * to_stride + c) = make_uint4(v[0], v[1], v[2], v[3]);
+            to[i] = make_uint4(v[0], v[1], v[2], v[3]);
         }
     }
 }
@@ -1152,7 +1156,7 @@ struct Packing {
         a.stride[count] = stride;
         a.rows[count] = rows;
         a.cols[count++] = cols;
-        most = std::max(most, rows);
+        most = std::max(most, rows * ((cols + 7) / 8));
         stride = up(cols, 8);
         return to;
     }
@@ -1160,10 +1164,10 @@ struct Packing {
     {
         const u32 pairs = count;
         if (!pairs) return MV_OK;
-        const dim3 grid((u32)std::min<u64>((most + 7) / 8, 8192), pairs);
+        const dim3 grid((u32)std::min<u64>((most + kPackThreads * kPackAhead - 1) / (kPackThreads * kPackAhead), 1u << 16), pairs);
         count = 0;
         most = 0;
-        return launch(k_pack, grid, 256, 0, stream, a);
+        return launch(k_pack, grid, kPackThreads, 0, stream, a);
     }
 };
 
