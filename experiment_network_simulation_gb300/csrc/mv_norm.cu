@@ -44,9 +44,9 @@ template <class T, int N, int E, bool WHOLE> struct RawRow {
     }
 };
 
-template <class T, class P, int N, int E, bool WHOLE, bool FEW> __global__ void __launch_bounds__(FEW ? kFewThreads : kMostThreads, FEW ? 2 : 1) k_norm(const NormArgs a)
+template <class T, class P, int N, int E, bool WHOLE, bool FEW> __global__ void __launch_bounds__(FEW ? kFewThreads : N == 1 ? 1024 : kMostThreads, FEW ? 2 : 1) k_norm(const NormArgs a)
 {
-    __shared__ __align__(16) float part[2][2][16];
+    __shared__ __align__(16) float part[2][2][32];
     const u32 threads = blockDim.x, hidden = a.hidden;
     const bool layer = a.layer;
     Reducer sum = {part, 0, threads / 32};
@@ -165,7 +165,7 @@ template <class T> __global__ void __launch_bounds__(32 * kAddWarps) k_norm_add(
 NormShape shape_of(u32 hidden, u32 size, bool wide)
 {
     const u32 n = wide ? 16 / size : 1, few = wide ? n : 4;
-    const u32 e = hidden <= 32 * few ? few : hidden <= 16 * kMostThreads ? 16 : 32;
+    const u32 e = hidden <= 32 * few ? few : !wide ? (hidden <= 8192 ? 8 : 16) : hidden <= 16 * kMostThreads ? 16 : 32;
     const u32 threads = (hidden + e - 1) / e;
     return {n, e / n, (threads + 31) / 32 * 32, hidden % (32 * e) == 0};
 }
@@ -223,7 +223,7 @@ template <class T, class P> int run_norm(const NormArgs &a, const NormShape &s, 
 {
     const u32 e = s.n * s.pieces;
     const bool few = s.n > 1 && e <= 16 && s.threads <= kFewThreads;          // single elements take more registers
-    const u32 an_sm = std::max(1u, std::min(16u, (few ? 2 * kFewThreads : kMostThreads) / s.threads));
+    const u32 an_sm = std::max(1u, std::min(16u, (few ? 2 * kFewThreads : s.n == 1 ? 1024 : kMostThreads) / s.threads));
     const dim3 grid((u32)std::min<u64>(a.tokens, (u64)sms * an_sm));
     constexpr int N = 16 / sizeof(T);
     auto run = [&](auto kernel) { return launch(kernel, grid, s.threads, 0, stream, a); };
@@ -234,8 +234,8 @@ template <class T, class P> int run_norm(const NormArgs &a, const NormShape &s, 
         return run(k_norm<T, P, N, 32, false, false>);
     }
     if (e == 4) return run(k_norm<T, P, 1, 4, false, false>);
-    if (e == 16) return run(k_norm<T, P, 1, 16, false, false>);
-    return run(k_norm<T, P, 1, 32, false, false>);
+    if (e == 8) return run(k_norm<T, P, 1, 8, false, false>);
+    return run(k_norm<T, P, 1, 16, false, false>);
 }
 template <class T> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, cudaStream_t stream)
 {

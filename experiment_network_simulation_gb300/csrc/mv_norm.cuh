@@ -101,13 +101,13 @@ template <int E> __device__ __forceinline__ float dot_row(const float (&a)[E], c
 // every thread adds the warps' sums itself: a second round of shuffles would
 // take twice as long.
 struct Reducer {
-    float (*part)[2][16];
+    float (*part)[2][32];
     u32 turn, warps;
     __device__ __forceinline__ static float warps_sum(const float *p, u32 warps)
     {
         float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (u32 i = 0; i < 16; i += 4) {
+        for (u32 i = 0; i < 32; i += 4) {
             if (i >= warps) break;
             const float4 w = *reinterpret_cast<const float4 *>(p + i);
             s = __fadd2_rn(s, __fadd2_rn(make_float2(w.x, w.y), make_float2(w.z, w.w)));
@@ -117,7 +117,7 @@ struct Reducer {
     __device__ __forceinline__ void start()         // warps that are not there add nothing
     {
         if (threadIdx.x < 32)
-            for (u32 i = threadIdx.x; i < 64; i += 32) part[0][0][i] = 0.0f;
+            for (u32 i = threadIdx.x; i < 128; i += 32) part[0][0][i] = 0.0f;
         __syncthreads();
     }
     __device__ __forceinline__ float2 operator()(float a, float b)
