@@ -10,11 +10,11 @@
 
 namespace mvblock {
 
-// Rows of up to 16 elements a thread go by blocks of at most 320 threads, two an SM
-// with 96 registers a thread, or by larger ones alone: 16384 x 7168 with both norms
-// took 214 us in two blocks of 64 registers, 195 in one; 16384 x 5120 with biases
-// 152 us in one.
-constexpr u32 kFewThreads = 320;
+// Registers decide: blocks of at most 320 threads go two an SM with 96 registers a
+// thread, larger ones alone.  16384 x 7168 with both norms took 214 us in two blocks of
+// 64 registers, 195 in one; 16384 x 5120 with biases 152 us in one block, 115 in two;
+// unaligned rows, 16384 x 1437 in 16 bits, 99 us with 64 registers, 66 with 96.
+constexpr int kFewThreads = 320, kMoreThreads = 640;
 
 // A row as it lies in memory, so that the next one costs few registers.
 template <class T, int N, int E, bool WHOLE> struct RawRow {
@@ -24,14 +24,9 @@ template <class T, int N, int E, bool WHOLE> struct RawRow {
     {
 #pragma unroll
         for (int i = 0; i < kPieces; i++) {
-            const u32 c = (i * threads + threadIdx.x) * N;
-            if constexpr (N == 1) {
-                if constexpr (!WHOLE) piece[i] = from_float<T>(0.0f);
-                if (WHOLE || c < hidden) piece[i] = row[c];
-            } else {
-                if constexpr (!WHOLE) piece[i] = make_uint4(0, 0, 0, 0);
-                if (WHOLE || c < hidden) piece[i] = *reinterpret_cast<const uint4 *>(row + c);
-            }
+            const u32 c = WHOLE ? (i * threads + threadIdx.x) * N : column_of<N>(i, hidden, threads);
+            if constexpr (N == 1) piece[i] = row[c];
+            else piece[i] = *reinterpret_cast<const uint4 *>(row + c);
         }
     }
     __device__ __forceinline__ void widen(float (&v)[E]) const
@@ -44,7 +39,7 @@ template <class T, int N, int E, bool WHOLE> struct RawRow {
     }
 };
 
-template <class T, class P, int N, int E, bool WHOLE, bool FEW> __global__ void __launch_bounds__(FEW ? kFewThreads : N == 1 ? 1024 : kMostThreads, FEW ? 2 : 1) k_norm(const NormArgs a)
+template <class T, class P, int N, int E, bool WHOLE, int MOST> __global__ void __launch_bounds__(MOST, MOST == kFewThreads ? 2 : 1) k_norm(const NormArgs a)
 {
     __shared__ __align__(16) float part[2][2][32];
     const u32 threads = blockDim.x, hidden = a.hidden;
@@ -221,21 +216,21 @@ NormArgs arguments(const mv_norm_desc *d)
 
 template <class T, class P> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, cudaStream_t stream)
 {
-    const u32 e = s.n * s.pieces;
-    const bool few = s.n > 1 && e <= 16 && s.threads <= kFewThreads;          // single elements take more registers
-    const u32 an_sm = std::max(1u, std::min(16u, (few ? 2 * kFewThreads : s.n == 1 ? 1024 : kMostThreads) / s.threads));
+    const u32 e = s.n * s.pieces, few = e <= 16 && s.threads <= kFewThreads;
+    const u32 an_sm = few ? std::min(16u, 2 * kFewThreads / s.threads) : 1;
     const dim3 grid((u32)std::min<u64>(a.tokens, (u64)sms * an_sm));
-    constexpr int N = 16 / sizeof(T);
+    constexpr int N = 16 / sizeof(T), kFew = kFewThreads, kMost = kMostThreads;
     auto run = [&](auto kernel) { return launch(kernel, grid, s.threads, 0, stream, a); };
     if (s.n > 1) {
-        if (e == N) return run(k_norm<T, P, N, N, false, true>);
-        if (e == 16 && s.whole) return few ? run(k_norm<T, P, N, 16, true, true>) : run(k_norm<T, P, N, 16, true, false>);
-        if (e == 16) return few ? run(k_norm<T, P, N, 16, false, true>) : run(k_norm<T, P, N, 16, false, false>);
-        return run(k_norm<T, P, N, 32, false, false>);
+        if (e == N) return run(k_norm<T, P, N, N, false, kFew>);
+        if (e == 16 && s.whole) return few ? run(k_norm<T, P, N, 16, true, kFew>) : run(k_norm<T, P, N, 16, true, kMost>);
+        if (e == 16) return few ? run(k_norm<T, P, N, 16, false, kFew>) : run(k_norm<T, P, N, 16, false, kMost>);
+        return run(k_norm<T, P, N, 32, false, kMost>);
     }
-    if (e == 4) return run(k_norm<T, P, 1, 4, false, false>);
-    if (e == 8) return run(k_norm<T, P, 1, 8, false, false>);
-    return run(k_norm<T, P, 1, 16, false, false>);
+    if (e == 4) return run(k_norm<T, P, 1, 4, false, kFew>);
+    if (e == 8) return few ? run(k_norm<T, P, 1, 8, false, kFew>) : s.threads <= kMoreThreads ? run(k_norm<T, P, 1, 8, false, kMoreThreads>)
+                                                                                              : run(k_norm<T, P, 1, 8, false, 1024>);
+    return run(k_norm<T, P, 1, 16, false, 1024>);
 }
 template <class T> int run_norm(const NormArgs &a, const NormShape &s, u32 sms, cudaStream_t stream)
 {

@@ -27,18 +27,27 @@ template <class T> int run_norm_grad(const NormArgs &a, const NormShape &s, u64 
 // A thread's E elements of a row: pieces of N neighbours (16 bytes, or one
 // where rows lie on no 16-byte boundary), threads next to each other.  Beyond
 // the row they are 0.  Arithmetic goes by pairs, two values an instruction.
-// Elements of a row (or of a parameter), 0 beyond `hidden`; to a row.  WHOLE:
-// the threads' pieces are the row, and nothing lies beyond.
+// Elements of a row (or of a parameter); to a row.  WHOLE: the threads' pieces
+// are the row, and nothing lies beyond.  Else a piece beyond it is its first one
+// over again, read without a branch, and is hidden where it would count.
+template <int N> __device__ __forceinline__ u32 column_of(u32 i, u32 hidden, u32 threads)
+{
+    const u32 c = (i * threads + threadIdx.x) * N;
+    return c < hidden ? c : 0;
+}
 template <class T, int N, bool WHOLE, int E> __device__ __forceinline__ void get_row(const T *row, u32 hidden, u32 threads, float (&v)[E])
 {
-    row += threadIdx.x * N;
 #pragma unroll
-    for (int i = 0; i < E / N; i++) {
-        if constexpr (!WHOLE)
+    for (int i = 0; i < E / N; i++) get<T, N>(row + (WHOLE ? (i * threads + threadIdx.x) * N : column_of<N>(i, hidden, threads)), &v[i * N]);
+}
+template <int N, bool WHOLE, int E> __device__ __forceinline__ void hide(u32 hidden, u32 threads, float (&v)[E])
+{
+    if constexpr (!WHOLE)
 #pragma unroll
-            for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
-        if (WHOLE || (i * threads + threadIdx.x) * N < hidden) get<T, N>(row + i * threads * N, &v[i * N]);
-    }
+        for (int i = 0; i < E / N; i++)
+            if ((i * threads + threadIdx.x) * N >= hidden)
+#pragma unroll
+                for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
 }
 template <class T, int N, bool WHOLE, int E> __device__ __forceinline__ void put_row(T *row, u32 hidden, u32 threads, const float (&v)[E])
 {
@@ -151,15 +160,11 @@ struct Reducer {
 template <int N, bool WHOLE, int E> __device__ __forceinline__ float2 normalise(const NormArgs &a, bool layer, Reducer &sum, float (&v)[E], u32 threads)
 {
     float mean = 0.0f;
+    hide<N, WHOLE>(a.hidden, threads, v);
     if (layer) {
         mean = sum(sum_row(v)) * a.inv_hidden;
         add_row(v, v, -mean);
-        if constexpr (!WHOLE)
-#pragma unroll
-            for (int i = 0; i < E / N; i++)
-                if ((i * threads + threadIdx.x) * N >= a.hidden)
-#pragma unroll
-                    for (int j = 0; j < N; j++) v[i * N + j] = 0.0f;
+        hide<N, WHOLE>(a.hidden, threads, v);
     }
     const float inverse = rsqrtf(fmaf(sum(dot_row(v, v)), a.inv_hidden, a.eps));
     mul_row(v, v, inverse);
