@@ -400,6 +400,9 @@ template <class T, class P> int run_grad(const NormArgs &a, const NormShape &s, 
         return bias ? run_grad<T, P, N, 8, 2, true, true, kMany>(a, s, blocks, smem, stream)
                     : run_grad<T, P, N, 8, 2, true, false, kMany>(a, s, blocks, smem, stream);
     }
+    if (s.pieces * s.n == 8 && few)
+        return post ? run_grad<T, P, 1, 8, 2, true, true, kFew>(a, s, blocks, smem, stream)
+                    : run_grad<T, P, 1, 8, 2, false, true, kFew>(a, s, blocks, smem, stream);
     if (s.pieces * s.n == 8)
         return post ? run_grad<T, P, 1, 8, 2, true, true, kMany>(a, s, blocks, smem, stream)
                     : run_grad<T, P, 1, 8, 2, false, true, kMany>(a, s, blocks, smem, stream);
