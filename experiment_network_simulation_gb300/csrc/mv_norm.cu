@@ -2,7 +2,14 @@
 // residual between them (mv_norm, mv_norm_backward in include/mv.h):
 //   u = N(y) post + post_bias,   r = alpha residual + gate u,   n = N(r) weight + bias
 // A block holds a row: it is read once, the next one on its way, and the stream
-// between the two norms is normed from its 32-bit values.  Memory bounds it.
+// between the two norms is normed from its 32-bit values.
+//
+// Memory bounds it where a row is normed once: 16384 x 5120 bfloat16, layer, with
+// residual and gates (671 MB) 111 us, 6.0 TB/s.  With both norms it is the row's
+// chain of sums and the instructions between them: 16384 x 7168, 195 us, 4.8 TB/s.
+// Steps on the way to the first figure: 191 us; the next row's loads ahead and
+// arithmetic by pairs 111; registers by block size, for parameters of 32 bits and
+// biases.  Rows on no 16-byte boundary go element by element: 16384 x 1437, 2.8 TB/s.
 #include <algorithm>
 #include <cmath>
 

@@ -24,12 +24,11 @@ struct NormShape {
 };
 template <class T> int run_norm_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream);
 
-// A thread's E elements of a row: pieces of N neighbours (16 bytes, or one
-// where rows lie on no 16-byte boundary), threads next to each other.  Beyond
-// the row they are 0.  Arithmetic goes by pairs, two values an instruction.
-// Elements of a row (or of a parameter); to a row.  WHOLE: the threads' pieces
-// are the row, and nothing lies beyond.  Else a piece beyond it is its first one
-// over again, read without a branch, and is hidden where it would count.
+// A thread's E elements of a row (or of a parameter): pieces of N neighbours (16
+// bytes, or one where rows lie on no 16-byte boundary), threads next to each
+// other.  WHOLE: the threads' pieces are the row, and nothing lies beyond.  Else a
+// piece beyond it is its first one over again, read without a branch, and is
+// hidden where it would count.  Arithmetic goes by pairs, two values an instruction.
 template <int N> __device__ __forceinline__ u32 column_of(u32 i, u32 hidden, u32 threads)
 {
     const u32 c = (i * threads + threadIdx.x) * N;
