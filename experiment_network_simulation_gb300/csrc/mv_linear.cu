@@ -133,46 +133,27 @@ __device__ __forceinline__ float value_as(u32 type, const void *p, u64 at)
     return type == MV_BF16 ? to_float(static_cast<const __nv_bfloat16 *>(p)[at])
          : type == MV_F16 ? to_float(static_cast<const __half *>(p)[at]) : static_cast<const float *>(p)[at];
 }
-__device__ __forceinline__ void put_as(u32 type, void *p, u64 at, float v)
+// Column c of N rows from r on, a lane's of a warp whose lanes have neighbours, so
+// that their accesses are whole; rows may lie anywhere.  ALL: of as many rows.
+// Residuals are read first and all at once (each in its turn, 3604 x 80 to 2448 with
+// residual and pre-activations took 70 us, so 42).
+template <class OUT, int N> __device__ __forceinline__ void read_residual(const Finish &f, u64 r, u64 c, u32 rows, OUT (&residual)[N])
 {
-    if (type == MV_BF16) static_cast<__nv_bfloat16 *>(p)[at] = from_float<__nv_bfloat16>(v);
-    else if (type == MV_F16) static_cast<__half *>(p)[at] = from_float<__half>(v);
-    else static_cast<float *>(p)[at] = v;
-}
-__device__ __forceinline__ void finish1(const Finish &f, u64 r, u64 c, float v)
-{
-    if (f.bias) v += value_as(f.bias_type, f.bias, c);
-    if (f.z) put_as(f.dtype, f.z, r * f.n + c, v);
-    v = activation(f.act, v);
-    v = f.residual ? fmaf(f.scale, v, value_as(f.out, f.residual, r * f.residual_stride + c)) : f.scale * v;
-    put_as(f.out, f.y, r * f.y_stride + c, v);
-}
-
-// A warp's 32 x 32 of a tile from shared memory, where rows lie anywhere: a lane
-// has column c of the rows from r on, so that a warp's accesses are neighbours.
-// ALL: of 32 rows.  Residuals are read first and all at once (each in its turn,
-// 3604 x 80 to 2448 with residual and pre-activations took 70 us, so 42).
-template <class OUT, bool ALL> __device__ __forceinline__ void finish_column(const Finish &f, u32 mine, u32 lane, u64 r, u64 c, u32 rows)
-{
-    OUT residual[32];
-    if (f.residual) {
-        const OUT *from = static_cast<const OUT *>(f.residual) + r * f.residual_stride + c;
+    const OUT *from = static_cast<const OUT *>(f.residual) + r * f.residual_stride + c;
 #pragma unroll
-        for (u32 j = 0; j < 32; j++) residual[j] = ALL || j < rows ? from[j * f.residual_stride] : from_float<OUT>(0.0f);
-    }
-    float v[32];
-#pragma unroll
-    for (u32 j = 0; j < 32; j++)
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(mine + j * 128 + (((lane >> 2) ^ (j & 7)) * 16) + (lane & 3) * 4));
+    for (u32 j = 0; j < N; j++) residual[j] = j < rows ? from[j * f.residual_stride] : from_float<OUT>(0.0f);
+}
+template <class OUT, int N> __device__ __forceinline__ void finish_column(const Finish &f, u64 r, u64 c, u32 rows, float (&v)[N], const OUT (&residual)[N])
+{
     if (f.bias) {
         const float b = value_as(f.bias_type, f.bias, c);
 #pragma unroll
-        for (u32 j = 0; j < 32; j++) v[j] += b;
+        for (u32 j = 0; j < N; j++) v[j] += b;
     }
     if (f.z) {
         unsigned short *z = static_cast<unsigned short *>(f.z) + r * f.n + c;
 #pragma unroll
-        for (u32 j = 0; j < 32; j++) {
+        for (u32 j = 0; j < N; j++) {
             unsigned short w;
             if (f.dtype == MV_BF16) {
                 const __nv_bfloat16 t = from_float<__nv_bfloat16>(v[j]);
@@ -181,16 +162,28 @@ template <class OUT, bool ALL> __device__ __forceinline__ void finish_column(con
                 const __half t = from_float<__half>(v[j]);
                 memcpy(&w, &t, 2);
             }
-            if (ALL || j < rows) z[j * f.n] = w;
+            if (j < rows) z[j * f.n] = w;
         }
     }
-    activate<32, sizeof(OUT) == 2>(f.act, v);
+    activate<N, sizeof(OUT) == 2>(f.act, v);
     OUT *y = static_cast<OUT *>(f.y) + r * f.y_stride + c;
 #pragma unroll
-    for (u32 j = 0; j < 32; j++) {
+    for (u32 j = 0; j < N; j++) {
         const float t = f.residual ? fmaf(f.scale, v[j], to_float(residual[j])) : f.scale * v[j];
-        if (ALL || j < rows) y[j * f.y_stride] = from_float<OUT>(t);
+        if (j < rows) y[j * f.y_stride] = from_float<OUT>(t);
     }
+}
+// The same of a warp's 32 x 32 in shared memory.
+template <class OUT, bool ALL> __device__ __forceinline__ void finish_column(const Finish &f, u32 mine, u32 lane, u64 r, u64 c, u32 some)
+{
+    const u32 rows = ALL ? 32 : some;
+    OUT residual[32];
+    if (f.residual) read_residual(f, r, c, rows, residual);
+    float v[32];
+#pragma unroll
+    for (u32 j = 0; j < 32; j++)
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(mine + j * 128 + (((lane >> 2) ^ (j & 7)) * 16) + (lane & 3) * 4));
+    finish_column(f, r, c, rows, v, residual);
 }
 template <class OUT> __device__ __noinline__ void finish_column(const Finish &from, u32 mine, u32 lane, u64 r, u64 c)
 {
@@ -688,15 +681,32 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
                 // lanes are columns of the result, TMEM's columns its rows
                 const u64 column = row0 + lane;
                 constexpr int kAtOnce = BN < 32 ? BN : 32;
-                for (u32 c = 0; c < BN && col0 + c < args.f.m; c += kAtOnce) {
-                    u32 v[kAtOnce];
-                    load_all(c, v);
-#pragma unroll
-                    for (int j = 0; j < kAtOnce; j++) {
-                        if (u.parts > 1)                           // [rows][128 columns], in the copies' place
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + j) * 128 + w * 32 + lane) * 4), "r"(v[j]) : "memory");
-                        else if (col0 + c + j < args.f.m && column < args.f.n) finish1(args.f, col0 + c + j, column, __uint_as_float(v[j]));
+                const auto all = [&](auto type) {
+                    using OUT = decltype(type);
+                    for (u32 c = 0; c < BN && col0 + c < args.f.m; c += kAtOnce) {
+                        const u32 rows = (u32)min((u64)kAtOnce, args.f.m - (col0 + c));
+                        const bool inside = column < args.f.n;
+                        OUT residual[kAtOnce];
+                        if (args.f.residual && inside) read_residual(args.f, col0 + c, column, rows, residual);
+                        float v[kAtOnce];
+                        load_all(c, *reinterpret_cast<u32(*)[kAtOnce]>(&v[0]));
+                        if (inside) finish_column(args.f, col0 + c, column, rows, v, residual);
                     }
+                };
+                if (u.parts > 1) {                                // [rows][128 columns], in the copies' place
+                    for (u32 c = 0; c < BN && col0 + c < args.f.m; c += kAtOnce) {
+                        u32 v[kAtOnce];
+                        load_all(c, v);
+#pragma unroll
+                        for (int j = 0; j < kAtOnce; j++)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + j) * 128 + w * 32 + lane) * 4), "r"(v[j]) : "memory");
+                    }
+                } else if (args.f.out == MV_BF16) {
+                    all(__nv_bfloat16());
+                } else if (args.f.out == MV_F16) {
+                    all(__half());
+                } else {
+                    all(0.0f);
                 }
             } else if (args.f.by_tma && !part) {
                 const auto all = [&](auto type) {

@@ -76,7 +76,8 @@ def check_linear(x, w, bias=None, act="none", residual=None, scale=1.0, out=None
 SHAPES = [  # tokens, cols, rows: one token, few, tiles' edges and one beyond, odd, whole tiles
     (1, 8, 8), (1, 1, 1), (1, 20480, 33), (2, 64, 128), (7, 100, 60), (16, 72, 129), (17, 640, 256), (33, 513, 257),
     (64, 128, 1000), (65, 1437, 101), (127, 63, 127), (128, 64, 64), (129, 65, 65), (255, 320, 384), (257, 257, 255),
-    (300, 1000, 777), (1000, 64, 520), (513, 2048, 1024), (2048, 192, 2560)]
+    (300, 1000, 777), (1000, 64, 520), (513, 2048, 1024), (2048, 192, 2560),
+    (1000, 64, 1), (300, 7, 3), (5, 3, 300), (64, 512, 20480), (200, 136, 30000)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -164,6 +165,32 @@ def test_linear_backward_parts_and_extremes():
             close("dx", got, want, 2.0 ** -17 * np.abs(want))
         else:
             assert (got[:, :24] == (np.inf if v > 0 else -np.inf)).all()
+
+
+def test_beyond_two_to_the_31():
+    """Offsets that 32 bits do not hold: results of more than 2^32 bytes and 2^31 elements."""
+    t, n = 70001, 32768
+    x, w = randn((t, 64), 1, BF16), randn((n, 64), 2, BF16)
+    y, z = block.linear(x, w, act="relu", keep=True)
+    g = block.activation_backward(y, z, act="relu", scale=2.0)
+    rows = [0, 1, 65535, 65536, 70000]
+    want = host(x[rows]) @ host(w).T
+    m = np.abs(host(x[rows])) @ np.abs(host(w)).T
+    close("z", z[rows], want, product_slack(m, 64, BF16))
+    assert torch.equal(y[rows], z[rows].clamp_min(0)) and torch.equal(g[rows], 2 * y[rows])
+    del z, g
+    dx = block.linear_backward(y, x, w, dw=False)[0]
+    a, b = host(y[rows]), host(w)
+    close("dx", dx[rows], a @ b, product_slack(np.abs(a) @ np.abs(b), n, BF16))
+    h = 4096
+    s = y.view(-1)[:t * n // h * h].view(-1, h)              # 560008 rows
+    p = randn((h,), 3, F32)
+    nn, r = block.norm(s, p, residual=s)
+    rows = [0, 524288, len(s) - 1]
+    close("n", nn[rows], R.norm(host(s[rows]), host(p), residual=host(s[rows]))[0][0], 2.0 ** -16)
+    dy = block.norm_backward(nn, s, p, dr=r, residual=s).dy
+    want = R.norm_backward(host(nn[rows]), host(s[rows]), host(p), dr=host(r[rows]), residual=host(s[rows]))["dy"]
+    close("dy", dy[rows], want[0], 256 * U * want[1])
 
 
 def test_linear_zero_sizes():
