@@ -24,10 +24,11 @@ from collections import namedtuple
 import torch
 
 from . import mv
-from .moe import _DTYPES, _On, _choice, _descriptor, _elsewhere, _raw_stream, _stride, _tensor, _u64, _vp
+from .moe import _DTYPES, _On, _choice, _descriptor, _raw_stream, _tensor, _u64, _vp
 
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _HALVES = (torch.float16, torch.bfloat16)
+_current_device = torch._C._cuda_getDevice
 _MAX_SCALE = torch.finfo(torch.float32).max        # the descriptors hold it in 32 bits
 
 LinearDesc, _linear_desc = _descriptor(
@@ -88,6 +89,11 @@ def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+def _apart(t, rows: int, cols: int) -> int:
+    """How far the rows of ``t`` (or None) lie apart; of one row, its columns."""
+    return cols if rows < 2 or t is None else t.stride(0)
+
+
 def _scale(name: str, v: float):
     if not abs(v) <= _MAX_SCALE:
         raise ValueError(f"{name} is {v}")
@@ -122,7 +128,7 @@ def linear(x, w, bias=None, *, act: str = "none", residual=None, scale: float = 
         _tensor("residual", residual, (out,), (tokens, rows), dev, rows_apart=True)
     a = _choice("act", act, ACTS)
     _scale("scale", scale)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _On(dev, stream, (x, w, bias, residual)):
             return _linear(x, w, bias, residual, tokens, cols, rows, dt, out, a, scale, keep, dev)
     return _linear(x, w, bias, residual, tokens, cols, rows, dt, out, a, scale, keep, dev)
@@ -133,7 +139,7 @@ def _linear(x, w, bias, residual, tokens, cols, rows, dt, out, act, scale, keep,
     z = torch.empty((tokens, rows), dtype=dt, device=dev) if keep else None
     if tokens and rows:
         _run("mv_linear", _linear_desc(
-            tokens, cols, rows, _stride(x), _stride(w), 0 if residual is None else _stride(residual),
+            tokens, cols, rows, _apart(x, tokens, cols), _apart(w, rows, cols), _apart(residual, tokens, rows),
             _DTYPES[dt], _DTYPES[out], _DTYPES[dt if bias is None else bias.dtype], act, scale,
             x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(z)), dev)
     return (y, z) if keep else y
@@ -157,7 +163,7 @@ def linear_backward(dz, x, w, *, dx: bool = True, dw: bool = True, bias: bool = 
     if not cols:
         raise ValueError("a product of no columns")
     _tensor("dz", dz, (dt, torch.float32) if dt is torch.bfloat16 else (dt,), (tokens, rows), dev, rows_apart=True)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _On(dev, stream, (dz, x, w)):
             return _linear_backward(dz, x, w, tokens, cols, rows, dt, dx, dw, bias, dev)
     return _linear_backward(dz, x, w, tokens, cols, rows, dt, dx, dw, bias, dev)
@@ -172,7 +178,7 @@ def _linear_backward(dz, x, w, tokens, cols, rows, dt, dx, dw, bias, dev):
             gx.zero_()
         return gx, gw, gb
     _run("mv_linear_backward", _linear_grad_desc(
-        tokens, cols, rows, _stride(x), _stride(w), _stride(dz), _DTYPES[dt], _DTYPES[dz.dtype],
+        tokens, cols, rows, _apart(x, tokens, cols), _apart(w, rows, cols), _apart(dz, tokens, rows), _DTYPES[dt], _DTYPES[dz.dtype],
         dz.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(gx), _ptr(gw), _ptr(gb)), dev)
     return gx, gw, gb
 
@@ -189,7 +195,7 @@ def activation_backward(dy, z, *, act: str, scale: float = 1.0, stream=None):
     a = _choice("act", act, ACTS)
     _scale("scale", scale)
     dev = z.device
-    if _elsewhere(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _On(dev, stream, (dy, z)):
             return _activation_backward(dy, z, tokens, cols, a, scale, dev)
     return _activation_backward(dy, z, tokens, cols, a, scale, dev)
@@ -198,7 +204,7 @@ def activation_backward(dy, z, *, act: str, scale: float = 1.0, stream=None):
 def _activation_backward(dy, z, tokens, cols, act, scale, dev):
     dz = torch.empty((tokens, cols), dtype=z.dtype, device=dev)
     rc = (_lib or _library()).mv_activation_backward(_act_grad_desc(
-        tokens, cols, _stride(dy), _stride(z), _DTYPES[z.dtype], act, scale, dy.data_ptr(), z.data_ptr(),
+        tokens, cols, _apart(dy, tokens, cols), _apart(z, tokens, cols), _DTYPES[z.dtype], act, scale, dy.data_ptr(), z.data_ptr(),
         dz.data_ptr()), _raw_stream(dev.index))
     if rc != mv.MV_OK:
         raise mv.MVError(rc, "mv_activation_backward")
@@ -224,7 +230,7 @@ def norm(y, weight, bias=None, *, residual=None, alpha: float = 1.0, post=None, 
     gate there is no new stream, and r is ``y`` itself.
     """
     tokens, hidden, gates, k, params, dev = _norm_checks(y, weight, bias, residual, alpha, post, post_bias, gate, kind, eps)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _On(dev, stream, (y, weight, bias, residual, post, post_bias, gate)):
             return _norm(y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates, k, params, eps, dev)
     return _norm(y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates, k, params, eps, dev)
@@ -268,7 +274,7 @@ def _norm(y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidde
     same = residual is None and post is None and gate is None
     r = y if same else torch.empty((tokens, hidden), dtype=y.dtype, device=dev)
     rc = (_lib or _library()).mv_norm(_norm_desc(
-        tokens, hidden, gates, _stride(y), 0 if residual is None else _stride(residual), _DTYPES[y.dtype],
+        tokens, hidden, gates, _apart(y, tokens, hidden), _apart(residual, tokens, hidden), _DTYPES[y.dtype],
         _DTYPES[params], kind, alpha, eps, y.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(post),
         _ptr(post_bias), _ptr(gate)), n.data_ptr(), 0 if same else r.data_ptr(), _raw_stream(dev.index))
     if rc != mv.MV_OK:
@@ -290,7 +296,7 @@ def norm_backward(dn, y, weight, bias=None, *, dr=None, residual=None, alpha: fl
     _tensor("dn", dn, (y.dtype,), (tokens, hidden), dev, rows_apart=True)
     if dr is not None:
         _tensor("dr", dr, (y.dtype,), (tokens, hidden), dev, rows_apart=True)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _On(dev, stream, (dn, dr, y, weight, bias, residual, post, post_bias, gate)):
             return _norm_backward(dn, dr, y, weight, bias, residual, alpha, post, post_bias, gate, tokens, hidden, gates,
                                   k, params, eps, dev)
@@ -307,10 +313,10 @@ def _norm_backward(dn, dr, y, weight, bias, residual, alpha, post, post_bias, ga
                   like(bias, params, hidden), like(post, params, hidden), like(post_bias, params, hidden),
                   None if gate is None else like(gate, params, *gate.shape))
     d = _norm_desc(
-        tokens, hidden, gates, _stride(y), 0 if residual is None else _stride(residual), _DTYPES[y.dtype],
+        tokens, hidden, gates, _apart(y, tokens, hidden), _apart(residual, tokens, hidden), _DTYPES[y.dtype],
         _DTYPES[params], kind, alpha, eps, y.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(post),
         _ptr(post_bias), _ptr(gate))
-    e = _norm_grad_desc(_stride(dn), 0 if dr is None else _stride(dr), dn.data_ptr(), _ptr(dr), *map(_ptr, g))
+    e = _norm_grad_desc(_apart(dn, tokens, hidden), _apart(dr, tokens, hidden), dn.data_ptr(), _ptr(dr), *map(_ptr, g))
     lib, need = _lib or _library(), _u64()
     rc = lib.mv_norm_backward_workspace_bytes(d, e, C.byref(need))
     if rc == mv.MV_OK:
