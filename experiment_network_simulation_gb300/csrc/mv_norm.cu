@@ -169,7 +169,7 @@ NormShape shape_of(u32 hidden, u32 size, bool wide)
     const u32 n = wide ? 16 / size : 1, few = wide ? n : 4;
     const u32 e = hidden <= 32 * few ? few : !wide ? (hidden <= 8192 ? 8 : 16) : hidden <= 16 * kMostThreads ? 16 : 32;
     const u32 threads = (hidden + e - 1) / e;
-    return {n, e / n, (threads + 31) / 32 * 32, hidden % (32 * e) == 0};
+    return {n, e / n, (threads + 31) / 32 * 32, hidden % (32 * e) == 0, 1};
 }
 
 bool dense(const void *p, u64 stride, u32 n, u32 size) { return !p || (aligned(p, 16) && stride % n == 0 && (n * size == 16)); }
@@ -254,14 +254,18 @@ GradPlan grad_plan(const mv_norm_desc *d, bool wide)
     GradPlan p = {};
     const u32 size = (u32)dtype_size(d->dtype);
     const u32 hidden = (u32)d->hidden, n = wide ? 16 / size : 1;
-    // eight elements a thread and two rows at a time, copied ahead; sixteen and one where a row is too long for that
-    auto shape = [&](u32 e) { return NormShape{n, e / n, ((hidden + e - 1) / e + 31) / 32 * 32, false}; };
-    auto copies = [&](const NormShape &s) { return n * size >= 4 ? 5 * 2 * 8 * s.threads * size : 0; };
-    p.shape = shape(8);
-    p.smem = copies(p.shape);
-    if (p.shape.threads > (u32)kGradThreads<false> || p.smem > 216 * 1024) {
-        p.shape = shape(16);
-        p.smem = 0;
+    // eight elements a thread and two rows at a time (or one, where two do not fit), copied ahead;
+    // sixteen and one where a row is too long for that
+    auto shape = [&](u32 e, u32 at_once) { return NormShape{n, e / n, ((hidden + e - 1) / e + 31) / 32 * 32, false, at_once}; };
+    p.shape = shape(8, 2);
+    if (p.shape.threads <= 1024) {
+        p.smem = n * size >= 4 ? 5 * 2 * 8 * p.shape.threads * size : 0;
+        if (p.smem > 216 * 1024) {
+            p.shape.at_once = 1;
+            p.smem /= 2;
+        }
+    } else {
+        p.shape = shape(16, 1);
     }
     const u32 threads = p.shape.threads;
     const u32 sms = std::max(1u, sm_count());

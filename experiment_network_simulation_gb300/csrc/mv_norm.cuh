@@ -21,6 +21,7 @@ struct NormArgs {
 struct NormShape {
     u32 n, pieces, threads;
     bool whole;                                     // the threads' pieces are the row, and no more
+    u32 at_once;                                    // rows that go together (backward)
 };
 template <class T> int run_norm_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream);
 
@@ -172,7 +173,7 @@ template <int N, bool WHOLE, int E> __device__ __forceinline__ float2 normalise(
 
 constexpr u32 kMostThreads = MV_NORM_MAX_HIDDEN / 32;   // a block: 32 elements a thread where rows are longest
 
-// The backward pass: threads a block where each has 96 registers, and where it has 72.
+// The backward pass: threads a block where each has 96 registers, and where it has 72 (beyond: 64).
 template <bool FEW> constexpr int kGradThreads = FEW ? 640 : 896;
 
 }  // namespace mvblock

@@ -33,7 +33,7 @@ template <class T, class P, int N, int E, int R, bool POST, bool BIAS, int MOST>
 __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
 {
     // pieces of 2 bytes cannot be copied, and the longest rows do not fit: they are read where they are used
-    constexpr bool staged = N * sizeof(T) >= 4 && R == 2;
+    constexpr bool staged = N * sizeof(T) >= 4 && E == 8;
     constexpr u32 kBytes = N * sizeof(T), kPieces = E / N;        // in five places: y twice, residual, dn, dr
     extern __shared__ __align__(16) unsigned char stage[];
     __shared__ float2 part[2][R][32];
@@ -396,28 +396,33 @@ int run_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, cudaSt
     return launch(kernel, dim3((u32)blocks), s.threads, smem, stream, a);
 }
 // Fewer threads leave more registers to each, which the kernels with the most
-// sums need.  Rarer rows (longest, or on no 16-byte boundary) have kernels with
-// more sums than they may need.
+// sums need.  Rarer rows (longest, of 32 bits and long, or on no 16-byte boundary)
+// have kernels with more sums than they may need.
+template <class T, class P, int N, int R, int MOST>
+int run_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream)
+{
+    constexpr int kMany = kGradThreads<false>, kPlain = N > 1 && MOST < kMany ? kMany : MOST;       // without post: as many threads as may be
+    if constexpr (N > 1 && R == 2 && MOST <= kMany)
+        if (!bias) return post ? run_grad<T, P, N, 8, R, true, false, MOST>(a, s, blocks, smem, stream)
+                               : run_grad<T, P, N, 8, R, false, false, kPlain>(a, s, blocks, smem, stream);
+    return post ? run_grad<T, P, N, 8, R, true, true, MOST>(a, s, blocks, smem, stream)
+                : run_grad<T, P, N, 8, R, false, true, kPlain>(a, s, blocks, smem, stream);
+}
+template <class T, class P, int N> int run_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream)
+{
+    constexpr int kFew = kGradThreads<true>, kMany = kGradThreads<false>;
+    if (s.pieces * s.n == 16) return run_grad<T, P, N, 16, 1, true, true, 1024>(a, s, blocks, smem, stream);
+    if constexpr (sizeof(T) == 4)           // two rows at a time do not fit where they are long
+        if (s.at_once == 1)
+            return s.threads <= kMany ? run_grad<T, P, N, 1, kMany>(a, s, blocks, smem, post, bias, stream)
+                                      : run_grad<T, P, N, 1, 1024>(a, s, blocks, smem, post, bias, stream);
+    if (s.threads <= kFew) return run_grad<T, P, N, 2, kFew>(a, s, blocks, smem, post, bias, stream);
+    return s.threads <= kMany ? run_grad<T, P, N, 2, kMany>(a, s, blocks, smem, post, bias, stream)
+                              : run_grad<T, P, N, 2, 1024>(a, s, blocks, smem, post, bias, stream);
+}
 template <class T, class P> int run_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream)
 {
-    constexpr int N = 16 / sizeof(T), kFew = kGradThreads<true>, kMany = kGradThreads<false>;
-    const bool few = s.threads <= kFew;
-    if (s.pieces * s.n == 8 && s.n > 1) {
-        if (!post) return bias ? run_grad<T, P, N, 8, 2, false, true, kMany>(a, s, blocks, smem, stream)
-                               : run_grad<T, P, N, 8, 2, false, false, kMany>(a, s, blocks, smem, stream);
-        if (few) return bias ? run_grad<T, P, N, 8, 2, true, true, kFew>(a, s, blocks, smem, stream)
-                             : run_grad<T, P, N, 8, 2, true, false, kFew>(a, s, blocks, smem, stream);
-        return bias ? run_grad<T, P, N, 8, 2, true, true, kMany>(a, s, blocks, smem, stream)
-                    : run_grad<T, P, N, 8, 2, true, false, kMany>(a, s, blocks, smem, stream);
-    }
-    if (s.pieces * s.n == 8 && few)
-        return post ? run_grad<T, P, 1, 8, 2, true, true, kFew>(a, s, blocks, smem, stream)
-                    : run_grad<T, P, 1, 8, 2, false, true, kFew>(a, s, blocks, smem, stream);
-    if (s.pieces * s.n == 8)
-        return post ? run_grad<T, P, 1, 8, 2, true, true, kMany>(a, s, blocks, smem, stream)
-                    : run_grad<T, P, 1, 8, 2, false, true, kMany>(a, s, blocks, smem, stream);
-    return s.n > 1 ? run_grad<T, P, N, 16, 1, true, true, 1024>(a, s, blocks, smem, stream)
-                   : run_grad<T, P, 1, 16, 1, true, true, 1024>(a, s, blocks, smem, stream);
+    return s.n > 1 ? run_grad<T, P, 16 / (int)sizeof(T)>(a, s, blocks, smem, post, bias, stream) : run_grad<T, P, 1>(a, s, blocks, smem, post, bias, stream);
 }
 
 template <class T> int run_norm_grad(const NormArgs &a, const NormShape &s, u64 blocks, u32 smem, bool post, bool bias, cudaStream_t stream)
