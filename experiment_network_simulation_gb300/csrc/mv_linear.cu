@@ -135,8 +135,8 @@ __device__ __forceinline__ float value_as(u32 type, const void *p, u64 at)
 }
 // Column c of N rows from r on, a lane's of a warp whose lanes have neighbours, so
 // that their accesses are whole; rows may lie anywhere.  ALL: of as many rows.
-// Residuals are read first and all at once (each in its turn, 3604 x 80 to 2448 with
-// residual and pre-activations took 70 us, so 42).
+// Residuals are read first and all at once (each in its turn, 3604 x 80 to 2449 with
+// gelu, residual and pre-activations took 97 us, so 53).
 template <class OUT, int N> __device__ __forceinline__ void read_residual(const Finish &f, u64 r, u64 c, u32 rows, OUT (&residual)[N])
 {
     const OUT *from = static_cast<const OUT *>(f.residual) + r * f.residual_stride + c;
@@ -389,6 +389,25 @@ __device__ __forceinline__ void finish_tile(const Finish &f, u32 mine, u32 lane,
         if (f.bias_type == MV_F32) add_bias<float>(f, c, v);
         else if (f.bias_type == MV_BF16) add_bias<__nv_bfloat16>(f, c, v);
         else add_bias<__half>(f, c, v);
+    }
+    if (f.z && f.residual) {            // z needs the place that the residual is in
+        constexpr int kEach = 16 / sizeof(OUT);
+        uint4 residual[8];
+#pragma unroll
+        for (u32 j = 0; j < 8; j++)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(residual[j].x), "=r"(residual[j].y), "=r"(residual[j].z), "=r"(residual[j].w)
+                         : "r"(mine + lane * 128 + ((j ^ (lane & 7)) * 16)) : "memory");
+        store_tile<OUT, false>(mine, lane, z_map, (int)c, (int)row0, v, 1.0f);
+        activate<N, sizeof(OUT) == 2>(f.act, v);
+#pragma unroll
+        for (u32 j = 0; j < 8; j++) {
+            OUT t[kEach];
+            memcpy(t, &residual[j], 16);
+#pragma unroll
+            for (u32 i = 0; i < kEach; i++) v[j * kEach + i] = fmaf(f.scale, v[j * kEach + i], to_float(t[i]));
+        }
+        store_tile<OUT, false>(mine, lane, y_map, (int)c, (int)row0, v, 1.0f);
+        return;
     }
     if (f.z) store_tile<OUT, false>(mine, lane, z_map, (int)c, (int)row0, v, 1.0f);
     activate<N, sizeof(OUT) == 2>(f.act, v);
@@ -1100,7 +1119,7 @@ int run_kind(const Side &a, const void *a2, const Side &b, u32 dtype, const Plan
     maps[3] = maps[4] = maps[5] = maps[0];
     Finish &f = args.f;
     const u64 size = dtype_size(f.out);
-    f.by_tma = !SWAP && f.n * size % 16 == 0 && aligned(f.y, 16) && aligned(f.z, 16) && !(f.z && (f.residual || f.out == MV_F32)) &&
+    f.by_tma = !SWAP && f.n * size % 16 == 0 && aligned(f.y, 16) && aligned(f.z, 16) && !(f.z && f.out == MV_F32) &&
                (!f.residual || (aligned(f.residual, 16) && f.residual_stride * size % 16 == 0));
     if (f.by_tma && (!map_result(&maps[3], f.y, f.m, f.n, f.n, f.out) || (f.z && !map_result(&maps[4], f.z, f.m, f.n, f.n, f.out)) ||
                      (f.residual && !map_result(&maps[5], const_cast<void *>(f.residual), f.m, f.n, f.residual_stride, f.out))))
