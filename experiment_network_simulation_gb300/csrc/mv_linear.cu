@@ -639,7 +639,7 @@ k_product(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUt
             const bool fetched = !SWAP && !part && args.f.by_tma && args.f.residual && row0 < args.f.m && col0 + share * kShare < args.f.n;
             if (fetched) fetch_residual(mine, lane, residual_bar, &residual_map, (int)(col0 + share * kShare), (int)row0);
             // The tensor core's additions cut what is beyond 32 bits off, so an error of a long
-            // chain grows with its length (2e-6 after 2048 products): where the result has 32 bits
+            // chain grows with its length (2.4e-6 of the norm after 2048 products): where the result has 32 bits
             // or the chain is very long, it is summed in runs of u.chain steps, and a run's sum is
             // added, rounded to nearest, to the sum of those before it (in TMEM too).
             const u32 earlier = tmem + 2 * S::kColumns + (w << 21);
