@@ -444,6 +444,7 @@ template <int CTAS, int BN> struct Tile {
 
 struct Units {                      // what the blocks (or pairs) do, in order
     u32 tiles_m, tiles_n;
+    u32 columns;                    // columns of tiles that come first
     u32 whole;                      // tiles done in one piece; of each one after them
     u32 parts;                      // this many pieces along k
     u32 total;                      // units in all
@@ -460,12 +461,20 @@ struct Args {
     float *partial;                 // sums of tiles in pieces
 };
 
-// Tiles go in columns of eight along m, so that those under way share both operands in L2.
+// Tiles go in columns of eight along m, so that those under way share both operands in L2:
+// first those of the first u.columns columns, then the others.
 __device__ __forceinline__ void tile_at(const Units &u, u32 i, u32 &m, u32 &n)
 {
-    const u32 band = 8 * u.tiles_n, b = i / band, rows = min(8u, u.tiles_m - 8 * b), j = i - b * band;
+    u32 start = 0, across = u.columns;
+    if (i >= across * u.tiles_m) {
+        i -= across * u.tiles_m;
+        start = across;
+        across = u.tiles_n - across;
+    }
+    const u32 band = 8 * across, b = i / band, rows = min(8u, u.tiles_m - 8 * b), j = i - b * band;
     n = j / rows;
     m = 8 * b + j - n * rows;
+    n += start;
 }
 
 template <bool MN> __device__ __forceinline__ u64 operand(u32 at)
@@ -1038,7 +1047,13 @@ struct Plan {
 // (128 x 128), 70.3 (128 x 64); 1 x 20480 to 5120: 39 (swapped, 16), 42
 // (swapped, 64), 50 (128 x 128), 64 (pairs); 64 x 5120 to 5120: 20 (swapped, 64),
 // 25 (swapped, 16), 23 (128 x 128).
-Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 chain, u32 sms, double &best)
+//
+// alike: every row's sums are to be made of the same pieces, so that equal rows have
+// equal results: tiles go in pieces by whole columns.  What that costs: by this estimate
+// 0.2% on average over sizes spread over their logarithm, and more than 6% for one product in a
+// hundred, where few columns have many tiles each (20000 x 7168 to 256 took 78 us, so 104;
+// 3000 x 4096 to 4096 in 32 bits 131, so 134; 2048 x 5120 to 5120 78 either way).
+Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 chain, bool alike, u32 sms, double &best)
 {
     const KindOf &k = kKind[kind];
     const bool pair = kind <= kPair128;
@@ -1052,15 +1067,16 @@ Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 chain, u32 sms, double &b
         // TMEM has no room for earlier sums beside the largest tiles
         if (kind == kPair256 && (steps + (whole ? 1 : parts) - 1) / (whole ? 1 : parts) > chain) return;
         const double step = kind == kPair256 ? 530 : kind == kPair128 ? 400 : std::max(bytes / 64 * (two ? 2 : 1), two || kind == kOne128 ? 400.0 : 250.0);
-        const double rounds = (double)((left * parts + slots - 1) / slots);
-        const double work = ((double)whole / (double)slots) * ((double)steps * step + 400) +
-                            rounds * ((double)((steps + parts - 1) / parts) * step + 2000);
+        // rounds of whole tiles, the last of which pieces may fill up, and of pieces
+        const u64 full = (whole + slots - 1) / slots, rounds = (whole + left * parts + slots - 1) / slots - full;
+        const double work = (double)full * ((double)steps * step + 400) +
+                            (double)rounds * ((double)((steps + parts - 1) / parts) * step + 2000);
         const double cost = std::max(work, memory) + 0.35 * std::min(work, memory) + join + 2000;
         if (cost >= best) return;
         best = cost;
         p.kind = kind;
         p.two = two;
-        p.u = {(u32)tm, (u32)tn, (u32)(k.swap || parts == 1 ? tiles : whole), (u32)parts,
+        p.u = {(u32)tm, (u32)tn, (u32)(k.swap || parts == 1 || !alike ? tn : whole / tm), (u32)(k.swap || parts == 1 ? tiles : whole), (u32)parts,
                (u32)(k.swap || parts == 1 ? tiles : whole + left * parts), (u32)steps, 0, chain, 0};
         p.blocks = blocks;
         p.partial = k.swap || parts == 1 ? 0 : left * parts * (u64)k.rows * k.cols * 4;
@@ -1078,28 +1094,37 @@ Plan plan_kind(Kind kind, u64 m, u64 n, u64 steps, u32 chain, u32 sms, double &b
     }
     // whole tiles in rounds of all slots, and what is left in pieces: as many as fill one to four more rounds, or fewer
     const bool two = k.two && tiles > sms;
-    const u64 slots = std::max<u64>(1, (u64)sms * (two ? 2 : 1) / each), whole = tiles / slots * slots, left = tiles - whole;
-    auto in_parts = [&](u64 parts) {
+    const u64 slots = std::max<u64>(1, (u64)sms * (two ? 2 : 1) / each), rest = tiles % slots;
+    auto in_parts = [&](u64 left, u64 parts) {
+        const u64 whole = tiles - left;
         const double join = parts > 1 ? 6000 + (double)(parts * left) * k.rows * k.cols * 4 / (sms * 24.0) : 0;
         consider(whole, left, parts, std::min<u64>(whole + left * parts, slots) * each, slots, two, join);
     };
-    in_parts(1);
-    if (!left) return p;
-    for (u64 round = 1; round <= 4; round++) in_parts(std::max<u64>(1, std::min<u64>(steps, round * slots / left)));
-    for (u64 parts : {2, 4, 8, 12})
-        if (parts < slots / left && parts <= steps) in_parts(parts);
+    in_parts(rest, 1);
+    if (!rest) return p;
+    // what goes in pieces: the rest, or columns, as few as hold that many tiles or up to two more
+    const u64 unit = alike ? tm : rest, fewest = (rest + unit - 1) / unit, most = alike ? std::min(tn, fewest + 2) : 1;
+    for (u64 units = fewest; units <= most; units++) {
+        const u64 left = units * unit, begun = (tiles - left) % slots;      // of a round, by whole tiles
+        for (u64 round = 1; round <= 4; round++) {
+            const u64 parts = std::min<u64>(steps, (round * slots - begun) / left);
+            if (parts > 1) in_parts(left, parts);
+        }
+        for (u64 parts : {2, 4, 8, 12})
+            if (parts < slots / left && parts <= steps) in_parts(left, parts);
+    }
     return p;
 }
 
 // chain: the longest run of steps that may be summed in one go.
-Plan plan(u64 m, u64 n, u64 steps, u32 chain, bool swaps, u32 sms)
+Plan plan(u64 m, u64 n, u64 steps, u32 chain, bool swaps, bool alike, u32 sms)
 {
     Plan best = {};
     double least = INFINITY;
     for (int kind = 0; kind < kKinds; kind++) {
         if (kKind[kind].swap && !swaps) continue;
         double cost;
-        const Plan p = plan_kind((Kind)kind, m, n, steps, chain, sms, cost);
+        const Plan p = plan_kind((Kind)kind, m, n, steps, chain, alike, sms, cost);
         if (cost < least) { least = cost; best = p; }
     }
     return best;
@@ -1243,7 +1268,7 @@ LinearLayout layout(const mv_linear_desc *d)
     LinearLayout l = {};
     u64 at = 0;
     auto take = [&](u64 bytes) { const u64 here = at; at += up(bytes, 256); return here; };
-    l.plan = plan(d->tokens, d->rows, steps_of(d->cols), d->out_dtype == MV_F32 ? kChain32 : kChain16, d->tokens <= 256, planned_sms());
+    l.plan = plan(d->tokens, d->rows, steps_of(d->cols), d->out_dtype == MV_F32 ? kChain32 : kChain16, d->tokens <= 256, true, planned_sms());
     l.x = take(copies(d->x, d->x_stride) ? 0 : d->tokens * up(d->cols, 8) * 2);
     l.w = take(copies(d->w, d->w_stride) ? 0 : d->rows * up(d->cols, 8) * 2);
     l.partial = take(l.plan.partial);
@@ -1269,8 +1294,8 @@ GradLayout layout(const mv_linear_grad_desc *d)
     u64 at = 0;
     auto take = [&](u64 bytes) { const u64 here = at; at += up(bytes, 256); return here; };
     const u64 parts = d->dz_dtype == MV_F32 ? 2 : 1, sms = planned_sms();
-    if (d->dx) l.dx = plan(d->tokens, d->cols, parts * steps_of(d->rows), kChain16, false, (u32)sms);
-    if (d->dw) l.dw = plan(d->rows, d->cols, parts * steps_of(d->tokens), kChain16, false, (u32)sms);
+    if (d->dx) l.dx = plan(d->tokens, d->cols, parts * steps_of(d->rows), kChain16, false, false, (u32)sms);
+    if (d->dw) l.dw = plan(d->rows, d->cols, parts * steps_of(d->tokens), kChain16, false, false, (u32)sms);
     l.x = take(!d->dw || copies(d->x, d->x_stride) ? 0 : d->tokens * up(d->cols, 8) * 2);
     l.w = take(!d->dx || copies(d->w, d->w_stride) ? 0 : d->rows * up(d->cols, 8) * 2);
     l.dz = take(parts == 1 && copies(d->dz, d->dz_stride) ? 0 : parts * d->tokens * up(d->rows, 8) * 2);

@@ -518,8 +518,8 @@ int mv_experts(const mv_experts_desc *desc, void *workspace, uint64_t ws_bytes, 
  * where it is not NULL, gets the pre-activations in `dtype`; act sees them
  * unrounded.  Rows of x and w that are not 16-byte aligned (an odd size, a
  * stride that is no multiple of 8) are first copied into the workspace: right, but slower.
- * cols is at least 1.  What a sum is made of depends on the sizes alone, but
- * not on which row it is: equal rows of x give equal rows.
+ * cols is at least 1.  What a sum is made of depends on the sizes and out_dtype
+ * alone, not on which row it is: equal rows of x (and of the residual) give equal rows.
  */
 typedef struct mv_linear_desc {
     uint64_t tokens, cols, rows, x_stride, w_stride, residual_stride;
