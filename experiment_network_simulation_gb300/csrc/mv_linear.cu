@@ -1460,5 +1460,7 @@ extern "C" int mv_linear_backward(const mv_linear_grad_desc *d, void *workspace,
 extern "C" int mv_block_status(uint32_t *gave_up)
 {
     if (!gave_up) return MV_EINVAL;
+    // the copy alone waits for the default stream, and not for those that do not wait for it either
+    if (cudaDeviceSynchronize() != cudaSuccess) return MV_ECUDA;
     return cudaMemcpyFromSymbol(gave_up, g_gave_up, sizeof *gave_up) == cudaSuccess ? MV_OK : MV_ECUDA;
 }
