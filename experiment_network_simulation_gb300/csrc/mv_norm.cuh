@@ -166,7 +166,8 @@ template <int N, bool WHOLE, int E> __device__ __forceinline__ float2 normalise(
         add_row(v, v, -mean);
         hide<N, WHOLE>(a.hidden, threads, v);
     }
-    const float inverse = rsqrtf(fmaf(sum(dot_row(v, v)), a.inv_hidden, a.eps));
+    // divided before they are added up: the sum of a long row's squares may be beyond 32 bits where their mean is not
+    const float inverse = rsqrtf(sum(dot_row(v, v) * a.inv_hidden) + a.eps);
     mul_row(v, v, inverse);
     return make_float2(mean, inverse);
 }

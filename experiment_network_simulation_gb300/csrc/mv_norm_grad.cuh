@@ -191,10 +191,10 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_grad(const NormArgs a)
             for (int r = 0; r < R; r++) { mean[r] = s[r] * a.inv_hidden; add_row(v[r], v[r], -mean[r]); }
         }
 #pragma unroll
-        for (int r = 0; r < R; r++) { hide(v[r]); s[r] = dot_row(v[r], v[r]); }
+        for (int r = 0; r < R; r++) { hide(v[r]); s[r] = dot_row(v[r], v[r]) * a.inv_hidden; }
         sums(s);
 #pragma unroll
-        for (int r = 0; r < R; r++) { inverse[r] = rsqrtf(fmaf(s[r], a.inv_hidden, a.eps)); mul_row(v[r], v[r], inverse[r]); }
+        for (int r = 0; r < R; r++) { inverse[r] = rsqrtf(s[r] + a.eps); mul_row(v[r], v[r], inverse[r]); }
     };
     // means of g and of g x^, of every row
     auto slopes = [&](const float (&g)[R][E], const float (&x)[R][E], float (&mean)[R], float (&slope)[R]) {

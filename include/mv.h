@@ -584,7 +584,7 @@ int mv_activation_backward(const mv_act_grad_desc *desc, void *stream);
  * its rows is shared by as many tokens in a row (1: by all).  post_bias needs
  * post.  n comes from r before its rounding; r may be NULL.  hidden is 1 to
  * MV_NORM_MAX_HIDDEN.  Squares are held in 32 bits: rows of magnitudes beyond 1e18
- * are out of range.
+ * are out of range and, with an eps under 1e-32, those of magnitudes below 1e-16.
  */
 typedef struct mv_norm_desc {
     uint64_t tokens, hidden, gates, y_stride, residual_stride;
