@@ -148,7 +148,8 @@ def _linear(x, w, bias, residual, tokens, cols, rows, dt, out, act, scale, keep,
 def linear_backward(dz, x, w, *, dx: bool = True, dw: bool = True, bias: bool = False, stream=None):
     """Gradients of z = x w^T + bias, given z's: (dx, dw, dbias), of x's type.
 
-    ``dz`` [tokens, rows] is of x's type, or float32 where that is bfloat16; its
+    ``dz`` [tokens, rows] is of x's type, or float32 where that is bfloat16 (each
+    value then counts to 2^-17 of itself, and times an infinity is a NaN); its
     rows may lie apart.  ``dx = dz w`` [tokens, cols], ``dw = dz^T x`` [rows,
     cols] and, with ``bias``, ``dbias`` [rows], the sum over the tokens; None
     for what is not asked for.  A gradient at the output of :func:`linear` goes

@@ -865,7 +865,8 @@ template <int CTAS, int BN, u32 GROUPS> __global__ void __launch_bounds__(256) k
 // ---- operands as the copies want them ---------------------------------------
 // Rows that lie on no 16-byte boundary are copied to where they do, and 32-bit
 // values are split into two bfloat16, the nearest and the nearest to what that
-// leaves: within 2^-17 of the value together, at any magnitude.
+// leaves: together within 2^-17 of the value or, under 2^-117, within half of
+// bfloat16's smallest step, 2^-134.
 struct PackArgs {
     const unsigned short *from[2];
     unsigned short *to[2];

@@ -539,8 +539,10 @@ int mv_linear(const mv_linear_desc *desc, void *workspace, uint64_t ws_bytes, vo
  * Gradients of z = x w^T + bias, given z's:
  *   dx = dz w,   dw = dz^T x,   dbias[n] = sum over t of dz[t, n],
  * each of type `dtype`, or not computed where its pointer is NULL.  dz is of
- * type `dz_dtype`: dtype, or MV_F32 where dtype is MV_BF16 (it then counts to
- * 2^-17 of each value in the products: two bfloat16).  No tokens: dw and dbias are zeros.
+ * type `dz_dtype`: dtype, or MV_F32 where dtype is MV_BF16.  In the products it is
+ * then two bfloat16 that are added: each value counts to 2^-17 of itself, or to 2^-134
+ * where that is more, and times an infinite x or w it is a NaN, not an infinity.
+ * No tokens: dw and dbias are zeros.
  * x is read for dw, w for dx.
  */
 typedef struct mv_linear_grad_desc {
