@@ -48,7 +48,7 @@ template <class T, int N, int E, bool WHOLE> struct RawRow {
 
 template <class T, class P, int N, int E, bool WHOLE, int MOST> __global__ void __launch_bounds__(MOST, MOST == kFewThreads ? 2 : 1) k_norm(const NormArgs a)
 {
-    __shared__ __align__(16) float part[2][2][32];
+    __shared__ __align__(16) float part[2][32];
     const u32 threads = blockDim.x, hidden = a.hidden;
     const bool layer = a.layer;
     Reducer sum = {part, 0, threads / 32};
@@ -161,9 +161,11 @@ template <class T> __global__ void __launch_bounds__(32 * kAddWarps) k_norm_add(
 }
 
 // ---- host ---------------------------------------------------------------
-// Sixteen elements a thread: fewer make the block's sums a larger part of the
-// work, more do not fit the registers of the backward pass (32, for rows
-// that 512 threads would not hold otherwise).  Short rows are one warp's.
+// Sixteen elements a thread: with eight the block's sums are a larger part of the
+// work (16384 x 7168 with both norms 220 us instead of 214, 16384 x 5120 layer 160
+// instead of 128, when they were measured), with 32, for rows that 512 threads would not hold
+// otherwise, registers leave one block an SM.  Rows on no 16-byte boundary have eight, or
+// sixteen where 1024 threads need them.  Short rows are one warp's.
 NormShape shape_of(u32 hidden, u32 size, bool wide)
 {
     const u32 n = wide ? 16 / size : 1, few = wide ? n : 4;
@@ -172,7 +174,8 @@ NormShape shape_of(u32 hidden, u32 size, bool wide)
     return {n, e / n, (threads + 31) / 32 * 32, hidden % (32 * e) == 0, 1};
 }
 
-bool dense(const void *p, u64 stride, u32 n, u32 size) { return !p || (aligned(p, 16) && stride % n == 0 && (n * size == 16)); }
+// rows of pieces of n elements, 16 bytes
+bool dense(const void *p, u64 stride, u32 n) { return !p || (aligned(p, 16) && stride % n == 0); }
 
 int check(const mv_norm_desc *d)
 {
@@ -193,8 +196,8 @@ int check(const mv_norm_desc *d)
 
 bool wide_row(const mv_norm_desc *d)
 {
-    const u32 size = (u32)dtype_size(d->dtype), n = 16 / size;
-    return d->hidden % n == 0 && dense(d->y, d->y_stride, n, size) && dense(d->residual, d->residual_stride, n, size) &&
+    const u32 n = 16 / (u32)dtype_size(d->dtype);
+    return d->hidden % n == 0 && dense(d->y, d->y_stride, n) && dense(d->residual, d->residual_stride, n) &&
            aligned(d->weight, 16) && aligned(d->bias, 16) && aligned(d->post, 16) && aligned(d->post_bias, 16) && aligned(d->gate, 16);
 }
 
@@ -320,8 +323,8 @@ static int check_grad(const mv_norm_desc *d, const mv_norm_grads *g)
 }
 static bool wide_grad(const mv_norm_desc *d, const mv_norm_grads *g)
 {
-    const u32 size = (u32)dtype_size(d->dtype), n = 16 / size;
-    return wide_row(d) && dense(g->dn, g->dn_stride, n, size) && dense(g->dr, g->dr_stride, n, size) && aligned(g->dy, 16) &&
+    const u32 n = 16 / (u32)dtype_size(d->dtype);
+    return wide_row(d) && dense(g->dn, g->dn_stride, n) && dense(g->dr, g->dr_stride, n) && aligned(g->dy, 16) &&
            aligned(g->dresidual, 16) && aligned(g->dgate, 16);
 }
 

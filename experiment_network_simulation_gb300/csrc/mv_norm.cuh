@@ -105,12 +105,12 @@ template <int E> __device__ __forceinline__ float dot_row(const float (&a)[E], c
     return s.x + s.y;
 }
 
-// Sums over the block of one or two values a thread, in a fixed order; the two
-// halves of `part` are used in turn, so that one barrier is enough.  After it
+// Sums over the block of a value a thread, in a fixed order; the two halves of
+// `part` are used in turn, so that one barrier is enough.  After it
 // every thread adds the warps' sums itself: a second round of shuffles would
 // take twice as long.
 struct Reducer {
-    float (*part)[2][32];
+    float (*part)[32];
     u32 turn, warps;
     __device__ __forceinline__ static float warps_sum(const float *p, u32 warps)
     {
@@ -126,50 +126,33 @@ struct Reducer {
     __device__ __forceinline__ void start()         // warps that are not there add nothing
     {
         if (threadIdx.x < 32)
-            for (u32 i = threadIdx.x; i < 128; i += 32) part[0][0][i] = 0.0f;
+            for (u32 i = threadIdx.x; i < 64; i += 32) part[0][i] = 0.0f;
         __syncthreads();
-    }
-    __device__ __forceinline__ float2 operator()(float a, float b)
-    {
-        // the first exchange leaves a to the lower half-warp, b to the upper
-        const bool upper = threadIdx.x & 16;
-        float v = (upper ? b : a) + __shfl_xor_sync(kFull, upper ? a : b, 16);
-        v = group_sum<16>(v);
-        if (warps == 1) return make_float2(__shfl_sync(kFull, v, 0), __shfl_sync(kFull, v, 16));
-        if ((threadIdx.x & 15) == 0) part[turn][upper][threadIdx.x >> 5] = v;
-        __syncthreads();
-        const float2 s = make_float2(warps_sum(part[turn][0], warps), warps_sum(part[turn][1], warps));
-        turn ^= 1;
-        return s;
     }
     __device__ __forceinline__ float operator()(float a)
     {
         a = group_sum<32>(a);
         if (warps == 1) return a;
-        if ((threadIdx.x & 31) == 0) part[turn][0][threadIdx.x >> 5] = a;
+        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = a;
         __syncthreads();
-        const float s = warps_sum(part[turn][0], warps);
+        const float s = warps_sum(part[turn], warps);
         turn ^= 1;
         return s;
     }
 };
 
-// v becomes N(v) without its parameters; its mean (0 where that stays in) and
-// one over what it was divided by come back.  The deviation is taken from the differences to the mean, so a mean
+// v becomes N(v) without its parameters.  The deviation is taken from the differences to the mean, so a mean
 // far from 0 costs it nothing.
-template <int N, bool WHOLE, int E> __device__ __forceinline__ float2 normalise(const NormArgs &a, bool layer, Reducer &sum, float (&v)[E], u32 threads)
+template <int N, bool WHOLE, int E> __device__ __forceinline__ void normalise(const NormArgs &a, bool layer, Reducer &sum, float (&v)[E], u32 threads)
 {
-    float mean = 0.0f;
     hide<N, WHOLE>(a.hidden, threads, v);
     if (layer) {
-        mean = sum(sum_row(v)) * a.inv_hidden;
-        add_row(v, v, -mean);
+        add_row(v, v, -(sum(sum_row(v)) * a.inv_hidden));
         hide<N, WHOLE>(a.hidden, threads, v);
     }
     // divided before they are added up: the sum of a long row's squares may be beyond 32 bits where their mean is not
     const float inverse = rsqrtf(sum(dot_row(v, v) * a.inv_hidden) + a.eps);
     mul_row(v, v, inverse);
-    return make_float2(mean, inverse);
 }
 
 constexpr u32 kMostThreads = MV_NORM_MAX_HIDDEN / 32;   // a block: 32 elements a thread where rows are longest
