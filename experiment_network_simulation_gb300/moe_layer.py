@@ -12,8 +12,9 @@ simulator steps dispatch, that work, and combine over a fabric
 free choice, choice within few groups (a group's experts share a server, so a
 token's copies go to fewer servers), and a balance bias that :func:`balance`
 moves from step to step.  Before the router stand the norm, the residual and the
-router's product of the block (:func:`dense`, :func:`block_step`), whose time a rank
-spends before its dispatch (:func:`dense_ns`).
+router's product of the block (:func:`choose`, :func:`block_step`); their time, the
+same for every router, is measured (:func:`dense_ns`) and is no part of the simulated
+step, which begins with the dispatch.
 
     python -m experiment_network_simulation_gb300.moe_layer
 """
