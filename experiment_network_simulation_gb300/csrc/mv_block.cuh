@@ -10,7 +10,8 @@ namespace mvblock {
 
 using namespace mvmoe;
 
-// 1 / (1 + exp(-v)) to some units of 2^-22 of its value; 0 under -88, where the exponential is infinite.
+// 1 / (1 + exp(-v)) to some units of 2^-22 of its value, and |v| 2^-23 more where v is negative (the
+// exponent's rounding); 0 under -88, where the exponential is infinite.
 __device__ __forceinline__ float logistic(float v) { return reciprocal_fast(1.0f + exp2_fast(-kLog2e * v)); }
 
 constexpr float kRootHalf = 0.70710678118654752f;
