@@ -15,6 +15,8 @@ outputs, workspaces and errors are as there: enqueued on ``stream`` (default:
 the current one of the inputs' device) without waiting, outputs and workspaces
 from torch's allocator, nothing recorded for autograd, ValueError for malformed
 arguments, :class:`.mv.MVError` for what the library refuses, no CPU fallback.
+A product whose kernel waited two seconds in vain (a broken device, or one that was
+stopped) is incomplete, and only :func:`gave_up` tells.
 """
 from __future__ import annotations
 
